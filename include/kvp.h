@@ -76,6 +76,7 @@ typedef enum kvp_status {
 
 enum { KVP_SCORER_LINEAR = 0, KVP_SCORER_MLP = 1, KVP_SCORER_LINEAR_SPLIT = 2 };
 enum { KVP_MASK_KVZAP = 0, KVP_MASK_DMS = 1 };
+enum { KVP_BLOCK8_E4M3 = 0, KVP_BLOCK8_INT8 = 1 };
 
 #define KVP_PAGE_TOKENS 16            /* rows per page of the compacted cache */
 #define KVP_WINDOW_DEFAULT 128        /* KVzap: the last 128 tokens are always kept */
@@ -683,6 +684,194 @@ KVP_API kvp_status kvp_decode_attn_mla(int batch, int n_q_heads, int latent_dim,
                                        const int32_t* page_table, int max_pages, const int32_t* count, int now,
                                        float scale, float* out, int n_splits, void* workspace,
                                        size_t workspace_bytes, int32_t* status, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* The block-scaled 8-bit cache: a paged cache like kvp_compact's whose K and V
+ * rows are all held in 8 bits, with one scale for each page (16 tokens of one
+ * (b, h)) and tensor. It takes the keep rules of the bf16 cache (KVzap summary,
+ * "실제 적용"; DMS article, "지연 삭제 (Delayed Eviction)") and its paging (DeInfer
+ * summary, "나. 페이지드 KV 캐시 및 CUDA Graph 통합"); the BeaconKV article's "low-
+ * precision quantization" fixes no format, and this library's reading is:
+ *
+ *   fmt        KVP_BLOCK8_E4M3 (largest number M = 448) or KVP_BLOCK8_INT8
+ *              (two's complement, M = 127, -128 unused)
+ *   scale      of a set of values whose largest finite magnitude is a: the
+ *              smallest power of two s = 2^e, e >= -126, with a <= M s; 0 when
+ *              a is 0
+ *   code       x / s rounded to nearest even; infinities saturate; a NaN
+ *              becomes E4M3's NaN, or 0 in int8 (s = 0: the same of x itself,
+ *              whose finite values are all 0)
+ *   value      code * s
+ *
+ * With a power of two, x / s is exact and a code is rounded once; a page whose
+ * scale has to grow takes its rows' codes along, exactly in E4M3 (but for
+ * values that become subnormal there) and within half a step of each new
+ * scale in int8, one step of the last scale in all.
+ *
+ * Buffers (device), shared by the calls below:
+ *   kq_pool, vq_pool  uint8 [n_pages_cap, 16, head_dim] codes, 16-byte aligned
+ *   scale_pool        fp32 [n_pages_cap, 2]: K scale, V scale, 16-byte aligned
+ *   expire_pool       int32 [n_pages_cap, 16], as in the bf16 cache
+ *   page_table, remap, count: as kvp_compact's, of widths max_pages and
+ *                     max_pages * 16
+ * head_dim is 64 or 128, B*H at most 65535; status is required.
+ */
+
+/* kvp_compact_block8 - kvp_compact_masked into the block-scaled 8-bit cache:
+ * the mask applied on the fly, the survivors' rows of a page quantised
+ * together as it is written. Counts, page table, remap list and expire values
+ * are kvp_compact_masked's; rows past count in a (b, h)'s pages are zero codes
+ * (expire 0), and reserved pages without rows have scale 0.
+ *
+ * Sources, strides, mode, scores, tau, flag_step, window, delay, now, reserve
+ * and errors: kvp_compact_masked's. n_pos + reserve < 2^31 - 16, and
+ * B * H * ceil((n_pos + reserve) / 16) < 2^31 (else KVP_ERR_UNSUPPORTED).
+ * workspace  device, >= kvp_compact_block8_workspace_bytes(...), 16-byte
+ *            aligned; needs no clearing. Calls that share a workspace must
+ *            not overlap on the GPU.
+ */
+KVP_API size_t kvp_compact_block8_workspace_bytes(int batch, int n_kv_heads, int n_pos, int n_pages_cap);
+KVP_API kvp_status kvp_compact_block8(int fmt, int mode, int batch, int n_kv_heads, int head_dim, int n_pos,
+                                      const void* k_src, const void* v_src,
+                                      int64_t stride_b, int64_t stride_t, int64_t stride_h,
+                                      const float* scores, const float* tau, const int32_t* flag_step,
+                                      int window, int delay, int now, int reserve,
+                                      void* kq_pool, void* vq_pool, float* scale_pool, int32_t* expire_pool,
+                                      int n_pages_cap, int32_t* page_table, int max_pages, int32_t* remap,
+                                      int32_t* count, void* workspace, size_t workspace_bytes, int32_t* status,
+                                      void* stream);
+
+/* kvp_append_block8 - kvp_append into the block-scaled 8-bit cache: the token
+ * at position `pos` goes into slot count[b, h] of every (b, h). The first row
+ * of a page gives the page its scale, whatever it held before; a later row
+ * whose own scale is larger than the page's makes it the page's, and the rows
+ * before it are rounded to the new scale (code * old / new, to nearest even).
+ *
+ * k_new, v_new  device bf16, row (b, h) at b*stride_b + h*stride_h elements
+ *            (each its own strides, >= 0 and multiples of 8), 16-byte aligned:
+ *            views of a step's projection need no copy
+ * Everything else, and the errors: kvp_append's. A (b, h) that records an
+ * error is left unchanged.
+ */
+KVP_API kvp_status kvp_append_block8(int fmt, int mode, int batch, int n_kv_heads, int head_dim, int pos,
+                                     const void* k_new, const void* v_new, int64_t k_stride_b, int64_t k_stride_h,
+                                     int64_t v_stride_b, int64_t v_stride_h,
+                                     const float* score, const float* tau, const int32_t* flag_step,
+                                     int window, int delay, void* kq_pool, void* vq_pool, float* scale_pool,
+                                     int32_t* expire_pool, int n_pages_cap, const int32_t* page_table, int max_pages,
+                                     int32_t* remap, int32_t* count, int32_t* status, void* stream);
+
+/* kvp_append_block8_devpos - kvp_append_block8 with the position read from
+ * device memory, as kvp_append_devpos's.
+ */
+KVP_API kvp_status kvp_append_block8_devpos(int fmt, int mode, int batch, int n_kv_heads, int head_dim,
+                                            const int32_t* pos_dev, const void* k_new, const void* v_new,
+                                            int64_t k_stride_b, int64_t k_stride_h, int64_t v_stride_b,
+                                            int64_t v_stride_h, const float* score, const float* tau,
+                                            const int32_t* flag_step, int window, int delay, void* kq_pool,
+                                            void* vq_pool, float* scale_pool, int32_t* expire_pool, int n_pages_cap,
+                                            const int32_t* page_table, int max_pages, int32_t* remap, int32_t* count,
+                                            int32_t* status, void* stream);
+
+/* kvp_read_block8 - slots first_slot .. first_slot + n_slots - 1 of every
+ * (b, h) back as bf16 rows (to pass a cache on, or to compact it anew from
+ * its remap and expire values): slot s goes to element
+ * b*stride_b + (s - first_slot)*stride_t + h*stride_h of k_out and v_out, as
+ * code * scale rounded to bf16 (exact unless it is a bf16 subnormal). Slots at
+ * or past count[b, h] (clamped to max_pages*16) give zero rows. Expired slots
+ * are read like the others. A page id outside [0, n_pages_cap) records
+ * KVP_ERR_BOUNDS and its slots give zero rows.
+ *
+ * k_out, v_out  device bf16, 16-byte aligned; strides in elements, multiples
+ *            of 8, and at least head_dim along every dimension longer than 1
+ * first_slot, n_slots  >= 0; n_slots 0 does nothing. Slots may lie past the
+ *            page table.
+ */
+KVP_API kvp_status kvp_read_block8(int fmt, int batch, int n_kv_heads, int head_dim, const void* kq_pool,
+                                   const void* vq_pool, const float* scale_pool, int n_pages_cap,
+                                   const int32_t* page_table, int max_pages, const int32_t* count, int first_slot,
+                                   int n_slots, void* k_out, void* v_out, int64_t stride_b, int64_t stride_t,
+                                   int64_t stride_h, int32_t* status, void* stream);
+
+/* kvp_decode_attn_block8 - kvp_decode_attn over the block-scaled 8-bit cache,
+ * with the log-sum-exp of kvp_decode_attn_lse:
+ *
+ *   out[b, j] = sum_i softmax_i(scale * q[b, j] . k_i) v_i
+ *   lse[b, j] = ln sum_i exp(scale * q[b, j] . k_i)
+ *
+ * over the slots i < count[b, h] of kv head h = j / (Hq / H) whose expire is
+ * greater than `now`; an empty set gives a zero row and lse -inf. K and V are
+ * the codes' exact values; products run on the tensor cores (fp16 operands,
+ * fp32 accumulation; the weights as an fp16 pair, about 22 bits).
+ *
+ * Hq a multiple of H, Hq/H from 1 to 8, B*H <= 4096. q device bf16
+ * [B, Hq, head_dim], 16-byte aligned. scale > 0, or 0 for 1/sqrt(head_dim).
+ * out        device fp32 [B, Hq, head_dim], 16-byte aligned
+ * lse        device fp32 [B, Hq] (output), or NULL
+ * grid_limit, count's clamping, page ids out of range, status (may be NULL):
+ *            as kvp_decode_attn
+ * workspace  device, >= kvp_decode_attn_block8_workspace_bytes(...), 16-byte
+ *            aligned, zero-filled before its first use; every call, also one
+ *            that records an error, leaves it ready for the next. Calls that
+ *            share a workspace must not overlap on the GPU.
+ */
+KVP_API size_t kvp_decode_attn_block8_workspace_bytes(int batch, int n_q_heads, int n_kv_heads, int head_dim);
+KVP_API kvp_status kvp_decode_attn_block8(int fmt, int batch, int n_q_heads, int n_kv_heads, int head_dim,
+                                          const void* q, const void* kq_pool, const void* vq_pool,
+                                          const float* scale_pool, const int32_t* expire_pool, int n_pages_cap,
+                                          const int32_t* page_table, int max_pages, const int32_t* count, int now,
+                                          float scale, float* out, float* lse, int grid_limit, void* workspace,
+                                          size_t workspace_bytes, int32_t* status, void* stream);
+
+/* kvp_decode_attn_block8_devpos - the same with the decode position read from
+ * device memory, as kvp_decode_attn_devpos's.
+ */
+KVP_API kvp_status kvp_decode_attn_block8_devpos(int fmt, int batch, int n_q_heads, int n_kv_heads, int head_dim,
+                                                 const void* q, const void* kq_pool, const void* vq_pool,
+                                                 const float* scale_pool, const int32_t* expire_pool, int n_pages_cap,
+                                                 const int32_t* page_table, int max_pages, const int32_t* count,
+                                                 const int32_t* now_dev, float scale, float* out, float* lse,
+                                                 int grid_limit, void* workspace, size_t workspace_bytes,
+                                                 int32_t* status, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* kvp_qk_norm_rope - what a decode step (or a prompt) does to its queries and
+ * keys before kvp_append* and kvp_decode_attn*: the norm of each head's row,
+ * then the position rotation, in one pass. No page describes it; the caches of
+ * this library hold rotated keys, and this makes them.
+ *
+ *   y = x / sqrt(mean(x^2) + eps) * w   (w NULL: y = x)
+ *   the pair (y[i], y[i + rot_dim/2])   (interleaved: (y[2i], y[2i + 1])),
+ *   i < rot_dim/2, is rotated by the angle pos[t] * inv_freq[i]; values from
+ *   rot_dim on are y
+ *
+ * Everything in fp32, rounded to bf16 once at the end. Angles are exact to
+ * about 2^-32 turns at every position: `turns` holds inv_freq[i] / (2 pi) as
+ * 64-bit fixed-point fractions of a turn (kvp_rope_turns makes them, on the
+ * host), and pos * turns is taken modulo one turn in 64-bit integers.
+ *
+ * n_tok      tokens (>= 0; 0 does nothing)
+ * n_q_heads, n_k_heads  >= 0, not both 0; q (k) may be NULL when its count is 0
+ * head_dim   64 or 128;  rot_dim a multiple of 16, 0..head_dim
+ * q, k       device bf16, head h of token t at t*stride_t + h*stride_h
+ *            (elements, each tensor its own, >= 0, multiples of 8), 16-byte
+ *            aligned: views of one projection's output need no copy
+ * pos        device int32 [n_tok] (any value; NULL when rot_dim is 0)
+ * turns      device uint64 [rot_dim / 2], 8-byte aligned (NULL when rot_dim is 0)
+ * wq, wk     device fp32 [head_dim] norm weights, 16-byte aligned, or NULL for no
+ *            norm (of queries, of keys)
+ * eps        >= 0, finite
+ * q_out, k_out  as q, k, strides at least head_dim along every dimension longer
+ *            than 1; each may be its input itself (same address and strides),
+ *            and may not overlap an input otherwise
+ */
+KVP_API kvp_status kvp_rope_turns(int n, const double* inv_freq, uint64_t* turns);
+KVP_API kvp_status kvp_qk_norm_rope(int64_t n_tok, int n_q_heads, int n_k_heads, int head_dim, int rot_dim,
+                                    int interleaved, const void* q, int64_t q_stride_t, int64_t q_stride_h,
+                                    const void* k, int64_t k_stride_t, int64_t k_stride_h, const int32_t* pos,
+                                    const uint64_t* turns, const float* wq, const float* wk, float eps, void* q_out,
+                                    int64_t qo_stride_t, int64_t qo_stride_h, void* k_out, int64_t ko_stride_t,
+                                    int64_t ko_stride_h, void* stream);
 
 #ifdef __cplusplus
 }

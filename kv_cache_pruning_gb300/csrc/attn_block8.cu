@@ -1,0 +1,667 @@
+// kvp_decode_attn_block8: single-query GQA attention over a paged cache held
+// in 8 bits with one power-of-two scale per page for K and one for V.
+//
+//   out[b, j] = sum_i softmax_i(scale q[b, j] . k_i) v_i,  k = ks c_k, v = vs c_v
+//
+// A page's scales leave the sums: its logits are ks times the products of q
+// with the codes, its share of the output is vs times the weighted sum of the
+// codes. So the codes themselves are the tensor-core operands, as fp16 (exact
+// for both formats), and nothing is dequantised to memory.
+//
+// One warp takes a page at a time, in two products of mma.sync m16n8k16:
+//   S = K q^T    16 tokens x 8 query heads, K's codes as the A operand
+//   O += V^T P   16 channels x 8 query heads, V's codes transposed as A
+// Both products may run over their summed index in any order, and the output's
+// channels may sit in any row, so the operands' layouts are chosen such that
+// every lane's fragment is made of 16-byte runs of a page's rows: codes go
+// from global memory straight to registers, with no shared memory, and V's
+// transposition is two byte permutes per pair of tokens. The weights cross
+// from the first product's result to the second's operand by two movmatrix.
+// tcgen05 does not fit here: its smallest tile has 64 or 128 rows of one
+// operand in shared memory, of which a page and 8 heads fill a fraction.
+//
+// Precision: q is scaled by a power of two per head and turned into fp16
+// exactly (but for elements 2^-28 of the largest). The weights
+// (at most 2^15; the largest of a row is 2^12 or more) enter the second product
+// as an fp16 pair hi + lo: 22 bits, and never further off than 2^-25, 2^-37 of
+// the row's sum. With at most 4 heads per kv head the pair fills the 8 columns of one product
+// (hi in columns 0..3, lo in 4..7), with 5 to 8 it takes two. A page's product
+// starts from zero and is added to the fp32 accumulators with the V scale by
+// fused multiply-adds.
+//
+// The running maximum is lazy: it moves only when a logit exceeds it by more
+// than 2^3 (a vote per page), so most pages need no shuffles and no rescaling.
+//
+// Work split: all pages of all (b, h) form one list (b-major, h-minor, page
+// order), cut evenly over the CTAs and, within a CTA, over its warps. Partial
+// results of a (b, h) that several warps share are merged in shared memory;
+// those that several CTAs share go to the workspace, and the last CTA to
+// arrive merges them. Nothing ever waits on another CTA.
+#include "block8.cuh"
+
+namespace kvp {
+namespace {
+
+constexpr int kWarps = 16;
+constexpr int kThreads = kWarps * 32;
+constexpr int kMaxBH = 4096;     // (b, h) pairs whose page prefix fits in shared memory
+constexpr int kMaxCtas = 512;    // grid bound used to size the workspace
+constexpr float kLazy = 3.f;     // how far a base-2 logit may pass the reference before it moves
+constexpr float kBias = 12.f;    // weights are 2^(x - m + kBias): at most 2^(kLazy + kBias) in fp16
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct Params {
+  const uint16_t* q;
+  const uint8_t* k_pool;
+  const uint8_t* v_pool;
+  const float2* scale_pool;
+  const int32_t* expire_pool;
+  const int32_t* page_table;
+  const int32_t* count;
+  const int32_t* now_dev;
+  int BH, G, max_pages, n_pages_cap, now;
+  float qscale;        // scale * log2(e)
+  float* out;          // [B, Hq, D]
+  float* lse;          // [B, Hq] or null
+  int32_t* arrived;    // [BH] counters, zero at entry and exit
+  float* part_acc;     // [2 * grid, G, D]
+  float* part_ml;      // [2 * grid, G, 2]
+  int32_t* status;
+};
+
+KVP_DEV uint32_t movmatrix_trans(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+// d = A B with a zero accumulator.
+KVP_DEV void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// The four codes of a word as two fp16 pairs (codes 0, 1 and 2, 3). int8: the
+// byte with its sign bit flipped becomes 1024 + (c + 128) as fp16 (0x64 in the
+// high byte), less 1152.
+template <int FMT>
+KVP_DEV void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if constexpr (FMT == KVP_BLOCK8_E4M3) {
+    lo = cvt_e4m3x2_to_f16x2(w);
+    hi = cvt_e4m3x2_to_f16x2(w >> 16);
+  } else {
+    const uint32_t u = w ^ 0x80808080u;
+    const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));  // 1152
+    uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 x = __hsub2(*reinterpret_cast<__half2*>(&a), bias), y = __hsub2(*reinterpret_cast<__half2*>(&b), bias);
+    lo = *reinterpret_cast<const uint32_t*>(&x);
+    hi = *reinterpret_cast<const uint32_t*>(&y);
+  }
+}
+
+KVP_DEV uint32_t pack_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// A warp's share of one (b, h): fp32 accumulators, reference and sum of its
+// lane's two heads (2t, 2t + 1; t = lane % 4). Lane (g, t) holds channels
+// g * D/8 .. + D/8 of both heads: acc[i] = {channel 2i head 2t, channel 2i
+// head 2t+1, channel 2i+1 head 2t, channel 2i+1 head 2t+1}.
+template <int D>
+struct State {
+  float acc[D / 16][4];
+  float m[2], l[2];
+  KVP_DEV void clear() {
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[i][c] = 0.f;
+    m[0] = m[1] = -INFINITY;
+    l[0] = l[1] = 0.f;
+  }
+};
+
+// The words of a page that a lane holds. K: row g's (and g + 8's) 16-byte runs
+// t * 16 and, at D = 128, 64 + t * 16. V: the run g * D/8 of the rows 2t,
+// 2t + 1, 2t + 8, 2t + 9.
+template <int D>
+struct KWords {
+  uint32_t w[2][D / 16];
+};
+template <int D>
+struct VWords {
+  uint32_t w[4][D / 32];
+};
+
+template <int D>
+KVP_DEV void load_k(KWords<D>& x, const uint8_t* page, int g, int t) {
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) {
+      const uint4 y = __ldg(reinterpret_cast<const uint4*>(page + (g + 8 * r) * D + c * 64 + t * 16));
+      x.w[r][4 * c] = y.x;
+      x.w[r][4 * c + 1] = y.y;
+      x.w[r][4 * c + 2] = y.z;
+      x.w[r][4 * c + 3] = y.w;
+    }
+}
+template <int D>
+KVP_DEV void load_v(VWords<D>& x, const uint8_t* page, int g, int t) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const uint8_t* row = page + (2 * t + (r & 1) + 8 * (r >> 1)) * D + g * (D / 8);
+    if constexpr (D == 128) {
+      const uint4 y = __ldg(reinterpret_cast<const uint4*>(row));
+      x.w[r][0] = y.x;
+      x.w[r][1] = y.y;
+      x.w[r][2] = y.z;
+      x.w[r][3] = y.w;
+    } else {
+      const uint2 y = __ldg(reinterpret_cast<const uint2*>(row));
+      x.w[r][0] = y.x;
+      x.w[r][1] = y.y;
+    }
+  }
+}
+
+// Shared memory: page prefix, then each warp's two partial results (the (b, h)
+// its range starts in, and the one it ends in).
+template <int D>
+__host__ __device__ constexpr int part_floats(int G) {
+  return (G * (D + 2) + 3) & ~3;
+}
+template <int D>
+size_t smem_bytes(int BH, int G) {
+  return (static_cast<size_t>(BH) + 1 + 3) / 4 * 16 + static_cast<size_t>(kWarps) * 2 * part_floats<D>(G) * 4;
+}
+
+// Writes head h's row: channels' sums over acc (already summed over parts) / l.
+KVP_DEV void write_lse(const Params& p, int64_t row, float m, float l) {
+  if (p.lse != nullptr) p.lse[row] = l > 0.f ? (m - kBias + log2f(l)) * 0.69314718055994531f : (l == 0.f ? -INFINITY : l);
+}
+
+// kDup: at most 4 heads per kv head, hi and lo weights in one product.
+template <int D, int FMT, bool kDup>
+__global__ void __launch_bounds__(kThreads, 1) attn_block8_kernel(const Params p) {
+  extern __shared__ __align__(16) uint8_t sm[];
+  __shared__ int warp_sum[kWarps];
+  __shared__ int part_unit[kWarps][2];
+  __shared__ int last_s;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int G = p.G;
+  int* prefix = reinterpret_cast<int*>(sm);
+  float* parts = reinterpret_cast<float*>(sm + (static_cast<size_t>(p.BH) + 1 + 3) / 4 * 16);
+  const int pf = part_floats<D>(G);
+
+  // ---- pages before each (b, h)
+  const int cap = p.max_pages * kPage;
+  const int each = (p.BH + kThreads - 1) / kThreads;
+  {
+    int sum = 0;
+    for (int i = tid * each; i < min(p.BH, (tid + 1) * each); ++i) sum += (min(max(p.count[i], 0), cap) + kPage - 1) / kPage;
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    if (tid < kWarps * 2) part_unit[tid >> 1][tid & 1] = -1;
+    __syncthreads();
+    int at = incl - sum;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) at += w < warp ? warp_sum[w] : 0;
+    for (int i = tid * each; i < min(p.BH, (tid + 1) * each); ++i) {
+      prefix[i] = at;
+      at += (min(max(p.count[i], 0), cap) + kPage - 1) / kPage;
+    }
+    if (tid == kThreads - 1) prefix[p.BH] = at;
+    __syncthreads();
+  }
+  const int total = prefix[p.BH];
+  const int now = p.now_dev != nullptr ? *p.now_dev : p.now;
+
+  // rows of (b, h) without pages
+  for (int u = blockIdx.x; u < p.BH; u += gridDim.x) {
+    if (prefix[u + 1] > prefix[u]) continue;
+    for (int i = tid; i < G * D; i += kThreads) p.out[static_cast<int64_t>(u) * G * D + i] = 0.f;
+    if (p.lse != nullptr && tid < G) p.lse[static_cast<int64_t>(u) * G + tid] = -INFINITY;
+  }
+
+  // ---- this CTA's and this warp's pages
+  const int ctas = min(static_cast<int>(gridDim.x), (total + kWarps - 1) / kWarps);
+  if (static_cast<int>(blockIdx.x) >= ctas) return;
+  auto cta_begin = [&](int c) { return static_cast<int>(static_cast<int64_t>(c) * total / ctas); };
+  const int c_lo = cta_begin(blockIdx.x), c_hi = cta_begin(blockIdx.x + 1);
+  const int lo = c_lo + static_cast<int>(static_cast<int64_t>(warp) * (c_hi - c_lo) / kWarps);
+  const int hi = c_lo + static_cast<int>(static_cast<int64_t>(warp + 1) * (c_hi - c_lo) / kWarps);
+  // the (b, h) of a page of the list: the last one whose pages start at or before it and that has any
+  auto unit_of = [&](int page) {
+    int a = 0, b = p.BH;
+    while (b - a > 1) {
+      const int mid = (a + b) >> 1;
+      if (prefix[mid] <= page) a = mid; else b = mid;
+    }
+    return a;
+  };
+
+  if (lo < hi) {
+    int at = lo;
+    int u = unit_of(lo);
+    while (at < hi) {
+      while (prefix[u + 1] <= at) ++u;
+      const int u_lo = prefix[u], u_hi = prefix[u + 1];
+      const int end = min(hi, u_hi);
+      const int cnt = min(max(p.count[u], 0), cap);
+      const int32_t* table = p.page_table + static_cast<int64_t>(u) * p.max_pages - u_lo;
+
+      // ---- this (b, h)'s queries as B fragments: lane (g, t) holds head g (kDup: g % 4), its words' channels
+      uint32_t qf[D / 16][2];
+      float qs[2];   // logits' factors of the lane's heads 2t, 2t + 1
+      {
+        const int head = kDup ? (g & 3) : g;
+        const uint16_t* row = p.q + (static_cast<int64_t>(u) * G + head) * D;
+        uint4 x[D / 32];
+        uint32_t big = 0;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          x[i] = make_uint4(0, 0, 0, 0);
+          if (head < G) x[i] = *reinterpret_cast<const uint4*>(row + (i >> 1) * 64 + t * 16 + (i & 1) * 8);
+          big = __vmaxu2(big, __vmaxu2(__vmaxu2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu),
+                                       __vmaxu2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu)));
+        }
+        uint32_t a = max(big & 0xFFFFu, big >> 16);
+        a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+        a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
+        // the head's largest element to 2^14 .. 2^15 (a row that is not finite keeps its infinities and NaNs)
+        const int e = min(max(static_cast<int>(a >> 7), 16), 254);   // biased exponent
+        const float up = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          // words 4 (i >> 1) + 2 (i & 1) and the next: 4 channels each
+          qf[2 * i][0] = pack_half2(bf16_lo(x[i].x) * up, bf16_hi(x[i].x) * up);
+          qf[2 * i][1] = pack_half2(bf16_lo(x[i].y) * up, bf16_hi(x[i].y) * up);
+          qf[2 * i + 1][0] = pack_half2(bf16_lo(x[i].z) * up, bf16_hi(x[i].z) * up);
+          qf[2 * i + 1][1] = pack_half2(bf16_lo(x[i].w) * up, bf16_hi(x[i].w) * up);
+        }
+        const float f = p.qscale / up;
+        qs[0] = __shfl_sync(0xffffffffu, f, 4 * (2 * t));
+        qs[1] = __shfl_sync(0xffffffffu, f, 4 * (2 * t + 1));
+      }
+
+      State<D> s;
+      s.clear();
+      for (int i = at; i < end; ++i) {
+        int pg = table[i];
+        const bool good = pg >= 0 && pg < p.n_pages_cap;
+        if (!good) {
+          if (lane == 0) record_error(p.status, KVP_ERR_BOUNDS);
+          continue;
+        }
+        KWords<D> kw;
+        VWords<D> vw;
+        const int64_t row0 = static_cast<int64_t>(pg) * kPage;
+        load_k<D>(kw, p.k_pool + row0 * D, g, t);
+        load_v<D>(vw, p.v_pool + row0 * D, g, t);
+        const float2 sc = p.scale_pool[pg];
+        const int slot = (i - u_lo) * kPage;
+        const bool in0 = slot + g < cnt && p.expire_pool[row0 + g] > now;
+        const bool in1 = slot + g + 8 < cnt && p.expire_pool[row0 + g + 8] > now;
+
+        float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+          uint32_t a0, a1, a2, a3;
+          codes_to_f16<FMT>(kw.w[0][j], a0, a2);
+          codes_to_f16<FMT>(kw.w[1][j], a1, a3);
+          mma_f16_16816(x, a0, a1, a2, a3, qf[j][0], qf[j][1]);
+        }
+        const float f0 = qs[0] * sc.x, f1 = qs[1] * sc.x;
+        x[0] = in0 ? x[0] * f0 : -INFINITY;
+        x[1] = in0 ? x[1] * f1 : -INFINITY;
+        x[2] = in1 ? x[2] * f0 : -INFINITY;
+        x[3] = in1 ? x[3] * f1 : -INFINITY;
+        // a reference that has fallen behind (or none yet) moves to the page's maximum
+        const float top0 = fmaxf(x[0], x[2]), top1 = fmaxf(x[1], x[3]);
+        if (__any_sync(0xffffffffu, top0 > s.m[0] + kLazy || top1 > s.m[1] + kLazy)) {
+          float m0 = top0, m1 = top1;
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) {
+            m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+            m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+          }
+          m0 = fmaxf(m0, s.m[0]);
+          m1 = fmaxf(m1, s.m[1]);
+          const float r0 = m0 == s.m[0] ? 1.f : ex2_approx(s.m[0] - m0), r1 = m1 == s.m[1] ? 1.f : ex2_approx(s.m[1] - m1);
+          s.m[0] = m0;
+          s.m[1] = m1;
+          s.l[0] *= r0;
+          s.l[1] *= r1;
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) {
+            s.acc[j][0] *= r0;
+            s.acc[j][1] *= r1;
+            s.acc[j][2] *= r0;
+            s.acc[j][3] *= r1;
+          }
+        }
+        // a head whose reference is still -inf has only -inf logits: weight 0, not NaN
+        const float c0 = s.m[0] == -INFINITY ? 0.f : kBias - s.m[0], c1 = s.m[1] == -INFINITY ? 0.f : kBias - s.m[1];
+        const float w0 = ex2_approx(x[0] + c0), w1 = ex2_approx(x[1] + c1);
+        const float w2 = ex2_approx(x[2] + c0), w3 = ex2_approx(x[3] + c1);
+        s.l[0] += w0 + w2;
+        s.l[1] += w1 + w3;
+        const uint32_t h0 = pack_half2(w0, w1), h1 = pack_half2(w2, w3);
+        const float2 q0 = __half22float2(*reinterpret_cast<const __half2*>(&h0));
+        const float2 q1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
+        const uint32_t e0 = pack_half2(w0 - q0.x, w1 - q0.y), e1 = pack_half2(w2 - q1.x, w3 - q1.y);
+        uint32_t b0, b1, d0 = 0, d1 = 0;
+        if constexpr (kDup) {
+          b0 = movmatrix_trans(t < 2 ? h0 : e0);
+          b1 = movmatrix_trans(t < 2 ? h1 : e1);
+        } else {
+          b0 = movmatrix_trans(h0);
+          b1 = movmatrix_trans(h1);
+          d0 = movmatrix_trans(e0);
+          d1 = movmatrix_trans(e1);
+        }
+        // a masked token's codes may be anything (an E4M3 NaN times a zero weight is NaN): its words become zero
+        const unsigned live0 = __ballot_sync(0xffffffffu, in0), live1 = __ballot_sync(0xffffffffu, in1);
+        if ((live0 & live1) != 0xffffffffu) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            // row 2t + (r & 1) + 8 (r >> 1): its flag is lane 4 * row's
+            const bool on = ((r >> 1 ? live1 : live0) >> (4 * (2 * t + (r & 1)))) & 1u;
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w) vw.w[r][w] = on ? vw.w[r][w] : 0u;
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) {
+          // byte pairs (token 2t, token 2t + 1) of channels 4w, 4w + 1 | 4w + 2, 4w + 3, and of tokens 2t + 8, 2t + 9
+          const uint32_t ab0 = __byte_perm(vw.w[0][w], vw.w[1][w], 0x5140), ab1 = __byte_perm(vw.w[0][w], vw.w[1][w], 0x7362);
+          const uint32_t cd0 = __byte_perm(vw.w[2][w], vw.w[3][w], 0x5140), cd1 = __byte_perm(vw.w[2][w], vw.w[3][w], 0x7362);
+          uint32_t a0, a1, a2, a3;
+          float y[4];
+          codes_to_f16<FMT>(ab0, a0, a1);
+          codes_to_f16<FMT>(cd0, a2, a3);
+          mma_f16_zero(y, a0, a1, a2, a3, b0, b1);
+          if constexpr (!kDup) mma_f16_16816(y, a0, a1, a2, a3, d0, d1);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) s.acc[2 * w][c] = fmaf(y[c], sc.y, s.acc[2 * w][c]);
+          codes_to_f16<FMT>(ab1, a0, a1);
+          codes_to_f16<FMT>(cd1, a2, a3);
+          mma_f16_zero(y, a0, a1, a2, a3, b0, b1);
+          if constexpr (!kDup) mma_f16_16816(y, a0, a1, a2, a3, d0, d1);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) s.acc[2 * w + 1][c] = fmaf(y[c], sc.y, s.acc[2 * w + 1][c]);
+        }
+      }
+
+      // ---- the warp's share of this (b, h) is done
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        s.l[0] += __shfl_xor_sync(0xffffffffu, s.l[0], o);
+        s.l[1] += __shfl_xor_sync(0xffffffffu, s.l[1], o);
+      }
+      if constexpr (kDup) {  // lanes t and t + 2 hold the hi and the lo products of the same heads
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) s.acc[j][c] += __shfl_xor_sync(0xffffffffu, s.acc[j][c], 2);
+      }
+      const bool whole = at == u_lo && end == u_hi;
+      // partial 0: the (b, h) the range starts in, unless it starts there too and ends elsewhere
+      const int which = at == lo && !(at == u_lo) ? 0 : (end == u_hi ? 0 : 1);
+      float* part = parts + (warp * 2 + which) * pf;
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        const int head = 2 * t + hh;
+        if (head < G && (!kDup || t < 2)) {
+          float* dst = whole ? p.out + (static_cast<int64_t>(u) * G + head) * D : part + head * D;
+          const float inv = whole ? (s.l[hh] == 0.f ? 0.f : 1.f / s.l[hh]) : 1.f;
+#pragma unroll
+          for (int j = 0; j < D / 32; ++j)
+            reinterpret_cast<float4*>(dst + g * (D / 8))[j] =
+                make_float4(s.acc[2 * j][hh] * inv, s.acc[2 * j][2 + hh] * inv, s.acc[2 * j + 1][hh] * inv,
+                            s.acc[2 * j + 1][2 + hh] * inv);
+          if (g == 0) {
+            if (whole) {
+              write_lse(p, static_cast<int64_t>(u) * G + head, s.m[hh], s.l[hh]);
+            } else {
+              part[G * D + 2 * head] = s.m[hh];
+              part[G * D + 2 * head + 1] = s.l[hh];
+            }
+          }
+        }
+      }
+      if (!whole && lane == 0) part_unit[warp][which] = u;
+      at = end;
+    }
+  }
+  __syncthreads();
+
+  // ---- merge the CTA's partial results, one (b, h) after another; a run of entries of one (b, h) starts at its first
+  for (int e = 0; e < 2 * kWarps; ++e) {
+    const int u = part_unit[e >> 1][e & 1];
+    if (u < 0) continue;
+    int last = e;
+    bool start = true;
+    for (int k = e - 1; k >= 0; --k) {
+      const int v = part_unit[k >> 1][k & 1];
+      if (v >= 0) {
+        start = v != u;
+        break;
+      }
+    }
+    if (!start) continue;
+    for (int k = e + 1; k < 2 * kWarps; ++k)
+      if (part_unit[k >> 1][k & 1] == u) last = k;
+    const int u_lo = prefix[u], u_hi = prefix[u + 1];
+    const bool whole = u_lo >= c_lo && u_hi <= c_hi;
+    const int slot = blockIdx.x * 2 + (u_lo <= c_lo ? 0 : 1);
+    for (int i = tid; i < G * D / 4; i += kThreads) {
+      const int head = i / (D / 4);
+      float m = -INFINITY;
+      for (int k = e; k <= last; ++k)
+        if (part_unit[k >> 1][k & 1] == u) m = fmaxf(m, parts[k * pf + G * D + 2 * head]);
+      float l = 0.f;
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = e; k <= last; ++k) {
+        if (part_unit[k >> 1][k & 1] != u) continue;
+        const float* part = parts + k * pf;
+        const float pm = part[G * D + 2 * head];
+        const float w = pm == m ? 1.f : ex2_approx(pm - m);
+        const float4 x = *reinterpret_cast<const float4*>(part + 4 * i);
+        l = fmaf(w, part[G * D + 2 * head + 1], l);
+        a.x = fmaf(w, x.x, a.x);
+        a.y = fmaf(w, x.y, a.y);
+        a.z = fmaf(w, x.z, a.z);
+        a.w = fmaf(w, x.w, a.w);
+      }
+      if (whole) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        reinterpret_cast<float4*>(p.out + static_cast<int64_t>(u) * G * D)[i] =
+            make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+        if (i % (D / 4) == 0) write_lse(p, static_cast<int64_t>(u) * G + head, m, l);
+      } else {
+        reinterpret_cast<float4*>(p.part_acc + static_cast<int64_t>(slot) * G * D)[i] = a;
+        if (i % (D / 4) == 0)
+          reinterpret_cast<float2*>(p.part_ml)[static_cast<int64_t>(slot) * G + head] = make_float2(m, l);
+      }
+    }
+    if (whole) continue;
+
+    // ---- shared with other CTAs: the last one to arrive merges
+    auto cta_of = [&](int page) {
+      int c = static_cast<int>(static_cast<int64_t>(page) * ctas / total);
+      while (cta_begin(c + 1) <= page) ++c;
+      while (cta_begin(c) > page) --c;
+      return c;
+    };
+    const int first_cta = cta_of(u_lo), last_cta = cta_of(u_hi - 1);
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) last_s = atomicAdd(&p.arrived[u], 1) == last_cta - first_cta;
+    __syncthreads();
+    if (last_s) {
+      __threadfence();
+      for (int i = tid; i < G * D / 4; i += kThreads) {
+        const int head = i / (D / 4);
+        float m = -INFINITY;
+        for (int c = first_cta; c <= last_cta; ++c) {
+          const int sl = c * 2 + (u_lo <= cta_begin(c) ? 0 : 1);
+          m = fmaxf(m, __ldcg(p.part_ml + (static_cast<int64_t>(sl) * G + head) * 2));
+        }
+        float l = 0.f;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = first_cta; c <= last_cta; ++c) {
+          const int sl = c * 2 + (u_lo <= cta_begin(c) ? 0 : 1);
+          const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + static_cast<int64_t>(sl) * G + head);
+          const float w = ml.x == m ? 1.f : ex2_approx(ml.x - m);
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(p.part_acc + static_cast<int64_t>(sl) * G * D) + i);
+          l = fmaf(w, ml.y, l);
+          a.x = fmaf(w, x.x, a.x);
+          a.y = fmaf(w, x.y, a.y);
+          a.z = fmaf(w, x.z, a.z);
+          a.w = fmaf(w, x.w, a.w);
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        reinterpret_cast<float4*>(p.out + static_cast<int64_t>(u) * G * D)[i] =
+            make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+        if (i % (D / 4) == 0) write_lse(p, static_cast<int64_t>(u) * G + head, m, l);
+      }
+      if (tid == 0) p.arrived[u] = 0;
+    }
+  }
+}
+
+int device_sms() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return 0;
+  }
+  return n;
+}
+
+bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+size_t counters_bytes(int64_t BH) { return static_cast<size_t>((BH * 4 + 15) & ~int64_t{15}); }
+size_t attn_ws_bytes(int64_t BH, int G, int D) {
+  return counters_bytes(BH) + static_cast<size_t>(2) * kMaxCtas * G * (D + 2) * sizeof(float);
+}
+
+template <int D, int FMT, bool kDup>
+kvp_status launch(const Params& p, int grid, cudaStream_t st) {
+  const size_t smem = smem_bytes<D>(p.BH, p.G);
+  // per device, so set at every call (it is a host-side attribute write)
+  if (cudaFuncSetAttribute(attn_block8_kernel<D, FMT, kDup>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(smem)) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return KVP_ERR_CUDA;
+  }
+  return launch_pdl(attn_block8_kernel<D, FMT, kDup>, dim3(grid), dim3(kThreads), smem, st, p) == cudaSuccess
+             ? KVP_OK
+             : KVP_ERR_CUDA;
+}
+
+kvp_status attn_block8_impl(int fmt, int batch, int n_q_heads, int n_kv_heads, int head_dim, const void* q,
+                            const void* kq_pool, const void* vq_pool, const float* scale_pool,
+                            const int32_t* expire_pool, int n_pages_cap, const int32_t* page_table, int max_pages,
+                            const int32_t* count, int now, const int32_t* now_dev, float scale, float* out, float* lse,
+                            int grid_limit, void* workspace, size_t workspace_bytes, int32_t* status, void* stream) {
+  if (fmt != KVP_BLOCK8_E4M3 && fmt != KVP_BLOCK8_INT8) return KVP_ERR_INVALID;
+  if (batch <= 0 || n_q_heads <= 0 || n_kv_heads <= 0 || max_pages < 0 || n_pages_cap < 0 || grid_limit < 0)
+    return KVP_ERR_INVALID;
+  if (!(scale >= 0.f) || scale > 3.402823466e38f) return KVP_ERR_INVALID;
+  if (head_dim != 64 && head_dim != 128) return KVP_ERR_UNSUPPORTED;
+  if (n_q_heads % n_kv_heads != 0) return KVP_ERR_UNSUPPORTED;
+  const int G = n_q_heads / n_kv_heads;
+  const int64_t BH = static_cast<int64_t>(batch) * n_kv_heads;
+  if (G > 8 || BH > kMaxBH) return KVP_ERR_UNSUPPORTED;
+  if (BH * max_pages > 0x7fffffff || static_cast<int64_t>(max_pages) * kPage > 0x7fffffff) return KVP_ERR_UNSUPPORTED;
+  if (q == nullptr || kq_pool == nullptr || vq_pool == nullptr || scale_pool == nullptr || expire_pool == nullptr ||
+      page_table == nullptr || count == nullptr || out == nullptr)
+    return KVP_ERR_INVALID;
+  if (!al16(q) || !al16(kq_pool) || !al16(vq_pool) || !al16(scale_pool) || !al16(out)) return KVP_ERR_ALIGN;
+  if ((reinterpret_cast<uintptr_t>(now_dev) & 3u) != 0 || (reinterpret_cast<uintptr_t>(lse) & 3u) != 0)
+    return KVP_ERR_ALIGN;
+  if (workspace == nullptr || workspace_bytes < attn_ws_bytes(BH, G, head_dim)) return KVP_ERR_WORKSPACE;
+  if (!al16(workspace)) return KVP_ERR_ALIGN;
+  const int sms = device_sms();
+  if (sms == 0) return KVP_ERR_CUDA;
+  int grid = sms < kMaxCtas ? sms : kMaxCtas;
+  if (grid_limit > 0 && grid_limit < grid) grid = grid_limit;
+  Params p;
+  p.q = static_cast<const uint16_t*>(q);
+  p.k_pool = static_cast<const uint8_t*>(kq_pool);
+  p.v_pool = static_cast<const uint8_t*>(vq_pool);
+  p.scale_pool = reinterpret_cast<const float2*>(scale_pool);
+  p.expire_pool = expire_pool;
+  p.page_table = page_table;
+  p.count = count;
+  p.now_dev = now_dev;
+  p.BH = static_cast<int>(BH);
+  p.G = G;
+  p.max_pages = max_pages;
+  p.n_pages_cap = n_pages_cap;
+  p.now = now;
+  p.qscale = (scale > 0.f ? scale : 1.f / sqrtf(static_cast<float>(head_dim))) * kLog2e;
+  p.out = out;
+  p.lse = lse;
+  p.arrived = static_cast<int32_t*>(workspace);
+  p.part_acc = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + counters_bytes(BH));
+  p.part_ml = p.part_acc + static_cast<size_t>(2) * kMaxCtas * G * head_dim;
+  p.status = status;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool dup = G <= 4;
+#define KVP_ATTN8(D, F) (dup ? launch<D, F, true>(p, grid, st) : launch<D, F, false>(p, grid, st))
+  if (fmt == KVP_BLOCK8_E4M3) return head_dim == 128 ? KVP_ATTN8(128, KVP_BLOCK8_E4M3) : KVP_ATTN8(64, KVP_BLOCK8_E4M3);
+  return head_dim == 128 ? KVP_ATTN8(128, KVP_BLOCK8_INT8) : KVP_ATTN8(64, KVP_BLOCK8_INT8);
+#undef KVP_ATTN8
+}
+
+}  // namespace
+}  // namespace kvp
+
+using namespace kvp;
+
+extern "C" size_t kvp_decode_attn_block8_workspace_bytes(int batch, int n_q_heads, int n_kv_heads, int head_dim) {
+  if (batch <= 0 || n_q_heads <= 0 || n_kv_heads <= 0 || n_q_heads % n_kv_heads != 0) return 0;
+  if (head_dim != 64 && head_dim != 128) return 0;
+  const int64_t BH = static_cast<int64_t>(batch) * n_kv_heads;
+  if (n_q_heads / n_kv_heads > 8 || BH > kMaxBH) return 0;
+  return attn_ws_bytes(BH, n_q_heads / n_kv_heads, head_dim);
+}
+
+extern "C" kvp_status kvp_decode_attn_block8(int fmt, int batch, int n_q_heads, int n_kv_heads, int head_dim,
+                                             const void* q, const void* kq_pool, const void* vq_pool,
+                                             const float* scale_pool, const int32_t* expire_pool, int n_pages_cap,
+                                             const int32_t* page_table, int max_pages, const int32_t* count, int now,
+                                             float scale, float* out, float* lse, int grid_limit, void* workspace,
+                                             size_t workspace_bytes, int32_t* status, void* stream) {
+  return attn_block8_impl(fmt, batch, n_q_heads, n_kv_heads, head_dim, q, kq_pool, vq_pool, scale_pool, expire_pool,
+                          n_pages_cap, page_table, max_pages, count, now, nullptr, scale, out, lse, grid_limit,
+                          workspace, workspace_bytes, status, stream);
+}
+
+extern "C" kvp_status kvp_decode_attn_block8_devpos(int fmt, int batch, int n_q_heads, int n_kv_heads, int head_dim,
+                                                    const void* q, const void* kq_pool, const void* vq_pool,
+                                                    const float* scale_pool, const int32_t* expire_pool,
+                                                    int n_pages_cap, const int32_t* page_table, int max_pages,
+                                                    const int32_t* count, const int32_t* now_dev, float scale,
+                                                    float* out, float* lse, int grid_limit, void* workspace,
+                                                    size_t workspace_bytes, int32_t* status, void* stream) {
+  if (now_dev == nullptr) return KVP_ERR_INVALID;
+  return attn_block8_impl(fmt, batch, n_q_heads, n_kv_heads, head_dim, q, kq_pool, vq_pool, scale_pool, expire_pool,
+                          n_pages_cap, page_table, max_pages, count, 0, now_dev, scale, out, lse, grid_limit, workspace,
+                          workspace_bytes, status, stream);
+}

@@ -1,0 +1,581 @@
+// kvp_compact_block8, kvp_append_block8, kvp_append_block8_devpos and
+// kvp_read_block8: writing and reading a paged cache held in 8 bits with one
+// scale per page (16 tokens of one (b, h)) for K and one for V.
+//
+// The bulk write runs four passes. The count pass is the other compactions'
+// (present entries per 128-entry segment and per (b, h)). The list pass, one
+// warp per segment, writes the remapping list, the expire values and the page
+// table, and names each page's owner. The page pass gives one warp a page: it
+// gathers the page's 16 K and V rows through the list (all 16 row loads of a
+// lane in flight before the first is used), takes the two largest magnitudes,
+// and writes codes and scales, so every row is read once and every code
+// written once. Pages are dealt out by their ids over a persistent grid, which
+// keeps the warps even whatever the (b, h)'s counts are.
+#include "block8.cuh"
+#include "compact_prep.cuh"
+
+namespace kvp {
+namespace {
+
+// Workspace: the preparation passes' words, then the number of pages in use,
+// then each page's owner (its (b, h) and its index in that (b, h)).
+size_t prep_bytes(int64_t BH, int NS) { return (compact_ws_bytes(BH, NS) + 15) & ~static_cast<size_t>(15); }
+size_t block8_ws_bytes(int64_t BH, int NS, int n_pages_cap) {
+  return prep_bytes(BH, NS) + 16 + static_cast<size_t>(n_pages_cap) * sizeof(int2);
+}
+
+// ------------------------------------------------------------------ list pass
+template <bool kFused>
+__global__ void __launch_bounds__(kWarpsPerCta * 32) list_kernel(MaskedSrc src, int now, int NS, int reserve,
+                                                                  int max_pages, int n_pages_cap, int BH, CompactWs ws,
+                                                                  const int32_t* __restrict__ count,
+                                                                  int32_t* __restrict__ status,
+                                                                  int32_t* __restrict__ expire_pool,
+                                                                  int32_t* __restrict__ page_table,
+                                                                  int32_t* __restrict__ remap,
+                                                                  int32_t* __restrict__ n_used,
+                                                                  int2* __restrict__ owner) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int bh = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sg = blockIdx.y * kWarpsPerCta + warp;
+  const bool live = sg < NS;
+  const bool first_cta = blockIdx.x == 0 && blockIdx.y == 0;
+
+  // loads that do not depend on one another, all issued first
+  const auto sv = src.view(bh);
+  const int n = sv.length();
+  const int lo = sg * kSeg, hi = min(lo + kSeg, n);
+  int32_t exps[kSeg / 32];
+#pragma unroll
+  for (int u = 0; u < kSeg / 32; ++u) {
+    const int t = lo + u * 32 + lane;
+    int64_t row;
+    exps[u] = live && t < hi ? sv.expire_row(t, row) : 0;
+  }
+  int slot0 = 0;
+  if (live)
+    for (int c0 = 0; c0 < sg; c0 += 32)
+      slot0 += c0 + lane < sg ? ws.seg_cnt[static_cast<int64_t>(bh) * NS + c0 + lane] : 0;
+  int base;
+  if constexpr (kFused) {
+    __shared__ int64_t red_s[3][kWarpsPerCta];
+    int64_t before = 0, total = 0, bad = 0;
+    for (int i = threadIdx.x; i < BH; i += kWarpsPerCta * 32) {
+      const int64_t pg = (static_cast<int64_t>(count[i]) + reserve + kPage - 1) / kPage;
+      before += i < bh ? pg : 0;
+      total += pg;
+      bad |= pg > max_pages;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      before += __shfl_xor_sync(0xffffffffu, before, o);
+      total += __shfl_xor_sync(0xffffffffu, total, o);
+      bad |= __shfl_xor_sync(0xffffffffu, bad, o);
+    }
+    if (lane == 0) {
+      red_s[0][warp] = before;
+      red_s[1][warp] = total;
+      red_s[2][warp] = bad;
+    }
+    __syncthreads();
+    before = total = bad = 0;
+#pragma unroll
+    for (int w = 0; w < kWarpsPerCta; ++w) {
+      before += red_s[0][w];
+      total += red_s[1][w];
+      bad |= red_s[2][w];
+    }
+    const bool ok = !bad && total <= n_pages_cap;
+    if (first_cta && threadIdx.x == 0) {
+      *n_used = ok ? static_cast<int32_t>(total) : 0;
+      if (!ok) record_error(status, KVP_ERR_CAPACITY);
+    }
+    if (!ok) return;
+    base = static_cast<int>(before);
+  } else {
+    const bool ok = ws.ok[0] != 0;
+    if (first_cta && threadIdx.x == 0)
+      *n_used = ok ? static_cast<int32_t>(ws.base[BH - 1] + (static_cast<int64_t>(count[BH - 1]) + reserve + kPage - 1) / kPage)
+                   : 0;
+    if (!ok) return;
+    base = ws.base[bh];
+  }
+  if (!live) return;
+  slot0 = __reduce_add_sync(0xffffffffu, slot0);
+  const int cnt = count[bh];
+  const int pages = static_cast<int>((static_cast<int64_t>(cnt) + reserve + kPage - 1) / kPage);
+  const int64_t cap = static_cast<int64_t>(max_pages) * kPage;
+  int32_t* remap_bh = remap + bh * cap;
+  // this segment's share of the page-table row, the owners and the remap tail
+  const int seg = (max_pages + NS - 1) / NS;
+  for (int64_t p = static_cast<int64_t>(sg) * seg + lane; p < min(static_cast<int64_t>(max_pages), (sg + int64_t{1}) * seg);
+       p += 32) {
+    page_table[static_cast<int64_t>(bh) * max_pages + p] = p < pages ? base + static_cast<int>(p) : -1;
+    if (p < pages) owner[base + p] = make_int2(bh, static_cast<int>(p));
+  }
+  const int64_t rseg = (cap + NS - 1) / NS;
+  const int64_t rlo = sg * rseg > cnt ? sg * rseg : static_cast<int64_t>(cnt);
+  for (int64_t j = rlo + lane; j < min(cap, (sg + 1) * rseg); j += 32) remap_bh[j] = -1;
+
+  int nk = 0;
+#pragma unroll
+  for (int u = 0; u < kSeg / 32; ++u) {
+    const int t = lo + u * 32 + lane;
+    const int32_t e = exps[u];
+    const bool keep = t < hi && sv.keep(e, now);
+    const unsigned bal = __ballot_sync(0xffffffffu, keep);
+    if (keep) {
+      const int j = slot0 + nk + __popc(bal & ((1u << lane) - 1u));
+      expire_pool[static_cast<int64_t>(base + (j >> 4)) * kPage + (j & 15)] = e;
+      remap_bh[j] = t;
+    }
+    nk += __popc(bal);
+  }
+}
+
+// ------------------------------------------------------------------ page pass
+constexpr int kPageWarps = 8;  // warps per CTA of the page and read passes
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(kPageWarps * 32) page_kernel(const uint16_t* __restrict__ k,
+                                                               const uint16_t* __restrict__ v, int64_t sb, int64_t st,
+                                                               int64_t sh, int H, const int32_t* __restrict__ n_used,
+                                                               const int2* __restrict__ owner,
+                                                               const int32_t* __restrict__ count, int max_pages,
+                                                               const int32_t* __restrict__ remap,
+                                                               uint8_t* __restrict__ kq_pool,
+                                                               uint8_t* __restrict__ vq_pool,
+                                                               float2* __restrict__ scale_pool,
+                                                               int32_t* __restrict__ expire_pool) {
+  constexpr int LPR = D / 8;          // lanes a row takes, 16 bytes each
+  constexpr int RPI = 32 / LPR;       // rows a warp instruction takes
+  constexpr int NI = kPage / RPI;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, piece = lane % LPR, sub = lane / LPR;
+  const int total = *n_used;
+  for (int pg = blockIdx.x * kPageWarps + (threadIdx.x >> 5); pg < total; pg += gridDim.x * kPageWarps) {
+    const int2 ow = owner[pg];
+    const int b = ow.x / H, h = ow.x - b * H;
+    const int64_t first = static_cast<int64_t>(ow.y) * kPage;
+    const int n = static_cast<int>(min(max(count[ow.x] - first, int64_t{0}), int64_t{kPage}));
+    const int32_t mine = lane < n ? remap[static_cast<int64_t>(ow.x) * max_pages * kPage + first + lane] : 0;
+    const int64_t off = b * sb + h * sh + piece * 8;
+    uint4 kw[NI], vw[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int r = i * RPI + sub;
+      const int64_t at = off + __shfl_sync(0xffffffffu, mine, r) * st;
+      kw[i] = vw[i] = make_uint4(0, 0, 0, 0);
+      if (r < n) {
+        kw[i] = *reinterpret_cast<const uint4*>(k + at);
+        vw[i] = *reinterpret_cast<const uint4*>(v + at);
+      }
+    }
+    uint32_t ka = 0, va = 0;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      ka = __vmaxu2(ka, __vmaxu2(__vmaxu2(finite_abs2(kw[i].x), finite_abs2(kw[i].y)),
+                                 __vmaxu2(finite_abs2(kw[i].z), finite_abs2(kw[i].w))));
+      va = __vmaxu2(va, __vmaxu2(__vmaxu2(finite_abs2(vw[i].x), finite_abs2(vw[i].y)),
+                                 __vmaxu2(finite_abs2(vw[i].z), finite_abs2(vw[i].w))));
+    }
+    ka = __reduce_max_sync(0xffffffffu, max(ka & 0xFFFFu, ka >> 16));
+    va = __reduce_max_sync(0xffffffffu, max(va & 0xFFFFu, va >> 16));
+    const uint32_t ks = scale_bits_for<FMT>(ka), vs = scale_bits_for<FMT>(va);
+    const float ki = inverse_of_scale(ks), vi = inverse_of_scale(vs);
+    const int64_t row0 = static_cast<int64_t>(pg) * kPage;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int64_t at = (row0 + i * RPI + sub) * D + piece * 8;
+      *reinterpret_cast<uint2*>(kq_pool + at) = encode8<FMT>(kw[i], ki);
+      *reinterpret_cast<uint2*>(vq_pool + at) = encode8<FMT>(vw[i], vi);
+    }
+    if (lane == 0) scale_pool[pg] = make_float2(__uint_as_float(ks), __uint_as_float(vs));
+    if (lane >= n && lane < kPage) expire_pool[row0 + lane] = 0;
+  }
+}
+
+// ------------------------------------------------------------------ append
+constexpr int kAppendWarps = 4;
+
+// One row (x, EPL bf16 values a lane, element 0 in the low half of x.x) into
+// row r of a page whose scale is `old` (0 when r is 0): returns the page's scale.
+template <int D, int FMT>
+KVP_DEV uint32_t append_row(uint2 x, uint8_t* page, int r, uint32_t old, int lane) {
+  constexpr int EPL = D / 32;
+  uint32_t a = finite_abs2(x.x);
+  if constexpr (EPL == 4) a = __vmaxu2(a, finite_abs2(x.y));
+  a = __reduce_max_sync(0xffffffffu, max(a & 0xFFFFu, a >> 16));
+  const uint32_t mine = scale_bits_for<FMT>(a);
+  const uint32_t now = max(old, mine);  // positive floats order like their bits
+  if (now > old && old != 0) {          // the rows before this one take the larger scale (0: they are zero codes)
+    const float ratio = __fdiv_rn(__uint_as_float(old), __uint_as_float(now));
+    for (int i = lane; i < r * D / 16; i += 32) {
+      uint4 w = reinterpret_cast<uint4*>(page)[i];
+      w.x = rescale4<FMT>(w.x, ratio);
+      w.y = rescale4<FMT>(w.y, ratio);
+      w.z = rescale4<FMT>(w.z, ratio);
+      w.w = rescale4<FMT>(w.w, ratio);
+      reinterpret_cast<uint4*>(page)[i] = w;
+    }
+  }
+  const float inv = inverse_of_scale(now);
+  uint8_t* dst = page + r * D + lane * EPL;
+  const uint32_t c0 = encode2<FMT>(__fmul_rn(bf16_lo(x.x), inv), __fmul_rn(bf16_hi(x.x), inv));
+  if constexpr (EPL == 4) {
+    const uint32_t c1 = encode2<FMT>(__fmul_rn(bf16_lo(x.y), inv), __fmul_rn(bf16_hi(x.y), inv));
+    *reinterpret_cast<uint32_t*>(dst) = c0 | (c1 << 16);
+  } else {
+    *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(c0);
+  }
+  return now;
+}
+
+template <int EPL>
+KVP_DEV uint2 load_row_part(const uint16_t* row, int lane) {
+  if constexpr (EPL == 4) return reinterpret_cast<const uint2*>(row)[lane];
+  return make_uint2(reinterpret_cast<const uint32_t*>(row)[lane], 0u);
+}
+
+// One warp per (b, h).
+template <int D, int FMT>
+__global__ void __launch_bounds__(kAppendWarps * 32) append_block8_kernel(
+    int mode, int BH, int H, int pos_arg, const int32_t* __restrict__ pos_dev, const uint16_t* __restrict__ k_new,
+    const uint16_t* __restrict__ v_new, int64_t k_sb, int64_t k_sh, int64_t v_sb, int64_t v_sh,
+    const float* __restrict__ score, const float* __restrict__ tau, const int32_t* __restrict__ flag, int window,
+    int delay, uint8_t* __restrict__ kq_pool, uint8_t* __restrict__ vq_pool, float2* __restrict__ scale_pool,
+    int32_t* __restrict__ expire_pool, int n_pages_cap, const int32_t* __restrict__ page_table, int max_pages,
+    int32_t* __restrict__ remap, int32_t* __restrict__ count, int32_t* __restrict__ status) {
+  constexpr int EPL = D / 32;
+  const int bh = blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (bh >= BH) return;
+  const int b = bh / H, h = bh - b * H;
+  const int pos = pos_dev != nullptr ? *pos_dev : pos_arg;
+  const int j = count[bh];
+  const uint2 kx = load_row_part<EPL>(k_new + b * k_sb + h * k_sh, lane);
+  const uint2 vx = load_row_part<EPL>(v_new + b * v_sb + h * v_sh, lane);
+  if (pos < 0 || static_cast<int64_t>(pos) + window + delay >= kNever) {
+    if (lane == 0) record_error(status, KVP_ERR_INVALID);
+    return;
+  }
+  const int32_t e = (mode == KVP_MASK_KVZAP) ? expire_kvzap(score[bh], tau[bh], pos, window)
+                                             : expire_dms(flag[bh], pos, delay, window);
+  if (j < 0) {
+    if (lane == 0) record_error(status, KVP_ERR_BOUNDS);
+    return;
+  }
+  const int p = j >> 4, r = j & 15;
+  const int page = (p < max_pages) ? page_table[static_cast<int64_t>(bh) * max_pages + p] : -1;
+  if (page < 0) {
+    if (lane == 0) record_error(status, KVP_ERR_CAPACITY);
+    return;
+  }
+  if (page >= n_pages_cap) {
+    if (lane == 0) record_error(status, KVP_ERR_BOUNDS);
+    return;
+  }
+  const int64_t row0 = static_cast<int64_t>(page) * kPage;
+  // a page's first row starts its scale anew, whatever the page held before
+  const float2 old = r > 0 ? scale_pool[page] : make_float2(0.f, 0.f);
+  const uint32_t ks = append_row<D, FMT>(kx, kq_pool + row0 * D, r, __float_as_uint(old.x), lane);
+  const uint32_t vs = append_row<D, FMT>(vx, vq_pool + row0 * D, r, __float_as_uint(old.y), lane);
+  if (lane == 0) {
+    scale_pool[page] = make_float2(__uint_as_float(ks), __uint_as_float(vs));
+    expire_pool[row0 + r] = e;
+    remap[static_cast<int64_t>(bh) * max_pages * kPage + j] = pos;
+    count[bh] = j + 1;
+  }
+}
+
+// ------------------------------------------------------------------ read
+template <int FMT>
+KVP_DEV uint32_t value2(uint32_t two, float scale) {
+  const float2 x = decode2<FMT>(two);
+  const __nv_bfloat162 y = __floats2bfloat162_rn(__fmul_rn(x.x, scale), __fmul_rn(x.y, scale));
+  return *reinterpret_cast<const uint32_t*>(&y);
+}
+
+// One warp per page of a (b, h): 16 codes a lane, LPR lanes a row.
+template <int D, int FMT>
+__global__ void __launch_bounds__(kPageWarps * 32) read_block8_kernel(
+    int H, int64_t n_items, int pages_each, const uint8_t* __restrict__ kq_pool, const uint8_t* __restrict__ vq_pool,
+    const float2* __restrict__ scale_pool, int n_pages_cap, const int32_t* __restrict__ page_table, int max_pages,
+    const int32_t* __restrict__ count, int first, int n_slots, uint16_t* __restrict__ k_out,
+    uint16_t* __restrict__ v_out, int64_t sb, int64_t st, int64_t sh, int32_t* __restrict__ status) {
+  constexpr int LPR = D / 16;
+  constexpr int RPI = 32 / LPR;
+  constexpr int NI = kPage / RPI;
+  const int lane = threadIdx.x & 31, piece = lane % LPR, sub = lane / LPR;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * kPageWarps + (threadIdx.x >> 5);
+  if (item >= n_items) return;
+  const int bh = static_cast<int>(item / pages_each);
+  const int p = first / kPage + static_cast<int>(item % pages_each);
+  const int b = bh / H, h = bh - b * H;
+  const int64_t cap = static_cast<int64_t>(max_pages) * kPage;
+  const int64_t cnt = min(max(static_cast<int64_t>(count[bh]), int64_t{0}), cap);
+  const int64_t slot0 = static_cast<int64_t>(p) * kPage;
+  int n = static_cast<int>(min(max(cnt - slot0, int64_t{0}), int64_t{kPage}));  // rows the cache holds here
+  int page = 0;
+  if (n > 0) {
+    page = page_table[static_cast<int64_t>(bh) * max_pages + p];
+    if (page < 0 || page >= n_pages_cap) {
+      if (lane == 0) record_error(status, KVP_ERR_BOUNDS);
+      n = 0;
+    }
+  }
+  const float2 s = n > 0 ? scale_pool[page] : make_float2(0.f, 0.f);
+  uint4 kw[NI], vw[NI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int r = i * RPI + sub;
+    const int64_t at = (static_cast<int64_t>(page) * kPage + r) * D + piece * 16;
+    kw[i] = vw[i] = make_uint4(0, 0, 0, 0);
+    if (r < n) {
+      kw[i] = *reinterpret_cast<const uint4*>(kq_pool + at);
+      vw[i] = *reinterpret_cast<const uint4*>(vq_pool + at);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int64_t slot = slot0 + i * RPI + sub - first;
+    if (slot < 0 || slot >= n_slots) continue;
+    const int64_t at = b * sb + slot * st + h * sh + piece * 16;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const uint4 c = w ? vw[i] : kw[i];
+      const float f = w ? s.y : s.x;
+      uint4* dst = reinterpret_cast<uint4*>((w ? v_out : k_out) + at);
+      dst[0] = make_uint4(value2<FMT>(c.x, f), value2<FMT>(c.x >> 16, f), value2<FMT>(c.y, f), value2<FMT>(c.y >> 16, f));
+      dst[1] = make_uint4(value2<FMT>(c.z, f), value2<FMT>(c.z >> 16, f), value2<FMT>(c.w, f), value2<FMT>(c.w >> 16, f));
+    }
+  }
+}
+
+// SM count of the current device (0 when it cannot be asked).
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return 0;
+  }
+  return n;
+}
+
+// The buffers that every call on this cache takes.
+kvp_status check_block8(int fmt, int batch, int n_kv_heads, int head_dim, const void* kq_pool, const void* vq_pool,
+                        const void* scale_pool, int n_pages_cap, const void* page_table, int max_pages,
+                        const void* count, const void* status) {
+  if (fmt != KVP_BLOCK8_E4M3 && fmt != KVP_BLOCK8_INT8) return KVP_ERR_INVALID;
+  if (batch <= 0 || n_kv_heads <= 0 || n_pages_cap < 0 || max_pages < 0) return KVP_ERR_INVALID;
+  if (head_dim != 64 && head_dim != 128) return KVP_ERR_UNSUPPORTED;
+  if (kq_pool == nullptr || vq_pool == nullptr || scale_pool == nullptr || page_table == nullptr || count == nullptr ||
+      status == nullptr)
+    return KVP_ERR_INVALID;
+  if (!aligned16(kq_pool) || !aligned16(vq_pool) || !aligned16(scale_pool)) return KVP_ERR_ALIGN;
+  if (static_cast<int64_t>(max_pages) * kPage > 0x7fffffff) return KVP_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(batch) * n_kv_heads > kMaxCompactBH) return KVP_ERR_UNSUPPORTED;
+  return KVP_OK;
+}
+
+template <int D, int FMT>
+kvp_status launch_compact(const MaskedSrc& src, int BH, int NS, int now, int reserve, uint8_t* kq_pool,
+                          uint8_t* vq_pool, float* scale_pool, int32_t* expire_pool, int n_pages_cap,
+                          int32_t* page_table, int max_pages, int32_t* remap, int32_t* count, void* workspace,
+                          int32_t* status, cudaStream_t st) {
+  const CompactWs ws = carve(workspace, BH, NS);
+  int32_t* n_used = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + prep_bytes(BH, NS));
+  int2* owner = reinterpret_cast<int2*>(n_used + 4);
+  const int sms = sm_count();
+  if (sms == 0) return KVP_ERR_CUDA;
+  const int segs = (NS + kWarpsPerCta - 1) / kWarpsPerCta;
+  if (cudaMemsetAsync(count, 0, static_cast<size_t>(BH) * sizeof(int32_t), st) != cudaSuccess) return KVP_ERR_CUDA;
+  count_kernel<MaskedSrc><<<dim3(segs, BH), kWarpsPerCta * 32, 0, st>>>(src, now, NS, ws.seg_cnt, count);
+  const int32_t* cnt = count;
+  if (BH <= kFusedBH) {
+    if (launch_pdl(list_kernel<true>, dim3(BH, segs), dim3(kWarpsPerCta * 32), 0, st, src, now, NS, reserve, max_pages,
+                   n_pages_cap, BH, ws, cnt, status, expire_pool, page_table, remap, n_used, owner) != cudaSuccess)
+      return KVP_ERR_CUDA;
+  } else {
+    base_kernel<<<1, 1024, 0, st>>>(BH, reserve, max_pages, n_pages_cap, ws, cnt, status);
+    if (launch_pdl(list_kernel<false>, dim3(BH, segs), dim3(kWarpsPerCta * 32), 0, st, src, now, NS, reserve, max_pages,
+                   n_pages_cap, BH, ws, cnt, status, expire_pool, page_table, remap, n_used, owner) != cudaSuccess)
+      return KVP_ERR_CUDA;
+  }
+  // at most one page for each 16 positions and reserved slots: small calls take a small grid
+  const int64_t most = static_cast<int64_t>(BH) * ((static_cast<int64_t>(src.n) + reserve + kPage - 1) / kPage);
+  const int64_t need = (most < n_pages_cap ? most : n_pages_cap) / kPageWarps + 1;
+  const int grid = static_cast<int>(need < sms * 2 ? need : sms * 2);
+  if (launch_pdl(page_kernel<D, FMT>, dim3(grid), dim3(kPageWarps * 32), 0, st, src.k, src.v, src.sb, src.st, src.sh,
+                 src.H, static_cast<const int32_t*>(n_used), static_cast<const int2*>(owner), cnt, max_pages,
+                 static_cast<const int32_t*>(remap), kq_pool, vq_pool, reinterpret_cast<float2*>(scale_pool),
+                 expire_pool) != cudaSuccess)
+    return KVP_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
+}
+
+kvp_status append_block8_impl(int fmt, int mode, int batch, int n_kv_heads, int head_dim, int pos,
+                              const int32_t* pos_dev, const void* k_new, const void* v_new, int64_t k_stride_b,
+                              int64_t k_stride_h, int64_t v_stride_b, int64_t v_stride_h, const float* score,
+                              const float* tau, const int32_t* flag_step, int window, int delay, void* kq_pool,
+                              void* vq_pool, float* scale_pool, int32_t* expire_pool, int n_pages_cap,
+                              const int32_t* page_table, int max_pages, int32_t* remap, int32_t* count,
+                              int32_t* status, void* stream) {
+  if (pos < 0 || window < 0 || delay < 0) return KVP_ERR_INVALID;
+  const kvp_status s = check_block8(fmt, batch, n_kv_heads, head_dim, kq_pool, vq_pool, scale_pool, n_pages_cap,
+                                    page_table, max_pages, count, status);
+  if (s != KVP_OK) return s;
+  if ((reinterpret_cast<uintptr_t>(pos_dev) & 3u) != 0) return KVP_ERR_ALIGN;
+  if (mode == KVP_MASK_KVZAP) {
+    if (score == nullptr || tau == nullptr || flag_step != nullptr) return KVP_ERR_INVALID;
+  } else if (mode == KVP_MASK_DMS) {
+    if (flag_step == nullptr || score != nullptr || tau != nullptr) return KVP_ERR_INVALID;
+  } else {
+    return KVP_ERR_INVALID;
+  }
+  if (k_new == nullptr || v_new == nullptr || expire_pool == nullptr || remap == nullptr) return KVP_ERR_INVALID;
+  if (!aligned16(k_new) || !aligned16(v_new)) return KVP_ERR_ALIGN;
+  if (k_stride_b < 0 || k_stride_h < 0 || v_stride_b < 0 || v_stride_h < 0) return KVP_ERR_INVALID;
+  if (k_stride_b % 8 || k_stride_h % 8 || v_stride_b % 8 || v_stride_h % 8) return KVP_ERR_ALIGN;
+  if (static_cast<int64_t>(pos) + window + delay >= kNever) return KVP_ERR_INVALID;
+  const int BH = batch * n_kv_heads;
+  auto go = [&](auto kern) {
+    kern<<<(BH + kAppendWarps - 1) / kAppendWarps, kAppendWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(
+        mode, BH, n_kv_heads, pos, pos_dev, static_cast<const uint16_t*>(k_new), static_cast<const uint16_t*>(v_new),
+        k_stride_b, k_stride_h, v_stride_b, v_stride_h, score, tau, flag_step, window, delay,
+        static_cast<uint8_t*>(kq_pool), static_cast<uint8_t*>(vq_pool), reinterpret_cast<float2*>(scale_pool),
+        expire_pool, n_pages_cap, page_table, max_pages, remap, count, status);
+    return cudaGetLastError() == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
+  };
+  if (fmt == KVP_BLOCK8_E4M3)
+    return head_dim == 128 ? go(append_block8_kernel<128, KVP_BLOCK8_E4M3>) : go(append_block8_kernel<64, KVP_BLOCK8_E4M3>);
+  return head_dim == 128 ? go(append_block8_kernel<128, KVP_BLOCK8_INT8>) : go(append_block8_kernel<64, KVP_BLOCK8_INT8>);
+}
+
+}  // namespace
+}  // namespace kvp
+
+using namespace kvp;
+
+extern "C" size_t kvp_compact_block8_workspace_bytes(int batch, int n_kv_heads, int n_pos, int n_pages_cap) {
+  if (batch <= 0 || n_kv_heads <= 0 || n_pos < 0 || n_pages_cap < 0) return 0;
+  return block8_ws_bytes(static_cast<int64_t>(batch) * n_kv_heads, n_segments(n_pos), n_pages_cap);
+}
+
+extern "C" kvp_status kvp_compact_block8(int fmt, int mode, int batch, int n_kv_heads, int head_dim, int n_pos,
+                                         const void* k_src, const void* v_src, int64_t stride_b, int64_t stride_t,
+                                         int64_t stride_h, const float* scores, const float* tau,
+                                         const int32_t* flag_step, int window, int delay, int now, int reserve,
+                                         void* kq_pool, void* vq_pool, float* scale_pool, int32_t* expire_pool,
+                                         int n_pages_cap, int32_t* page_table, int max_pages, int32_t* remap,
+                                         int32_t* count, void* workspace, size_t workspace_bytes, int32_t* status,
+                                         void* stream) {
+  if (n_pos < 0 || window < 0 || delay < 0 || reserve < 0) return KVP_ERR_INVALID;
+  const kvp_status s = check_block8(fmt, batch, n_kv_heads, head_dim, kq_pool, vq_pool, scale_pool, n_pages_cap,
+                                    page_table, max_pages, count, status);
+  if (s != KVP_OK) return s;
+  if (expire_pool == nullptr || remap == nullptr) return KVP_ERR_INVALID;
+  // the per-position inputs may be NULL when there are no positions; tau is read per (b, h)
+  if (mode == KVP_MASK_KVZAP) {
+    if (flag_step != nullptr || tau == nullptr || (n_pos > 0 && scores == nullptr)) return KVP_ERR_INVALID;
+  } else if (mode == KVP_MASK_DMS) {
+    if (scores != nullptr || tau != nullptr || (n_pos > 0 && flag_step == nullptr)) return KVP_ERR_INVALID;
+  } else {
+    return KVP_ERR_INVALID;
+  }
+  if (static_cast<int64_t>(n_pos) + window + delay >= kNever) return KVP_ERR_INVALID;
+  if (static_cast<int64_t>(n_pos) + reserve > 0x7fffffff - kPage) return KVP_ERR_UNSUPPORTED;
+  if (n_pos > 0 && (k_src == nullptr || v_src == nullptr)) return KVP_ERR_INVALID;
+  if (!aligned16(k_src) || !aligned16(v_src) || stride_b % 8 || stride_t % 8 || stride_h % 8) return KVP_ERR_ALIGN;
+  if (stride_b < 0 || stride_t < 0 || stride_h < 0) return KVP_ERR_INVALID;
+  const int BH = batch * n_kv_heads;
+  const int NS = n_segments(n_pos);
+  // page ids are 32-bit: with every position kept they have to be countable, or the budget check could wrap
+  if (BH * ((static_cast<int64_t>(n_pos) + reserve + kPage - 1) / kPage) > 0x7fffffff) return KVP_ERR_UNSUPPORTED;
+  if (workspace == nullptr || workspace_bytes < block8_ws_bytes(BH, NS, n_pages_cap)) return KVP_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return KVP_ERR_ALIGN;
+  const MaskedSrc src{static_cast<const uint16_t*>(k_src),
+                      static_cast<const uint16_t*>(v_src),
+                      stride_b,
+                      stride_t,
+                      stride_h,
+                      mode,
+                      scores,
+                      tau,
+                      flag_step,
+                      window,
+                      delay,
+                      n_kv_heads,
+                      n_pos};
+  auto go = [&](auto run) {
+    return run(src, BH, NS, now, reserve, static_cast<uint8_t*>(kq_pool), static_cast<uint8_t*>(vq_pool), scale_pool,
+               expire_pool, n_pages_cap, page_table, max_pages, remap, count, workspace, status,
+               static_cast<cudaStream_t>(stream));
+  };
+  if (fmt == KVP_BLOCK8_E4M3)
+    return head_dim == 128 ? go(launch_compact<128, KVP_BLOCK8_E4M3>) : go(launch_compact<64, KVP_BLOCK8_E4M3>);
+  return head_dim == 128 ? go(launch_compact<128, KVP_BLOCK8_INT8>) : go(launch_compact<64, KVP_BLOCK8_INT8>);
+}
+
+extern "C" kvp_status kvp_append_block8(int fmt, int mode, int batch, int n_kv_heads, int head_dim, int pos,
+                                        const void* k_new, const void* v_new, int64_t k_stride_b, int64_t k_stride_h,
+                                        int64_t v_stride_b, int64_t v_stride_h, const float* score, const float* tau,
+                                        const int32_t* flag_step, int window, int delay, void* kq_pool, void* vq_pool,
+                                        float* scale_pool, int32_t* expire_pool, int n_pages_cap,
+                                        const int32_t* page_table, int max_pages, int32_t* remap, int32_t* count,
+                                        int32_t* status, void* stream) {
+  return append_block8_impl(fmt, mode, batch, n_kv_heads, head_dim, pos, nullptr, k_new, v_new, k_stride_b, k_stride_h,
+                            v_stride_b, v_stride_h, score, tau, flag_step, window, delay, kq_pool, vq_pool, scale_pool,
+                            expire_pool, n_pages_cap, page_table, max_pages, remap, count, status, stream);
+}
+
+extern "C" kvp_status kvp_append_block8_devpos(int fmt, int mode, int batch, int n_kv_heads, int head_dim,
+                                               const int32_t* pos_dev, const void* k_new, const void* v_new,
+                                               int64_t k_stride_b, int64_t k_stride_h, int64_t v_stride_b,
+                                               int64_t v_stride_h, const float* score, const float* tau,
+                                               const int32_t* flag_step, int window, int delay, void* kq_pool,
+                                               void* vq_pool, float* scale_pool, int32_t* expire_pool, int n_pages_cap,
+                                               const int32_t* page_table, int max_pages, int32_t* remap,
+                                               int32_t* count, int32_t* status, void* stream) {
+  if (pos_dev == nullptr) return KVP_ERR_INVALID;
+  return append_block8_impl(fmt, mode, batch, n_kv_heads, head_dim, 0, pos_dev, k_new, v_new, k_stride_b, k_stride_h,
+                            v_stride_b, v_stride_h, score, tau, flag_step, window, delay, kq_pool, vq_pool, scale_pool,
+                            expire_pool, n_pages_cap, page_table, max_pages, remap, count, status, stream);
+}
+
+extern "C" kvp_status kvp_read_block8(int fmt, int batch, int n_kv_heads, int head_dim, const void* kq_pool,
+                                      const void* vq_pool, const float* scale_pool, int n_pages_cap,
+                                      const int32_t* page_table, int max_pages, const int32_t* count, int first_slot,
+                                      int n_slots, void* k_out, void* v_out, int64_t stride_b, int64_t stride_t,
+                                      int64_t stride_h, int32_t* status, void* stream) {
+  if (first_slot < 0 || n_slots < 0) return KVP_ERR_INVALID;
+  const kvp_status s = check_block8(fmt, batch, n_kv_heads, head_dim, kq_pool, vq_pool, scale_pool, n_pages_cap,
+                                    page_table, max_pages, count, status);
+  if (s != KVP_OK) return s;
+  if (static_cast<int64_t>(first_slot) + n_slots > 0x7fffffff - kPage) return KVP_ERR_UNSUPPORTED;
+  if (n_slots == 0) return KVP_OK;
+  if (k_out == nullptr || v_out == nullptr) return KVP_ERR_INVALID;
+  if (!aligned16(k_out) || !aligned16(v_out) || stride_b % 8 || stride_t % 8 || stride_h % 8) return KVP_ERR_ALIGN;
+  // rows that two slots, heads or sequences share would be written twice
+  if ((batch > 1 && stride_b < head_dim) || (n_slots > 1 && stride_t < head_dim) ||
+      (n_kv_heads > 1 && stride_h < head_dim))
+    return KVP_ERR_INVALID;
+  const int pages_each = (first_slot + n_slots - 1) / kPage - first_slot / kPage + 1;
+  const int64_t items = static_cast<int64_t>(batch) * n_kv_heads * pages_each;
+  const int64_t ctas = (items + kPageWarps - 1) / kPageWarps;
+  if (ctas > 0x7fffffff) return KVP_ERR_UNSUPPORTED;
+  auto go = [&](auto kern) {
+    kern<<<static_cast<unsigned>(ctas), kPageWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(
+        n_kv_heads, items, pages_each, static_cast<const uint8_t*>(kq_pool), static_cast<const uint8_t*>(vq_pool),
+        reinterpret_cast<const float2*>(scale_pool), n_pages_cap, page_table, max_pages, count, first_slot, n_slots,
+        static_cast<uint16_t*>(k_out), static_cast<uint16_t*>(v_out), stride_b, stride_t, stride_h, status);
+    return cudaGetLastError() == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
+  };
+  if (fmt == KVP_BLOCK8_E4M3)
+    return head_dim == 128 ? go(read_block8_kernel<128, KVP_BLOCK8_E4M3>) : go(read_block8_kernel<64, KVP_BLOCK8_E4M3>);
+  return head_dim == 128 ? go(read_block8_kernel<128, KVP_BLOCK8_INT8>) : go(read_block8_kernel<64, KVP_BLOCK8_INT8>);
+}

@@ -1,0 +1,245 @@
+// kvp_qk_norm_rope: the norm of each query and key head's row and the position
+// rotation of its first rot_dim values, in one pass over q and k; and
+// kvp_rope_turns, its table of angles per position.
+//
+//   y = x / sqrt(mean(x^2) + eps) * w;  (a, b) -> (a cos - b sin, b cos + a sin)
+//
+// Bound by memory (2 bytes in, 2 out a value). D / 16 lanes take a head's row,
+// 16 values each in two 16-byte runs that lie half a rotation apart, so that
+// both members of every pair are in one lane (for interleaved pairs any run
+// does) and a lane's loads and stores stay 16 bytes wide; a row's norm is three
+// (two at D = 64) shuffles. A warp takes one token's heads, or a share of them
+// when there are few tokens, with the token's cosines and sines in registers.
+//
+// An angle is a 64-bit product: turns[i] = inv_freq[i] / (2 pi) as a 64-bit
+// fraction of a turn, times the position modulo one turn (the integer wraps
+// exactly there), whose top 32 bits go to sincospif. No far position loses
+// digits, and no argument reduction is needed.
+#include <cmath>
+
+#include "kvp_common.cuh"
+
+namespace kvp {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kUnroll = 2;  // head rows a lane has in flight
+
+struct RotateParams {
+  const uint16_t* x[2];   // q, k
+  uint16_t* y[2];
+  int64_t xt[2], xh[2], yt[2], yh[2];
+  const float* w[2];
+  const int32_t* pos;
+  const uint64_t* turns;
+  int heads[2];
+  int64_t n_items;
+  int parts;              // warps a token's heads are dealt to
+  int rot;
+  float eps;
+};
+
+KVP_DEV uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+KVP_DEV void unpack_row(const uint4& a, const uint4& b, float (&f)[16]) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    f[2 * i] = bf16_lo(w[i]);
+    f[2 * i + 1] = bf16_hi(w[i]);
+  }
+}
+
+template <int D, bool kPairs>
+__global__ void __launch_bounds__(kWarps * 32) rotate_kernel(const RotateParams p) {
+  constexpr int LPH = D / 16;       // lanes a head takes
+  constexpr int HPI = 32 / LPH;     // heads a warp takes at once
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  if (item >= p.n_items) return;
+  const int lane = threadIdx.x & 31, j = lane % LPH, sub = lane / LPH;
+  const int64_t tok = item / p.parts;
+  const int part = static_cast<int>(item - tok * p.parts);
+
+  // the lane's two runs of 8 values: pairs of rotated runs first, then what is left of the row in the same manner
+  const int nh = p.rot / 16;
+  const bool turns_here = j < nh;
+  const int run0 = turns_here ? j : nh + j;
+  const int run1 = run0 + (turns_here ? nh : LPH - nh);
+
+  // cosines and sines of the lane's 8 pairs: 2 (1 at D = 64) are computed, the others
+  // fetched from the lanes of the warp's other heads, which share the token's angles
+  float cs[8], sn[8];
+  if (nh > 0) {
+    constexpr int kMine = 8 / HPI > 0 ? 8 / HPI : 1;
+    const uint64_t pos = static_cast<uint64_t>(static_cast<int64_t>(p.pos[tok]));
+    float c[kMine], s[kMine];
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const int e = sub * kMine + i;   // of the lane's 8 pairs
+      const int pair = kPairs ? (e < 4 ? 4 * run0 + e : 4 * run1 + e - 4) : 8 * run0 + e;
+      const uint64_t turn = turns_here ? p.turns[pair] * pos : 0;
+      sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * (1.f / 2147483648.f), &s[i], &c[i]);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      cs[e] = __shfl_sync(0xffffffffu, c[e % kMine], (e / kMine) * LPH + j);
+      sn[e] = __shfl_sync(0xffffffffu, s[e % kMine], (e / kMine) * LPH + j);
+    }
+  }
+
+  const int it_q = (p.heads[0] + HPI - 1) / HPI, it_all = it_q + (p.heads[1] + HPI - 1) / HPI;
+  const int lo = static_cast<int>(static_cast<int64_t>(part) * it_all / p.parts);
+  const int hi = static_cast<int>(static_cast<int64_t>(part + 1) * it_all / p.parts);
+#pragma unroll 1
+  for (int which = 0; which < 2; ++which) {
+    const int i_lo = which == 0 ? lo : max(lo, it_q) - it_q, i_hi = which == 0 ? min(hi, it_q) : hi - it_q;
+    if (i_lo >= i_hi) continue;
+    const int heads = p.heads[which];
+    const uint16_t* x = p.x[which] + tok * p.xt[which];
+    uint16_t* y = p.y[which] + tok * p.yt[which];
+    const float* wp = p.w[which];
+    float w[16];
+    if (wp != nullptr) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 v = __ldg(reinterpret_cast<const float4*>(wp + (i < 2 ? run0 : run1) * 8) + (i & 1));
+        w[4 * i] = v.x;
+        w[4 * i + 1] = v.y;
+        w[4 * i + 2] = v.z;
+        w[4 * i + 3] = v.w;
+      }
+    }
+#pragma unroll 1
+    for (int i0 = i_lo; i0 < i_hi; i0 += kUnroll) {
+      uint4 a[kUnroll], b[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int h = (i0 + u) * HPI + sub;
+        a[u] = b[u] = make_uint4(0, 0, 0, 0);
+        if (i0 + u < i_hi && h < heads) {
+          a[u] = *reinterpret_cast<const uint4*>(x + h * p.xh[which] + run0 * 8);
+          b[u] = *reinterpret_cast<const uint4*>(x + h * p.xh[which] + run1 * 8);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int h = (i0 + u) * HPI + sub;
+        float f[16];
+        unpack_row(a[u], b[u], f);
+        if (wp != nullptr) {
+          float sum = 0.f;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) sum = fmaf(f[e], f[e], sum);
+#pragma unroll
+          for (int o = 1; o < LPH; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          const float r = rsqrtf(sum * (1.f / D) + p.eps);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) f[e] *= r * w[e];
+        }
+        if (turns_here) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int i = kPairs ? 2 * e : e, k = kPairs ? 2 * e + 1 : e + 8;
+            const float m = f[i], n = f[k];
+            f[i] = m * cs[e] - n * sn[e];
+            f[k] = n * cs[e] + m * sn[e];
+          }
+        }
+        if (i0 + u < i_hi && h < heads) {
+          uint4* dst = reinterpret_cast<uint4*>(y + h * p.yh[which]);
+          dst[run0] = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+          dst[run1] = make_uint4(pack_bf16(f[8], f[9]), pack_bf16(f[10], f[11]), pack_bf16(f[12], f[13]),
+                                 pack_bf16(f[14], f[15]));
+        }
+      }
+    }
+  }
+}
+
+bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+}  // namespace
+}  // namespace kvp
+
+using namespace kvp;
+
+extern "C" kvp_status kvp_rope_turns(int n, const double* inv_freq, uint64_t* turns) {
+  if (n < 0) return KVP_ERR_INVALID;
+  if (n == 0) return KVP_OK;
+  if (inv_freq == nullptr || turns == nullptr) return KVP_ERR_INVALID;
+  for (int i = 0; i < n; ++i) {
+    if (!std::isfinite(inv_freq[i])) return KVP_ERR_INVALID;
+    const double t = std::fabs(inv_freq[i]) / 6.283185307179586476925;
+    const uint64_t u = static_cast<uint64_t>((t - std::floor(t)) * 18446744073709551616.0);  // exact: t - floor(t) < 1
+    turns[i] = inv_freq[i] < 0 ? 0 - u : u;
+  }
+  return KVP_OK;
+}
+
+extern "C" kvp_status kvp_qk_norm_rope(int64_t n_tok, int n_q_heads, int n_k_heads, int head_dim, int rot_dim,
+                                       int interleaved, const void* q, int64_t q_stride_t, int64_t q_stride_h,
+                                       const void* k, int64_t k_stride_t, int64_t k_stride_h, const int32_t* pos,
+                                       const uint64_t* turns, const float* wq, const float* wk, float eps,
+                                       void* q_out, int64_t qo_stride_t, int64_t qo_stride_h, void* k_out,
+                                       int64_t ko_stride_t, int64_t ko_stride_h, void* stream) {
+  if (n_tok < 0 || n_q_heads < 0 || n_k_heads < 0 || (n_q_heads == 0 && n_k_heads == 0)) return KVP_ERR_INVALID;
+  if (!(eps >= 0.f) || eps > 3.402823466e38f) return KVP_ERR_INVALID;
+  if (head_dim != 64 && head_dim != 128) return KVP_ERR_UNSUPPORTED;
+  if (rot_dim < 0 || rot_dim > head_dim) return KVP_ERR_INVALID;
+  if (rot_dim % 16 != 0) return KVP_ERR_UNSUPPORTED;
+  if (n_q_heads > 65536 || n_k_heads > 65536) return KVP_ERR_UNSUPPORTED;
+  if (n_tok == 0) return KVP_OK;
+  if (rot_dim > 0 && (pos == nullptr || turns == nullptr)) return KVP_ERR_INVALID;
+  if ((reinterpret_cast<uintptr_t>(pos) & 3u) != 0 || (reinterpret_cast<uintptr_t>(turns) & 7u) != 0)
+    return KVP_ERR_ALIGN;
+  RotateParams p;
+  p.x[0] = static_cast<const uint16_t*>(q);
+  p.x[1] = static_cast<const uint16_t*>(k);
+  p.y[0] = static_cast<uint16_t*>(q_out);
+  p.y[1] = static_cast<uint16_t*>(k_out);
+  p.xt[0] = q_stride_t, p.xh[0] = q_stride_h, p.yt[0] = qo_stride_t, p.yh[0] = qo_stride_h;
+  p.xt[1] = k_stride_t, p.xh[1] = k_stride_h, p.yt[1] = ko_stride_t, p.yh[1] = ko_stride_h;
+  p.w[0] = wq;
+  p.w[1] = wk;
+  p.heads[0] = n_q_heads;
+  p.heads[1] = n_k_heads;
+  for (int i = 0; i < 2; ++i) {
+    if (p.heads[i] == 0) continue;
+    if (p.x[i] == nullptr || p.y[i] == nullptr) return KVP_ERR_INVALID;
+    if (!al16(p.x[i]) || !al16(p.y[i]) || !al16(p.w[i])) return KVP_ERR_ALIGN;
+    for (const int64_t s : {p.xt[i], p.xh[i], p.yt[i], p.yh[i]}) {
+      if (s < 0) return KVP_ERR_INVALID;
+      if (s % 8 != 0) return KVP_ERR_ALIGN;
+    }
+    // rows that two tokens or heads share would be written twice
+    if ((n_tok > 1 && p.yt[i] < head_dim) || (p.heads[i] > 1 && p.yh[i] < head_dim)) return KVP_ERR_INVALID;
+    if (p.x[i] == p.y[i] && ((n_tok > 1 && p.xt[i] != p.yt[i]) || (p.heads[i] > 1 && p.xh[i] != p.yh[i])))
+      return KVP_ERR_INVALID;
+  }
+  p.pos = pos;
+  p.turns = turns;
+  p.rot = rot_dim;
+  p.eps = eps;
+  const int hpi = 32 / (head_dim / 16);
+  const int its = (n_q_heads + hpi - 1) / hpi + (n_k_heads + hpi - 1) / hpi;
+  // Few tokens: their heads are dealt to more warps, down to one step of hpi heads each, until there are
+  // about 4,096 warps (27 for each SM) to hide the loads' latency.
+  int64_t parts = (4096 + n_tok - 1) / n_tok;
+  if (parts > its) parts = its;
+  p.parts = static_cast<int>(parts);
+  p.n_items = n_tok * parts;
+  const int64_t ctas = (p.n_items + kWarps - 1) / kWarps;
+  if (n_tok > 0x7fffffffll || ctas > 0x7fffffff) return KVP_ERR_UNSUPPORTED;
+  auto go = [&](auto kern) {
+    return launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(kWarps * 32), 0, static_cast<cudaStream_t>(stream),
+                      p) == cudaSuccess
+               ? KVP_OK
+               : KVP_ERR_CUDA;
+  };
+  if (head_dim == 128) return interleaved ? go(rotate_kernel<128, true>) : go(rotate_kernel<128, false>);
+  return interleaved ? go(rotate_kernel<64, true>) : go(rotate_kernel<64, false>);
+}
