@@ -37,6 +37,8 @@
 // results of a (b, h) that several warps share are merged in shared memory;
 // those that several CTAs share go to the workspace, and the last CTA to
 // arrive merges them. Nothing ever waits on another CTA.
+#include <atomic>
+
 #include "block8.cuh"
 
 namespace kvp {
@@ -48,6 +50,7 @@ constexpr int kMaxBH = 4096;     // (b, h) pairs whose page prefix fits in share
 constexpr int kMaxCtas = 512;    // grid bound used to size the workspace
 constexpr float kLazy = 3.f;     // how far a base-2 logit may pass the reference before it moves
 constexpr float kBias = 12.f;    // weights are 2^(x - m + kBias): at most 2^(kLazy + kBias) in fp16
+constexpr int kAhead = 2;        // pages whose lines are brought into L2 before their loads
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Params {
@@ -169,17 +172,21 @@ KVP_DEV void load_v(VWords<D>& x, const uint8_t* page, int g, int t) {
 }
 
 // Shared memory: page prefix, then each warp's two partial results (the (b, h)
-// its range starts in, and the one it ends in).
+// its range starts in, and the one it ends in), then what a merge over CTAs
+// takes: (reference, sum) of each head and CTA, and a row of partial sums for
+// each thread.
 template <int D>
 __host__ __device__ constexpr int part_floats(int G) {
   return (G * (D + 2) + 3) & ~3;
 }
+__host__ __device__ constexpr size_t prefix_bytes(int BH) { return static_cast<size_t>(BH + 4) / 4 * 16; }
 template <int D>
-size_t smem_bytes(int BH, int G) {
-  return (static_cast<size_t>(BH) + 1 + 3) / 4 * 16 + static_cast<size_t>(kWarps) * 2 * part_floats<D>(G) * 4;
+__host__ __device__ constexpr size_t smem_bytes(int BH, int G) {
+  return prefix_bytes(BH) + static_cast<size_t>(kWarps) * 2 * part_floats<D>(G) * 4 +
+         static_cast<size_t>(G) * kMaxCtas * 8 + kThreads * 16;
 }
 
-// Writes head h's row: channels' sums over acc (already summed over parts) / l.
+// A row's log-sum-exp from its reference and sum (0 for a row without slots; NaN passes through).
 KVP_DEV void write_lse(const Params& p, int64_t row, float m, float l) {
   if (p.lse != nullptr) p.lse[row] = l > 0.f ? (m - kBias + log2f(l)) * 0.69314718055994531f : (l == 0.f ? -INFINITY : l);
 }
@@ -189,15 +196,19 @@ template <int D, int FMT, bool kDup>
 __global__ void __launch_bounds__(kThreads, 1) attn_block8_kernel(const Params p) {
   extern __shared__ __align__(16) uint8_t sm[];
   __shared__ int warp_sum[kWarps];
-  __shared__ int part_unit[kWarps][2];
+  __shared__ int part_unit[kWarps * 2];
+  __shared__ float wts[8][2 * kWarps];   // a merge's weights: head, partial result
+  __shared__ float2 merged_ml[8];
   __shared__ int last_s;
   pdl_launch_dependents();
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int G = p.G;
   int* prefix = reinterpret_cast<int*>(sm);
-  float* parts = reinterpret_cast<float*>(sm + (static_cast<size_t>(p.BH) + 1 + 3) / 4 * 16);
   const int pf = part_floats<D>(G);
+  float* parts = reinterpret_cast<float*>(sm + prefix_bytes(p.BH));
+  float2* cta_ml = reinterpret_cast<float2*>(parts + kWarps * 2 * pf);
+  float4* rows = reinterpret_cast<float4*>(cta_ml + G * kMaxCtas);
 
   // ---- pages before each (b, h)
   const int cap = p.max_pages * kPage;
@@ -212,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block8_kernel(const Params p
       if (lane >= o) incl += y;
     }
     if (lane == 31) warp_sum[warp] = incl;
-    if (tid < kWarps * 2) part_unit[tid >> 1][tid & 1] = -1;
+    if (tid < kWarps * 2) part_unit[tid] = -1;
     __syncthreads();
     int at = incl - sum;
 #pragma unroll
@@ -259,7 +270,54 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block8_kernel(const Params p
       const int u_lo = prefix[u], u_hi = prefix[u + 1];
       const int end = min(hi, u_hi);
       const int cnt = min(max(p.count[u], 0), cap);
-      const int32_t* table = p.page_table + static_cast<int64_t>(u) * p.max_pages - u_lo;
+      const int32_t* table = p.page_table + static_cast<int64_t>(u) * p.max_pages + (at - u_lo);
+      const int n = end - at;            // pages of this (b, h) in the warp's range
+
+      // ---- page ids, 32 at a time in the lanes, two blocks of them
+      int ids0 = lane < n ? table[lane] : -1, ids1 = 32 + lane < n ? table[32 + lane] : -1, block = 0;
+      auto id_of = [&](int i) {
+        const int k = i - block;
+        const int id = k < 32 ? __shfl_sync(0xffffffffu, ids0, k & 31) : __shfl_sync(0xffffffffu, ids1, k & 31);
+        return id < p.n_pages_cap ? id : -1;
+      };
+      // A page's loads. One page ahead its K words and scales are requested as soon as the page before is
+      // through the first product, its V words as soon as it is through the second; kAhead pages ahead its
+      // lines are brought into L2 (one line a lane), which leaves the register loads an L2 latency to cover.
+      KWords<D> kw;
+      VWords<D> vw;
+      float2 sc_next = make_float2(0.f, 0.f);
+      int32_t e0_next = INT32_MIN, e1_next = INT32_MIN;
+      auto request_k = [&](int id) {
+        if (id >= 0) {
+          load_k<D>(kw, p.k_pool + static_cast<int64_t>(id) * kPage * D, g, t);
+          sc_next = p.scale_pool[id];
+          e0_next = p.expire_pool[static_cast<int64_t>(id) * kPage + g];
+          e1_next = p.expire_pool[static_cast<int64_t>(id) * kPage + g + 8];
+        } else {  // a page that is not there: all of its slots absent
+          if (lane == 0) record_error(p.status, KVP_ERR_BOUNDS);
+          e0_next = e1_next = INT32_MIN;
+        }
+      };
+      auto request_v = [&](int id) {
+        if (id >= 0) load_v<D>(vw, p.v_pool + static_cast<int64_t>(id) * kPage * D, g, t);
+      };
+      auto bring = [&](int i) {
+        if (i >= n) return;
+        const int id = id_of(i);
+        constexpr int kLines = D * kPage / 128;
+        if (id >= 0 && lane < 2 * kLines) {
+          const uint8_t* a = (lane < kLines ? p.k_pool : p.v_pool) + static_cast<int64_t>(id) * kPage * D +
+                             (lane % kLines) * 128;
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(a));
+        }
+      };
+      {
+        const int id = id_of(0);
+        request_k(id);
+        request_v(id);
+      }
+#pragma unroll
+      for (int i = 1; i <= kAhead; ++i) bring(i);
 
       // ---- this (b, h)'s queries as B fragments: lane (g, t) holds head g (kDup: g % 4), its words' channels
       uint32_t qf[D / 16][2];
@@ -297,23 +355,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block8_kernel(const Params p
 
       State<D> s;
       s.clear();
-      for (int i = at; i < end; ++i) {
-        int pg = table[i];
-        const bool good = pg >= 0 && pg < p.n_pages_cap;
-        if (!good) {
-          if (lane == 0) record_error(p.status, KVP_ERR_BOUNDS);
-          continue;
-        }
-        KWords<D> kw;
-        VWords<D> vw;
-        const int64_t row0 = static_cast<int64_t>(pg) * kPage;
-        load_k<D>(kw, p.k_pool + row0 * D, g, t);
-        load_v<D>(vw, p.v_pool + row0 * D, g, t);
-        const float2 sc = p.scale_pool[pg];
-        const int slot = (i - u_lo) * kPage;
-        const bool in0 = slot + g < cnt && p.expire_pool[row0 + g] > now;
-        const bool in1 = slot + g + 8 < cnt && p.expire_pool[row0 + g + 8] > now;
-
+      for (int i = 0; i < n; ++i) {
+        const int slot = (at - u_lo + i) * kPage;
+        const bool in0 = slot + g < cnt && e0_next > now, in1 = slot + g + 8 < cnt && e1_next > now;
+        const float2 sc = sc_next;
         float x[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
@@ -322,6 +367,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block8_kernel(const Params p
           codes_to_f16<FMT>(kw.w[1][j], a1, a3);
           mma_f16_16816(x, a0, a1, a2, a3, qf[j][0], qf[j][1]);
         }
+        const int id_next = i + 1 < n ? id_of(i + 1) : -1;
+        if (i + 1 < n) request_k(id_next);
         const float f0 = qs[0] * sc.x, f1 = qs[1] * sc.x;
         x[0] = in0 ? x[0] * f0 : -INFINITY;
         x[1] = in0 ? x[1] * f1 : -INFINITY;
@@ -402,6 +449,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block8_kernel(const Params p
 #pragma unroll
           for (int c = 0; c < 4; ++c) s.acc[2 * w + 1][c] = fmaf(y[c], sc.y, s.acc[2 * w + 1][c]);
         }
+        if (i + 1 < n) {
+          request_v(id_next);
+          bring(i + 1 + kAhead);
+          if (i + 1 - block == 32) {  // the first block of ids is used up
+            ids0 = ids1;
+            block += 32;
+            ids1 = block + 32 + lane < n ? table[block + 32 + lane] : -1;
+          }
+        }
       }
 
       // ---- the warp's share of this (b, h) is done
@@ -441,62 +497,66 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block8_kernel(const Params p
           }
         }
       }
-      if (!whole && lane == 0) part_unit[warp][which] = u;
+      if (!whole && lane == 0) part_unit[warp * 2 + which] = u;
       at = end;
     }
   }
   __syncthreads();
 
-  // ---- merge the CTA's partial results, one (b, h) after another; a run of entries of one (b, h) starts at its first
-  for (int e = 0; e < 2 * kWarps; ++e) {
-    const int u = part_unit[e >> 1][e & 1];
-    if (u < 0) continue;
-    int last = e;
-    bool start = true;
-    for (int k = e - 1; k >= 0; --k) {
-      const int v = part_unit[k >> 1][k & 1];
-      if (v >= 0) {
-        start = v != u;
-        break;
-      }
-    }
-    if (!start) continue;
-    for (int k = e + 1; k < 2 * kWarps; ++k)
-      if (part_unit[k >> 1][k & 1] == u) last = k;
+  // ---- merge the CTA's partial results, one (b, h) after another: entry e of part_unit is lane e's
+  const int my_unit = part_unit[lane];
+  const unsigned same = __match_any_sync(0xffffffffu, my_unit);
+  unsigned leaders = __ballot_sync(0xffffffffu, my_unit >= 0 && (same & ((1u << lane) - 1u)) == 0);
+  while (leaders != 0) {
+    const int lead = __ffs(leaders) - 1;
+    leaders &= leaders - 1;
+    const int u = __shfl_sync(0xffffffffu, my_unit, lead);
+    const unsigned entries = __shfl_sync(0xffffffffu, same, lead);
     const int u_lo = prefix[u], u_hi = prefix[u + 1];
     const bool whole = u_lo >= c_lo && u_hi <= c_hi;
-    const int slot = blockIdx.x * 2 + (u_lo <= c_lo ? 0 : 1);
+    if (warp < G) {  // one warp a head: the partial results' weights
+      const bool in = (entries >> lane) & 1u;
+      const float2 ml = in ? *reinterpret_cast<const float2*>(parts + lane * pf + G * D + 2 * warp)
+                           : make_float2(-INFINITY, 0.f);
+      float m = ml.x;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const float w = ml.x == m ? 1.f : ex2_approx(ml.x - m);
+      float l = in ? w * ml.y : 0.f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      wts[warp][lane] = w;
+      if (lane == 0) merged_ml[warp] = make_float2(m, l);
+    }
+    __syncthreads();
+    const int64_t slot = blockIdx.x * 2 + (u_lo <= c_lo ? 0 : 1);
     for (int i = tid; i < G * D / 4; i += kThreads) {
       const int head = i / (D / 4);
-      float m = -INFINITY;
-      for (int k = e; k <= last; ++k)
-        if (part_unit[k >> 1][k & 1] == u) m = fmaxf(m, parts[k * pf + G * D + 2 * head]);
-      float l = 0.f;
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int k = e; k <= last; ++k) {
-        if (part_unit[k >> 1][k & 1] != u) continue;
-        const float* part = parts + k * pf;
-        const float pm = part[G * D + 2 * head];
-        const float w = pm == m ? 1.f : ex2_approx(pm - m);
-        const float4 x = *reinterpret_cast<const float4*>(part + 4 * i);
-        l = fmaf(w, part[G * D + 2 * head + 1], l);
+      for (unsigned left = entries; left != 0; left &= left - 1) {
+        const int e = __ffs(left) - 1;
+        const float w = wts[head][e];
+        const float4 x = reinterpret_cast<const float4*>(parts + e * pf)[i];
         a.x = fmaf(w, x.x, a.x);
         a.y = fmaf(w, x.y, a.y);
         a.z = fmaf(w, x.z, a.z);
         a.w = fmaf(w, x.w, a.w);
       }
+      const float2 ml = merged_ml[head];
       if (whole) {
-        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;
         reinterpret_cast<float4*>(p.out + static_cast<int64_t>(u) * G * D)[i] =
             make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
-        if (i % (D / 4) == 0) write_lse(p, static_cast<int64_t>(u) * G + head, m, l);
+        if (i % (D / 4) == 0) write_lse(p, static_cast<int64_t>(u) * G + head, ml.x, ml.y);
       } else {
-        reinterpret_cast<float4*>(p.part_acc + static_cast<int64_t>(slot) * G * D)[i] = a;
-        if (i % (D / 4) == 0)
-          reinterpret_cast<float2*>(p.part_ml)[static_cast<int64_t>(slot) * G + head] = make_float2(m, l);
+        reinterpret_cast<float4*>(p.part_acc + slot * G * D)[i] = a;
+        if (i % (D / 4) == 0) reinterpret_cast<float2*>(p.part_ml)[slot * G + head] = ml;
       }
     }
-    if (whole) continue;
+    if (whole) {
+      __syncthreads();  // the weights are read before the next (b, h) writes its own
+      continue;
+    }
 
     // ---- shared with other CTAs: the last one to arrive merges
     auto cta_of = [&](int page) {
@@ -505,51 +565,70 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block8_kernel(const Params p
       while (cta_begin(c) > page) --c;
       return c;
     };
-    const int first_cta = cta_of(u_lo), last_cta = cta_of(u_hi - 1);
+    const int first_cta = cta_of(u_lo), pieces = cta_of(u_hi - 1) - first_cta + 1;
     __threadfence();
     __syncthreads();
-    if (tid == 0) last_s = atomicAdd(&p.arrived[u], 1) == last_cta - first_cta;
+    if (tid == 0) last_s = atomicAdd(&p.arrived[u], 1) == pieces - 1;
     __syncthreads();
-    if (last_s) {
-      __threadfence();
-      for (int i = tid; i < G * D / 4; i += kThreads) {
-        const int head = i / (D / 4);
-        float m = -INFINITY;
-        for (int c = first_cta; c <= last_cta; ++c) {
-          const int sl = c * 2 + (u_lo <= cta_begin(c) ? 0 : 1);
-          m = fmaxf(m, __ldcg(p.part_ml + (static_cast<int64_t>(sl) * G + head) * 2));
-        }
-        float l = 0.f;
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int c = first_cta; c <= last_cta; ++c) {
-          const int sl = c * 2 + (u_lo <= cta_begin(c) ? 0 : 1);
-          const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + static_cast<int64_t>(sl) * G + head);
-          const float w = ml.x == m ? 1.f : ex2_approx(ml.x - m);
-          const float4 x = __ldcg(reinterpret_cast<const float4*>(p.part_acc + static_cast<int64_t>(sl) * G * D) + i);
-          l = fmaf(w, ml.y, l);
-          a.x = fmaf(w, x.x, a.x);
-          a.y = fmaf(w, x.y, a.y);
-          a.z = fmaf(w, x.z, a.z);
-          a.w = fmaf(w, x.w, a.w);
-        }
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        reinterpret_cast<float4*>(p.out + static_cast<int64_t>(u) * G * D)[i] =
-            make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
-        if (i % (D / 4) == 0) write_lse(p, static_cast<int64_t>(u) * G + head, m, l);
+    if (!last_s) continue;
+    __threadfence();
+    // a CTA's partial result lies in its slot 0 if the (b, h) has begun where the CTA's pages begin, else in slot 1
+    auto slot_of = [&](int c) { return static_cast<int64_t>(first_cta + c) * 2 + (c > 0 || u_lo <= cta_begin(first_cta) ? 0 : 1); };
+    if (warp < G) {
+      float m = -INFINITY;
+      for (int c = lane; c < pieces; c += 32) {
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + slot_of(c) * G + warp);
+        cta_ml[warp * kMaxCtas + c] = ml;
+        m = fmaxf(m, ml.x);
       }
-      if (tid == 0) p.arrived[u] = 0;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      float l = 0.f;
+      for (int c = lane; c < pieces; c += 32) {
+        float2& ml = cta_ml[warp * kMaxCtas + c];
+        const float w = ml.x == m ? 1.f : ex2_approx(ml.x - m);
+        l = fmaf(w, ml.y, l);
+        ml.x = w;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      if (lane == 0) merged_ml[warp] = make_float2(m, l);
     }
+    __syncthreads();
+    // the threads in groups of G * D / 4, each group taking every `groups`-th CTA's partial result
+    const int items = G * D / 4, groups = kThreads / items;
+    const int i = tid % items, grp = tid / items, head = i / (D / 4);
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (grp < groups) {
+#pragma unroll 4
+      for (int c = grp; c < pieces; c += groups) {
+        const float w = cta_ml[head * kMaxCtas + c].x;
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(p.part_acc + slot_of(c) * G * D) + i);
+        a.x = fmaf(w, x.x, a.x);
+        a.y = fmaf(w, x.y, a.y);
+        a.z = fmaf(w, x.z, a.z);
+        a.w = fmaf(w, x.w, a.w);
+      }
+    }
+    rows[tid] = a;
+    __syncthreads();
+    if (grp == 0) {
+      for (int k = 1; k < groups; ++k) {
+        const float4 x = rows[k * items + i];
+        a.x += x.x;
+        a.y += x.y;
+        a.z += x.z;
+        a.w += x.w;
+      }
+      const float2 ml = merged_ml[head];
+      const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;
+      reinterpret_cast<float4*>(p.out + static_cast<int64_t>(u) * G * D)[i] =
+          make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+      if (i % (D / 4) == 0) write_lse(p, static_cast<int64_t>(u) * G + head, ml.x, ml.y);
+    }
+    if (tid == 0) p.arrived[u] = 0;
+    __syncthreads();
   }
-}
-
-int device_sms() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-    (void)cudaGetLastError();
-    return 0;
-  }
-  return n;
 }
 
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -560,15 +639,19 @@ size_t attn_ws_bytes(int64_t BH, int G, int D) {
 }
 
 template <int D, int FMT, bool kDup>
-kvp_status launch(const Params& p, int grid, cudaStream_t st) {
-  const size_t smem = smem_bytes<D>(p.BH, p.G);
-  // per device, so set at every call (it is a host-side attribute write)
-  if (cudaFuncSetAttribute(attn_block8_kernel<D, FMT, kDup>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(smem)) != cudaSuccess) {
-    (void)cudaGetLastError();
-    return KVP_ERR_CUDA;
+kvp_status launch(const Params& p, int device, int grid, cudaStream_t st) {
+  // the shared-memory limit is a property of the kernel on each device: set once there, for the largest call
+  static std::atomic<uint64_t> ready{0};
+  if (device > 63 || !((ready.load(std::memory_order_relaxed) >> device) & 1u)) {
+    if (cudaFuncSetAttribute(attn_block8_kernel<D, FMT, kDup>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(smem_bytes<D>(kMaxBH, kDup ? 4 : 8))) != cudaSuccess) {
+      (void)cudaGetLastError();
+      return KVP_ERR_CUDA;
+    }
+    if (device <= 63) ready.fetch_or(uint64_t{1} << device, std::memory_order_relaxed);
   }
-  return launch_pdl(attn_block8_kernel<D, FMT, kDup>, dim3(grid), dim3(kThreads), smem, st, p) == cudaSuccess
+  return launch_pdl(attn_block8_kernel<D, FMT, kDup>, dim3(grid), dim3(kThreads), smem_bytes<D>(p.BH, p.G), st, p) ==
+                 cudaSuccess
              ? KVP_OK
              : KVP_ERR_CUDA;
 }
@@ -596,7 +679,8 @@ kvp_status attn_block8_impl(int fmt, int batch, int n_q_heads, int n_kv_heads, i
     return KVP_ERR_ALIGN;
   if (workspace == nullptr || workspace_bytes < attn_ws_bytes(BH, G, head_dim)) return KVP_ERR_WORKSPACE;
   if (!al16(workspace)) return KVP_ERR_ALIGN;
-  const int sms = device_sms();
+  int device = 0;
+  const int sms = current_sms(&device);
   if (sms == 0) return KVP_ERR_CUDA;
   int grid = sms < kMaxCtas ? sms : kMaxCtas;
   if (grid_limit > 0 && grid_limit < grid) grid = grid_limit;
@@ -623,7 +707,7 @@ kvp_status attn_block8_impl(int fmt, int batch, int n_q_heads, int n_kv_heads, i
   p.status = status;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool dup = G <= 4;
-#define KVP_ATTN8(D, F) (dup ? launch<D, F, true>(p, grid, st) : launch<D, F, false>(p, grid, st))
+#define KVP_ATTN8(D, F) (dup ? launch<D, F, true>(p, device, grid, st) : launch<D, F, false>(p, device, grid, st))
   if (fmt == KVP_BLOCK8_E4M3) return head_dim == 128 ? KVP_ATTN8(128, KVP_BLOCK8_E4M3) : KVP_ATTN8(64, KVP_BLOCK8_E4M3);
   return head_dim == 128 ? KVP_ATTN8(128, KVP_BLOCK8_INT8) : KVP_ATTN8(64, KVP_BLOCK8_INT8);
 #undef KVP_ATTN8

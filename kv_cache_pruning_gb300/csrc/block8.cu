@@ -355,17 +355,6 @@ __global__ void __launch_bounds__(kPageWarps * 32) read_block8_kernel(
   }
 }
 
-// SM count of the current device (0 when it cannot be asked).
-int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-    (void)cudaGetLastError();
-    return 0;
-  }
-  return n;
-}
-
 // The buffers that every call on this cache takes.
 kvp_status check_block8(int fmt, int batch, int n_kv_heads, int head_dim, const void* kq_pool, const void* vq_pool,
                         const void* scale_pool, int n_pages_cap, const void* page_table, int max_pages,
@@ -390,7 +379,8 @@ kvp_status launch_compact(const MaskedSrc& src, int BH, int NS, int now, int res
   const CompactWs ws = carve(workspace, BH, NS);
   int32_t* n_used = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + prep_bytes(BH, NS));
   int2* owner = reinterpret_cast<int2*>(n_used + 4);
-  const int sms = sm_count();
+  int device = 0;
+  const int sms = current_sms(&device);
   if (sms == 0) return KVP_ERR_CUDA;
   const int segs = (NS + kWarpsPerCta - 1) / kWarpsPerCta;
   if (cudaMemsetAsync(count, 0, static_cast<size_t>(BH) * sizeof(int32_t), st) != cudaSuccess) return KVP_ERR_CUDA;

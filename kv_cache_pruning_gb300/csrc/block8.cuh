@@ -12,6 +12,8 @@
 // int8's range and lose half a step at every growth.
 #pragma once
 
+#include <atomic>
+
 #include <cuda_fp16.h>
 
 #include "kvp_common.cuh"
@@ -79,6 +81,23 @@ KVP_DEV uint32_t rescale4(uint32_t w, float ratio) {
   const float2 a = decode2<FMT>(w), b = decode2<FMT>(w >> 16);
   return encode2<FMT>(__fmul_rn(a.x, ratio), __fmul_rn(a.y, ratio)) |
          (encode2<FMT>(__fmul_rn(b.x, ratio), __fmul_rn(b.y, ratio)) << 16);
+}
+
+// SM count of the current device, whose number goes to *device (0 when it cannot be asked); asked once per device.
+inline int current_sms(int* device) {
+  static std::atomic<int> known[64];
+  int n = 0;
+  if (cudaGetDevice(device) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return 0;
+  }
+  if (*device < 64 && (n = known[*device].load(std::memory_order_relaxed)) != 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, *device) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return 0;
+  }
+  if (*device < 64) known[*device].store(n, std::memory_order_relaxed);
+  return n;
 }
 
 }  // namespace
