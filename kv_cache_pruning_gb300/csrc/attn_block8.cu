@@ -50,6 +50,8 @@ constexpr int kMaxBH = 4096;     // (b, h) pairs whose page prefix fits in share
 constexpr int kMaxCtas = 512;    // grid bound used to size the workspace
 constexpr float kLazy = 3.f;     // how far a base-2 logit may pass the reference before it moves
 constexpr float kBias = 12.f;    // weights are 2^(x - m + kBias): at most 2^(kLazy + kBias) in fp16
+constexpr int kFewPieces = 8;    // CTAs whose partial results of one (b, h) are merged in one round trip
+constexpr int kOwnPages = 64;    // pages of a (b, h) that one CTA of its own takes: 4 a warp
 constexpr int kAhead = 2;        // pages whose lines are brought into L2 before their loads
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -63,6 +65,7 @@ struct Params {
   const int32_t* count;
   const int32_t* now_dev;
   int BH, G, max_pages, n_pages_cap, now;
+  int64_t table_lines, q_lines;  // 128-byte lines of the page table and the queries worth bringing into L2 early
   float qscale;        // scale * log2(e)
   float* out;          // [B, Hq, D]
   float* lse;          // [B, Hq] or null
@@ -77,6 +80,7 @@ KVP_DEV uint32_t movmatrix_trans(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
+KVP_DEV void prefetch_l2(const void* a) { asm volatile("prefetch.global.L2 [%0];" ::"l"(a)); }
 // d = A B with a zero accumulator.
 KVP_DEV void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -199,23 +203,50 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block8_kernel(const Params p
   __shared__ int part_unit[kWarps * 2];
   __shared__ float wts[8][2 * kWarps];   // a merge's weights: head, partial result
   __shared__ float2 merged_ml[8];
-  __shared__ int last_s;
+  __shared__ int last_s[2];
   pdl_launch_dependents();
-  pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int G = p.G;
-  int* prefix = reinterpret_cast<int*>(sm);
   const int pf = part_floats<D>(G);
+  int* prefix = reinterpret_cast<int*>(sm);
   float* parts = reinterpret_cast<float*>(sm + prefix_bytes(p.BH));
   float2* cta_ml = reinterpret_cast<float2*>(parts + kWarps * 2 * pf);
   float4* rows = reinterpret_cast<float4*>(cta_ml + G * kMaxCtas);
+  // the page table's and the queries' lines on their way to L2 while the counts are read and summed up
+  {
+    const int64_t line = static_cast<int64_t>(blockIdx.x) * kThreads + tid;
+    if (line < p.table_lines) prefetch_l2(reinterpret_cast<const uint8_t*>(p.page_table) + line * 128);
+    else if (line - p.table_lines < p.q_lines) prefetch_l2(reinterpret_cast<const uint8_t*>(p.q) + (line - p.table_lines) * 128);
+  }
+  pdl_wait();
+  const int now = p.now_dev != nullptr ? *p.now_dev : p.now;
 
   // ---- pages before each (b, h)
   const int cap = p.max_pages * kPage;
   const int each = (p.BH + kThreads - 1) / kThreads;
-  {
-    int sum = 0;
-    for (int i = tid * each; i < min(p.BH, (tid + 1) * each); ++i) sum += (min(max(p.count[i], 0), cap) + kPage - 1) / kPage;
+  auto pages_of = [&](int u) { return (min(max(p.count[u], 0), cap) + kPage - 1) / kPage; };
+  bool none = false, many = p.BH > static_cast<int>(gridDim.x);
+  int sum = 0;
+  for (int i = tid * each; i < min(p.BH, (tid + 1) * each); ++i) {
+    const int pages = pages_of(i);
+    sum += pages;
+    none |= pages == 0;
+    many |= pages > kOwnPages;
+  }
+  if (tid < kWarps * 2) part_unit[tid] = -1;
+  const bool any_empty = __syncthreads_or(none);
+  // A CTA for each (b, h), where there are enough of them and no (b, h) keeps a warp for long: nothing to merge
+  // between CTAs. Otherwise all pages are dealt out evenly.
+  const bool own = !__syncthreads_or(many);
+  int total, ctas;
+  if (own) {
+    ctas = p.BH;
+    if (tid == 0 && static_cast<int>(blockIdx.x) < p.BH) {
+      prefix[blockIdx.x] = 0;
+      prefix[blockIdx.x + 1] = pages_of(blockIdx.x);
+    }
+    total = 0;
+  } else {
     int incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -223,35 +254,38 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block8_kernel(const Params p
       if (lane >= o) incl += y;
     }
     if (lane == 31) warp_sum[warp] = incl;
-    if (tid < kWarps * 2) part_unit[tid] = -1;
     __syncthreads();
     int at = incl - sum;
+    total = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) at += w < warp ? warp_sum[w] : 0;
+    for (int w = 0; w < kWarps; ++w) {
+      at += w < warp ? warp_sum[w] : 0;
+      total += warp_sum[w];
+    }
     for (int i = tid * each; i < min(p.BH, (tid + 1) * each); ++i) {
       prefix[i] = at;
-      at += (min(max(p.count[i], 0), cap) + kPage - 1) / kPage;
+      at += pages_of(i);
     }
-    if (tid == kThreads - 1) prefix[p.BH] = at;
-    __syncthreads();
+    if (tid == 0) prefix[p.BH] = total;
+    ctas = min(static_cast<int>(gridDim.x), (total + kWarps - 1) / kWarps);
   }
-  const int total = prefix[p.BH];
-  const int now = p.now_dev != nullptr ? *p.now_dev : p.now;
+  __syncthreads();
 
   // rows of (b, h) without pages
-  for (int u = blockIdx.x; u < p.BH; u += gridDim.x) {
+  for (int u = blockIdx.x; any_empty && u < p.BH; u += gridDim.x) {
     if (prefix[u + 1] > prefix[u]) continue;
     for (int i = tid; i < G * D; i += kThreads) p.out[static_cast<int64_t>(u) * G * D + i] = 0.f;
     if (p.lse != nullptr && tid < G) p.lse[static_cast<int64_t>(u) * G + tid] = -INFINITY;
   }
 
   // ---- this CTA's and this warp's pages
-  const int ctas = min(static_cast<int>(gridDim.x), (total + kWarps - 1) / kWarps);
   if (static_cast<int>(blockIdx.x) >= ctas) return;
-  auto cta_begin = [&](int c) { return static_cast<int>(static_cast<int64_t>(c) * total / ctas); };
-  const int c_lo = cta_begin(blockIdx.x), c_hi = cta_begin(blockIdx.x + 1);
-  const int lo = c_lo + static_cast<int>(static_cast<int64_t>(warp) * (c_hi - c_lo) / kWarps);
-  const int hi = c_lo + static_cast<int>(static_cast<int64_t>(warp + 1) * (c_hi - c_lo) / kWarps);
+  // CTA c takes pages cta_begin(c) .. cta_begin(c + 1) - 1: `share` each, the first `extra` CTAs one more
+  const int share = own ? 0 : total / ctas, extra = own ? 0 : total - share * ctas;
+  auto cta_begin = [&](int c) { return c * share + min(c, extra); };
+  const int c_lo = own ? 0 : cta_begin(blockIdx.x), c_hi = own ? prefix[blockIdx.x + 1] : cta_begin(blockIdx.x + 1);
+  const int lo = c_lo + warp * ((c_hi - c_lo) / kWarps) + min(warp, (c_hi - c_lo) % kWarps);
+  const int hi = c_lo + (warp + 1) * ((c_hi - c_lo) / kWarps) + min(warp + 1, (c_hi - c_lo) % kWarps);
   // the (b, h) of a page of the list: the last one whose pages start at or before it and that has any
   auto unit_of = [&](int page) {
     int a = 0, b = p.BH;
@@ -264,12 +298,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block8_kernel(const Params p
 
   if (lo < hi) {
     int at = lo;
-    int u = unit_of(lo);
+    int u = own ? static_cast<int>(blockIdx.x) : unit_of(lo);
     while (at < hi) {
       while (prefix[u + 1] <= at) ++u;
       const int u_lo = prefix[u], u_hi = prefix[u + 1];
       const int end = min(hi, u_hi);
       const int cnt = min(max(p.count[u], 0), cap);
+      // ---- this (b, h)'s queries, requested first: lane (g, t) takes head g's (kDup: g % 4's) channels of its words
+      uint4 x[D / 32];
+      {
+        const int head = kDup ? (g & 3) : g;
+        const uint16_t* row = p.q + (static_cast<int64_t>(u) * G + head) * D;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          x[i] = make_uint4(0, 0, 0, 0);
+          if (head < G) x[i] = __ldg(reinterpret_cast<const uint4*>(row + (i >> 1) * 64 + t * 16 + (i & 1) * 8));
+        }
+      }
       const int32_t* table = p.page_table + static_cast<int64_t>(u) * p.max_pages + (at - u_lo);
       const int n = end - at;            // pages of this (b, h) in the warp's range
 
@@ -308,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block8_kernel(const Params p
         if (id >= 0 && lane < 2 * kLines) {
           const uint8_t* a = (lane < kLines ? p.k_pool : p.v_pool) + static_cast<int64_t>(id) * kPage * D +
                              (lane % kLines) * 128;
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(a));
+          prefetch_l2(a);
         }
       };
       {
@@ -319,21 +364,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block8_kernel(const Params p
 #pragma unroll
       for (int i = 1; i <= kAhead; ++i) bring(i);
 
-      // ---- this (b, h)'s queries as B fragments: lane (g, t) holds head g (kDup: g % 4), its words' channels
+      // ---- the queries as B fragments
       uint32_t qf[D / 16][2];
       float qs[2];   // logits' factors of the lane's heads 2t, 2t + 1
       {
-        const int head = kDup ? (g & 3) : g;
-        const uint16_t* row = p.q + (static_cast<int64_t>(u) * G + head) * D;
-        uint4 x[D / 32];
         uint32_t big = 0;
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          x[i] = make_uint4(0, 0, 0, 0);
-          if (head < G) x[i] = *reinterpret_cast<const uint4*>(row + (i >> 1) * 64 + t * 16 + (i & 1) * 8);
+        for (int i = 0; i < D / 32; ++i)
           big = __vmaxu2(big, __vmaxu2(__vmaxu2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu),
                                        __vmaxu2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu)));
-        }
         uint32_t a = max(big & 0xFFFFu, big >> 16);
         a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
         a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
@@ -507,6 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block8_kernel(const Params p
   const int my_unit = part_unit[lane];
   const unsigned same = __match_any_sync(0xffffffffu, my_unit);
   unsigned leaders = __ballot_sync(0xffffffffu, my_unit >= 0 && (same & ((1u << lane) - 1u)) == 0);
+  int shared0 = -1, shared1 = -1;  // the (b, h)s that other CTAs share: at most the CTA's first (slot 0) and last (slot 1)
   while (leaders != 0) {
     const int lead = __ffs(leaders) - 1;
     leaders &= leaders - 1;
@@ -529,18 +569,31 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block8_kernel(const Params p
       if (lane == 0) merged_ml[warp] = make_float2(m, l);
     }
     __syncthreads();
-    const int64_t slot = blockIdx.x * 2 + (u_lo <= c_lo ? 0 : 1);
+    const int side = u_lo <= c_lo ? 0 : 1;
+    const int64_t slot = blockIdx.x * 2 + side;
+    if (!whole && side == 0) shared0 = u;
+    if (!whole && side == 1) shared1 = u;
     for (int i = tid; i < G * D / 4; i += kThreads) {
       const int head = i / (D / 4);
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (unsigned left = entries; left != 0; left &= left - 1) {
-        const int e = __ffs(left) - 1;
-        const float w = wts[head][e];
-        const float4 x = reinterpret_cast<const float4*>(parts + e * pf)[i];
-        a.x = fmaf(w, x.x, a.x);
-        a.y = fmaf(w, x.y, a.y);
-        a.z = fmaf(w, x.z, a.z);
-        a.w = fmaf(w, x.w, a.w);
+      unsigned left = entries;
+      while (left != 0) {  // four at a time, so that their reads overlap
+        int e[4];
+        float w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          e[k] = left != 0 ? __ffs(left) - 1 : lead;
+          w[k] = left != 0 ? wts[head][e[k]] : 0.f;
+          left &= left - 1;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float4 x = reinterpret_cast<const float4*>(parts + e[k] * pf)[i];
+          a.x = fmaf(w[k], x.x, a.x);
+          a.y = fmaf(w[k], x.y, a.y);
+          a.z = fmaf(w[k], x.z, a.z);
+          a.w = fmaf(w[k], x.w, a.w);
+        }
       }
       const float2 ml = merged_ml[head];
       if (whole) {
@@ -553,27 +606,68 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block8_kernel(const Params p
         if (i % (D / 4) == 0) reinterpret_cast<float2*>(p.part_ml)[slot * G + head] = ml;
       }
     }
-    if (whole) {
-      __syncthreads();  // the weights are read before the next (b, h) writes its own
-      continue;
-    }
+    __syncthreads();  // the weights are read before the next (b, h) writes its own
+  }
+  if (shared0 < 0 && shared1 < 0) return;
 
-    // ---- shared with other CTAs: the last one to arrive merges
-    auto cta_of = [&](int page) {
-      int c = static_cast<int>(static_cast<int64_t>(page) * ctas / total);
-      while (cta_begin(c + 1) <= page) ++c;
-      while (cta_begin(c) > page) --c;
-      return c;
-    };
-    const int first_cta = cta_of(u_lo), pieces = cta_of(u_hi - 1) - first_cta + 1;
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) last_s = atomicAdd(&p.arrived[u], 1) == pieces - 1;
-    __syncthreads();
-    if (!last_s) continue;
-    __threadfence();
+  // ---- shared with other CTAs: the last one to arrive merges
+  auto cta_of = [&](int page) {
+    const int longer = extra * (share + 1);  // pages of the CTAs with one more
+    return page < longer ? page / (share + 1) : extra + (page - longer) / share;
+  };
+  // the barrier above saw the CTA's partial results written; each thread's fence publishes them before it counts
+  if (tid < 2) {
+    const int u = tid == 0 ? shared0 : shared1;
+    last_s[tid] = 0;
+    if (u >= 0) {
+      const int pieces = cta_of(prefix[u + 1] - 1) - cta_of(prefix[u]) + 1;
+      fence_acq_rel_gpu();
+      last_s[tid] = atomicAdd(&p.arrived[u], 1) == pieces - 1;
+      fence_acq_rel_gpu();
+    }
+  }
+  __syncthreads();
+  for (int side = 0; side < 2; ++side) {
+    if (!last_s[side]) continue;
+    const int u = side == 0 ? shared0 : shared1;
+    const int u_lo = prefix[u], first_cta = cta_of(u_lo), pieces = cta_of(prefix[u + 1] - 1) - first_cta + 1;
     // a CTA's partial result lies in its slot 0 if the (b, h) has begun where the CTA's pages begin, else in slot 1
     auto slot_of = [&](int c) { return static_cast<int64_t>(first_cta + c) * 2 + (c > 0 || u_lo <= cta_begin(first_cta) ? 0 : 1); };
+    if (pieces <= kFewPieces) {  // everything a thread needs in one round trip
+      for (int i = tid; i < G * D / 4; i += kThreads) {
+        const int head = i / (D / 4);
+        float2 ml[kFewPieces];
+        float4 x[kFewPieces];
+#pragma unroll
+        for (int c = 0; c < kFewPieces; ++c) {
+          ml[c] = make_float2(-INFINITY, 0.f);
+          x[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (c < pieces) {
+            ml[c] = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + slot_of(c) * G + head);
+            x[c] = __ldcg(reinterpret_cast<const float4*>(p.part_acc + slot_of(c) * G * D) + i);
+          }
+        }
+        float m = ml[0].x, l = 0.f;
+#pragma unroll
+        for (int c = 1; c < kFewPieces; ++c) m = fmaxf(m, ml[c].x);
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < kFewPieces; ++c) {
+          const float w = ml[c].x == m ? 1.f : ex2_approx(ml[c].x - m);
+          l = fmaf(w, ml[c].y, l);
+          a.x = fmaf(w, x[c].x, a.x);
+          a.y = fmaf(w, x[c].y, a.y);
+          a.z = fmaf(w, x[c].z, a.z);
+          a.w = fmaf(w, x[c].w, a.w);
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        reinterpret_cast<float4*>(p.out + static_cast<int64_t>(u) * G * D)[i] =
+            make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+        if (i % (D / 4) == 0) write_lse(p, static_cast<int64_t>(u) * G + head, m, l);
+      }
+      if (tid == 0) p.arrived[u] = 0;
+      continue;
+    }
     if (warp < G) {
       float m = -INFINITY;
       for (int c = lane; c < pieces; c += 32) {
@@ -705,6 +799,13 @@ kvp_status attn_block8_impl(int fmt, int batch, int n_q_heads, int n_kv_heads, i
   p.part_acc = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + counters_bytes(BH));
   p.part_ml = p.part_acc + static_cast<size_t>(2) * kMaxCtas * G * head_dim;
   p.status = status;
+  // bringing lines into L2 early pays while one instruction of each thread does it; a table with more lines than
+  // that is larger than its used part is likely to be
+  const int64_t threads = static_cast<int64_t>(grid) * kThreads;
+  p.table_lines = (BH * max_pages * 4 + 127) / 128;
+  p.q_lines = (BH * G * head_dim * 2 + 127) / 128;
+  if (p.table_lines + p.q_lines > threads) p.table_lines = 0;
+  if (p.q_lines > threads) p.q_lines = 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool dup = G <= 4;
 #define KVP_ATTN8(D, F) (dup ? launch<D, F, true>(p, device, grid, st) : launch<D, F, false>(p, device, grid, st))
