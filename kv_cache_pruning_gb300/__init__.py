@@ -802,66 +802,78 @@ def kvp_decode_attn_mla(q, cache: LatentPagedKV, now, *, scale=0.0, out=None, n_
 
 
 # --------------------------------------------------------------------------- block-scaled 8-bit cache
+#
+# These calls are made once a layer and step, often on little work, so their checks are written to be cheap: a device
+# is its index, a handle checks its buffers when it is made and keeps their sizes (they cannot be replaced in it).
 
-def _on(t, dtype, name, device, shape=None):
-    """Device pointer of a contiguous tensor that has to be on `device` (None: NULL)."""
-    if t is None:
-        return None
-    if t.dtype != dtype:
+_raw_stream = torch._C._cuda_getCurrentRawStream   # the current stream of a device, without a Stream object
+_current_device = torch._C._cuda_getDevice
+
+
+def _refuse(t, dtype, name, dev, shape=None):
+    """The error of a tensor that _on or _rows does not take."""
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, not on {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, not on {t.device}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must be of shape {tuple(shape)}, not {tuple(t.shape)}")
+    raise ValueError(f"{name} must be contiguous (of q, k, v and their outputs: its last dimension)")
+
+
+def _on(t, dtype, name, dev, shape=None):
+    """Device pointer of a contiguous tensor that has to be on CUDA device `dev` (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous() or (shape is not None and t.shape != shape):
+        _refuse(t, dtype, name, dev, shape)
     return t.data_ptr()
 
 
-def _rows(t, name, device):
-    """Device pointer of a bf16 tensor on `device` whose last dimension is contiguous."""
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, not on {t.device}")
-    if t.stride(-1) != 1 and t.shape[-1] != 1:
-        raise ValueError(f"{name} rows must be contiguous")
+def _rows(t, name, dev):
+    """Device pointer of a bf16 tensor on `dev` whose last dimension is contiguous."""
+    if t.dtype is not torch.bfloat16 or t.get_device() != dev or (t.stride(-1) != 1 and t.shape[-1] != 1):
+        _refuse(t, torch.bfloat16, name, dev)
     return t.data_ptr()
 
 
 def _strides(t):
     """Strides of a tensor's outer dimensions, 0 for those of length 1 (whose stride says nothing)."""
-    return tuple(0 if n == 1 else s for n, s in zip(t.shape[:-1], t.stride()))
+    shape, st = t.shape, t.stride()
+    if 1 in shape:
+        return tuple(0 if n == 1 else s for n, s in zip(shape[:-1], st))
+    return st[:-1]
 
 
-def _status(status, device):
+def _status(status, dev):
     """Device pointer of the status word (None: NULL)."""
     if status is not None and status.numel() < 1:
         raise ValueError("status must hold one value")
-    return _on(status, torch.int32, "status", device)
+    return _on(status, torch.int32, "status", dev)
 
 
-def _call(fn: str, device, stream, *args):
-    """One library call on `device`, whichever device is current, and on `stream` or that device's current stream."""
+def _call(fn, dev, stream, *args):
+    """One library call on device `dev`, whichever device is current, and on `stream` or dev's current stream."""
     if stream is None:
-        raw = torch.cuda.current_stream(device).cuda_stream
+        raw = _raw_stream(dev)
     elif isinstance(stream, torch.cuda.Stream):
-        if stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
+        if stream.device.index != dev:
+            raise ValueError(f"stream is on {stream.device}, the tensors are on cuda:{dev}")
         raw = stream.cuda_stream
     else:
         raw = int(stream)
-    if device.index == torch.cuda.current_device():
-        code = getattr(_lib, fn)(*args, raw)
+    if _current_device() == dev:
+        code = fn(*args, raw)
     else:
-        with torch.cuda.device(device):
-            code = getattr(_lib, fn)(*args, raw)
+        with torch.cuda.device(dev):
+            code = fn(*args, raw)
     if code != KVP_OK:
-        raise KvpError(fn, code)
+        raise KvpError(fn.__name__, code)
 
 
-def _new(make, shape, dtype, device, stream):
+def _new(make, shape, dtype, dev, stream):
     """A new tensor that work on `stream` may use at once: memory of that stream's own, filled in its order."""
+    device = torch.device("cuda", dev)
     if stream is None:
         return make(shape, dtype=dtype, device=device)
     if not isinstance(stream, torch.cuda.Stream):
@@ -870,15 +882,17 @@ def _new(make, shape, dtype, device, stream):
         return make(shape, dtype=dtype, device=device)
 
 
-def _space(nbytes, workspace, device, stream, make=torch.empty):
-    """(pointer, bytes) of the caller's workspace, or of a new one, and the tensor."""
+def _space(nbytes, workspace, dev, stream, make=torch.empty):
+    """The caller's workspace, checked, or a new one, and its size in bytes."""
     if workspace is None:
-        workspace = _new(make, max(nbytes, 16), torch.uint8, device, stream)
-    elif workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be contiguous and on {device}")
-    elif workspace.numel() * workspace.element_size() < nbytes:
+        n = max(nbytes, 16)
+        return _new(make, n, torch.uint8, dev, stream), n
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on cuda:{dev}")
+    have = workspace.numel() * workspace.element_size()
+    if have < nbytes:
         raise ValueError("workspace too small")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+    return workspace, have
 
 
 @dataclass(frozen=True)
@@ -897,9 +911,9 @@ class Block8PagedKV:
     def __post_init__(self):
         if self.fmt not in (KVP_BLOCK8_E4M3, KVP_BLOCK8_INT8):
             raise ValueError("fmt must be KVP_BLOCK8_E4M3 or KVP_BLOCK8_INT8")
-        dev = self.kq_pool.device
-        if dev.type != "cuda":
+        if not self.kq_pool.is_cuda:
             raise ValueError("kq_pool must be a CUDA tensor")
+        dev = self.kq_pool.get_device()
         if self.kq_pool.dim() != 3 or self.kq_pool.shape[1] != PAGE:
             raise ValueError("kq_pool must be [n_pages_cap, 16, d]")
         if self.page_table.dim() != 3:
@@ -912,6 +926,7 @@ class Block8PagedKV:
         _on(self.page_table, torch.int32, "page_table", dev)
         _on(self.remap, torch.int32, "remap", dev, (b, h, width * PAGE))
         _on(self.count, torch.int32, "count", dev, (b, h))
+        object.__setattr__(self, "_dims", (dev, self.fmt, b, h, self.kq_pool.shape[2], cap, width))
 
     @staticmethod
     def allocate(batch, n_kv_heads, head_dim, n_pages_cap, max_pages, fmt=KVP_BLOCK8_E4M3, device="cuda"):
@@ -936,9 +951,6 @@ class Block8PagedKV:
     def head_dim(self):
         return self.kq_pool.shape[2]
 
-    def _pools(self):
-        return (self.kq_pool.data_ptr(), self.vq_pool.data_ptr(), self.scale_pool.data_ptr())
-
 
 def kvp_compact_block8_workspace_bytes(batch, n_kv_heads, n_pos, n_pages_cap) -> int:
     return _lib.kvp_compact_block8_workspace_bytes(batch, n_kv_heads, n_pos, n_pages_cap)
@@ -949,51 +961,49 @@ def kvp_compact_block8(k, v, now, reserve, dst: Block8PagedKV, *, mode, scores=N
     """Dense K, V [B, T, H, d] (any strides with d contiguous) with the mask applied on the fly (KVzap scores [B, T, H]
     or [B*T, H] + tau [B, H], or DMS flag_step [B, H, T]) -> dst, quantised page by page. Counts, page table and remap
     list are kvp_compact_masked's."""
-    B, T, H, d = k.shape
-    dev = dst.kq_pool.device
-    kp, vp = _rows(k, "k", dev), _rows(v, "v", dev)
-    st = _strides(k)
-    if k.shape != v.shape or st != _strides(v):
+    dev, fmt, B, H, d, cap, width = dst._dims
+    T = k.shape[1]
+    kp, vp, st = _rows(k, "k", dev), _rows(v, "v", dev), _strides(k)
+    if k.shape != (B, T, H, d):
+        raise ValueError("k must be [B, T, H, d] of dst's batch, heads and head_dim")
+    if v.shape != k.shape or _strides(v) != st:
         raise ValueError("k and v need the same shape and strides")
-    if dst.count.shape != (B, H) or dst.head_dim != d:
-        raise ValueError("dst must be a cache of k's batch, heads and head_dim")
     if scores is not None and scores.numel() != B * T * H:
         raise ValueError("scores must hold B*T*H values")
     if tau is not None and tau.numel() != B * H:
         raise ValueError("tau must hold B*H values")
     if flag_step is not None and flag_step.numel() != B * H * T:
         raise ValueError("flag_step must hold B*H*T values")
-    sp, tp, fp = (_on(scores, torch.float32, "scores", dev), _on(tau, torch.float32, "tau", dev),
-                  _on(flag_step, torch.int32, "flag_step", dev))
-    cap = dst.n_pages_cap
-    wp, wn, ws = _space(kvp_compact_block8_workspace_bytes(B, H, T, cap), workspace, dev, stream)
-    _call("kvp_compact_block8", dev, stream, dst.fmt, mode, B, H, d, T, kp, vp, *st,
-          sp, tp, fp, window, delay, now, reserve, *dst._pools(), dst.expire_pool.data_ptr(), cap,
-          dst.page_table.data_ptr(), dst.max_pages, dst.remap.data_ptr(), dst.count.data_ptr(), wp, wn,
+    ws, ws_bytes = _space(kvp_compact_block8_workspace_bytes(B, H, T, cap), workspace, dev, stream)
+    _call(_lib.kvp_compact_block8, dev, stream, fmt, mode, B, H, d, T, kp, vp, *st,
+          _on(scores, torch.float32, "scores", dev), _on(tau, torch.float32, "tau", dev),
+          _on(flag_step, torch.int32, "flag_step", dev), window, delay, now, reserve, dst.kq_pool.data_ptr(),
+          dst.vq_pool.data_ptr(), dst.scale_pool.data_ptr(), dst.expire_pool.data_ptr(), cap,
+          dst.page_table.data_ptr(), width, dst.remap.data_ptr(), dst.count.data_ptr(), ws.data_ptr(), ws_bytes,
           _status(status, dev))
     return dst
 
 
 def _append_block8(fn, cache, k_new, v_new, pos, mode, score, tau, flag_step, window, delay, status, stream):
-    B, H, d = k_new.shape
-    dev = cache.kq_pool.device
-    if v_new.shape != k_new.shape or cache.count.shape != (B, H) or cache.head_dim != d:
+    dev, fmt, B, H, d, cap, width = cache._dims
+    if k_new.shape != (B, H, d) or v_new.shape != (B, H, d):
         raise ValueError("k_new and v_new must be [B, H, d] of the cache's batch, heads and head_dim")
     for t, nm in ((score, "score"), (tau, "tau"), (flag_step, "flag_step")):
         if t is not None and t.numel() != B * H:
             raise ValueError(f"{nm} must hold B*H values")
-    _call(fn, dev, stream, cache.fmt, mode, B, H, d, pos, _rows(k_new, "k_new", dev), _rows(v_new, "v_new", dev),
+    _call(fn, dev, stream, fmt, mode, B, H, d, pos, _rows(k_new, "k_new", dev), _rows(v_new, "v_new", dev),
           *_strides(k_new), *_strides(v_new), _on(score, torch.float32, "score", dev),
           _on(tau, torch.float32, "tau", dev), _on(flag_step, torch.int32, "flag_step", dev), window, delay,
-          *cache._pools(), cache.expire_pool.data_ptr(), cache.n_pages_cap, cache.page_table.data_ptr(),
-          cache.max_pages, cache.remap.data_ptr(), cache.count.data_ptr(), _status(status, dev))
+          cache.kq_pool.data_ptr(), cache.vq_pool.data_ptr(), cache.scale_pool.data_ptr(),
+          cache.expire_pool.data_ptr(), cap, cache.page_table.data_ptr(), width, cache.remap.data_ptr(),
+          cache.count.data_ptr(), _status(status, dev))
 
 
 def kvp_append_block8(cache: Block8PagedKV, k_new, v_new, pos, *, mode, score=None, tau=None, flag_step=None,
                       window=WINDOW, delay=0, status, stream=None):
     """Quantises the token at position `pos` (k_new, v_new [B, H, d], any strides with d contiguous) into every
     (b, h)'s next slot; a page whose scale has to grow is rounded to the new one."""
-    _append_block8("kvp_append_block8", cache, k_new, v_new, pos, mode, score, tau, flag_step, window, delay, status,
+    _append_block8(_lib.kvp_append_block8, cache, k_new, v_new, pos, mode, score, tau, flag_step, window, delay, status,
                    stream)
 
 
@@ -1001,8 +1011,8 @@ def kvp_append_block8_devpos(cache: Block8PagedKV, k_new, v_new, pos_dev, *, mod
                              flag_step=None, window=WINDOW, delay=0, status, stream=None):
     """kvp_append_block8 with the position taken from pos_dev (a device int32 tensor of one element) when the call
     runs on the stream."""
-    pos = _on(pos_dev, torch.int32, "pos_dev", cache.kq_pool.device)
-    _append_block8("kvp_append_block8_devpos", cache, k_new, v_new, pos, mode, score, tau, flag_step, window, delay,
+    pos = _on(pos_dev, torch.int32, "pos_dev", cache._dims[0])
+    _append_block8(_lib.kvp_append_block8_devpos, cache, k_new, v_new, pos, mode, score, tau, flag_step, window, delay,
                    status, stream)
 
 
@@ -1010,23 +1020,22 @@ def kvp_read_block8(cache: Block8PagedKV, first_slot, n_slots, *, k_out=None, v_
     """(k, v): slots first_slot .. first_slot + n_slots - 1 of every (b, h) as bf16 [B, n_slots, H, d] rows (k_out and
     v_out, if given, may have any strides with d contiguous, the same for both); zero rows past the counts. With
     status None, a page id out of range raises nothing: its rows come back as zeros."""
-    dev = cache.kq_pool.device
-    (B, H), d = cache.count.shape, cache.head_dim
+    dev, fmt, B, H, d, cap, width = cache._dims
     shape = (B, n_slots, H, d)
     if n_slots < 0:
         raise ValueError("n_slots must not be negative")
     if k_out is None:
         k_out = _new(torch.empty, shape, torch.bfloat16, dev, stream)
     if v_out is None:
-        v_out = _new(torch.empty, shape, torch.bfloat16, dev, stream) if k_out.is_contiguous() else None
-    if v_out is None or k_out.shape != shape or v_out.shape != shape or _strides(k_out) != _strides(v_out):
+        v_out = _new(torch.empty, shape, torch.bfloat16, dev, stream)
+    st = _strides(k_out)
+    if k_out.shape != shape or v_out.shape != shape or _strides(v_out) != st:
         raise ValueError("k_out and v_out must be [B, n_slots, H, d] of the same strides")
     if status is None:
         status = _new(torch.zeros, 1, torch.int32, dev, stream)
-    _call("kvp_read_block8", dev, stream, cache.fmt, B, H, d, *cache._pools(), cache.n_pages_cap,
-          cache.page_table.data_ptr(), cache.max_pages, cache.count.data_ptr(), first_slot, n_slots,
-          _rows(k_out, "k_out", dev), _rows(v_out, "v_out", dev), *_strides(k_out),
-          _status(status, dev))
+    _call(_lib.kvp_read_block8, dev, stream, fmt, B, H, d, cache.kq_pool.data_ptr(), cache.vq_pool.data_ptr(),
+          cache.scale_pool.data_ptr(), cap, cache.page_table.data_ptr(), width, cache.count.data_ptr(), first_slot,
+          n_slots, _rows(k_out, "k_out", dev), _rows(v_out, "v_out", dev), *st, _status(status, dev))
     return k_out, v_out
 
 
@@ -1035,20 +1044,19 @@ def kvp_decode_attn_block8_workspace_bytes(batch, n_q_heads, n_kv_heads, head_di
 
 
 def _attn_block8(fn, q, cache, now, scale, out, lse, grid_limit, workspace, status, stream):
-    B, Hq, d = q.shape
-    dev = cache.kq_pool.device
-    H = cache.count.shape[1]
-    if cache.count.shape[0] != B or cache.head_dim != d:
+    dev, fmt, B, H, d, cap, width = cache._dims
+    shape = q.shape
+    if len(shape) != 3 or shape[0] != B or shape[2] != d:
         raise ValueError("q must be [B, Hq, d] of the cache's batch and head_dim")
+    Hq = shape[1]
     qp = _on(q, torch.bfloat16, "q", dev)
     if out is None:
-        out = _new(torch.empty, (B, Hq, d), torch.float32, dev, stream)
-    op = _on(out, torch.float32, "out", dev, q.shape)
-    lp = _on(lse, torch.float32, "lse", dev, (B, Hq))
-    wp, wn, ws = _space(kvp_decode_attn_block8_workspace_bytes(B, Hq, H, d), workspace, dev, stream, torch.zeros)
-    _call(fn, dev, stream, cache.fmt, B, Hq, H, d, qp, *cache._pools(), cache.expire_pool.data_ptr(),
-          cache.n_pages_cap, cache.page_table.data_ptr(), cache.max_pages, cache.count.data_ptr(), now, float(scale),
-          op, lp, grid_limit, wp, wn, _status(status, dev))
+        out = _new(torch.empty, shape, torch.float32, dev, stream)
+    ws, ws_bytes = _space(_lib.kvp_decode_attn_block8_workspace_bytes(B, Hq, H, d), workspace, dev, stream, torch.zeros)
+    _call(fn, dev, stream, fmt, B, Hq, H, d, qp, cache.kq_pool.data_ptr(), cache.vq_pool.data_ptr(),
+          cache.scale_pool.data_ptr(), cache.expire_pool.data_ptr(), cap, cache.page_table.data_ptr(), width,
+          cache.count.data_ptr(), now, scale, _on(out, torch.float32, "out", dev, shape),
+          _on(lse, torch.float32, "lse", dev, (B, Hq)), grid_limit, ws.data_ptr(), ws_bytes, _status(status, dev))
     return out
 
 
@@ -1057,16 +1065,17 @@ def kvp_decode_attn_block8(q, cache: Block8PagedKV, now, *, scale=0.0, out=None,
     """out[B, Hq, d] fp32 = attention of q [B, Hq, d] (bf16) over the slots of the 8-bit `cache` present at `now`; lse
     (fp32 [B, Hq], if given) receives each row's log-sum-exp, for kvp_attn_merge. A caller-provided workspace must be
     zero-filled before its first use (torch.zeros); every call leaves it that way."""
-    return _attn_block8("kvp_decode_attn_block8", q, cache, now, scale, out, lse, grid_limit, workspace, status, stream)
+    return _attn_block8(_lib.kvp_decode_attn_block8, q, cache, now, scale, out, lse, grid_limit, workspace, status,
+                        stream)
 
 
 def kvp_decode_attn_block8_devpos(q, cache: Block8PagedKV, now_dev, *, scale=0.0, out=None, lse=None, grid_limit=0,
                                   workspace=None, status=None, stream=None):
     """kvp_decode_attn_block8 with the decode position taken from now_dev (a device int32 tensor of one element) when
     the call runs on the stream."""
-    now = _on(now_dev, torch.int32, "now_dev", cache.kq_pool.device)
-    return _attn_block8("kvp_decode_attn_block8_devpos", q, cache, now, scale, out, lse, grid_limit, workspace, status,
-                        stream)
+    now = _on(now_dev, torch.int32, "now_dev", cache._dims[0])
+    return _attn_block8(_lib.kvp_decode_attn_block8_devpos, q, cache, now, scale, out, lse, grid_limit, workspace,
+                        status, stream)
 
 
 # --------------------------------------------------------------------------- norm and rotation of queries and keys
@@ -1083,6 +1092,22 @@ def kvp_rope_turns(inv_freq, *, device=None):
     return turns.to(device)
 
 
+def _head_rows(x, y, name, dev, n, d, stream):
+    """(heads, in, its strides, out, its strides) of q or k for kvp_qk_norm_rope, and the output."""
+    if x is None:
+        if y is not None:
+            raise ValueError(f"{name}_out without {name}")
+        return (0, None, 0, 0, None, 0, 0), None
+    shape = x.shape
+    if len(shape) != 3 or shape[0] != n or shape[2] != d:
+        raise ValueError(f"{name} must be [n, heads, d]")
+    if y is None:
+        y = _new(torch.empty, shape, torch.bfloat16, dev, stream)
+    elif y.shape != shape:
+        raise ValueError(f"{name}_out must be of {name}'s shape")
+    return (shape[1], _rows(x, name, dev), *_strides(x), _rows(y, name, dev), *_strides(y)), y
+
+
 def kvp_qk_norm_rope(q, k, pos, turns, *, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, q_out=None,
                      k_out=None, stream=None):
     """(q_out, k_out): the heads of q [n, Hq, d] and k [n, Hk, d] (bf16, any strides with d contiguous; either may be
@@ -1092,38 +1117,22 @@ def kvp_qk_norm_rope(q, k, pos, turns, *, q_weight=None, k_weight=None, eps=1e-6
     some = q if q is not None else k
     if some is None:
         raise ValueError("q or k is required")
-    dev, n, d = some.device, some.shape[0], some.shape[-1]
-    if dev.type != "cuda":
+    if not some.is_cuda:
         raise ValueError("q and k must be CUDA tensors")
+    dev, n, d = some.get_device(), some.shape[0], some.shape[-1]
     rot = 0
     if turns is not None:
         rot = 2 * turns.numel()
         if pos is None:
             raise ValueError("pos is required with turns")
-    args = []
-    outs = []
-    for x, y, name in ((q, q_out, "q"), (k, k_out, "k")):
-        if x is None:
-            if y is not None:
-                raise ValueError(f"{name}_out without {name}")
-            args.append((0, None, 0, 0, None, 0, 0))
-            outs.append(None)
-            continue
-        if x.dim() != 3 or x.shape[0] != n or x.shape[2] != d:
-            raise ValueError(f"{name} must be [n, heads, d]")
-        if y is None:
-            y = _new(torch.empty, x.shape, torch.bfloat16, dev, stream)
-        elif y.shape != x.shape:
-            raise ValueError(f"{name}_out must be of {name}'s shape")
-        args.append((x.shape[1], _rows(x, name, dev), *_strides(x), _rows(y, name + "_out", dev), *_strides(y)))
-        outs.append(y)
-    (hq, qp, q0, q1, qo, qo0, qo1), (hk, kp, k0, k1, ko, ko0, ko1) = args
-    _call("kvp_qk_norm_rope", dev, stream, n, hq, hk, d, rot, int(interleaved), qp, q0, q1, kp, k0, k1,
+    (hq, qp, q0, q1, qo, qo0, qo1), q_out = _head_rows(q, q_out, "q", dev, n, d, stream)
+    (hk, kp, k0, k1, ko, ko0, ko1), k_out = _head_rows(k, k_out, "k", dev, n, d, stream)
+    _call(_lib.kvp_qk_norm_rope, dev, stream, n, hq, hk, d, rot, interleaved, qp, q0, q1, kp, k0, k1,
           _on(pos, torch.int32, "pos", dev, (n,)) if rot else None,
           _on(turns, torch.int64, "turns", dev) if rot else None,
           _on(q_weight, torch.float32, "q_weight", dev, (d,)), _on(k_weight, torch.float32, "k_weight", dev, (d,)),
-          float(eps), qo, qo0, qo1, ko, ko0, ko1)
-    return outs[0], outs[1]
+          eps, qo, qo0, qo1, ko, ko0, ko1)
+    return q_out, k_out
 
 
 __all__ = [n for n in dir() if n.startswith(("kvp_", "KVP_", "PagedKV", "QuantPagedKV", "LatentPagedKV",

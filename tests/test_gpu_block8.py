@@ -1,5 +1,6 @@
 """The block-scaled 8-bit cache on the GPU against the float64 restatement: bulk write, append, read back and
 attention, alone and together."""
+import dataclasses
 import math
 
 import numpy as np
@@ -646,6 +647,7 @@ def test_binding_refusals(kvp):
                                flag_step=torch.zeros(4, dtype=torch.int32, device="cuda"), status=st)
     with pytest.raises(Exception):
         cache.fmt = 1                                    # a handle's buffers and format stay
-    bad = dict(cache.__dict__, scale_pool=torch.zeros(4, device="cuda"))
+    bad = {f.name: getattr(cache, f.name) for f in dataclasses.fields(cache)}
+    bad["scale_pool"] = torch.zeros(4, device="cuda")
     with pytest.raises(ValueError):
         kvp.Block8PagedKV(**bad)
