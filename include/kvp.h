@@ -724,8 +724,9 @@ KVP_API kvp_status kvp_decode_attn_mla(int batch, int n_q_heads, int latent_dim,
  * (expire 0), and reserved pages without rows have scale 0.
  *
  * Sources, strides, mode, scores, tau, flag_step, window, delay, now, reserve
- * and errors: kvp_compact_masked's. n_pos + reserve < 2^31 - 16, and
- * B * H * ceil((n_pos + reserve) / 16) < 2^31 (else KVP_ERR_UNSUPPORTED).
+ * and errors: kvp_compact_masked's. n_pos at most 65535 * 512, n_pos + reserve
+ * < 2^31 - 16, and B * H * ceil((n_pos + reserve) / 16) < 2^31 (else
+ * KVP_ERR_UNSUPPORTED).
  * workspace  device, >= kvp_compact_block8_workspace_bytes(...), 16-byte
  *            aligned; needs no clearing. Calls that share a workspace must
  *            not overlap on the GPU.

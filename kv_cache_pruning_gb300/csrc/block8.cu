@@ -2,15 +2,26 @@
 // kvp_read_block8: writing and reading a paged cache held in 8 bits with one
 // scale per page (16 tokens of one (b, h)) for K and one for V.
 //
-// The bulk write runs four passes. The count pass is the other compactions'
-// (present entries per 128-entry segment and per (b, h)). The list pass, one
-// warp per segment, writes the remapping list, the expire values and the page
-// table, and names each page's owner. The page pass gives one warp a page: it
-// gathers the page's 16 K and V rows through the list (all 16 row loads of a
-// lane in flight before the first is used), takes the two largest magnitudes,
-// and writes codes and scales, so every row is read once and every code
-// written once. Pages are dealt out by their ids over a persistent grid, which
-// keeps the warps even whatever the (b, h)'s counts are.
+// The bulk write runs three passes after zeroing the counts, each launched early
+// behind the one before it. The count pass counts the present entries of every
+// 128-entry segment and (b, h). The list pass, one warp per segment, writes the
+// remapping list, the expire values and the page table, and names each page's
+// owner. The page pass gives one warp a page: it gathers the page's 16 K and V
+// rows through the list (all row loads of a lane in flight before the first is
+// used), takes the two largest magnitudes, and writes codes and scales, so every
+// row is read once and every code written once. Pages are dealt out by their ids
+// over a persistent grid, which keeps the warps even whatever the counts are.
+//
+// The page pass is bound by memory (a row's 4 D bytes in, 2 D out) with the
+// conversions close behind. Measured on a GB300, 16 x 8192 x 8 heads of 128,
+// 26 % kept, E4M3 / 65,521 x 64 heads, half kept, int8 (whole calls): 65 / 440 us
+// with the list read page by page, 55 / 337 with owners and positions read ahead,
+// 54 / 329 with cached instead of streaming loads, 51 / 274 with magnitudes on
+// packed pairs and int8 rounded by the multiply-add, 47 / 274 with the passes
+// launched early. Not kept: K and V in separate warps (55 / 343), a third CTA per
+// SM (52 / 306), pages in position order over all heads (no faster reads, a dearer
+// list), and listing and quantising in one pass (61 / 364: its warps idle while
+// they list).
 #include "block8.cuh"
 #include "compact_prep.cuh"
 
@@ -18,10 +29,49 @@ namespace kvp {
 namespace {
 
 // Workspace: the preparation passes' words, then the number of pages in use,
-// then each page's owner (its (b, h) and its index in that (b, h)).
+// then each page's owner: its (b, h), and its index in that (b, h) with the
+// number of its rows in the low 5 bits (an index is below 2^27).
 size_t prep_bytes(int64_t BH, int NS) { return (compact_ws_bytes(BH, NS) + 15) & ~static_cast<size_t>(15); }
 size_t block8_ws_bytes(int64_t BH, int NS, int n_pages_cap) {
   return prep_bytes(BH, NS) + 16 + static_cast<size_t>(n_pages_cap) * sizeof(int2);
+}
+
+// ------------------------------------------------------------------ count pass
+// Zeroes the counts. It is the only launch of a call that waits for the work before it as a whole; those after it
+// start early, read the call's inputs at once, and wait only for what the launch before them writes.
+__global__ void __launch_bounds__(1024) zero_counts_kernel(int BH, int32_t* __restrict__ count) {
+  pdl_launch_dependents();
+  for (int i = threadIdx.x; i < BH; i += 1024) count[i] = 0;
+}
+
+// Present entries of each 128-entry segment (one warp each), and of each (b, h) (one atomic a CTA).
+__global__ void __launch_bounds__(kWarpsPerCta * 32) count_block8_kernel(MaskedSrc src, int now, int NS,
+                                                                          int32_t* __restrict__ seg_cnt,
+                                                                          int32_t* __restrict__ count) {
+  __shared__ int cta_kept[kWarpsPerCta];
+  pdl_launch_dependents();
+  const int bh = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sg = blockIdx.y * kWarpsPerCta + warp;
+  const auto sv = src.view(bh);
+  const int lo = sg * kSeg, hi = min(lo + kSeg, sv.length());
+  int kept = 0;
+#pragma unroll
+  for (int u = 0; u < kSeg / 32; ++u) {
+    const int t = lo + u * 32 + lane;
+    int64_t row;
+    if (sg < NS && t < hi) kept += sv.keep(sv.expire_row(t, row), now);
+  }
+  kept = __reduce_add_sync(0xffffffffu, kept);
+  if (lane == 0) cta_kept[warp] = kept;
+  pdl_wait();  // the counts are zero
+  if (lane == 0 && sg < NS) seg_cnt[static_cast<int64_t>(bh) * NS + sg] = kept;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int t = 0;
+#pragma unroll
+    for (int w = 0; w < kWarpsPerCta; ++w) t += cta_kept[w];
+    if (t) atomicAdd(&count[bh], t);
+  }
 }
 
 // ------------------------------------------------------------------ list pass
@@ -36,14 +86,13 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32) list_kernel(MaskedSrc src, 
                                                                   int32_t* __restrict__ n_used,
                                                                   int2* __restrict__ owner) {
   pdl_launch_dependents();
-  pdl_wait();
-  const int bh = blockIdx.x;
+  const int bh = blockIdx.x;  // pairs vary fastest: CTAs resident together read the same positions of all heads
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sg = blockIdx.y * kWarpsPerCta + warp;
   const bool live = sg < NS;
   const bool first_cta = blockIdx.x == 0 && blockIdx.y == 0;
 
-  // loads that do not depend on one another, all issued first
+  // the call's inputs first, then what the count pass wrote
   const auto sv = src.view(bh);
   const int n = sv.length();
   const int lo = sg * kSeg, hi = min(lo + kSeg, n);
@@ -54,6 +103,7 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32) list_kernel(MaskedSrc src, 
     int64_t row;
     exps[u] = live && t < hi ? sv.expire_row(t, row) : 0;
   }
+  pdl_wait();
   int slot0 = 0;
   if (live)
     for (int c0 = 0; c0 < sg; c0 += 32)
@@ -113,7 +163,7 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32) list_kernel(MaskedSrc src, 
   for (int64_t p = static_cast<int64_t>(sg) * seg + lane; p < min(static_cast<int64_t>(max_pages), (sg + int64_t{1}) * seg);
        p += 32) {
     page_table[static_cast<int64_t>(bh) * max_pages + p] = p < pages ? base + static_cast<int>(p) : -1;
-    if (p < pages) owner[base + p] = make_int2(bh, static_cast<int>(p));
+    if (p < pages) owner[base + p] = make_int2(bh, static_cast<int>(p << 5 | min(max(cnt - p * kPage, int64_t{0}), int64_t{kPage})));
   }
   const int64_t rseg = (cap + NS - 1) / NS;
   const int64_t rlo = sg * rseg > cnt ? sg * rseg : static_cast<int64_t>(cnt);
@@ -137,31 +187,45 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32) list_kernel(MaskedSrc src, 
 
 // ------------------------------------------------------------------ page pass
 constexpr int kPageWarps = 8;  // warps per CTA of the page and read passes
+constexpr int kPageCtas = 2;   // CTAs per SM of the page pass: 16 warps, each with a page's rows (8 KB at 128) in flight
+
+// The largest magnitude among a warp's words (NI uint4 a lane), as bf16 bits; kFinite: among the finite ones.
+template <int NI, bool kFinite>
+KVP_DEV uint32_t largest(const uint4 (&w)[NI]) {
+  uint32_t a = 0;
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) a = __vmaxu2(a, kFinite ? finite_abs2(x[c]) : x[c] & 0x7FFF7FFFu);
+  }
+  return __reduce_max_sync(0xffffffffu, max(a & 0xFFFFu, a >> 16));
+}
 
 template <int D, int FMT>
-__global__ void __launch_bounds__(kPageWarps * 32) page_kernel(const uint16_t* __restrict__ k,
-                                                               const uint16_t* __restrict__ v, int64_t sb, int64_t st,
-                                                               int64_t sh, int H, const int32_t* __restrict__ n_used,
-                                                               const int2* __restrict__ owner,
-                                                               const int32_t* __restrict__ count, int max_pages,
-                                                               const int32_t* __restrict__ remap,
-                                                               uint8_t* __restrict__ kq_pool,
-                                                               uint8_t* __restrict__ vq_pool,
-                                                               float2* __restrict__ scale_pool,
-                                                               int32_t* __restrict__ expire_pool) {
+__global__ void __launch_bounds__(kPageWarps * 32, kPageCtas) page_kernel(
+    const uint16_t* __restrict__ k, const uint16_t* __restrict__ v, int64_t sb, int64_t st, int64_t sh, int H,
+    const int32_t* __restrict__ n_used, const int2* __restrict__ owner, int max_pages,
+    const int32_t* __restrict__ remap, uint8_t* __restrict__ kq_pool, uint8_t* __restrict__ vq_pool,
+    float2* __restrict__ scale_pool, int32_t* __restrict__ expire_pool) {
   constexpr int LPR = D / 8;          // lanes a row takes, 16 bytes each
   constexpr int RPI = 32 / LPR;       // rows a warp instruction takes
   constexpr int NI = kPage / RPI;
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, piece = lane % LPR, sub = lane / LPR;
-  const int total = *n_used;
-  for (int pg = blockIdx.x * kPageWarps + (threadIdx.x >> 5); pg < total; pg += gridDim.x * kPageWarps) {
-    const int2 ow = owner[pg];
+  const int total = *n_used, step = gridDim.x * kPageWarps;
+  // a page's owner is read two pages ahead and its rows' positions one page ahead, so that only the rows are waited for
+  const int first = blockIdx.x * kPageWarps + (threadIdx.x >> 5);
+  auto owner_of = [&](int64_t pg) { return pg < total ? owner[pg] : make_int2(0, 0); };
+  auto position_of = [&](int2 ow) {  // lane r: the position of row r
+    return lane < (ow.y & 31) ? remap[(static_cast<int64_t>(ow.x) * max_pages + (ow.y >> 5)) * kPage + lane] : 0;
+  };
+  int2 ow = owner_of(first), ow_next = owner_of(static_cast<int64_t>(first) + step);
+  int32_t mine = position_of(ow);
+  for (int64_t pg = first; pg < total; pg += step) {
     const int b = ow.x / H, h = ow.x - b * H;
-    const int64_t first = static_cast<int64_t>(ow.y) * kPage;
-    const int n = static_cast<int>(min(max(count[ow.x] - first, int64_t{0}), int64_t{kPage}));
-    const int32_t mine = lane < n ? remap[static_cast<int64_t>(ow.x) * max_pages * kPage + first + lane] : 0;
+    const int n = ow.y & 31;
     const int64_t off = b * sb + h * sh + piece * 8;
     uint4 kw[NI], vw[NI];
 #pragma unroll
@@ -170,28 +234,37 @@ __global__ void __launch_bounds__(kPageWarps * 32) page_kernel(const uint16_t* _
       const int64_t at = off + __shfl_sync(0xffffffffu, mine, r) * st;
       kw[i] = vw[i] = make_uint4(0, 0, 0, 0);
       if (r < n) {
-        kw[i] = *reinterpret_cast<const uint4*>(k + at);
-        vw[i] = *reinterpret_cast<const uint4*>(v + at);
+        kw[i] = __ldg(reinterpret_cast<const uint4*>(k + at));
+        vw[i] = __ldg(reinterpret_cast<const uint4*>(v + at));
       }
     }
-    uint32_t ka = 0, va = 0;
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      ka = __vmaxu2(ka, __vmaxu2(__vmaxu2(finite_abs2(kw[i].x), finite_abs2(kw[i].y)),
-                                 __vmaxu2(finite_abs2(kw[i].z), finite_abs2(kw[i].w))));
-      va = __vmaxu2(va, __vmaxu2(__vmaxu2(finite_abs2(vw[i].x), finite_abs2(vw[i].y)),
-                                 __vmaxu2(finite_abs2(vw[i].z), finite_abs2(vw[i].w))));
+    ow = ow_next;
+    mine = position_of(ow);
+    ow_next = owner_of(pg + 2 * static_cast<int64_t>(step));
+    // the largest magnitudes, as bf16 bits; only a page that holds infinities or NaNs looks at them one by one
+    uint32_t ka = largest<NI, false>(kw), va = largest<NI, false>(vw);
+    const bool odd = ka >= 0x7F80u || va >= 0x7F80u;
+    if (odd) {
+      ka = largest<NI, true>(kw);
+      va = largest<NI, true>(vw);
     }
-    ka = __reduce_max_sync(0xffffffffu, max(ka & 0xFFFFu, ka >> 16));
-    va = __reduce_max_sync(0xffffffffu, max(va & 0xFFFFu, va >> 16));
     const uint32_t ks = scale_bits_for<FMT>(ka), vs = scale_bits_for<FMT>(va);
     const float ki = inverse_of_scale(ks), vi = inverse_of_scale(vs);
-    const int64_t row0 = static_cast<int64_t>(pg) * kPage;
+    const int64_t row0 = pg * kPage;
+    uint8_t* kd = kq_pool + (row0 + sub) * D + piece * 8;
+    uint8_t* vd = vq_pool + (row0 + sub) * D + piece * 8;
+    if (!odd) {
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int64_t at = (row0 + i * RPI + sub) * D + piece * 8;
-      *reinterpret_cast<uint2*>(kq_pool + at) = encode8<FMT>(kw[i], ki);
-      *reinterpret_cast<uint2*>(vq_pool + at) = encode8<FMT>(vw[i], vi);
+      for (int i = 0; i < NI; ++i) {
+        *reinterpret_cast<uint2*>(kd + i * RPI * D) = encode8_finite<FMT>(kw[i], ki);
+        *reinterpret_cast<uint2*>(vd + i * RPI * D) = encode8_finite<FMT>(vw[i], vi);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        *reinterpret_cast<uint2*>(kd + i * RPI * D) = encode8<FMT>(kw[i], ki);
+        *reinterpret_cast<uint2*>(vd + i * RPI * D) = encode8<FMT>(vw[i], vi);
+      }
     }
     if (lane == 0) scale_pool[pg] = make_float2(__uint_as_float(ks), __uint_as_float(vs));
     if (lane >= n && lane < kPage) expire_pool[row0 + lane] = 0;
@@ -383,8 +456,11 @@ kvp_status launch_compact(const MaskedSrc& src, int BH, int NS, int now, int res
   const int sms = current_sms(&device);
   if (sms == 0) return KVP_ERR_CUDA;
   const int segs = (NS + kWarpsPerCta - 1) / kWarpsPerCta;
-  if (cudaMemsetAsync(count, 0, static_cast<size_t>(BH) * sizeof(int32_t), st) != cudaSuccess) return KVP_ERR_CUDA;
-  count_kernel<MaskedSrc><<<dim3(segs, BH), kWarpsPerCta * 32, 0, st>>>(src, now, NS, ws.seg_cnt, count);
+  zero_counts_kernel<<<1, 1024, 0, st>>>(BH, count);
+  if (cudaGetLastError() != cudaSuccess) return KVP_ERR_CUDA;
+  if (launch_pdl(count_block8_kernel, dim3(BH, segs), dim3(kWarpsPerCta * 32), 0, st, src, now, NS, ws.seg_cnt, count) !=
+      cudaSuccess)
+    return KVP_ERR_CUDA;
   const int32_t* cnt = count;
   if (BH <= kFusedBH) {
     if (launch_pdl(list_kernel<true>, dim3(BH, segs), dim3(kWarpsPerCta * 32), 0, st, src, now, NS, reserve, max_pages,
@@ -399,9 +475,9 @@ kvp_status launch_compact(const MaskedSrc& src, int BH, int NS, int now, int res
   // at most one page for each 16 positions and reserved slots: small calls take a small grid
   const int64_t most = static_cast<int64_t>(BH) * ((static_cast<int64_t>(src.n) + reserve + kPage - 1) / kPage);
   const int64_t need = (most < n_pages_cap ? most : n_pages_cap) / kPageWarps + 1;
-  const int grid = static_cast<int>(need < sms * 2 ? need : sms * 2);
+  const int grid = static_cast<int>(need < sms * kPageCtas ? need : sms * kPageCtas);
   if (launch_pdl(page_kernel<D, FMT>, dim3(grid), dim3(kPageWarps * 32), 0, st, src.k, src.v, src.sb, src.st, src.sh,
-                 src.H, static_cast<const int32_t*>(n_used), static_cast<const int2*>(owner), cnt, max_pages,
+                 src.H, static_cast<const int32_t*>(n_used), static_cast<const int2*>(owner), max_pages,
                  static_cast<const int32_t*>(remap), kq_pool, vq_pool, reinterpret_cast<float2*>(scale_pool),
                  expire_pool) != cudaSuccess)
     return KVP_ERR_CUDA;
@@ -484,6 +560,7 @@ extern "C" kvp_status kvp_compact_block8(int fmt, int mode, int batch, int n_kv_
   if (stride_b < 0 || stride_t < 0 || stride_h < 0) return KVP_ERR_INVALID;
   const int BH = batch * n_kv_heads;
   const int NS = n_segments(n_pos);
+  if ((NS + kWarpsPerCta - 1) / kWarpsPerCta > 65535) return KVP_ERR_UNSUPPORTED;  // the grid's second dimension
   // page ids are 32-bit: with every position kept they have to be countable, or the budget check could wrap
   if (BH * ((static_cast<int64_t>(n_pos) + reserve + kPage - 1) / kPage) > 0x7fffffff) return KVP_ERR_UNSUPPORTED;
   if (workspace == nullptr || workspace_bytes < block8_ws_bytes(BH, NS, n_pages_cap)) return KVP_ERR_WORKSPACE;

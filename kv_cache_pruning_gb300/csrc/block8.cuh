@@ -63,6 +63,21 @@ KVP_DEV uint2 encode8(const uint4& w, float inv) {
         (encode2<FMT>(__fmul_rn(bf16_lo(w.w), inv), __fmul_rn(bf16_hi(w.w), inv)) << 16);
   return r;
 }
+// The same for values known to be finite (so that |x| * inv is at most the format's largest number). int8: adding
+// 1.5 * 2^23 in the multiplication's own rounding leaves the rounded integer in the sum's low byte.
+template <int FMT>
+KVP_DEV uint2 encode8_finite(const uint4& w, float inv) {
+  if constexpr (FMT == KVP_BLOCK8_E4M3) {
+    return encode8<FMT>(w, inv);
+  } else {
+    auto four = [&](uint32_t a, uint32_t b) {
+      const uint32_t x = __float_as_uint(fmaf(bf16_lo(a), inv, 12582912.f)), y = __float_as_uint(fmaf(bf16_hi(a), inv, 12582912.f));
+      const uint32_t z = __float_as_uint(fmaf(bf16_lo(b), inv, 12582912.f)), u = __float_as_uint(fmaf(bf16_hi(b), inv, 12582912.f));
+      return __byte_perm(__byte_perm(x, y, 0x0040), __byte_perm(z, u, 0x0040), 0x5410);
+    };
+    return make_uint2(four(w.x, w.y), four(w.z, w.w));
+  }
+}
 
 // The two codes in the low 16 bits of `two` as numbers, exactly.
 template <int FMT>

@@ -51,6 +51,7 @@ def test_compact_refusals(k):
     assert call(b=70000, h=1) == k.KVP_ERR_UNSUPPORTED
     assert call(width=2**27) == k.KVP_ERR_UNSUPPORTED
     assert call(reserve=2**31 - 20) == k.KVP_ERR_UNSUPPORTED
+    assert call(b=1, h=1, n_pos=65535 * 512 + 1, wsb=1 << 40) == k.KVP_ERR_UNSUPPORTED
     assert call(b=65535, h=1, reserve=2**20, wsb=1 << 40) == k.KVP_ERR_UNSUPPORTED    # page ids past 2^31
     assert call(kp=8) == k.KVP_ERR_ALIGN
     assert call(kq=8) == k.KVP_ERR_ALIGN
