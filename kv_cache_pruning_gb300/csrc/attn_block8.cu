@@ -149,7 +149,7 @@ KVP_DEV void load_k(KWords<D>& x, const uint8_t* page, int g, int t) {
   for (int r = 0; r < 2; ++r)
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) {
-      const uint4 y = __ldg(reinterpret_cast<const uint4*>(page + (g + 8 * r) * D + c * 64 + t * 16));
+      const uint4 y = *reinterpret_cast<const uint4*>(page + (g + 8 * r) * D + c * 64 + t * 16);
       x.w[r][4 * c] = y.x;
       x.w[r][4 * c + 1] = y.y;
       x.w[r][4 * c + 2] = y.z;
@@ -162,13 +162,13 @@ KVP_DEV void load_v(VWords<D>& x, const uint8_t* page, int g, int t) {
   for (int r = 0; r < 4; ++r) {
     const uint8_t* row = page + (2 * t + (r & 1) + 8 * (r >> 1)) * D + g * (D / 8);
     if constexpr (D == 128) {
-      const uint4 y = __ldg(reinterpret_cast<const uint4*>(row));
+      const uint4 y = *reinterpret_cast<const uint4*>(row);
       x.w[r][0] = y.x;
       x.w[r][1] = y.y;
       x.w[r][2] = y.z;
       x.w[r][3] = y.w;
     } else {
-      const uint2 y = __ldg(reinterpret_cast<const uint2*>(row));
+      const uint2 y = *reinterpret_cast<const uint2*>(row);
       x.w[r][0] = y.x;
       x.w[r][1] = y.y;
     }
@@ -204,7 +204,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block8_kernel(const Params p
   __shared__ float wts[8][2 * kWarps];   // a merge's weights: head, partial result
   __shared__ float2 merged_ml[8];
   __shared__ int last_s[2];
-  pdl_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int G = p.G;
   const int pf = part_floats<D>(G);
@@ -312,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block8_kernel(const Params p
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
           x[i] = make_uint4(0, 0, 0, 0);
-          if (head < G) x[i] = __ldg(reinterpret_cast<const uint4*>(row + (i >> 1) * 64 + t * 16 + (i & 1) * 8));
+          if (head < G) x[i] = *reinterpret_cast<const uint4*>(row + (i >> 1) * 64 + t * 16 + (i & 1) * 8);
         }
       }
       const int32_t* table = p.page_table + static_cast<int64_t>(u) * p.max_pages + (at - u_lo);
@@ -643,8 +642,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block8_kernel(const Params p
           ml[c] = make_float2(-INFINITY, 0.f);
           x[c] = make_float4(0.f, 0.f, 0.f, 0.f);
           if (c < pieces) {
-            ml[c] = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + slot_of(c) * G + head);
-            x[c] = __ldcg(reinterpret_cast<const float4*>(p.part_acc + slot_of(c) * G * D) + i);
+            ml[c] = load8_l2(p.part_ml + (slot_of(c) * G + head) * 2);
+            x[c] = load16_l2(p.part_acc + slot_of(c) * G * D + 4 * i);
           }
         }
         float m = ml[0].x, l = 0.f;
@@ -671,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block8_kernel(const Params p
     if (warp < G) {
       float m = -INFINITY;
       for (int c = lane; c < pieces; c += 32) {
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + slot_of(c) * G + warp);
+        const float2 ml = load8_l2(p.part_ml + (slot_of(c) * G + warp) * 2);
         cta_ml[warp * kMaxCtas + c] = ml;
         m = fmaxf(m, ml.x);
       }
@@ -697,7 +696,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block8_kernel(const Params p
 #pragma unroll 4
       for (int c = grp; c < pieces; c += groups) {
         const float w = cta_ml[head * kMaxCtas + c].x;
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(p.part_acc + slot_of(c) * G * D) + i);
+        const float4 x = load16_l2(p.part_acc + slot_of(c) * G * D + 4 * i);
         a.x = fmaf(w, x.x, a.x);
         a.y = fmaf(w, x.y, a.y);
         a.z = fmaf(w, x.z, a.z);

@@ -17,7 +17,7 @@
 // 26 % kept, E4M3 / 65,521 x 64 heads, half kept, int8 (whole calls): 65 / 440 us
 // with the list read page by page, 55 / 337 with owners and positions read ahead,
 // 54 / 329 with cached instead of streaming loads, 51 / 274 with magnitudes on
-// packed pairs and int8 rounded by the multiply-add, 47 / 274 with the passes
+// packed pairs and int8 rounded by the multiply-add, 48 / 271 with the passes
 // launched early. Not kept: K and V in separate warps (55 / 343), a third CTA per
 // SM (52 / 306), pages in position order over all heads (no faster reads, a dearer
 // list), and listing and quantising in one pass (61 / 364: its warps idle while
@@ -37,19 +37,20 @@ size_t block8_ws_bytes(int64_t BH, int NS, int n_pages_cap) {
 }
 
 // ------------------------------------------------------------------ count pass
-// Zeroes the counts. It is the only launch of a call that waits for the work before it as a whole; those after it
-// start early, read the call's inputs at once, and wait only for what the launch before them writes.
-__global__ void __launch_bounds__(1024) zero_counts_kernel(int BH, int32_t* __restrict__ count) {
+// Zeroes the counts. The launches after it start early, but read nothing before their pdl_wait: what lies in an SM's
+// first-level cache may be older than the call's inputs until then.
+__global__ void __launch_bounds__(1024) zero_counts_kernel(int BH, int32_t* count) {
   pdl_launch_dependents();
   for (int i = threadIdx.x; i < BH; i += 1024) count[i] = 0;
 }
 
 // Present entries of each 128-entry segment (one warp each), and of each (b, h) (one atomic a CTA).
 __global__ void __launch_bounds__(kWarpsPerCta * 32) count_block8_kernel(MaskedSrc src, int now, int NS,
-                                                                          int32_t* __restrict__ seg_cnt,
-                                                                          int32_t* __restrict__ count) {
+                                                                          int32_t* seg_cnt,
+                                                                          int32_t* count) {
   __shared__ int cta_kept[kWarpsPerCta];
   pdl_launch_dependents();
+  pdl_wait();
   const int bh = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sg = blockIdx.y * kWarpsPerCta + warp;
   const auto sv = src.view(bh);
@@ -62,9 +63,10 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32) count_block8_kernel(MaskedS
     if (sg < NS && t < hi) kept += sv.keep(sv.expire_row(t, row), now);
   }
   kept = __reduce_add_sync(0xffffffffu, kept);
-  if (lane == 0) cta_kept[warp] = kept;
-  pdl_wait();  // the counts are zero
-  if (lane == 0 && sg < NS) seg_cnt[static_cast<int64_t>(bh) * NS + sg] = kept;
+  if (lane == 0) {
+    cta_kept[warp] = kept;
+    if (sg < NS) seg_cnt[static_cast<int64_t>(bh) * NS + sg] = kept;
+  }
   __syncthreads();
   if (threadIdx.x == 0) {
     int t = 0;
@@ -78,21 +80,22 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32) count_block8_kernel(MaskedS
 template <bool kFused>
 __global__ void __launch_bounds__(kWarpsPerCta * 32) list_kernel(MaskedSrc src, int now, int NS, int reserve,
                                                                   int max_pages, int n_pages_cap, int BH, CompactWs ws,
-                                                                  const int32_t* __restrict__ count,
-                                                                  int32_t* __restrict__ status,
-                                                                  int32_t* __restrict__ expire_pool,
-                                                                  int32_t* __restrict__ page_table,
-                                                                  int32_t* __restrict__ remap,
-                                                                  int32_t* __restrict__ n_used,
-                                                                  int2* __restrict__ owner) {
+                                                                  const int32_t* count,
+                                                                  int32_t* status,
+                                                                  int32_t* expire_pool,
+                                                                  int32_t* page_table,
+                                                                  int32_t* remap,
+                                                                  int32_t* n_used,
+                                                                  int2* owner) {
   pdl_launch_dependents();
+  pdl_wait();
   const int bh = blockIdx.x;  // pairs vary fastest: CTAs resident together read the same positions of all heads
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sg = blockIdx.y * kWarpsPerCta + warp;
   const bool live = sg < NS;
   const bool first_cta = blockIdx.x == 0 && blockIdx.y == 0;
 
-  // the call's inputs first, then what the count pass wrote
+  // loads that do not depend on one another, all issued first
   const auto sv = src.view(bh);
   const int n = sv.length();
   const int lo = sg * kSeg, hi = min(lo + kSeg, n);
@@ -103,7 +106,6 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32) list_kernel(MaskedSrc src, 
     int64_t row;
     exps[u] = live && t < hi ? sv.expire_row(t, row) : 0;
   }
-  pdl_wait();
   int slot0 = 0;
   if (live)
     for (int c0 = 0; c0 < sg; c0 += 32)
@@ -204,14 +206,13 @@ KVP_DEV uint32_t largest(const uint4 (&w)[NI]) {
 
 template <int D, int FMT>
 __global__ void __launch_bounds__(kPageWarps * 32, kPageCtas) page_kernel(
-    const uint16_t* __restrict__ k, const uint16_t* __restrict__ v, int64_t sb, int64_t st, int64_t sh, int H,
-    const int32_t* __restrict__ n_used, const int2* __restrict__ owner, int max_pages,
-    const int32_t* __restrict__ remap, uint8_t* __restrict__ kq_pool, uint8_t* __restrict__ vq_pool,
-    float2* __restrict__ scale_pool, int32_t* __restrict__ expire_pool) {
+    const uint16_t* k, const uint16_t* v, int64_t sb, int64_t st, int64_t sh, int H,
+    const int32_t* n_used, const int2* owner, int max_pages,
+    const int32_t* remap, uint8_t* kq_pool, uint8_t* vq_pool,
+    float2* scale_pool, int32_t* expire_pool) {
   constexpr int LPR = D / 8;          // lanes a row takes, 16 bytes each
   constexpr int RPI = 32 / LPR;       // rows a warp instruction takes
   constexpr int NI = kPage / RPI;
-  pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, piece = lane % LPR, sub = lane / LPR;
   const int total = *n_used, step = gridDim.x * kPageWarps;
@@ -234,8 +235,8 @@ __global__ void __launch_bounds__(kPageWarps * 32, kPageCtas) page_kernel(
       const int64_t at = off + __shfl_sync(0xffffffffu, mine, r) * st;
       kw[i] = vw[i] = make_uint4(0, 0, 0, 0);
       if (r < n) {
-        kw[i] = __ldg(reinterpret_cast<const uint4*>(k + at));
-        vw[i] = __ldg(reinterpret_cast<const uint4*>(v + at));
+        kw[i] = *reinterpret_cast<const uint4*>(k + at);
+        vw[i] = *reinterpret_cast<const uint4*>(v + at);
       }
     }
     ow = ow_next;
@@ -316,13 +317,14 @@ KVP_DEV uint2 load_row_part(const uint16_t* row, int lane) {
 // One warp per (b, h).
 template <int D, int FMT>
 __global__ void __launch_bounds__(kAppendWarps * 32) append_block8_kernel(
-    int mode, int BH, int H, int pos_arg, const int32_t* __restrict__ pos_dev, const uint16_t* __restrict__ k_new,
-    const uint16_t* __restrict__ v_new, int64_t k_sb, int64_t k_sh, int64_t v_sb, int64_t v_sh,
-    const float* __restrict__ score, const float* __restrict__ tau, const int32_t* __restrict__ flag, int window,
-    int delay, uint8_t* __restrict__ kq_pool, uint8_t* __restrict__ vq_pool, float2* __restrict__ scale_pool,
-    int32_t* __restrict__ expire_pool, int n_pages_cap, const int32_t* __restrict__ page_table, int max_pages,
-    int32_t* __restrict__ remap, int32_t* __restrict__ count, int32_t* __restrict__ status) {
+    int mode, int BH, int H, int pos_arg, const int32_t* pos_dev, const uint16_t* k_new,
+    const uint16_t* v_new, int64_t k_sb, int64_t k_sh, int64_t v_sb, int64_t v_sh,
+    const float* score, const float* tau, const int32_t* flag, int window,
+    int delay, uint8_t* kq_pool, uint8_t* vq_pool, float2* scale_pool,
+    int32_t* expire_pool, int n_pages_cap, const int32_t* page_table, int max_pages,
+    int32_t* remap, int32_t* count, int32_t* status) {
   constexpr int EPL = D / 32;
+  pdl_wait();
   const int bh = blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (bh >= BH) return;
@@ -375,13 +377,14 @@ KVP_DEV uint32_t value2(uint32_t two, float scale) {
 // One warp per page of a (b, h): 16 codes a lane, LPR lanes a row.
 template <int D, int FMT>
 __global__ void __launch_bounds__(kPageWarps * 32) read_block8_kernel(
-    int H, int64_t n_items, int pages_each, const uint8_t* __restrict__ kq_pool, const uint8_t* __restrict__ vq_pool,
-    const float2* __restrict__ scale_pool, int n_pages_cap, const int32_t* __restrict__ page_table, int max_pages,
-    const int32_t* __restrict__ count, int first, int n_slots, uint16_t* __restrict__ k_out,
-    uint16_t* __restrict__ v_out, int64_t sb, int64_t st, int64_t sh, int32_t* __restrict__ status) {
+    int H, int64_t n_items, int pages_each, const uint8_t* kq_pool, const uint8_t* vq_pool,
+    const float2* scale_pool, int n_pages_cap, const int32_t* page_table, int max_pages,
+    const int32_t* count, int first, int n_slots, uint16_t* k_out,
+    uint16_t* v_out, int64_t sb, int64_t st, int64_t sh, int32_t* status) {
   constexpr int LPR = D / 16;
   constexpr int RPI = 32 / LPR;
   constexpr int NI = kPage / RPI;
+  pdl_wait();
   const int lane = threadIdx.x & 31, piece = lane % LPR, sub = lane / LPR;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kPageWarps + (threadIdx.x >> 5);
   if (item >= n_items) return;
@@ -510,12 +513,14 @@ kvp_status append_block8_impl(int fmt, int mode, int batch, int n_kv_heads, int 
   if (static_cast<int64_t>(pos) + window + delay >= kNever) return KVP_ERR_INVALID;
   const int BH = batch * n_kv_heads;
   auto go = [&](auto kern) {
-    kern<<<(BH + kAppendWarps - 1) / kAppendWarps, kAppendWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(
-        mode, BH, n_kv_heads, pos, pos_dev, static_cast<const uint16_t*>(k_new), static_cast<const uint16_t*>(v_new),
-        k_stride_b, k_stride_h, v_stride_b, v_stride_h, score, tau, flag_step, window, delay,
-        static_cast<uint8_t*>(kq_pool), static_cast<uint8_t*>(vq_pool), reinterpret_cast<float2*>(scale_pool),
-        expire_pool, n_pages_cap, page_table, max_pages, remap, count, status);
-    return cudaGetLastError() == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
+    return launch_pdl(kern, dim3((BH + kAppendWarps - 1) / kAppendWarps), dim3(kAppendWarps * 32), 0,
+                      static_cast<cudaStream_t>(stream), mode, BH, n_kv_heads, pos, pos_dev,
+                      static_cast<const uint16_t*>(k_new), static_cast<const uint16_t*>(v_new), k_stride_b, k_stride_h,
+                      v_stride_b, v_stride_h, score, tau, flag_step, window, delay, static_cast<uint8_t*>(kq_pool),
+                      static_cast<uint8_t*>(vq_pool), reinterpret_cast<float2*>(scale_pool), expire_pool, n_pages_cap,
+                      page_table, max_pages, remap, count, status) == cudaSuccess
+               ? KVP_OK
+               : KVP_ERR_CUDA;
   };
   if (fmt == KVP_BLOCK8_E4M3)
     return head_dim == 128 ? go(append_block8_kernel<128, KVP_BLOCK8_E4M3>) : go(append_block8_kernel<64, KVP_BLOCK8_E4M3>);
@@ -636,11 +641,14 @@ extern "C" kvp_status kvp_read_block8(int fmt, int batch, int n_kv_heads, int he
   const int64_t ctas = (items + kPageWarps - 1) / kPageWarps;
   if (ctas > 0x7fffffff) return KVP_ERR_UNSUPPORTED;
   auto go = [&](auto kern) {
-    kern<<<static_cast<unsigned>(ctas), kPageWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(
-        n_kv_heads, items, pages_each, static_cast<const uint8_t*>(kq_pool), static_cast<const uint8_t*>(vq_pool),
-        reinterpret_cast<const float2*>(scale_pool), n_pages_cap, page_table, max_pages, count, first_slot, n_slots,
-        static_cast<uint16_t*>(k_out), static_cast<uint16_t*>(v_out), stride_b, stride_t, stride_h, status);
-    return cudaGetLastError() == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
+    return launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(kPageWarps * 32), 0,
+                      static_cast<cudaStream_t>(stream), n_kv_heads, items, pages_each,
+                      static_cast<const uint8_t*>(kq_pool), static_cast<const uint8_t*>(vq_pool),
+                      reinterpret_cast<const float2*>(scale_pool), n_pages_cap, page_table, max_pages, count, first_slot,
+                      n_slots, static_cast<uint16_t*>(k_out), static_cast<uint16_t*>(v_out), stride_b, stride_t, stride_h,
+                      status) == cudaSuccess
+               ? KVP_OK
+               : KVP_ERR_CUDA;
   };
   if (fmt == KVP_BLOCK8_E4M3)
     return head_dim == 128 ? go(read_block8_kernel<128, KVP_BLOCK8_E4M3>) : go(read_block8_kernel<64, KVP_BLOCK8_E4M3>);

@@ -21,6 +21,28 @@
 namespace kvp {
 namespace {
 
+// Loads of data that the launch before may have written. The kernels of this cache start early behind that launch and
+// wait for it on the device, so what they read must not be taken for constant while they run: a read-only load
+// (__ldg, or a const __restrict__ parameter) may be served from a first-level line older than that launch, and the
+// compiler may move it ahead of the wait. Hence no __restrict__ on what these kernels read, plain loads where nothing
+// else is said, and these, which stay in order with the wait. For the same reason the last kernel of a call does not
+// let its dependents start before it ends: they may be kernels that read what it writes with read-only loads.
+KVP_DEV uint4 load16_stream(const void* p) {  // read once: first to leave the caches
+  uint4 r;
+  asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+  return r;
+}
+KVP_DEV float4 load16_l2(const void* p) {  // other CTAs' results, from L2
+  float4 r;
+  asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w) : "l"(p) : "memory");
+  return r;
+}
+KVP_DEV float2 load8_l2(const void* p) {
+  float2 r;
+  asm volatile("ld.global.cg.v2.f32 {%0, %1}, [%2];" : "=f"(r.x), "=f"(r.y) : "l"(p) : "memory");
+  return r;
+}
+
 // The scale (fp32 bits) for largest magnitude `a`, given as finite bf16 bits
 // without the sign. With a = 2^(E - 127) (1 + f / 128): E4M3's largest number is
 // 2^8 * 1.75 (f = 96), int8's 2^6 * (1 + 126 / 128).

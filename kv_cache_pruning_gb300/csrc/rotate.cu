@@ -11,19 +11,27 @@
 // (two at D = 64) shuffles. A warp takes one token's heads, or a share of them
 // when there are few tokens, with the token's cosines and sines in registers.
 //
+// Measured on a GB300, 65,521 tokens x 40 heads of 128: 271 us at first, 239 with 64
+// registers a thread (four CTAs an SM instead of two), 229 with the norm's weights
+// folded into the cosines and sines, 231 (0.85 of measured HBM) in its final form
+// with ordered streaming loads. Not kept: the next step's rows requested before this
+// one's arithmetic (264: the registers spill), one step or three in flight instead of
+// two (239, 252).
+//
 // An angle is a 64-bit product: turns[i] = inv_freq[i] / (2 pi) as a 64-bit
 // fraction of a turn, times the position modulo one turn (the integer wraps
 // exactly there), whose top 32 bits go to sincospif. No far position loses
 // digits, and no argument reduction is needed.
 #include <cmath>
 
-#include "kvp_common.cuh"
+#include "block8.cuh"
 
 namespace kvp {
 namespace {
 
 constexpr int kWarps = 8;
 constexpr int kUnroll = 2;  // head rows a lane has in flight
+constexpr int kCtas = 4;    // CTAs per SM: 32 warps with 2 KB in flight each
 
 struct RotateParams {
   const uint16_t* x[2];   // q, k
@@ -53,10 +61,9 @@ KVP_DEV void unpack_row(const uint4& a, const uint4& b, float (&f)[16]) {
 }
 
 template <int D, bool kPairs>
-__global__ void __launch_bounds__(kWarps * 32) rotate_kernel(const RotateParams p) {
+__global__ void __launch_bounds__(kWarps * 32, kCtas) rotate_kernel(const RotateParams p) {
   constexpr int LPH = D / 16;       // lanes a head takes
   constexpr int HPI = 32 / LPH;     // heads a warp takes at once
-  pdl_launch_dependents();
   pdl_wait();
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   if (item >= p.n_items) return;
@@ -102,16 +109,18 @@ __global__ void __launch_bounds__(kWarps * 32) rotate_kernel(const RotateParams 
     const uint16_t* x = p.x[which] + tok * p.xt[which];
     uint16_t* y = p.y[which] + tok * p.yt[which];
     const float* wp = p.w[which];
-    float w[16];
-    if (wp != nullptr) {
+    // the rotation takes the norm's weights along: of a pair (a, b), a wa cos - b wb sin and b wb cos + a wa sin; values
+    // that are not rotated have cos 1 and no sin
+    float ac[8], as[8], bc[8], bs[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 v = __ldg(reinterpret_cast<const float4*>(wp + (i < 2 ? run0 : run1) * 8) + (i & 1));
-        w[4 * i] = v.x;
-        w[4 * i + 1] = v.y;
-        w[4 * i + 2] = v.z;
-        w[4 * i + 3] = v.w;
-      }
+    for (int e = 0; e < 8; ++e) {
+      const int i = kPairs ? 2 * e : e, k = kPairs ? 2 * e + 1 : e + 8;  // of the lane's 16 values
+      const float wa = wp != nullptr ? wp[i < 8 ? run0 * 8 + i : run1 * 8 + i - 8] : 1.f;
+      const float wb = wp != nullptr ? wp[k < 8 ? run0 * 8 + k : run1 * 8 + k - 8] : 1.f;
+      ac[e] = turns_here ? wa * cs[e] : wa;
+      bc[e] = turns_here ? wb * cs[e] : wb;
+      as[e] = turns_here ? wa * sn[e] : 0.f;
+      bs[e] = turns_here ? wb * sn[e] : 0.f;
     }
 #pragma unroll 1
     for (int i0 = i_lo; i0 < i_hi; i0 += kUnroll) {
@@ -121,8 +130,8 @@ __global__ void __launch_bounds__(kWarps * 32) rotate_kernel(const RotateParams 
         const int h = (i0 + u) * HPI + sub;
         a[u] = b[u] = make_uint4(0, 0, 0, 0);
         if (i0 + u < i_hi && h < heads) {
-          a[u] = *reinterpret_cast<const uint4*>(x + h * p.xh[which] + run0 * 8);
-          b[u] = *reinterpret_cast<const uint4*>(x + h * p.xh[which] + run1 * 8);
+          a[u] = load16_stream(x + h * p.xh[which] + run0 * 8);
+          b[u] = load16_stream(x + h * p.xh[which] + run1 * 8);
         }
       }
 #pragma unroll
@@ -130,30 +139,36 @@ __global__ void __launch_bounds__(kWarps * 32) rotate_kernel(const RotateParams 
         const int h = (i0 + u) * HPI + sub;
         float f[16];
         unpack_row(a[u], b[u], f);
+        float r = 1.f;
         if (wp != nullptr) {
           float sum = 0.f;
 #pragma unroll
           for (int e = 0; e < 16; ++e) sum = fmaf(f[e], f[e], sum);
 #pragma unroll
           for (int o = 1; o < LPH; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-          const float r = rsqrtf(sum * (1.f / D) + p.eps);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) f[e] *= r * w[e];
+          r = rsqrtf(sum * (1.f / D) + p.eps);
         }
         if (turns_here) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const int i = kPairs ? 2 * e : e, k = kPairs ? 2 * e + 1 : e + 8;
             const float m = f[i], n = f[k];
-            f[i] = m * cs[e] - n * sn[e];
-            f[k] = n * cs[e] + m * sn[e];
+            f[i] = (m * ac[e] - n * bs[e]) * r;
+            f[k] = (n * bc[e] + m * as[e]) * r;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int i = kPairs ? 2 * e : e, k = kPairs ? 2 * e + 1 : e + 8;
+            f[i] *= ac[e] * r;
+            f[k] *= bc[e] * r;
           }
         }
         if (i0 + u < i_hi && h < heads) {
           uint4* dst = reinterpret_cast<uint4*>(y + h * p.yh[which]);
-          dst[run0] = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
-          dst[run1] = make_uint4(pack_bf16(f[8], f[9]), pack_bf16(f[10], f[11]), pack_bf16(f[12], f[13]),
-                                 pack_bf16(f[14], f[15]));
+          __stcs(dst + run0, make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])));
+          __stcs(dst + run1, make_uint4(pack_bf16(f[8], f[9]), pack_bf16(f[10], f[11]), pack_bf16(f[12], f[13]),
+                                        pack_bf16(f[14], f[15])));
         }
       }
     }

@@ -221,6 +221,56 @@ def test_bulk_write_of_unusual_values(kvp, fmt):
     _check_cache(cache, heads, fmt, 0)
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+def test_bulk_writes_back_to_back(kvp, fmt):
+    """Many writes one behind the other, each into memory that the ones before it used, inputs made just before: every
+    pass sees what the launches before it wrote."""
+    T, H, d = 200, 2, 64
+    made = []
+    for seed in (0, 1):
+        k, v, sc = _bits(401 + seed, (1, T, H, d), 3), _bits(403 + seed, (1, T, H, d), 3), syn.normal_f32(seed, 405, (1, T, H))
+        heads = ref.compact(fmt, 0, ref.widen(k), ref.widen(v), T - 1, 40, 0, sc, np.zeros((1, H), np.float32))
+        made.append((k, v, sc, heads))
+    for i in range(60):
+        k, v, sc, heads = made[i % 2]
+        cache = _alloc(kvp, 1, H, d, 13 * H, 13, fmt)
+        st = status_word()
+        kvp.kvp_compact_block8(dev_bf16(k), dev_bf16(v), T - 1, 0, cache, mode=0, scores=dev_f32(sc),
+                               tau=torch.zeros(1, H, device="cuda"), window=40, status=st)
+        _check_cache(cache, heads, fmt, 0)
+        assert st.item() == 0
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_steps_back_to_back_give_the_bits_of_steps_apart(kvp, fmt):
+    """Rotation, append and attention of 60 steps launched without a pause, and again with the GPU waited for after
+    every call."""
+    B, H, G, d, steps = 4, 8, 4, 128, 60
+    got = []
+    turns = kvp.kvp_rope_turns(10000.0 ** (-np.arange(0, d, 2) / d))
+    x = dev_bf16(_bits(411, (steps, B, H * (G + 2), d), 1))
+    flag = torch.full((B, H), -1, dtype=torch.int32, device="cuda")
+    for wait in (torch.cuda.synchronize, lambda: None):
+        cache, _, now = _build(kvp, fmt, 412, B, 100, H, d, reserve=steps)
+        ws = torch.zeros(kvp.kvp_decode_attn_block8_workspace_bytes(B, H * G, H, d), dtype=torch.uint8, device="cuda")
+        q, k = torch.empty_like(x[0, :, :H * G]), torch.empty_like(x[0, :, :H])
+        pos = (now + 1 + torch.arange(steps, device="cuda", dtype=torch.int32))[:, None].repeat(1, B)
+        out, st = torch.empty(steps, B, H * G, d, device="cuda"), status_word()
+        torch.cuda.synchronize()
+        for i in range(steps):
+            kvp.kvp_qk_norm_rope(x[i, :, :H * G], x[i, :, H * G:H * (G + 1)], pos[i], turns, q_out=q, k_out=k)
+            wait()
+            kvp.kvp_append_block8(cache, k, x[i, :, H * (G + 1):], now + 1 + i, mode=1, flag_step=flag, status=st)
+            wait()
+            kvp.kvp_decode_attn_block8(q, cache, now + 1 + i, out=out[i], workspace=ws, status=st)
+            wait()
+        torch.cuda.synchronize()
+        assert st.item() == 0
+        got.append((out, cache.kq_pool, cache.vq_pool, cache.scale_pool, cache.expire_pool))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
 def test_bulk_write_records_a_full_pool(kvp):
     B, T, H, d = 2, 100, 2, 64
     k = dev_bf16(_bits(41, (B, T, H, d)))
