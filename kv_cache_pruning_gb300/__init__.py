@@ -821,6 +821,9 @@ def _refuse(t, dtype, name, dev, shape=None):
     raise ValueError(f"{name} must be contiguous (of q, k, v and their outputs: its last dimension)")
 
 
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+
+
 def _on(t, dtype, name, dev, shape=None):
     """Device pointer of a contiguous tensor that has to be on CUDA device `dev` (None: NULL)."""
     if t is None:
@@ -830,26 +833,25 @@ def _on(t, dtype, name, dev, shape=None):
     return t.data_ptr()
 
 
-def _rows(t, name, dev):
-    """Device pointer of a bf16 tensor on `dev` whose last dimension is contiguous."""
-    if t.dtype is not torch.bfloat16 or t.get_device() != dev or (t.stride(-1) != 1 and t.shape[-1] != 1):
-        _refuse(t, torch.bfloat16, name, dev)
-    return t.data_ptr()
-
-
-def _strides(t):
-    """Strides of a tensor's outer dimensions, 0 for those of length 1 (whose stride says nothing)."""
-    shape, st = t.shape, t.stride()
-    if 1 in shape:
-        return tuple(0 if n == 1 else s for n, s in zip(shape[:-1], st))
-    return st[:-1]
+def _rows(t, name, dev, shape=None):
+    """(device pointer, strides) of a bf16 tensor on `dev` whose last dimension is contiguous; the strides are its outer
+    dimensions', 0 for those of length 1 (whose stride says nothing)."""
+    own, st = t.shape, t.stride()
+    if (t.dtype is not _BF16 or t.get_device() != dev or st[-1] != 1 and own[-1] != 1
+            or shape is not None and own != shape):
+        _refuse(t, _BF16, name, dev, shape)
+    if 1 in own:
+        return t.data_ptr(), tuple(0 if n == 1 else x for n, x in zip(own[:-1], st))
+    return t.data_ptr(), st[:-1]
 
 
 def _status(status, dev):
     """Device pointer of the status word (None: NULL)."""
-    if status is not None and status.numel() < 1:
+    if status is None:
+        return None
+    if status.numel() < 1:
         raise ValueError("status must hold one value")
-    return _on(status, torch.int32, "status", dev)
+    return _on(status, _I32, "status", dev)
 
 
 def _call(fn, dev, stream, *args):
@@ -963,11 +965,9 @@ def kvp_compact_block8(k, v, now, reserve, dst: Block8PagedKV, *, mode, scores=N
     list are kvp_compact_masked's."""
     dev, fmt, B, H, d, cap, width = dst._dims
     T = k.shape[1]
-    kp, vp, st = _rows(k, "k", dev), _rows(v, "v", dev), _strides(k)
-    if k.shape != (B, T, H, d):
-        raise ValueError("k must be [B, T, H, d] of dst's batch, heads and head_dim")
-    if v.shape != k.shape or _strides(v) != st:
-        raise ValueError("k and v need the same shape and strides")
+    (kp, st), (vp, v_st) = _rows(k, "k", dev, (B, T, H, d)), _rows(v, "v", dev, (B, T, H, d))
+    if v_st != st:
+        raise ValueError("k and v need the same strides")
     if scores is not None and scores.numel() != B * T * H:
         raise ValueError("scores must hold B*T*H values")
     if tau is not None and tau.numel() != B * H:
@@ -984,16 +984,21 @@ def kvp_compact_block8(k, v, now, reserve, dst: Block8PagedKV, *, mode, scores=N
     return dst
 
 
+def _per_head(t, dtype, name, dev, n):
+    """Device pointer of a contiguous tensor of n values (None: NULL)."""
+    if t is None:
+        return None
+    if t.numel() != n:
+        raise ValueError(f"{name} must hold B*H values")
+    return _on(t, dtype, name, dev)
+
+
 def _append_block8(fn, cache, k_new, v_new, pos, mode, score, tau, flag_step, window, delay, status, stream):
     dev, fmt, B, H, d, cap, width = cache._dims
-    if k_new.shape != (B, H, d) or v_new.shape != (B, H, d):
-        raise ValueError("k_new and v_new must be [B, H, d] of the cache's batch, heads and head_dim")
-    for t, nm in ((score, "score"), (tau, "tau"), (flag_step, "flag_step")):
-        if t is not None and t.numel() != B * H:
-            raise ValueError(f"{nm} must hold B*H values")
-    _call(fn, dev, stream, fmt, mode, B, H, d, pos, _rows(k_new, "k_new", dev), _rows(v_new, "v_new", dev),
-          *_strides(k_new), *_strides(v_new), _on(score, torch.float32, "score", dev),
-          _on(tau, torch.float32, "tau", dev), _on(flag_step, torch.int32, "flag_step", dev), window, delay,
+    kp, (k0, k1) = _rows(k_new, "k_new", dev, (B, H, d))
+    vp, (v0, v1) = _rows(v_new, "v_new", dev, (B, H, d))
+    _call(fn, dev, stream, fmt, mode, B, H, d, pos, kp, vp, k0, k1, v0, v1, _per_head(score, _F32, "score", dev, B * H),
+          _per_head(tau, _F32, "tau", dev, B * H), _per_head(flag_step, _I32, "flag_step", dev, B * H), window, delay,
           cache.kq_pool.data_ptr(), cache.vq_pool.data_ptr(), cache.scale_pool.data_ptr(),
           cache.expire_pool.data_ptr(), cap, cache.page_table.data_ptr(), width, cache.remap.data_ptr(),
           cache.count.data_ptr(), _status(status, dev))
@@ -1028,14 +1033,14 @@ def kvp_read_block8(cache: Block8PagedKV, first_slot, n_slots, *, k_out=None, v_
         k_out = _new(torch.empty, shape, torch.bfloat16, dev, stream)
     if v_out is None:
         v_out = _new(torch.empty, shape, torch.bfloat16, dev, stream)
-    st = _strides(k_out)
-    if k_out.shape != shape or v_out.shape != shape or _strides(v_out) != st:
-        raise ValueError("k_out and v_out must be [B, n_slots, H, d] of the same strides")
+    (kp, st), (vp, v_st) = _rows(k_out, "k_out", dev, shape), _rows(v_out, "v_out", dev, shape)
+    if v_st != st:
+        raise ValueError("k_out and v_out need the same strides")
     if status is None:
         status = _new(torch.zeros, 1, torch.int32, dev, stream)
     _call(_lib.kvp_read_block8, dev, stream, fmt, B, H, d, cache.kq_pool.data_ptr(), cache.vq_pool.data_ptr(),
           cache.scale_pool.data_ptr(), cap, cache.page_table.data_ptr(), width, cache.count.data_ptr(), first_slot,
-          n_slots, _rows(k_out, "k_out", dev), _rows(v_out, "v_out", dev), *st, _status(status, dev))
+          n_slots, kp, vp, *st, _status(status, dev))
     return k_out, v_out
 
 
@@ -1097,15 +1102,15 @@ def _head_rows(x, y, name, dev, n, d, stream):
     if x is None:
         if y is not None:
             raise ValueError(f"{name}_out without {name}")
-        return (0, None, 0, 0, None, 0, 0), None
+        return 0, None, (0, 0), None, (0, 0), None
     shape = x.shape
     if len(shape) != 3 or shape[0] != n or shape[2] != d:
         raise ValueError(f"{name} must be [n, heads, d]")
     if y is None:
-        y = _new(torch.empty, shape, torch.bfloat16, dev, stream)
-    elif y.shape != shape:
-        raise ValueError(f"{name}_out must be of {name}'s shape")
-    return (shape[1], _rows(x, name, dev), *_strides(x), _rows(y, name, dev), *_strides(y)), y
+        y = _new(torch.empty, shape, _BF16, dev, stream)
+    xp, xs = _rows(x, name, dev)
+    yp, ys = _rows(y, name + "_out", dev, shape)
+    return shape[1], xp, xs, yp, ys, y
 
 
 def kvp_qk_norm_rope(q, k, pos, turns, *, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, q_out=None,
@@ -1117,21 +1122,21 @@ def kvp_qk_norm_rope(q, k, pos, turns, *, q_weight=None, k_weight=None, eps=1e-6
     some = q if q is not None else k
     if some is None:
         raise ValueError("q or k is required")
-    if not some.is_cuda:
+    dev, shape = some.get_device(), some.shape
+    if dev < 0:
         raise ValueError("q and k must be CUDA tensors")
-    dev, n, d = some.get_device(), some.shape[0], some.shape[-1]
+    n, d = shape[0], shape[-1]
     rot = 0
     if turns is not None:
         rot = 2 * turns.numel()
         if pos is None:
             raise ValueError("pos is required with turns")
-    (hq, qp, q0, q1, qo, qo0, qo1), q_out = _head_rows(q, q_out, "q", dev, n, d, stream)
-    (hk, kp, k0, k1, ko, ko0, ko1), k_out = _head_rows(k, k_out, "k", dev, n, d, stream)
+    hq, qp, (q0, q1), qo, (qo0, qo1), q_out = _head_rows(q, q_out, "q", dev, n, d, stream)
+    hk, kp, (k0, k1), ko, (ko0, ko1), k_out = _head_rows(k, k_out, "k", dev, n, d, stream)
     _call(_lib.kvp_qk_norm_rope, dev, stream, n, hq, hk, d, rot, interleaved, qp, q0, q1, kp, k0, k1,
-          _on(pos, torch.int32, "pos", dev, (n,)) if rot else None,
-          _on(turns, torch.int64, "turns", dev) if rot else None,
-          _on(q_weight, torch.float32, "q_weight", dev, (d,)), _on(k_weight, torch.float32, "k_weight", dev, (d,)),
-          eps, qo, qo0, qo1, ko, ko0, ko1)
+          _on(pos, _I32, "pos", dev, (n,)) if rot else None, _on(turns, torch.int64, "turns", dev) if rot else None,
+          _on(q_weight, _F32, "q_weight", dev, (d,)), _on(k_weight, _F32, "k_weight", dev, (d,)), eps, qo, qo0, qo1, ko,
+          ko0, ko1)
     return q_out, k_out
 
 

@@ -51,8 +51,9 @@ constexpr int kMaxCtas = 512;    // grid bound used to size the workspace
 constexpr float kLazy = 3.f;     // how far a base-2 logit may pass the reference before it moves
 constexpr float kBias = 12.f;    // weights are 2^(x - m + kBias): at most 2^(kLazy + kBias) in fp16
 constexpr int kFewPieces = 8;    // CTAs whose partial results of one (b, h) are merged in one round trip
-constexpr int kOwnPages = 64;    // pages of a (b, h) that one CTA of its own takes: 4 a warp
-constexpr int kAhead = 2;        // pages whose lines are brought into L2 before their loads
+constexpr int kOwnExtra = 96;    // pages by which the longest (b, h) may pass an even share to have a CTA of its own
+constexpr int kCtaPages = 2 * kWarps;  // fewest pages of an even share: more CTAs would have more to merge
+constexpr int kAhead = 1;        // pages whose lines are brought into L2 before their loads
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Params {
@@ -199,7 +200,7 @@ KVP_DEV void write_lse(const Params& p, int64_t row, float m, float l) {
 template <int D, int FMT, bool kDup>
 __global__ void __launch_bounds__(kThreads, 1) attn_block8_kernel(const Params p) {
   extern __shared__ __align__(16) uint8_t sm[];
-  __shared__ int warp_sum[kWarps];
+  __shared__ int4 warp_stat[kWarps];     // pages of a warp's (b, h)s: sum, most, fewest
   __shared__ int part_unit[kWarps * 2];
   __shared__ float wts[8][2 * kWarps];   // a merge's weights: head, partial result
   __shared__ float2 merged_ml[8];
@@ -224,54 +225,52 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block8_kernel(const Params p
   const int cap = p.max_pages * kPage;
   const int each = (p.BH + kThreads - 1) / kThreads;
   auto pages_of = [&](int u) { return (min(max(p.count[u], 0), cap) + kPage - 1) / kPage; };
-  bool none = false, many = p.BH > static_cast<int>(gridDim.x);
-  int sum = 0;
+  int sum = 0, most = 0, least = 1;
   for (int i = tid * each; i < min(p.BH, (tid + 1) * each); ++i) {
     const int pages = pages_of(i);
     sum += pages;
-    none |= pages == 0;
-    many |= pages > kOwnPages;
+    most = max(most, pages);
+    least = min(least, pages);
   }
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  most = __reduce_max_sync(0xffffffffu, most);
+  least = __reduce_min_sync(0xffffffffu, least);
+  if (lane == 31) warp_stat[warp] = make_int4(incl, most, least, 0);
   if (tid < kWarps * 2) part_unit[tid] = -1;
-  const bool any_empty = __syncthreads_or(none);
-  // A CTA for each (b, h), where there are enough of them and no (b, h) keeps a warp for long: nothing to merge
-  // between CTAs. Otherwise all pages are dealt out evenly.
-  const bool own = !__syncthreads_or(many);
-  int total, ctas;
+  __syncthreads();
+  const int4 st = lane < kWarps ? warp_stat[lane] : make_int4(0, 0, 1, 0);
+  const int total = __reduce_add_sync(0xffffffffu, st.x);
+  int at_page = incl - sum + __reduce_add_sync(0xffffffffu, lane < warp ? st.x : 0);
+  most = __reduce_max_sync(0xffffffffu, st.y);
+  least = __reduce_min_sync(0xffffffffu, st.z);
+  // A CTA for each (b, h), where there are enough of them and no (b, h) is much longer than an even share (or than
+  // kOwnPages): nothing to merge between CTAs. Otherwise all pages are dealt out evenly.
+  const bool own = p.BH <= static_cast<int>(gridDim.x) &&
+                   most - total / static_cast<int>(gridDim.x) <= kOwnExtra;
+  int ctas;
   if (own) {
     ctas = p.BH;
     if (tid == 0 && static_cast<int>(blockIdx.x) < p.BH) {
       prefix[blockIdx.x] = 0;
       prefix[blockIdx.x + 1] = pages_of(blockIdx.x);
     }
-    total = 0;
   } else {
-    int incl = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    if (lane == 31) warp_sum[warp] = incl;
-    __syncthreads();
-    int at = incl - sum;
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      at += w < warp ? warp_sum[w] : 0;
-      total += warp_sum[w];
-    }
     for (int i = tid * each; i < min(p.BH, (tid + 1) * each); ++i) {
-      prefix[i] = at;
-      at += pages_of(i);
+      prefix[i] = at_page;
+      at_page += pages_of(i);
     }
     if (tid == 0) prefix[p.BH] = total;
-    ctas = min(static_cast<int>(gridDim.x), (total + kWarps - 1) / kWarps);
+    ctas = min(static_cast<int>(gridDim.x), (total + kCtaPages - 1) / kCtaPages);
   }
   __syncthreads();
 
   // rows of (b, h) without pages
-  for (int u = blockIdx.x; any_empty && u < p.BH; u += gridDim.x) {
+  for (int u = blockIdx.x; least == 0 && u < p.BH; u += gridDim.x) {
     if (prefix[u + 1] > prefix[u]) continue;
     for (int i = tid; i < G * D; i += kThreads) p.out[static_cast<int64_t>(u) * G * D + i] = 0.f;
     if (p.lse != nullptr && tid < G) p.lse[static_cast<int64_t>(u) * G + tid] = -INFINITY;
@@ -622,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block8_kernel(const Params p
       const int pieces = cta_of(prefix[u + 1] - 1) - cta_of(prefix[u]) + 1;
       fence_acq_rel_gpu();
       last_s[tid] = atomicAdd(&p.arrived[u], 1) == pieces - 1;
-      fence_acq_rel_gpu();
+      if (last_s[tid]) fence_acq_rel_gpu();
     }
   }
   __syncthreads();
@@ -777,6 +776,9 @@ kvp_status attn_block8_impl(int fmt, int batch, int n_q_heads, int n_kv_heads, i
   if (sms == 0) return KVP_ERR_CUDA;
   int grid = sms < kMaxCtas ? sms : kMaxCtas;
   if (grid_limit > 0 && grid_limit < grid) grid = grid_limit;
+  // no more CTAs than a full page table keeps busy
+  const int64_t busy = (BH * max_pages + kCtaPages - 1) / kCtaPages;
+  if (grid > BH && grid > busy) grid = static_cast<int>(busy > BH ? busy : BH);
   Params p;
   p.q = static_cast<const uint16_t*>(q);
   p.k_pool = static_cast<const uint8_t*>(kq_pool);
