@@ -78,15 +78,10 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32) count_block8_kernel(MaskedS
 
 // ------------------------------------------------------------------ list pass
 template <bool kFused>
-__global__ void __launch_bounds__(kWarpsPerCta * 32) list_kernel(MaskedSrc src, int now, int NS, int reserve,
-                                                                  int max_pages, int n_pages_cap, int BH, CompactWs ws,
-                                                                  const int32_t* count,
-                                                                  int32_t* status,
-                                                                  int32_t* expire_pool,
-                                                                  int32_t* page_table,
-                                                                  int32_t* remap,
-                                                                  int32_t* n_used,
-                                                                  int2* owner) {
+__global__ void __launch_bounds__(kWarpsPerCta * 32) list_kernel(
+    MaskedSrc src, int now, int NS, int table_share, int reserve, int max_pages, int n_pages_cap, int BH, CompactWs ws,
+    const int32_t* count, int32_t* status, int32_t* expire_pool, int32_t* page_table, int32_t* remap, int32_t* n_used,
+    int2* owner) {
   pdl_launch_dependents();
   pdl_wait();
   const int bh = blockIdx.x;  // pairs vary fastest: CTAs resident together read the same positions of all heads
@@ -112,64 +107,54 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32) list_kernel(MaskedSrc src, 
       slot0 += c0 + lane < sg ? ws.seg_cnt[static_cast<int64_t>(bh) * NS + c0 + lane] : 0;
   int base;
   if constexpr (kFused) {
-    __shared__ int64_t red_s[3][kWarpsPerCta];
-    int64_t before = 0, total = 0, bad = 0;
+    // (page sums stay below 2^31: checked on the host)
+    __shared__ int3 red_s[kWarpsPerCta];
+    int before = 0, total = 0, most = 0;
     for (int i = threadIdx.x; i < BH; i += kWarpsPerCta * 32) {
-      const int64_t pg = (static_cast<int64_t>(count[i]) + reserve + kPage - 1) / kPage;
+      const int pg = (count[i] + reserve + kPage - 1) / kPage;
       before += i < bh ? pg : 0;
       total += pg;
-      bad |= pg > max_pages;
+      most = max(most, pg);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      before += __shfl_xor_sync(0xffffffffu, before, o);
-      total += __shfl_xor_sync(0xffffffffu, total, o);
-      bad |= __shfl_xor_sync(0xffffffffu, bad, o);
-    }
-    if (lane == 0) {
-      red_s[0][warp] = before;
-      red_s[1][warp] = total;
-      red_s[2][warp] = bad;
-    }
+    before = __reduce_add_sync(0xffffffffu, before);
+    total = __reduce_add_sync(0xffffffffu, total);
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) red_s[warp] = make_int3(before, total, most);
     __syncthreads();
-    before = total = bad = 0;
+    before = total = most = 0;
 #pragma unroll
     for (int w = 0; w < kWarpsPerCta; ++w) {
-      before += red_s[0][w];
-      total += red_s[1][w];
-      bad |= red_s[2][w];
+      before += red_s[w].x;
+      total += red_s[w].y;
+      most = max(most, red_s[w].z);
     }
-    const bool ok = !bad && total <= n_pages_cap;
+    const bool ok = most <= max_pages && total <= n_pages_cap;
     if (first_cta && threadIdx.x == 0) {
-      *n_used = ok ? static_cast<int32_t>(total) : 0;
+      *n_used = ok ? total : 0;
       if (!ok) record_error(status, KVP_ERR_CAPACITY);
     }
     if (!ok) return;
-    base = static_cast<int>(before);
+    base = before;
   } else {
     const bool ok = ws.ok[0] != 0;
     if (first_cta && threadIdx.x == 0)
-      *n_used = ok ? static_cast<int32_t>(ws.base[BH - 1] + (static_cast<int64_t>(count[BH - 1]) + reserve + kPage - 1) / kPage)
-                   : 0;
+      *n_used = ok ? ws.base[BH - 1] + (count[BH - 1] + reserve + kPage - 1) / kPage : 0;
     if (!ok) return;
     base = ws.base[bh];
   }
   if (!live) return;
   slot0 = __reduce_add_sync(0xffffffffu, slot0);
   const int cnt = count[bh];
-  const int pages = static_cast<int>((static_cast<int64_t>(cnt) + reserve + kPage - 1) / kPage);
-  const int64_t cap = static_cast<int64_t>(max_pages) * kPage;
-  int32_t* remap_bh = remap + bh * cap;
-  // this segment's share of the page-table row, the owners and the remap tail
-  const int seg = (max_pages + NS - 1) / NS;
-  for (int64_t p = static_cast<int64_t>(sg) * seg + lane; p < min(static_cast<int64_t>(max_pages), (sg + int64_t{1}) * seg);
-       p += 32) {
-    page_table[static_cast<int64_t>(bh) * max_pages + p] = p < pages ? base + static_cast<int>(p) : -1;
-    if (p < pages) owner[base + p] = make_int2(bh, static_cast<int>(p << 5 | min(max(cnt - p * kPage, int64_t{0}), int64_t{kPage})));
+  const int pages = (cnt + reserve + kPage - 1) / kPage;
+  int32_t* remap_bh = remap + static_cast<int64_t>(bh) * max_pages * kPage;
+  // this segment's share of the page-table row, the owners and the remap tail: table_share pages and their slots
+  const int p_lo = static_cast<int>(min(static_cast<int64_t>(sg) * table_share, static_cast<int64_t>(max_pages)));
+  const int p_hi = p_lo + min(table_share, max_pages - p_lo);
+  for (int p = p_lo + lane; p < p_hi; p += 32) {
+    page_table[static_cast<int64_t>(bh) * max_pages + p] = p < pages ? base + p : -1;
+    if (p < pages) owner[base + p] = make_int2(bh, p << 5 | min(max(cnt - p * kPage, 0), kPage));
   }
-  const int64_t rseg = (cap + NS - 1) / NS;
-  const int64_t rlo = sg * rseg > cnt ? sg * rseg : static_cast<int64_t>(cnt);
-  for (int64_t j = rlo + lane; j < min(cap, (sg + 1) * rseg); j += 32) remap_bh[j] = -1;
+  for (int64_t j = max(p_lo * kPage, cnt) + lane; j < p_hi * kPage; j += 32) remap_bh[j] = -1;
 
   int nk = 0;
 #pragma unroll
@@ -465,13 +450,14 @@ kvp_status launch_compact(const MaskedSrc& src, int BH, int NS, int now, int res
       cudaSuccess)
     return KVP_ERR_CUDA;
   const int32_t* cnt = count;
+  const int share = (max_pages + NS - 1) / NS;
   if (BH <= kFusedBH) {
-    if (launch_pdl(list_kernel<true>, dim3(BH, segs), dim3(kWarpsPerCta * 32), 0, st, src, now, NS, reserve, max_pages,
+    if (launch_pdl(list_kernel<true>, dim3(BH, segs), dim3(kWarpsPerCta * 32), 0, st, src, now, NS, share, reserve, max_pages,
                    n_pages_cap, BH, ws, cnt, status, expire_pool, page_table, remap, n_used, owner) != cudaSuccess)
       return KVP_ERR_CUDA;
   } else {
     base_kernel<<<1, 1024, 0, st>>>(BH, reserve, max_pages, n_pages_cap, ws, cnt, status);
-    if (launch_pdl(list_kernel<false>, dim3(BH, segs), dim3(kWarpsPerCta * 32), 0, st, src, now, NS, reserve, max_pages,
+    if (launch_pdl(list_kernel<false>, dim3(BH, segs), dim3(kWarpsPerCta * 32), 0, st, src, now, NS, share, reserve, max_pages,
                    n_pages_cap, BH, ws, cnt, status, expire_pool, page_table, remap, n_used, owner) != cudaSuccess)
       return KVP_ERR_CUDA;
   }
