@@ -396,14 +396,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block8_kernel(const Params p
         const int slot = (at - u_lo + i) * kPage;
         const bool in0 = slot + g < cnt && e0_next > now, in1 = slot + g + 8 < cnt && e1_next > now;
         const float2 sc = sc_next;
-        float x[4] = {0.f, 0.f, 0.f, 0.f};
+        // two sums, so that the products wait for one another half as often
+        float x[4] = {0.f, 0.f, 0.f, 0.f}, x2[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
           uint32_t a0, a1, a2, a3;
           codes_to_f16<FMT>(kw.w[0][j], a0, a2);
           codes_to_f16<FMT>(kw.w[1][j], a1, a3);
-          mma_f16_16816(x, a0, a1, a2, a3, qf[j][0], qf[j][1]);
+          mma_f16_16816(j & 1 ? x2 : x, a0, a1, a2, a3, qf[j][0], qf[j][1]);
         }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[c] += x2[c];
         const int id_next = i + 1 < n ? id_of(i + 1) : -1;
         if (i + 1 < n) request_k(id_next);
         const float f0 = qs[0] * sc.x, f1 = qs[1] * sc.x;
