@@ -19,6 +19,9 @@ runs measure the rest of the path on the shapes it is quoted for:
                  inverse of the kept fraction
   prune_sweep_long  the same sweep on one layer of the 65B-shaped MHA stack
                  (64 heads, 131,072 cached tokens, batch 1)
+  block8_decode  the same layer with its cache in 8 bits, a scale for each page: the
+                 prompt written, 64 steps of norm and rotation, append and
+                 attention, the cache read back; beside the same steps in bf16
 
 Decode loops are captured once in a CUDA graph (the C-ABI calls only enqueue
 work on the current stream) and replayed for timing, so host launch overhead
@@ -629,6 +632,114 @@ def quant_decode(kvp, dev, peaks, seed=0, steps=64, reps=3):
             "one_tier": res[1], "two_tier": res[2]}
 
 
+def block8_decode(kvp, dev, peaks, seed=0, steps=64, reps=3):
+    """The 8-bit cache with a scale for each page on the Llama-3-8B-shaped layer (batch 16, 8,192-token prompt, 32 q / 8
+    kv heads, head_dim 128), a quarter of the prompt kept (tau at each head's 75th-percentile score, 128-token window),
+    in both formats and, beside them, in bf16. The prompt's keys are normed and rotated (kvp_qk_norm_rope) and written
+    (kvp_compact_block8); each of 64 decode steps norms and rotates its queries and keys from one projection's output,
+    appends and attends (one CUDA graph, positions in device memory); the cache is read back at the end."""
+    B, T, H, Hq, d, W = 16, 8192, 8, 32, 128, 128
+    G = Hq // H
+    g = torch.Generator(device=dev)
+    g.manual_seed(seed)
+    K = _randn_bf16((B * T, H, d), g, dev)
+    V = _randn_bf16((B, T, H, d), g, dev)
+    qkv = _randn_bf16((steps, B, Hq + 2 * H, d), g, dev)
+    s = torch.randn((B, T, H), generator=g, device=dev)
+    s_new = torch.randn((steps, B, H), generator=g, device=dev)
+    st = torch.zeros(1, dtype=torch.int32, device=dev)
+    w = 1 + 0.1 * torch.randn(2, d, generator=g, device=dev)
+    turns = kvp.kvp_rope_turns(500000.0 ** (-torch.arange(0, d, 2, dtype=torch.float64) / d), device=dev)
+    tau = _tau_quantile(kvp, s, 0.75)
+    pos_prompt = torch.arange(T, device=dev, dtype=torch.int32).repeat(B)
+    Kr = torch.empty_like(K)
+
+    def rotate_prompt():
+        kvp.kvp_qk_norm_rope(None, K, pos_prompt, turns, k_weight=w[1], k_out=Kr)
+
+    ms_rot = _time(_graph(rotate_prompt), reps=reps)
+    Kr = Kr.view(B, T, H, d)
+    mp = (T + steps + 15) // 16
+    cap = B * H * mp
+    pos = torch.empty(B, dtype=torch.int32, device=dev)
+    q = torch.empty(B, Hq, d, dtype=torch.bfloat16, device=dev)
+    k = torch.empty(B, H, d, dtype=torch.bfloat16, device=dev)
+    out = torch.empty(B, Hq, d, device=dev)
+    res = {}
+    for name, fmt in (("bf16", None), ("e4m3", kvp.KVP_BLOCK8_E4M3), ("int8", kvp.KVP_BLOCK8_INT8)):
+        if fmt is None:
+            c = kvp.PagedKV.allocate(B, H, d, cap, mp, device=dev)
+            ws_c = torch.empty(kvp.kvp_compact_workspace_bytes(B, H, T), dtype=torch.uint8, device=dev)
+            ws_a = torch.zeros(kvp.kvp_decode_attn_workspace_bytes(B, Hq, H, d), dtype=torch.uint8, device=dev)
+            row_bytes = 2 * 2 * d + 4
+        else:
+            c = kvp.Block8PagedKV.allocate(B, H, d, cap, mp, fmt=fmt, device=dev)
+            ws_c = torch.empty(kvp.kvp_compact_block8_workspace_bytes(B, H, T, cap), dtype=torch.uint8, device=dev)
+            ws_a = torch.zeros(kvp.kvp_decode_attn_block8_workspace_bytes(B, Hq, H, d), dtype=torch.uint8, device=dev)
+            row_bytes = 2 * d + 4 + 8 / 16
+
+        def prefill():
+            fn = kvp.kvp_compact_masked if fmt is None else kvp.kvp_compact_block8
+            fn(Kr, V, T - 1, steps, c, mode=kvp.KVP_MASK_KVZAP, scores=s, tau=tau, window=W, status=st, workspace=ws_c)
+
+        def step(i):
+            kvp.kvp_qk_norm_rope(qkv[i, :, :Hq], qkv[i, :, Hq:Hq + H], pos, turns, q_weight=w[0], k_weight=w[1], q_out=q,
+                                 k_out=k)
+            v = qkv[i, :, Hq + H:]
+            kw = dict(mode=kvp.KVP_MASK_KVZAP, score=s_new[i], tau=tau, window=W, status=st)
+            if fmt is None:
+                kvp.kvp_append_devpos(c, k, v.contiguous(), pos[:1], **kw)
+                kvp.kvp_decode_attn_devpos(q, c, pos[:1], out=out, workspace=ws_a, status=st)
+            else:
+                kvp.kvp_append_block8_devpos(c, k, v, pos[:1], **kw)
+                kvp.kvp_decode_attn_block8_devpos(q, c, pos[:1], out=out, workspace=ws_a, status=st)
+
+        def loop():
+            pos.fill_(T - 1)
+            for i in range(steps):
+                pos.add_(1)
+                step(i)
+
+        ms_write = _time(_graph(prefill), reps=reps)
+        torch.cuda.synchronize()
+        kept = int(c.count.sum().item())
+
+        def attend():
+            for _ in range(steps):
+                if fmt is None:
+                    kvp.kvp_decode_attn(q, c, T - 1, out=out, workspace=ws_a, status=st)
+                else:
+                    kvp.kvp_decode_attn_block8(q, c, T - 1, out=out, workspace=ws_a, status=st)
+
+        step(0)                        # queries of a first step; the prompt's cache again for the measurements
+        prefill()
+        ms_attn = _time(_graph(attend), reps=reps) / steps
+        torch.cuda.synchronize()
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            loop()
+        best = 1e30
+        for _ in range(reps):
+            prefill()                  # the loop appends: start every replay from the prompt's cache
+            torch.cuda.synchronize()
+            best = min(best, _time(gr.replay))
+        res[name] = {"prompt_write_us": ms_write * 1e3, "attention_us": ms_attn * 1e3, "attention_bytes": kept * row_bytes,
+                     "attention_frac_of_hbm": kept * row_bytes / (ms_attn * 1e-3) / 1e9 / peaks[0],
+                     "us_per_step": best / steps * 1e3, "decode_tokens_per_s": B / (best / steps * 1e-3),
+                     "slots": int(c.count.sum().item())}
+        if fmt is not None:
+            rows = c.count.max().item()
+            ko = torch.empty(B, rows, H, d, dtype=torch.bfloat16, device=dev)
+            vo = torch.empty_like(ko)
+            res[name]["read_back_us"] = 1e3 * _time(
+                _graph(lambda: kvp.kvp_read_block8(c, 0, rows, k_out=ko, v_out=vo, status=st)), reps=reps)
+        assert st.item() == 0, kvp.status_string(st.item())
+    return {"workload": "block8_decode: Llama-3-8B layer, batch 16, 8192-token prompt, tau at the 75th percentile, window "
+                        "128, + 64 decode steps of norm and rotation, append, attention; one CUDA graph; the cache in "
+                        "bf16, and in 8 bits with a scale for each page",
+            "prompt_keys_rotation_us": ms_rot * 1e3, **res}
+
+
 def gqa_sweep(kvp, dev, peaks, seed=0, calls=10, reps=5):
     """Decode attention on the Llama-3-8B-shaped cache (batch 16, 8,192 cached
     tokens, 8 kv heads, head_dim 128) with 1, 2, 4 and 8 query heads per kv
@@ -866,7 +977,7 @@ def seq_split(kvp, dev, peaks, seed=0, calls=5, reps=3):
 RUNNERS = {"mlp_prefill": mlp_prefill, "dms_decode": dms_decode, "llama65b_mha": llama65b_mha,
            "prune_sweep": prune_sweep, "prune_sweep_long": prune_sweep_long, "threshold": threshold,
            "quant_tier": quant_tier, "quant_tier_mha": quant_tier_mha, "quant_decode": quant_decode, "gqa_sweep": gqa_sweep, "mla_sweep": mla_sweep,
-           "mla_dms_decode": mla_dms_decode, "seq_split": seq_split}
+           "mla_dms_decode": mla_dms_decode, "seq_split": seq_split, "block8_decode": block8_decode}
 
 
 def run(name, kvp, dev, peaks):
