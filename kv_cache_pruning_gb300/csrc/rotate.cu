@@ -11,12 +11,11 @@
 // (two at D = 64) shuffles. A warp takes one token's heads, or a share of them
 // when there are few tokens, with the token's cosines and sines in registers.
 //
-// Measured on a GB300, 65,521 tokens x 40 heads of 128: 271 us at first, 239 with 64
-// registers a thread (four CTAs an SM instead of two), 229 with the norm's weights
-// folded into the cosines and sines, 231 (0.85 of measured HBM) in its final form
-// with ordered streaming loads. Not kept: the next step's rows requested before this
-// one's arithmetic (264: the registers spill), one step or three in flight instead of
-// two (239, 252).
+// Measured on a GB300, 65,521 tokens x 40 heads of 128: 271 us at first, 239 with fewer
+// registers a thread, 229 with the norm's weights folded into the cosines and sines,
+// 235 (0.84 of measured HBM) in its final form with ordered streaming loads. Not kept:
+// the next step's rows requested before this one's arithmetic (264: the registers
+// spill), one step or three in flight instead of two (239, 252).
 //
 // An angle is a 64-bit product: turns[i] = inv_freq[i] / (2 pi) as a 64-bit
 // fraction of a turn, times the position modulo one turn (the integer wraps
@@ -30,8 +29,14 @@ namespace kvp {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kUnroll = 2;  // head rows a lane has in flight
-constexpr int kCtas = 4;    // CTAs per SM: 32 warps with 2 KB in flight each
+constexpr int kUnroll = 2;      // rows a lane has in flight
+constexpr int kCtas = 3;        // CTAs per SM: 24 warps (with four the registers spill more: 231 us for the 65,521 tokens above, but
+                                // short calls 5 % longer)
+constexpr int kTokenCtas = 3;   // the same of the kernel for few heads
+// Steps (of 32 / LPH rows) a token's heads may take for the kernel for few heads. Measured on a GB300, 131,072 tokens,
+// heads side by side / tokens side by side: 2 heads of 128 193 / 60 us, 5 185 / 89, 8 143 / 99, 12 212 / 161, 16 256 /
+// 208, 24 300 / 306; 24 heads of 64 216 / 148; 65,536 x 72 heads of 64 226 / 279; 65,521 x 40 of 128 231 / 272.
+constexpr int kFewSteps = 5;
 
 struct RotateParams {
   const uint16_t* x[2];   // q, k
@@ -42,7 +47,9 @@ struct RotateParams {
   const uint64_t* turns;
   int heads[2];
   int64_t n_items;
-  int parts;              // warps a token's heads are dealt to
+  int parts;              // warps that a token's (a group of tokens') heads are dealt to
+  int parts_q;            // rotate_tokens_kernel: those of them that take q's heads
+  int64_t n_tok;
   int rot;
   float eps;
 };
@@ -60,6 +67,69 @@ KVP_DEV void unpack_row(const uint4& a, const uint4& b, float (&f)[16]) {
   }
 }
 
+// A lane's share of the rotation's coefficients, the norm's weights taken along: of a pair (a, b), a wa cos - b wb sin and
+// b wb cos + a wa sin. Pair e of a lane's 16 values: e and e + 8, or 2 e and 2 e + 1 (kPairs).
+struct Turns {
+  float ac[8], as[8], bc[8], bs[8];
+  template <bool kPairs>
+  KVP_DEV void set(int e, const float* w, int run0, int run1, float c, float s) {
+    const int i = kPairs ? 2 * e : e, k = kPairs ? 2 * e + 1 : e + 8;
+    const float wa = w != nullptr ? w[i < 8 ? run0 * 8 + i : run1 * 8 + i - 8] : 1.f;
+    const float wb = w != nullptr ? w[k < 8 ? run0 * 8 + k : run1 * 8 + k - 8] : 1.f;
+    ac[e] = wa * c;
+    bc[e] = wb * c;
+    as[e] = wa * s;
+    bs[e] = wb * s;
+  }
+};
+
+// cos and sin of turns[pair] * pos
+KVP_DEV void angle(const uint64_t* turns, int pair, uint64_t pos, float& c, float& s) {
+  sincospif(static_cast<float>(static_cast<int32_t>((turns[pair] * pos) >> 32)) * (1.f / 2147483648.f), &s, &c);
+}
+
+// One row's 16 values of a lane (runs a, b): norm over the row's LPH lanes (if any), rotation, and to dst + run0 * 8 and
+// dst + run1 * 8. rotates: whether the lane's pairs are rotated ones (kept apart, so that an infinity of the others does
+// not meet a zero sine).
+template <int D, bool kPairs>
+KVP_DEV void turn_row(const uint4& a, const uint4& b, bool norm, float eps, bool rotates, const Turns& t, bool store,
+                      uint16_t* dst, int run0, int run1) {
+  float f[16];
+  unpack_row(a, b, f);
+  float r = 1.f;
+  if (norm) {
+    float sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) sum = fmaf(f[e], f[e], sum);
+#pragma unroll
+    for (int o = 1; o < D / 16; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    r = rsqrtf(sum * (1.f / D) + eps);
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int i = kPairs ? 2 * e : e, k = kPairs ? 2 * e + 1 : e + 8;
+    const float m = f[i], n = f[k];
+    f[i] = (rotates ? m * t.ac[e] - n * t.bs[e] : m * t.ac[e]) * r;
+    f[k] = (rotates ? n * t.bc[e] + m * t.as[e] : n * t.bc[e]) * r;
+  }
+  if (store) {
+    uint4* out = reinterpret_cast<uint4*>(dst);
+    __stcs(out + run0, make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])));
+    __stcs(out + run1, make_uint4(pack_bf16(f[8], f[9]), pack_bf16(f[10], f[11]), pack_bf16(f[12], f[13]),
+                                  pack_bf16(f[14], f[15])));
+  }
+}
+
+// The runs of 8 values that lane j of a row's LPH lanes takes: pairs of rotated runs first, then what is left of the row
+// in the same manner. Returns whether they are rotated ones.
+template <int LPH>
+KVP_DEV bool runs_of(int j, int rot, int& run0, int& run1) {
+  const int nh = rot / 16;
+  run0 = j < nh ? j : nh + j;
+  run1 = run0 + (j < nh ? nh : LPH - nh);
+  return j < nh;
+}
+
 template <int D, bool kPairs>
 __global__ void __launch_bounds__(kWarps * 32, kCtas) rotate_kernel(const RotateParams p) {
   constexpr int LPH = D / 16;       // lanes a head takes
@@ -71,25 +141,22 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) rotate_kernel(const Rotate
   const int64_t tok = item / p.parts;
   const int part = static_cast<int>(item - tok * p.parts);
 
-  // the lane's two runs of 8 values: pairs of rotated runs first, then what is left of the row in the same manner
-  const int nh = p.rot / 16;
-  const bool turns_here = j < nh;
-  const int run0 = turns_here ? j : nh + j;
-  const int run1 = run0 + (turns_here ? nh : LPH - nh);
+  int run0, run1;
+  const bool turns_here = runs_of<LPH>(j, p.rot, run0, run1);
 
   // cosines and sines of the lane's 8 pairs: 2 (1 at D = 64) are computed, the others
   // fetched from the lanes of the warp's other heads, which share the token's angles
   float cs[8], sn[8];
-  if (nh > 0) {
+  if (p.rot > 0) {
     constexpr int kMine = 8 / HPI > 0 ? 8 / HPI : 1;
     const uint64_t pos = static_cast<uint64_t>(static_cast<int64_t>(p.pos[tok]));
     float c[kMine], s[kMine];
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
       const int e = sub * kMine + i;   // of the lane's 8 pairs
-      const int pair = kPairs ? (e < 4 ? 4 * run0 + e : 4 * run1 + e - 4) : 8 * run0 + e;
-      const uint64_t turn = turns_here ? p.turns[pair] * pos : 0;
-      sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * (1.f / 2147483648.f), &s[i], &c[i]);
+      c[i] = 1.f;
+      s[i] = 0.f;
+      if (turns_here) angle(p.turns, kPairs ? (e < 4 ? 4 * run0 + e : 4 * run1 + e - 4) : 8 * run0 + e, pos, c[i], s[i]);
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -109,19 +176,9 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) rotate_kernel(const Rotate
     const uint16_t* x = p.x[which] + tok * p.xt[which];
     uint16_t* y = p.y[which] + tok * p.yt[which];
     const float* wp = p.w[which];
-    // the rotation takes the norm's weights along: of a pair (a, b), a wa cos - b wb sin and b wb cos + a wa sin; values
-    // that are not rotated have cos 1 and no sin
-    float ac[8], as[8], bc[8], bs[8];
+    Turns t;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int i = kPairs ? 2 * e : e, k = kPairs ? 2 * e + 1 : e + 8;  // of the lane's 16 values
-      const float wa = wp != nullptr ? wp[i < 8 ? run0 * 8 + i : run1 * 8 + i - 8] : 1.f;
-      const float wb = wp != nullptr ? wp[k < 8 ? run0 * 8 + k : run1 * 8 + k - 8] : 1.f;
-      ac[e] = turns_here ? wa * cs[e] : wa;
-      bc[e] = turns_here ? wb * cs[e] : wb;
-      as[e] = turns_here ? wa * sn[e] : 0.f;
-      bs[e] = turns_here ? wb * sn[e] : 0.f;
-    }
+    for (int e = 0; e < 8; ++e) t.set<kPairs>(e, wp, run0, run1, turns_here ? cs[e] : 1.f, turns_here ? sn[e] : 0.f);
 #pragma unroll 1
     for (int i0 = i_lo; i0 < i_hi; i0 += kUnroll) {
       uint4 a[kUnroll], b[kUnroll];
@@ -137,41 +194,62 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) rotate_kernel(const Rotate
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         const int h = (i0 + u) * HPI + sub;
-        float f[16];
-        unpack_row(a[u], b[u], f);
-        float r = 1.f;
-        if (wp != nullptr) {
-          float sum = 0.f;
-#pragma unroll
-          for (int e = 0; e < 16; ++e) sum = fmaf(f[e], f[e], sum);
-#pragma unroll
-          for (int o = 1; o < LPH; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-          r = rsqrtf(sum * (1.f / D) + p.eps);
-        }
-        if (turns_here) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int i = kPairs ? 2 * e : e, k = kPairs ? 2 * e + 1 : e + 8;
-            const float m = f[i], n = f[k];
-            f[i] = (m * ac[e] - n * bs[e]) * r;
-            f[k] = (n * bc[e] + m * as[e]) * r;
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int i = kPairs ? 2 * e : e, k = kPairs ? 2 * e + 1 : e + 8;
-            f[i] *= ac[e] * r;
-            f[k] *= bc[e] * r;
-          }
-        }
-        if (i0 + u < i_hi && h < heads) {
-          uint4* dst = reinterpret_cast<uint4*>(y + h * p.yh[which]);
-          __stcs(dst + run0, make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])));
-          __stcs(dst + run1, make_uint4(pack_bf16(f[8], f[9]), pack_bf16(f[10], f[11]), pack_bf16(f[12], f[13]),
-                                        pack_bf16(f[14], f[15])));
-        }
+        turn_row<D, kPairs>(a[u], b[u], wp != nullptr, p.eps, turns_here, t, i0 + u < i_hi && h < heads,
+                            y + h * p.yh[which], run0, run1);
       }
     }
+  }
+}
+
+// The same for few heads: a warp takes 32 / LPH tokens, a row of each at a time, and every lane works out its own
+// token's angles; a warp that took one token's heads side by side would leave lanes idle and spend most of its time on
+// angles. q's and k's rows are dealt to different warps.
+template <int D, bool kPairs>
+__global__ void __launch_bounds__(kWarps * 32, kTokenCtas) rotate_tokens_kernel(const RotateParams p) {
+  constexpr int LPH = D / 16, TPW = 32 / LPH;
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  if (item >= p.n_items) return;
+  const int64_t tok = item / p.parts * TPW + lane / LPH;
+  const int part = static_cast<int>(item % p.parts);
+  const bool live = tok < p.n_tok;
+  const int which = part < p.parts_q ? 0 : 1, mine = which == 0 ? part : part - p.parts_q;
+  const int of = which == 0 ? p.parts_q : p.parts - p.parts_q;
+  const int lo = mine * p.heads[which] / of, hi = (mine + 1) * p.heads[which] / of;
+  int run0, run1;
+  const bool turns_here = runs_of<LPH>(lane % LPH, p.rot, run0, run1);
+  const uint16_t* x = p.x[which] + tok * p.xt[which];
+  uint16_t* y = p.y[which] + tok * p.yt[which];
+  const int64_t xh = p.xh[which], yh = p.yh[which];
+  uint4 a[kUnroll], b[kUnroll];
+  auto request = [&](int h0) {
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      a[u] = b[u] = make_uint4(0, 0, 0, 0);
+      if (live && h0 + u < hi) {
+        a[u] = load16_stream(x + (h0 + u) * xh + run0 * 8);
+        b[u] = load16_stream(x + (h0 + u) * xh + run1 * 8);
+      }
+    }
+  };
+  request(lo);  // on their way while the angles are worked out
+  const float* w = p.w[which];
+  const uint64_t pos = turns_here && live ? static_cast<uint64_t>(static_cast<int64_t>(p.pos[tok])) : 0;
+  Turns t;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    float c = 1.f, s = 0.f;
+    if (turns_here) angle(p.turns, kPairs ? (e < 4 ? 4 * run0 + e : 4 * run1 + e - 4) : 8 * run0 + e, pos, c, s);
+    t.set<kPairs>(e, w, run0, run1, c, s);
+  }
+#pragma unroll 1
+  for (int h0 = lo; h0 < hi; h0 += kUnroll) {
+    if (h0 > lo) request(h0);
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+      turn_row<D, kPairs>(a[u], b[u], w != nullptr, p.eps, turns_here, t, live && h0 + u < hi, y + (h0 + u) * yh, run0,
+                          run1);
   }
 }
 
@@ -239,22 +317,35 @@ extern "C" kvp_status kvp_qk_norm_rope(int64_t n_tok, int n_q_heads, int n_k_hea
   p.turns = turns;
   p.rot = rot_dim;
   p.eps = eps;
-  const int hpi = 32 / (head_dim / 16);
-  const int its = (n_q_heads + hpi - 1) / hpi + (n_k_heads + hpi - 1) / hpi;
-  // Few tokens: their heads are dealt to more warps, down to one step of hpi heads each, until there are
-  // about 4,096 warps (27 for each SM) to hide the loads' latency.
-  int64_t parts = (4096 + n_tok - 1) / n_tok;
-  if (parts > its) parts = its;
-  p.parts = static_cast<int>(parts);
-  p.n_items = n_tok * parts;
+  if (n_tok > 0x7fffffffll) return KVP_ERR_UNSUPPORTED;
+  p.n_tok = n_tok;
+  const int rows = 32 / (head_dim / 16);  // rows a warp takes at a time
+  // Few tokens: their heads are dealt to more warps, until there are about 4,096 of them (27 for each SM) to hide the
+  // loads' latency.
+  const bool by_token = n_q_heads + n_k_heads <= kFewSteps * rows && n_tok * (n_q_heads + n_k_heads) >= 4096 * rows;
+  if (by_token) {
+    p.parts_q = n_q_heads > 0;
+    p.parts = p.parts_q + (n_k_heads > 0);
+    p.n_items = (n_tok + rows - 1) / rows * p.parts;
+  } else {
+    const int its = (n_q_heads + rows - 1) / rows + (n_k_heads + rows - 1) / rows;
+    const int64_t parts = (4096 + n_tok - 1) / n_tok;
+    p.parts = static_cast<int>(parts < its ? parts : its);
+    p.parts_q = 0;
+    p.n_items = n_tok * p.parts;
+  }
   const int64_t ctas = (p.n_items + kWarps - 1) / kWarps;
-  if (n_tok > 0x7fffffffll || ctas > 0x7fffffff) return KVP_ERR_UNSUPPORTED;
+  if (ctas > 0x7fffffff) return KVP_ERR_UNSUPPORTED;
   auto go = [&](auto kern) {
     return launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(kWarps * 32), 0, static_cast<cudaStream_t>(stream),
                       p) == cudaSuccess
                ? KVP_OK
                : KVP_ERR_CUDA;
   };
+  if (by_token) {
+    if (head_dim == 128) return interleaved ? go(rotate_tokens_kernel<128, true>) : go(rotate_tokens_kernel<128, false>);
+    return interleaved ? go(rotate_tokens_kernel<64, true>) : go(rotate_tokens_kernel<64, false>);
+  }
   if (head_dim == 128) return interleaved ? go(rotate_kernel<128, true>) : go(rotate_kernel<128, false>);
   return interleaved ? go(rotate_kernel<64, true>) : go(rotate_kernel<64, false>);
 }

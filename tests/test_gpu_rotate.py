@@ -37,7 +37,8 @@ def _check(got, x, w, eps, pos, freqs, interleaved):
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("n,hq,hk,rot_share,norm", [
     (1, 1, 1, 1.0, True), (1, 32, 8, 1.0, True), (16, 32, 8, 1.0, False), (3, 5, 7, 0.5, True), (7, 0, 3, 0.25, True),
-    (7, 9, 0, 0.5, False), (130, 6, 2, 1.0, True), (5000, 3, 1, 1.0, True), (33, 4, 4, 0.0, True), (2, 64, 64, 0.75, False)])
+    (7, 9, 0, 0.5, False), (130, 6, 2, 1.0, True), (5000, 3, 1, 1.0, True), (33, 4, 4, 0.0, True), (2, 64, 64, 0.75, False), (9001, 3, 2, 0.5, True),
+    (20011, 1, 1, 1.0, False), (4099, 0, 9, 0.25, True)])
 def test_rotation(kvp, d, interleaved, n, hq, hk, rot_share, norm):
     rot = int(d * rot_share) // 16 * 16
     freqs = _freqs(rot)
