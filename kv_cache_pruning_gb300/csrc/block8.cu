@@ -359,14 +359,15 @@ KVP_DEV uint32_t value2(uint32_t two, float scale) {
   return *reinterpret_cast<const uint32_t*>(&y);
 }
 
-// One warp per page of a (b, h): 16 codes a lane, LPR lanes a row.
+// One warp per page of a (b, h): 8 codes a lane, LPR lanes a row, so that a warp's stores are whole lines (with 16 codes
+// and two 16-byte stores a lane the first-level cache was 82 % busy with half-used sectors: 69 us at 16 x 4096 x 8 heads).
 template <int D, int FMT>
 __global__ void __launch_bounds__(kPageWarps * 32) read_block8_kernel(
     int H, int64_t n_items, int pages_each, const uint8_t* kq_pool, const uint8_t* vq_pool,
     const float2* scale_pool, int n_pages_cap, const int32_t* page_table, int max_pages,
     const int32_t* count, int first, int n_slots, uint16_t* k_out,
     uint16_t* v_out, int64_t sb, int64_t st, int64_t sh, int32_t* status) {
-  constexpr int LPR = D / 16;
+  constexpr int LPR = D / 8;
   constexpr int RPI = 32 / LPR;
   constexpr int NI = kPage / RPI;
   pdl_wait();
@@ -389,30 +390,28 @@ __global__ void __launch_bounds__(kPageWarps * 32) read_block8_kernel(
     }
   }
   const float2 s = n > 0 ? scale_pool[page] : make_float2(0.f, 0.f);
-  uint4 kw[NI], vw[NI];
+  uint2 kw[NI], vw[NI];
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     const int r = i * RPI + sub;
-    const int64_t at = (static_cast<int64_t>(page) * kPage + r) * D + piece * 16;
-    kw[i] = vw[i] = make_uint4(0, 0, 0, 0);
+    const int64_t at = (static_cast<int64_t>(page) * kPage + r) * D + piece * 8;
+    kw[i] = vw[i] = make_uint2(0, 0);
     if (r < n) {
-      kw[i] = *reinterpret_cast<const uint4*>(kq_pool + at);
-      vw[i] = *reinterpret_cast<const uint4*>(vq_pool + at);
+      kw[i] = *reinterpret_cast<const uint2*>(kq_pool + at);
+      vw[i] = *reinterpret_cast<const uint2*>(vq_pool + at);
     }
   }
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     const int64_t slot = slot0 + i * RPI + sub - first;
     if (slot < 0 || slot >= n_slots) continue;
-    const int64_t at = b * sb + slot * st + h * sh + piece * 16;
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      const uint4 c = w ? vw[i] : kw[i];
-      const float f = w ? s.y : s.x;
-      uint4* dst = reinterpret_cast<uint4*>((w ? v_out : k_out) + at);
-      dst[0] = make_uint4(value2<FMT>(c.x, f), value2<FMT>(c.x >> 16, f), value2<FMT>(c.y, f), value2<FMT>(c.y >> 16, f));
-      dst[1] = make_uint4(value2<FMT>(c.z, f), value2<FMT>(c.z >> 16, f), value2<FMT>(c.w, f), value2<FMT>(c.w >> 16, f));
-    }
+    const int64_t at = b * sb + slot * st + h * sh + piece * 8;
+    auto put = [&](uint16_t* dst, uint2 c, float f) {
+      *reinterpret_cast<uint4*>(dst + at) =
+          make_uint4(value2<FMT>(c.x, f), value2<FMT>(c.x >> 16, f), value2<FMT>(c.y, f), value2<FMT>(c.y >> 16, f));
+    };
+    put(k_out, kw[i], s.x);
+    put(v_out, vw[i], s.y);
   }
 }
 
