@@ -12,10 +12,11 @@
 // when there are few tokens, with the token's cosines and sines in registers.
 //
 // Measured on a GB300, 65,521 tokens x 40 heads of 128: 271 us at first, 239 with fewer
-// registers a thread, 229 with the norm's weights folded into the cosines and sines,
-// 235 (0.84 of measured HBM) in its final form with ordered streaming loads. Not kept:
-// the next step's rows requested before this one's arithmetic (264: the registers
-// spill), one step or three in flight instead of two (239, 252).
+// registers a thread, 231 with the norm's weights folded into the cosines and sines and
+// streaming loads, 210 (0.94 of measured HBM) with the weights in shared memory
+// instead, which leaves the registers of 32 warps an SM without spills to speak of.
+// Not kept: the next step's rows requested before this one's arithmetic (264), one
+// step or three in flight instead of two (239, 241).
 //
 // An angle is a 64-bit product: turns[i] = inv_freq[i] / (2 pi) as a 64-bit
 // fraction of a turn, times the position modulo one turn (the integer wraps
@@ -29,13 +30,11 @@ namespace kvp {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kUnroll = 2;      // rows a lane has in flight
-constexpr int kCtas = 3;        // CTAs per SM: 24 warps (with four the registers spill more: 231 us for the 65,521 tokens above, but
-                                // short calls 5 % longer)
-constexpr int kTokenCtas = 3;   // the same of the kernel for few heads
+constexpr int kUnroll = 2;  // rows a lane has in flight
+constexpr int kCtas = 4;    // CTAs per SM: 32 warps with 2 KB in flight each (three: 218 us at 65,521 x 40 heads, five 243, they spill)
 // Steps (of 32 / LPH rows) a token's heads may take for the kernel for few heads. Measured on a GB300, 131,072 tokens,
-// heads side by side / tokens side by side: 2 heads of 128 193 / 60 us, 5 185 / 89, 8 143 / 99, 12 212 / 161, 16 256 /
-// 208, 24 300 / 306; 24 heads of 64 216 / 148; 65,536 x 72 heads of 64 226 / 279; 65,521 x 40 of 128 231 / 272.
+// heads side by side / tokens side by side: 2 heads of 128 151 / 59 us, 5 154 / 81, 8 113 / 92, 12 170 / 146, 16 226 /
+// 195, 24 260 / 281; 24 heads of 64 174 / 136; 65,536 x 72 heads of 64 195 / 274; 65,521 x 40 of 128 210 / 255.
 constexpr int kFewSteps = 5;
 
 struct RotateParams {
@@ -67,50 +66,44 @@ KVP_DEV void unpack_row(const uint4& a, const uint4& b, float (&f)[16]) {
   }
 }
 
-// A lane's share of the rotation's coefficients, the norm's weights taken along: of a pair (a, b), a wa cos - b wb sin and
-// b wb cos + a wa sin. Pair e of a lane's 16 values: e and e + 8, or 2 e and 2 e + 1 (kPairs).
-struct Turns {
-  float ac[8], as[8], bc[8], bs[8];
-  template <bool kPairs>
-  KVP_DEV void set(int e, const float* w, int run0, int run1, float c, float s) {
-    const int i = kPairs ? 2 * e : e, k = kPairs ? 2 * e + 1 : e + 8;
-    const float wa = w != nullptr ? w[i < 8 ? run0 * 8 + i : run1 * 8 + i - 8] : 1.f;
-    const float wb = w != nullptr ? w[k < 8 ? run0 * 8 + k : run1 * 8 + k - 8] : 1.f;
-    ac[e] = wa * c;
-    bc[e] = wb * c;
-    as[e] = wa * s;
-    bs[e] = wb * s;
-  }
-};
-
 // cos and sin of turns[pair] * pos
 KVP_DEV void angle(const uint64_t* turns, int pair, uint64_t pos, float& c, float& s) {
   sincospif(static_cast<float>(static_cast<int32_t>((turns[pair] * pos) >> 32)) * (1.f / 2147483648.f), &s, &c);
 }
 
-// One row's 16 values of a lane (runs a, b): norm over the row's LPH lanes (if any), rotation, and to dst + run0 * 8 and
-// dst + run1 * 8. rotates: whether the lane's pairs are rotated ones (kept apart, so that an infinity of the others does
-// not meet a zero sine).
+// One row's 16 values of a lane (runs a, b): norm over the row's D / 16 lanes (if any), rotation, and to dst + run0 * 8
+// and dst + run1 * 8. The cosines and sines of the lane's 8 pairs (e and e + 8, or kPairs: 2 e and 2 e + 1) are in
+// registers, the norm's weights in shared memory (w4[c * D / 16]: the lane's values 4 c .. 4 c + 3): with them in
+// registers too, folded into the cosines and sines, an SM has room for fewer warps (235 us against 210 at 65,521 x 40).
 template <int D, bool kPairs>
-KVP_DEV void turn_row(const uint4& a, const uint4& b, bool norm, float eps, bool rotates, const Turns& t, bool store,
-                      uint16_t* dst, int run0, int run1) {
+KVP_DEV void turn_row(const uint4& a, const uint4& b, bool norm, float eps, bool rotates, const float (&cs)[8],
+                        const float (&sn)[8], const float4* w4, bool store, uint16_t* dst, int run0, int run1) {
   float f[16];
   unpack_row(a, b, f);
-  float r = 1.f;
   if (norm) {
     float sum = 0.f;
 #pragma unroll
     for (int e = 0; e < 16; ++e) sum = fmaf(f[e], f[e], sum);
 #pragma unroll
     for (int o = 1; o < D / 16; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    r = rsqrtf(sum * (1.f / D) + eps);
-  }
+    const float r = rsqrtf(sum * (1.f / D) + eps);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int i = kPairs ? 2 * e : e, k = kPairs ? 2 * e + 1 : e + 8;
-    const float m = f[i], n = f[k];
-    f[i] = (rotates ? m * t.ac[e] - n * t.bs[e] : m * t.ac[e]) * r;
-    f[k] = (rotates ? n * t.bc[e] + m * t.as[e] : n * t.bc[e]) * r;
+    for (int c = 0; c < 4; ++c) {
+      const float4 w = w4[c * (D / 16)];
+      f[4 * c] *= r * w.x;
+      f[4 * c + 1] *= r * w.y;
+      f[4 * c + 2] *= r * w.z;
+      f[4 * c + 3] *= r * w.w;
+    }
+  }
+  if (rotates) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int i = kPairs ? 2 * e : e, k = kPairs ? 2 * e + 1 : e + 8;
+      const float m = f[i], n = f[k];
+      f[i] = m * cs[e] - n * sn[e];
+      f[k] = n * cs[e] + m * sn[e];
+    }
   }
   if (store) {
     uint4* out = reinterpret_cast<uint4*>(dst);
@@ -130,11 +123,26 @@ KVP_DEV bool runs_of(int j, int rot, int& run0, int& run1) {
   return j < nh;
 }
 
+// The norm weights of q and of k, by lane: w_s[(which * 4 + c) * LPH + j] holds values 4 c .. 4 c + 3 of lane j's runs.
+template <int LPH>
+KVP_DEV void load_weights(const RotateParams& p, float4* w_s) {
+  for (int i = threadIdx.x; i < 2 * 4 * LPH; i += kWarps * 32) {
+    const float* w = p.w[i / (4 * LPH)];
+    int run0, run1;
+    runs_of<LPH>(i % LPH, p.rot, run0, run1);
+    const int c = i / LPH % 4;
+    if (w != nullptr) w_s[i] = *reinterpret_cast<const float4*>(w + (c < 2 ? run0 : run1) * 8 + (c & 1) * 4);
+  }
+  __syncthreads();
+}
+
 template <int D, bool kPairs>
 __global__ void __launch_bounds__(kWarps * 32, kCtas) rotate_kernel(const RotateParams p) {
   constexpr int LPH = D / 16;       // lanes a head takes
   constexpr int HPI = 32 / LPH;     // heads a warp takes at once
+  __shared__ float4 w_s[2 * 4 * LPH];
   pdl_wait();
+  load_weights<LPH>(p, w_s);
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   if (item >= p.n_items) return;
   const int lane = threadIdx.x & 31, j = lane % LPH, sub = lane / LPH;
@@ -176,9 +184,6 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) rotate_kernel(const Rotate
     const uint16_t* x = p.x[which] + tok * p.xt[which];
     uint16_t* y = p.y[which] + tok * p.yt[which];
     const float* wp = p.w[which];
-    Turns t;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) t.set<kPairs>(e, wp, run0, run1, turns_here ? cs[e] : 1.f, turns_here ? sn[e] : 0.f);
 #pragma unroll 1
     for (int i0 = i_lo; i0 < i_hi; i0 += kUnroll) {
       uint4 a[kUnroll], b[kUnroll];
@@ -194,8 +199,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) rotate_kernel(const Rotate
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         const int h = (i0 + u) * HPI + sub;
-        turn_row<D, kPairs>(a[u], b[u], wp != nullptr, p.eps, turns_here, t, i0 + u < i_hi && h < heads,
-                            y + h * p.yh[which], run0, run1);
+        turn_row<D, kPairs>(a[u], b[u], wp != nullptr, p.eps, turns_here, cs, sn, w_s + which * 4 * LPH + j,
+                              i0 + u < i_hi && h < heads, y + h * p.yh[which], run0, run1);
       }
     }
   }
@@ -205,9 +210,11 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) rotate_kernel(const Rotate
 // token's angles; a warp that took one token's heads side by side would leave lanes idle and spend most of its time on
 // angles. q's and k's rows are dealt to different warps.
 template <int D, bool kPairs>
-__global__ void __launch_bounds__(kWarps * 32, kTokenCtas) rotate_tokens_kernel(const RotateParams p) {
+__global__ void __launch_bounds__(kWarps * 32, kCtas) rotate_tokens_kernel(const RotateParams p) {
   constexpr int LPH = D / 16, TPW = 32 / LPH;
+  __shared__ float4 w_s[2 * 4 * LPH];
   pdl_wait();
+  load_weights<LPH>(p, w_s);
   const int lane = threadIdx.x & 31;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   if (item >= p.n_items) return;
@@ -234,22 +241,21 @@ __global__ void __launch_bounds__(kWarps * 32, kTokenCtas) rotate_tokens_kernel(
     }
   };
   request(lo);  // on their way while the angles are worked out
-  const float* w = p.w[which];
   const uint64_t pos = turns_here && live ? static_cast<uint64_t>(static_cast<int64_t>(p.pos[tok])) : 0;
-  Turns t;
+  float cs[8], sn[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    float c = 1.f, s = 0.f;
-    if (turns_here) angle(p.turns, kPairs ? (e < 4 ? 4 * run0 + e : 4 * run1 + e - 4) : 8 * run0 + e, pos, c, s);
-    t.set<kPairs>(e, w, run0, run1, c, s);
+    cs[e] = 1.f;
+    sn[e] = 0.f;
+    if (turns_here) angle(p.turns, kPairs ? (e < 4 ? 4 * run0 + e : 4 * run1 + e - 4) : 8 * run0 + e, pos, cs[e], sn[e]);
   }
 #pragma unroll 1
   for (int h0 = lo; h0 < hi; h0 += kUnroll) {
     if (h0 > lo) request(h0);
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
-      turn_row<D, kPairs>(a[u], b[u], w != nullptr, p.eps, turns_here, t, live && h0 + u < hi, y + (h0 + u) * yh, run0,
-                          run1);
+      turn_row<D, kPairs>(a[u], b[u], p.w[which] != nullptr, p.eps, turns_here, cs, sn,
+                          w_s + which * 4 * LPH + lane % LPH, live && h0 + u < hi, y + (h0 + u) * yh, run0, run1);
   }
 }
 
