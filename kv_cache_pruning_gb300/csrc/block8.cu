@@ -33,7 +33,7 @@ namespace {
 // number of its rows in the low 5 bits (an index is below 2^27).
 size_t prep_bytes(int64_t BH, int NS) { return (compact_ws_bytes(BH, NS) + 15) & ~static_cast<size_t>(15); }
 size_t block8_ws_bytes(int64_t BH, int NS, int n_pages_cap) {
-  return prep_bytes(BH, NS) + 16 + static_cast<size_t>(n_pages_cap) * sizeof(int2);
+  return prep_bytes(BH, NS) + 16 + static_cast<size_t>(n_pages_cap) * sizeof(uint2);
 }
 
 // ------------------------------------------------------------------ count pass
@@ -81,7 +81,7 @@ template <bool kFused>
 __global__ void __launch_bounds__(kWarpsPerCta * 32) list_kernel(
     MaskedSrc src, int now, int NS, int table_share, int reserve, int max_pages, int n_pages_cap, int BH, CompactWs ws,
     const int32_t* count, int32_t* status, int32_t* expire_pool, int32_t* page_table, int32_t* remap, int32_t* n_used,
-    int2* owner) {
+    uint2* owner) {
   pdl_launch_dependents();
   pdl_wait();
   const int bh = blockIdx.x;  // pairs vary fastest: CTAs resident together read the same positions of all heads
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32) list_kernel(
   const int p_hi = p_lo + min(table_share, max_pages - p_lo);
   for (int p = p_lo + lane; p < p_hi; p += 32) {
     page_table[static_cast<int64_t>(bh) * max_pages + p] = p < pages ? base + p : -1;
-    if (p < pages) owner[base + p] = make_int2(bh, p << 5 | min(max(cnt - p * kPage, 0), kPage));
+    if (p < pages) owner[base + p] = make_uint2(bh, static_cast<uint32_t>(p) << 5 | min(max(cnt - p * kPage, 0), kPage));
   }
   for (int64_t j = max(p_lo * kPage, cnt) + lane; j < p_hi * kPage; j += 32) remap_bh[j] = -1;
 
@@ -192,7 +192,7 @@ KVP_DEV uint32_t largest(const uint4 (&w)[NI]) {
 template <int D, int FMT>
 __global__ void __launch_bounds__(kPageWarps * 32, kPageCtas) page_kernel(
     const uint16_t* k, const uint16_t* v, int64_t sb, int64_t st, int64_t sh, int H,
-    const int32_t* n_used, const int2* owner, int max_pages,
+    const int32_t* n_used, const uint2* owner, int max_pages,
     const int32_t* remap, uint8_t* kq_pool, uint8_t* vq_pool,
     float2* scale_pool, int32_t* expire_pool) {
   constexpr int LPR = D / 8;          // lanes a row takes, 16 bytes each
@@ -203,15 +203,15 @@ __global__ void __launch_bounds__(kPageWarps * 32, kPageCtas) page_kernel(
   const int total = *n_used, step = gridDim.x * kPageWarps;
   // a page's owner is read two pages ahead and its rows' positions one page ahead, so that only the rows are waited for
   const int first = blockIdx.x * kPageWarps + (threadIdx.x >> 5);
-  auto owner_of = [&](int64_t pg) { return pg < total ? owner[pg] : make_int2(0, 0); };
-  auto position_of = [&](int2 ow) {  // lane r: the position of row r
-    return lane < (ow.y & 31) ? remap[(static_cast<int64_t>(ow.x) * max_pages + (ow.y >> 5)) * kPage + lane] : 0;
+  auto owner_of = [&](int64_t pg) { return pg < total ? owner[pg] : make_uint2(0, 0); };
+  auto position_of = [&](uint2 ow) {  // lane r: the position of row r
+    return lane < static_cast<int>(ow.y & 31u) ? remap[(static_cast<int64_t>(ow.x) * max_pages + (ow.y >> 5)) * kPage + lane] : 0;
   };
-  int2 ow = owner_of(first), ow_next = owner_of(static_cast<int64_t>(first) + step);
+  uint2 ow = owner_of(first), ow_next = owner_of(static_cast<int64_t>(first) + step);
   int32_t mine = position_of(ow);
   for (int64_t pg = first; pg < total; pg += step) {
-    const int b = ow.x / H, h = ow.x - b * H;
-    const int n = ow.y & 31;
+    const int b = static_cast<int>(ow.x) / H, h = static_cast<int>(ow.x) - b * H;
+    const int n = static_cast<int>(ow.y & 31u);
     const int64_t off = b * sb + h * sh + piece * 8;
     uint4 kw[NI], vw[NI];
 #pragma unroll
@@ -438,7 +438,7 @@ kvp_status launch_compact(const MaskedSrc& src, int BH, int NS, int now, int res
                           int32_t* status, cudaStream_t st) {
   const CompactWs ws = carve(workspace, BH, NS);
   int32_t* n_used = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + prep_bytes(BH, NS));
-  int2* owner = reinterpret_cast<int2*>(n_used + 4);
+  uint2* owner = reinterpret_cast<uint2*>(n_used + 4);
   int device = 0;
   const int sms = current_sms(&device);
   if (sms == 0) return KVP_ERR_CUDA;
@@ -465,7 +465,7 @@ kvp_status launch_compact(const MaskedSrc& src, int BH, int NS, int now, int res
   const int64_t need = (most < n_pages_cap ? most : n_pages_cap) / kPageWarps + 1;
   const int grid = static_cast<int>(need < sms * kPageCtas ? need : sms * kPageCtas);
   if (launch_pdl(page_kernel<D, FMT>, dim3(grid), dim3(kPageWarps * 32), 0, st, src.k, src.v, src.sb, src.st, src.sh,
-                 src.H, static_cast<const int32_t*>(n_used), static_cast<const int2*>(owner), max_pages,
+                 src.H, static_cast<const int32_t*>(n_used), static_cast<const uint2*>(owner), max_pages,
                  static_cast<const int32_t*>(remap), kq_pool, vq_pool, reinterpret_cast<float2*>(scale_pool),
                  expire_pool) != cudaSuccess)
     return KVP_ERR_CUDA;

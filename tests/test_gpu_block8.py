@@ -427,6 +427,49 @@ def test_attention_of_many_short_heads(kvp, fmt):
     assert not out[0, :8].any() and torch.isneginf(lse[0, :8]).all()
 
 
+@pytest.mark.parametrize("fmt,d,G", [(ref.E4M3, 128, 8), (ref.INT8, 64, 3)])
+def test_attention_of_the_most_heads(kvp, fmt, d, G):
+    """4,096 (b, h), the most a call takes."""
+    cache, heads, now = _build(kvp, fmt, 115, 64, 3, 64, d)
+    cache.count[5, 7:40] = 0
+    for h in range(7, 40):
+        heads[5][h] = ref.Head(d, fmt)
+    _attend(kvp, cache, heads, _bits(116, (64, 64 * G, d)), now)
+
+
+@pytest.mark.parametrize("fmt,d,G", [(ref.E4M3, 128, 4), (ref.INT8, 64, 6)])
+def test_attention_of_one_long_head(kvp, fmt, d, G):
+    """2,500 pages of one (b, h): over many CTAs, over a few, and 157 a warp in one."""
+    cache, heads, now = _build(kvp, fmt, 117, 1, 40000, 1, d, keep_all=True)
+    q = _bits(118, (1, G, d))
+    for limit in (0, 5, 1):
+        _attend(kvp, cache, heads, q, now, grid_limit=limit)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_attention_writes_its_outputs_only(kvp, fmt):
+    """Guard values around the output, the log-sum-exps, the workspace and the cache's buffers."""
+    cache, heads, now = _build(kvp, fmt, 119, 2, 700, 3, 64)
+    before = [t.clone() for t in (cache.kq_pool, cache.vq_pool, cache.scale_pool, cache.expire_pool, cache.page_table,
+                                  cache.count)]
+    q = _bits(120, (2, 15, 64))
+    need = kvp.kvp_decode_attn_block8_workspace_bytes(2, 15, 3, 64)
+    out, lse = torch.full((2 * 15 * 64 + 256,), 7.0, device="cuda"), torch.full((2 * 15 + 64,), 7.0, device="cuda")
+    ws = torch.full((need + 512,), 0x5A, dtype=torch.uint8, device="cuda")
+    ws[256:256 + need] = 0
+    o, l = out[128:128 + 1920].view(2, 15, 64), lse[32:62].view(2, 15)
+    for limit in (0, 4):
+        kvp.kvp_decode_attn_block8(dev_bf16(q), cache, now, out=o, lse=l, workspace=ws[256:256 + need], grid_limit=limit)
+        torch.cuda.synchronize()
+        _compare(o, l, heads, ref.widen(q), now, 1 / 8, 5)
+        assert (out[:128] == 7).all() and (out[128 + 1920:] == 7).all() and (lse[:32] == 7).all() and (lse[62:] == 7).all()
+        assert (ws[:256] == 0x5A).all() and (ws[256 + need:] == 0x5A).all()
+        assert not ws[256:256 + 24].any()                # the arrival counters are back at zero
+    for a, b in zip(before, (cache.kq_pool, cache.vq_pool, cache.scale_pool, cache.expire_pool, cache.page_table,
+                             cache.count)):
+        assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("G", [1, 4, 7])
 def test_attention_masks(kvp, fmt, G):
