@@ -189,71 +189,206 @@ KVP_DEV uint32_t largest(const uint4 (&w)[NI]) {
   return __reduce_max_sync(0xffffffffu, max(a & 0xFFFFu, a >> 16));
 }
 
+// A page's K and V rows in a warp's registers, 16 bytes of a row a lane.
+template <int D>
+struct PageRows {
+  static constexpr int LPR = D / 8;      // lanes a row takes
+  static constexpr int RPI = 32 / LPR;   // rows a warp instruction takes
+  static constexpr int NI = kPage / RPI;
+  uint4 k[NI], v[NI];
+  // rows r < n at base + position * st, lane r holding row r's position; the others zero
+  KVP_DEV void load(const uint16_t* kb, const uint16_t* vb, int64_t st, int32_t position, int n, int lane) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int r = i * RPI + lane / LPR;
+      const int64_t at = __shfl_sync(0xffffffffu, position, r) * st + lane % LPR * 8;
+      k[i] = v[i] = make_uint4(0, 0, 0, 0);
+      if (r < n) {
+        k[i] = *reinterpret_cast<const uint4*>(kb + at);
+        v[i] = *reinterpret_cast<const uint4*>(vb + at);
+      }
+    }
+  }
+  // codes and scales to page pg, and expire 0 to its rows from n on
+  template <int FMT>
+  KVP_DEV void store(int64_t pg, int n, uint8_t* kq_pool, uint8_t* vq_pool, float2* scale_pool, int32_t* expire_pool,
+                     int lane) const {
+    // the largest magnitudes, as bf16 bits; only a page that holds infinities or NaNs looks at them one by one
+    uint32_t ka = largest<NI, false>(k), va = largest<NI, false>(v);
+    const bool odd = ka >= 0x7F80u || va >= 0x7F80u;
+    if (odd) {
+      ka = largest<NI, true>(k);
+      va = largest<NI, true>(v);
+    }
+    const uint32_t ks = scale_bits_for<FMT>(ka), vs = scale_bits_for<FMT>(va);
+    const float ki = inverse_of_scale(ks), vi = inverse_of_scale(vs);
+    const int64_t row0 = pg * kPage;
+    uint8_t* kd = kq_pool + (row0 + lane / LPR) * D + lane % LPR * 8;
+    uint8_t* vd = vq_pool + (row0 + lane / LPR) * D + lane % LPR * 8;
+    if (!odd) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        *reinterpret_cast<uint2*>(kd + i * RPI * D) = encode8_finite<FMT>(k[i], ki);
+        *reinterpret_cast<uint2*>(vd + i * RPI * D) = encode8_finite<FMT>(v[i], vi);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        *reinterpret_cast<uint2*>(kd + i * RPI * D) = encode8<FMT>(k[i], ki);
+        *reinterpret_cast<uint2*>(vd + i * RPI * D) = encode8<FMT>(v[i], vi);
+      }
+    }
+    if (lane == 0) scale_pool[pg] = make_float2(__uint_as_float(ks), __uint_as_float(vs));
+    if (lane >= n && lane < kPage) expire_pool[row0 + lane] = 0;
+  }
+};
+
 template <int D, int FMT>
 __global__ void __launch_bounds__(kPageWarps * 32, kPageCtas) page_kernel(
-    const uint16_t* k, const uint16_t* v, int64_t sb, int64_t st, int64_t sh, int H,
-    const int32_t* n_used, const uint2* owner, int max_pages,
-    const int32_t* remap, uint8_t* kq_pool, uint8_t* vq_pool,
-    float2* scale_pool, int32_t* expire_pool) {
-  constexpr int LPR = D / 8;          // lanes a row takes, 16 bytes each
-  constexpr int RPI = 32 / LPR;       // rows a warp instruction takes
-  constexpr int NI = kPage / RPI;
+    const uint16_t* k, const uint16_t* v, int64_t sb, int64_t st, int64_t sh, int H, const int32_t* n_used,
+    const uint2* owner, int max_pages, const int32_t* remap, uint8_t* kq_pool, uint8_t* vq_pool, float2* scale_pool,
+    int32_t* expire_pool) {
   pdl_wait();
-  const int lane = threadIdx.x & 31, piece = lane % LPR, sub = lane / LPR;
+  const int lane = threadIdx.x & 31;
   const int total = *n_used, step = gridDim.x * kPageWarps;
   // a page's owner is read two pages ahead and its rows' positions one page ahead, so that only the rows are waited for
   const int first = blockIdx.x * kPageWarps + (threadIdx.x >> 5);
   auto owner_of = [&](int64_t pg) { return pg < total ? owner[pg] : make_uint2(0, 0); };
   auto position_of = [&](uint2 ow) {  // lane r: the position of row r
-    return lane < static_cast<int>(ow.y & 31u) ? remap[(static_cast<int64_t>(ow.x) * max_pages + (ow.y >> 5)) * kPage + lane] : 0;
+    return lane < static_cast<int>(ow.y & 31u)
+               ? remap[(static_cast<int64_t>(ow.x) * max_pages + (ow.y >> 5)) * kPage + lane]
+               : 0;
   };
   uint2 ow = owner_of(first), ow_next = owner_of(static_cast<int64_t>(first) + step);
   int32_t mine = position_of(ow);
   for (int64_t pg = first; pg < total; pg += step) {
     const int b = static_cast<int>(ow.x) / H, h = static_cast<int>(ow.x) - b * H;
     const int n = static_cast<int>(ow.y & 31u);
-    const int64_t off = b * sb + h * sh + piece * 8;
-    uint4 kw[NI], vw[NI];
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int r = i * RPI + sub;
-      const int64_t at = off + __shfl_sync(0xffffffffu, mine, r) * st;
-      kw[i] = vw[i] = make_uint4(0, 0, 0, 0);
-      if (r < n) {
-        kw[i] = *reinterpret_cast<const uint4*>(k + at);
-        vw[i] = *reinterpret_cast<const uint4*>(v + at);
-      }
-    }
+    const int64_t off = b * sb + h * sh;
+    PageRows<D> rows;
+    rows.load(k + off, v + off, st, mine, n, lane);
     ow = ow_next;
     mine = position_of(ow);
     ow_next = owner_of(pg + 2 * static_cast<int64_t>(step));
-    // the largest magnitudes, as bf16 bits; only a page that holds infinities or NaNs looks at them one by one
-    uint32_t ka = largest<NI, false>(kw), va = largest<NI, false>(vw);
-    const bool odd = ka >= 0x7F80u || va >= 0x7F80u;
-    if (odd) {
-      ka = largest<NI, true>(kw);
-      va = largest<NI, true>(vw);
-    }
-    const uint32_t ks = scale_bits_for<FMT>(ka), vs = scale_bits_for<FMT>(va);
-    const float ki = inverse_of_scale(ks), vi = inverse_of_scale(vs);
-    const int64_t row0 = pg * kPage;
-    uint8_t* kd = kq_pool + (row0 + sub) * D + piece * 8;
-    uint8_t* vd = vq_pool + (row0 + sub) * D + piece * 8;
-    if (!odd) {
+    rows.template store<FMT>(pg, n, kq_pool, vq_pool, scale_pool, expire_pool, lane);
+  }
+}
+
+// ------------------------------------------------------------------ short prompts
+// The whole write in one launch, a CTA for each (b, h): it counts every (b, h)'s present entries itself (which is
+// why all their positions together are few), lists its own and quantises its pages. Such calls are bound by the host's
+// launches: in us a call (on the device alone), one launch / four, measured on a GB300 with heads of 128, half kept:
+// 2 x 317 positions 12.0 (6.2) / 19.1 (7.1), 8 x 512 11.7 (7.5) / 19.1 (8.0), 32 x 256 10.4 (6.5) / 17.8 (8.0), 8 x 1000
+// 11.8 (11.2) / 19.3 (8.2), 128 x 128 10.8 (10.3) / 17.7 (8.7), 64 x 250 13.2 (13.2) / 17.8 (9.2); above kShortRounds
+// rounds of counting it loses: 512 x 30 63 / 18.
+constexpr int kShortWarps = 16;
+constexpr int kShortPositions = 1024;   // of a (b, h): its pages are one CTA's work
+constexpr int kShortRounds = 8;         // of counting, 8 loads a lane each
+
+// Present entries among a lane's positions lane, lane + 32, .. below n: their scores (or flags) loaded eight at a time.
+template <class Load, class Expire>
+KVP_DEV int present_among(int n, int lane, int now, Load load, Expire expire) {
+  int kept = 0;
+  for (int t0 = lane; t0 < n; t0 += 256) {
+    decltype(load(0)) x[8];
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        *reinterpret_cast<uint2*>(kd + i * RPI * D) = encode8_finite<FMT>(kw[i], ki);
-        *reinterpret_cast<uint2*>(vd + i * RPI * D) = encode8_finite<FMT>(vw[i], vi);
-      }
-    } else {
+    for (int u = 0; u < 8; ++u) x[u] = t0 + 32 * u < n ? load(t0 + 32 * u) : decltype(load(0)){};
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        *reinterpret_cast<uint2*>(kd + i * RPI * D) = encode8<FMT>(kw[i], ki);
-        *reinterpret_cast<uint2*>(vd + i * RPI * D) = encode8<FMT>(vw[i], vi);
-      }
+    for (int u = 0; u < 8; ++u) kept += t0 + 32 * u < n && now < expire(x[u], t0 + 32 * u);
+  }
+  return kept;
+}
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(kShortWarps * 32, 1) short_kernel(MaskedSrc src, int now, int reserve, int max_pages,
+                                                                    int n_pages_cap, int BH, uint8_t* kq_pool,
+                                                                    uint8_t* vq_pool, float2* scale_pool,
+                                                                    int32_t* expire_pool, int32_t* page_table,
+                                                                    int32_t* remap, int32_t* count, int32_t* status) {
+  constexpr int kThreads = kShortWarps * 32, kChunks = kShortPositions / 32;
+  __shared__ int32_t count_s[kFusedBH];
+  __shared__ int32_t list_s[kShortPositions];
+  __shared__ int32_t chunk_s[kChunks];
+  __shared__ int3 red_s[kShortWarps];
+  pdl_wait();
+  const int bh = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int n = src.n;
+  // ---- every (b, h)'s count, a warp each
+  for (int i = warp; i < BH; i += kShortWarps) {
+    const auto sv = src.view(i);
+    int kept = src.mode == KVP_MASK_KVZAP
+                   ? present_among(n, lane, now, [&](int t) { return sv.sc[static_cast<int64_t>(t) * sv.H]; },
+                                   [&](float x, int t) { return expire_kvzap(x, sv.th, t, sv.window); })
+                   : present_among(n, lane, now, [&](int t) { return sv.fl[t]; },
+                                   [&](int x, int t) { return expire_dms(x, t, sv.delay, sv.window); });
+    kept = __reduce_add_sync(0xffffffffu, kept);
+    if (lane == 0) count_s[i] = kept;
+  }
+  __syncthreads();
+  // ---- this (b, h)'s first page and the budget (page sums stay below 2^31: checked on the host)
+  int before = 0, total = 0, most = 0;
+  for (int i = tid; i < BH; i += kThreads) {
+    const int pg = (count_s[i] + reserve + kPage - 1) / kPage;
+    before += i < bh ? pg : 0;
+    total += pg;
+    most = max(most, pg);
+  }
+  before = __reduce_add_sync(0xffffffffu, before);
+  total = __reduce_add_sync(0xffffffffu, total);
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 0) red_s[warp] = make_int3(before, total, most);
+  // ---- its present entries, by chunks of 32 positions: first how many, then where
+  const auto sv = src.view(bh);
+  constexpr int kMine = kChunks / kShortWarps;
+  int32_t e[kMine];
+  unsigned bal[kMine];
+#pragma unroll
+  for (int c = 0; c < kMine; ++c) {
+    const int t = (warp * kMine + c) * 32 + lane;
+    int64_t row;
+    e[c] = t < n ? sv.expire_row(t, row) : 0;
+    bal[c] = __ballot_sync(0xffffffffu, t < n && sv.keep(e[c], now));
+    if (lane == 0) chunk_s[warp * kMine + c] = __popc(bal[c]);
+  }
+  __syncthreads();
+  before = total = most = 0;
+#pragma unroll
+  for (int w = 0; w < kShortWarps; ++w) {
+    before += red_s[w].x;
+    total += red_s[w].y;
+    most = max(most, red_s[w].z);
+  }
+  const int cnt = count_s[bh];
+  if (tid == 0) count[bh] = cnt;
+  if (most > max_pages || total > n_pages_cap) {
+    if (bh == 0 && tid == 0) record_error(status, KVP_ERR_CAPACITY);
+    return;
+  }
+  const int base = before, pages = (cnt + reserve + kPage - 1) / kPage;
+  int32_t* remap_bh = remap + static_cast<int64_t>(bh) * max_pages * kPage;
+#pragma unroll
+  for (int c = 0; c < kMine; ++c) {
+    const int chunk = warp * kMine + c;
+    const int slot0 = __reduce_add_sync(0xffffffffu, lane < chunk ? chunk_s[lane] : 0);
+    if ((bal[c] >> lane) & 1u) {
+      const int j = slot0 + __popc(bal[c] & ((1u << lane) - 1u));
+      list_s[j] = chunk * 32 + lane;
+      remap_bh[j] = chunk * 32 + lane;
+      expire_pool[static_cast<int64_t>(base + (j >> 4)) * kPage + (j & 15)] = e[c];
     }
-    if (lane == 0) scale_pool[pg] = make_float2(__uint_as_float(ks), __uint_as_float(vs));
-    if (lane >= n && lane < kPage) expire_pool[row0 + lane] = 0;
+  }
+  for (int p = tid; p < max_pages; p += kThreads)
+    page_table[static_cast<int64_t>(bh) * max_pages + p] = p < pages ? base + p : -1;
+  for (int64_t j = cnt + tid; j < static_cast<int64_t>(max_pages) * kPage; j += kThreads) remap_bh[j] = -1;
+  __syncthreads();
+  // ---- its pages, a warp each
+  const int b = bh / src.H, h = bh - b * src.H;
+  const int64_t off = b * src.sb + h * src.sh;
+  for (int p = warp; p < pages; p += kShortWarps) {
+    const int m = min(max(cnt - p * kPage, 0), kPage);
+    PageRows<D> rows;
+    rows.load(src.k + off, src.v + off, src.st, lane < m ? list_s[p * kPage + lane] : 0, m, lane);
+    rows.template store<FMT>(base + p, m, kq_pool, vq_pool, scale_pool, expire_pool, lane);
   }
 }
 
@@ -436,6 +571,14 @@ kvp_status launch_compact(const MaskedSrc& src, int BH, int NS, int now, int res
                           uint8_t* vq_pool, float* scale_pool, int32_t* expire_pool, int n_pages_cap,
                           int32_t* page_table, int max_pages, int32_t* remap, int32_t* count, void* workspace,
                           int32_t* status, cudaStream_t st) {
+  if (BH <= kFusedBH && src.n <= kShortPositions &&
+      (BH + kShortWarps - 1) / kShortWarps * ((src.n + 255) / 256) <= kShortRounds) {
+    return launch_pdl(short_kernel<D, FMT>, dim3(BH), dim3(kShortWarps * 32), 0, st, src, now, reserve, max_pages,
+                      n_pages_cap, BH, kq_pool, vq_pool, reinterpret_cast<float2*>(scale_pool), expire_pool, page_table,
+                      remap, count, status) == cudaSuccess
+               ? KVP_OK
+               : KVP_ERR_CUDA;
+  }
   const CompactWs ws = carve(workspace, BH, NS);
   int32_t* n_used = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + prep_bytes(BH, NS));
   uint2* owner = reinterpret_cast<uint2*>(n_used + 4);

@@ -137,6 +137,11 @@ def _compare(out, lse, heads, q, now, scale, G):
     (0, 2, 700, 4, 128, 128, 0, 5),
     (1, 1, 1300, 2, 128, 128, 50, 0),
     (0, 520, 37, 2, 64, 3, 0, 2),        # above 1,024 (b, h): the separate page-base pass
+    (0, 1, 1024, 32, 128, 30, 0, 3),     # the most a single launch takes
+    (0, 64, 256, 2, 64, 30, 0, 3),
+    (1, 1, 1025, 3, 64, 30, 5, 40),      # a position more: the passes
+    (0, 129, 110, 1, 64, 20, 0, 0),      # a (b, h) more: the passes
+    (1, 2, 1537, 5, 128, 0, 0, 17),
 ])
 def test_bulk_write_is_bit_exact(kvp, fmt, mode, B, T, H, d, window, delay, reserve):
     now = T - 1
@@ -222,10 +227,11 @@ def test_bulk_write_of_unusual_values(kvp, fmt):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
-def test_bulk_writes_back_to_back(kvp, fmt):
+@pytest.mark.parametrize("T", [200, 1040])
+def test_bulk_writes_back_to_back(kvp, fmt, T):
     """Many writes one behind the other, each into memory that the ones before it used, inputs made just before: every
     pass sees what the launches before it wrote."""
-    T, H, d = 200, 2, 64
+    H, d = 2, 64
     made = []
     for seed in (0, 1):
         k, v, sc = _bits(401 + seed, (1, T, H, d), 3), _bits(403 + seed, (1, T, H, d), 3), syn.normal_f32(seed, 405, (1, T, H))
@@ -233,7 +239,7 @@ def test_bulk_writes_back_to_back(kvp, fmt):
         made.append((k, v, sc, heads))
     for i in range(60):
         k, v, sc, heads = made[i % 2]
-        cache = _alloc(kvp, 1, H, d, 13 * H, 13, fmt)
+        cache = _alloc(kvp, 1, H, d, 69 * H, 69, fmt)
         st = status_word()
         kvp.kvp_compact_block8(dev_bf16(k), dev_bf16(v), T - 1, 0, cache, mode=0, scores=dev_f32(sc),
                                tau=torch.zeros(1, H, device="cuda"), window=40, status=st)
@@ -271,11 +277,13 @@ def test_steps_back_to_back_give_the_bits_of_steps_apart(kvp, fmt):
         assert torch.equal(a, b)
 
 
-def test_bulk_write_records_a_full_pool(kvp):
-    B, T, H, d = 2, 100, 2, 64
+@pytest.mark.parametrize("B,T", [(2, 100), (2, 1100), (600, 20)])     # one launch, the passes, the page-base pass
+def test_bulk_write_records_a_full_pool(kvp, B, T):
+    H, d = 2, 64
+    each = (T + 15) // 16
     k = dev_bf16(_bits(41, (B, T, H, d)))
     flag = torch.full((B, H, T), -1, dtype=torch.int32, device="cuda")
-    for cap, width in ((27, 7), (28, 6)):      # one page short; a table one page short
+    for cap, width in ((B * H * each - 1, each), (B * H * each, each - 1)):      # one page short; a table one page short
         cache = _alloc(kvp, B, H, d, cap, width, 0)
         st = status_word()
         kvp.kvp_compact_block8(k, k, T - 1, 0, cache, mode=1, flag_step=flag, status=st)
