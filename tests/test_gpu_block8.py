@@ -591,7 +591,7 @@ def test_attention_of_bad_pages(kvp, fmt):
 def test_attention_past_32_bit_offsets(kvp):
     """Pools of more than 2^32 bytes, the pages in use at their end."""
     cap, d = 2_200_000, 128                            # 4.5 GB each
-    small, heads, now = _build(kvp, 1, 161, 1, 300, 2, d)
+    small, heads, now = _build(kvp, 1, 161, 1, 300, 2, d, reserve=4)
     big = _alloc(kvp, 1, 2, d, cap, small.max_pages, 1)
     n = small.n_pages_cap
     for a, b in ((big.kq_pool, small.kq_pool), (big.vq_pool, small.vq_pool), (big.scale_pool, small.scale_pool),
@@ -605,6 +605,16 @@ def test_attention_past_32_bit_offsets(kvp):
     k, v = kvp.kvp_read_block8(big, 0, 60)
     k2, v2 = kvp.kvp_read_block8(small, 0, 60)
     assert torch.equal(k, k2) and torch.equal(v, v2)
+    st, flag = status_word(), torch.full((1, 2), -1, dtype=torch.int32, device="cuda")
+    for i in range(3):                                 # larger and larger: the page's rows are rounded anew
+        x = dev_bf16(_bits(163, (1, 2, d))) * 4.0**i
+        for c in (big, small):
+            kvp.kvp_append_block8(c, x, x, now + 1 + i, mode=1, flag_step=flag, status=st)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    for a, b in ((big.kq_pool, small.kq_pool), (big.vq_pool, small.vq_pool), (big.scale_pool, small.scale_pool),
+                 (big.expire_pool, small.expire_pool)):
+        assert torch.equal(a[cap - n:], b)
 
 
 @pytest.mark.parametrize("fmt", FMTS)
@@ -651,6 +661,24 @@ def test_two_streams_with_their_own_workspaces(kvp):
         _compare(*outs[i][0], made[i][1], ref.widen(q[i]), made[i][2], 1 / math.sqrt(128), 4)
         for o, l in outs[i][1:]:
             assert torch.equal(o, outs[i][0][0]) and torch.equal(l, outs[i][0][1])
+
+
+def test_calls_on_a_raw_stream(kvp):
+    """A stream given as its handle: outputs and workspaces that the binding makes belong to it."""
+    cache, heads, now = _build(kvp, 0, 187, 2, 400, 4, 64)
+    q = _bits(188, (2, 8, 64))
+    qd = dev_bf16(q)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs = [kvp.kvp_decode_attn_block8(qd, cache, now, stream=s.cuda_stream) for _ in range(10)]
+    k, v = kvp.kvp_read_block8(cache, 0, 30, stream=s.cuda_stream)
+    r, _ = kvp.kvp_qk_norm_rope(qd, None, None, None, stream=s.cuda_stream)
+    torch.cuda.synchronize()
+    lse = torch.empty(2, 8, device="cuda")
+    _compare(kvp.kvp_decode_attn_block8(qd, cache, now, lse=lse), lse, heads, ref.widen(q), now, 1 / 8, 2)
+    want = kvp.kvp_decode_attn_block8(qd, cache, now)
+    assert all(torch.equal(o, want) for o in outs) and torch.equal(r, qd)
+    assert torch.equal(k, kvp.kvp_read_block8(cache, 0, 30)[0])
 
 
 @pytest.mark.parametrize("fmt", FMTS)
