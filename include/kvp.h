@@ -813,8 +813,9 @@ KVP_API kvp_status kvp_read_block8(int fmt, int batch, int n_kv_heads, int head_
  *            as kvp_decode_attn
  * workspace  device, >= kvp_decode_attn_block8_workspace_bytes(...), 16-byte
  *            aligned, zero-filled before its first use; every call, also one
- *            that records an error, leaves it ready for the next. Calls that
- *            share a workspace must not overlap on the GPU.
+ *            that records an error, leaves it ready for the next, of whatever
+ *            sizes it is large enough for (but not for other entry points).
+ *            Calls that share a workspace must not overlap on the GPU.
  */
 KVP_API size_t kvp_decode_attn_block8_workspace_bytes(int batch, int n_q_heads, int n_kv_heads, int head_dim);
 KVP_API kvp_status kvp_decode_attn_block8(int fmt, int batch, int n_q_heads, int n_kv_heads, int head_dim,

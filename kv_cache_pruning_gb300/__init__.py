@@ -1069,7 +1069,7 @@ def kvp_decode_attn_block8(q, cache: Block8PagedKV, now, *, scale=0.0, out=None,
                            workspace=None, status=None, stream=None):
     """out[B, Hq, d] fp32 = attention of q [B, Hq, d] (bf16) over the slots of the 8-bit `cache` present at `now`; lse
     (fp32 [B, Hq], if given) receives each row's log-sum-exp, for kvp_attn_merge. A caller-provided workspace must be
-    zero-filled before its first use (torch.zeros); every call leaves it that way."""
+    zero-filled before its first use (torch.zeros); every call leaves it ready for the next one, of whatever sizes."""
     return _attn_block8(_lib.kvp_decode_attn_block8, q, cache, now, scale, out, lse, grid_limit, workspace, status,
                         stream)
 

@@ -248,8 +248,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block8_kernel(const Params p
   int at_page = incl - sum + __reduce_add_sync(0xffffffffu, lane < warp ? st.x : 0);
   most = __reduce_max_sync(0xffffffffu, st.y);
   least = __reduce_min_sync(0xffffffffu, st.z);
-  // A CTA for each (b, h), where there are enough of them and no (b, h) is much longer than an even share (or than
-  // kOwnPages): nothing to merge between CTAs. Otherwise all pages are dealt out evenly.
+  // A CTA for each (b, h), where there are enough of them and no (b, h) is much longer than an even share: nothing to
+  // merge between CTAs. Otherwise all pages are dealt out evenly.
   const bool own = p.BH <= static_cast<int>(gridDim.x) &&
                    most - total / static_cast<int>(gridDim.x) <= kOwnExtra;
   int ctas;
@@ -728,9 +728,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block8_kernel(const Params p
 
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-size_t counters_bytes(int64_t BH) { return static_cast<size_t>((BH * 4 + 15) & ~int64_t{15}); }
-size_t attn_ws_bytes(int64_t BH, int G, int D) {
-  return counters_bytes(BH) + static_cast<size_t>(2) * kMaxCtas * G * (D + 2) * sizeof(float);
+// The arrival counters of the most (b, h)s come first whatever a call's own number is, so that no call's partial results
+// lie where another call's counters have to be zero.
+constexpr size_t kCountersBytes = static_cast<size_t>(kMaxBH) * 4;
+size_t attn_ws_bytes(int G, int D) {
+  return kCountersBytes + static_cast<size_t>(2) * kMaxCtas * G * (D + 2) * sizeof(float);
 }
 
 template <int D, int FMT, bool kDup>
@@ -772,7 +774,7 @@ kvp_status attn_block8_impl(int fmt, int batch, int n_q_heads, int n_kv_heads, i
   if (!al16(q) || !al16(kq_pool) || !al16(vq_pool) || !al16(scale_pool) || !al16(out)) return KVP_ERR_ALIGN;
   if ((reinterpret_cast<uintptr_t>(now_dev) & 3u) != 0 || (reinterpret_cast<uintptr_t>(lse) & 3u) != 0)
     return KVP_ERR_ALIGN;
-  if (workspace == nullptr || workspace_bytes < attn_ws_bytes(BH, G, head_dim)) return KVP_ERR_WORKSPACE;
+  if (workspace == nullptr || workspace_bytes < attn_ws_bytes(G, head_dim)) return KVP_ERR_WORKSPACE;
   if (!al16(workspace)) return KVP_ERR_ALIGN;
   int device = 0;
   const int sms = current_sms(&device);
@@ -800,7 +802,7 @@ kvp_status attn_block8_impl(int fmt, int batch, int n_q_heads, int n_kv_heads, i
   p.out = out;
   p.lse = lse;
   p.arrived = static_cast<int32_t*>(workspace);
-  p.part_acc = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + counters_bytes(BH));
+  p.part_acc = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kCountersBytes);
   p.part_ml = p.part_acc + static_cast<size_t>(2) * kMaxCtas * G * head_dim;
   p.status = status;
   // bringing lines into L2 early pays while one instruction of each thread does it; a table with more lines than
@@ -828,7 +830,7 @@ extern "C" size_t kvp_decode_attn_block8_workspace_bytes(int batch, int n_q_head
   if (head_dim != 64 && head_dim != 128) return 0;
   const int64_t BH = static_cast<int64_t>(batch) * n_kv_heads;
   if (n_q_heads / n_kv_heads > 8 || BH > kMaxBH) return 0;
-  return attn_ws_bytes(BH, n_q_heads / n_kv_heads, head_dim);
+  return attn_ws_bytes(n_q_heads / n_kv_heads, head_dim);
 }
 
 extern "C" kvp_status kvp_decode_attn_block8(int fmt, int batch, int n_q_heads, int n_kv_heads, int head_dim,

@@ -454,6 +454,17 @@ def test_attention_of_one_long_head(kvp, fmt, d, G):
         _attend(kvp, cache, heads, q, now, grid_limit=limit)
 
 
+def test_one_workspace_for_calls_of_any_size(kvp):
+    """Few heads, many, and few again: no call's partial results lie where another's arrival counters are."""
+    few, few_heads, few_now = _build(kvp, ref.INT8, 127, 1, 4000, 1, 64, keep_all=True)
+    many, many_heads, many_now = _build(kvp, ref.E4M3, 128, 40, 300, 4, 128, keep_all=True)
+    ws = torch.zeros(max(kvp.kvp_decode_attn_block8_workspace_bytes(1, 8, 1, 64),
+                         kvp.kvp_decode_attn_block8_workspace_bytes(40, 16, 4, 128)), dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        _attend(kvp, few, few_heads, _bits(129, (1, 8, 64)), few_now, workspace=ws)
+        _attend(kvp, many, many_heads, _bits(130, (40, 16, 128)), many_now, workspace=ws)
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 def test_attention_writes_its_outputs_only(kvp, fmt):
     """Guard values around the output, the log-sum-exps, the workspace and the cache's buffers."""
