@@ -405,7 +405,7 @@ KVP_DEV uint32_t append_row(uint2 x, uint8_t* page, int r, uint32_t old, int lan
   a = __reduce_max_sync(0xffffffffu, max(a & 0xFFFFu, a >> 16));
   const uint32_t mine = scale_bits_for<FMT>(a);
   const uint32_t now = max(old, mine);  // positive floats order like their bits
-  if (now > old && old != 0) {          // the rows before this one take the larger scale (0: they are zero codes)
+  if (now > old) {  // the rows before this one take the larger scale (those of scale 0, infinities among them, become 0)
     const float ratio = __fdiv_rn(__uint_as_float(old), __uint_as_float(now));
     for (int i = lane; i < r * D / 16; i += 32) {
       uint4 w = reinterpret_cast<uint4*>(page)[i];

@@ -94,7 +94,7 @@ class Head:
                 self.scales[w].append(0.0)
             old = self.scales[w][-1]
             new = max(old, scale_of(x, self.fmt))
-            if r and new > old and old > 0:
+            if r and new > old:
                 rows = decode(self.codes[w][-r:], self.fmt) * (old / new)
                 self.codes[w][-r:] = encode(rows, 1.0, self.fmt)
             self.scales[w][-1] = new

@@ -328,6 +328,29 @@ def test_append_is_bit_exact(kvp, fmt, B, H, d, T):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+def test_append_to_a_page_of_zeros_and_infinities(kvp, fmt):
+    """A page without a finite value but zero has scale 0, where an infinity's code is worth 0 like any other; when a row
+    gives the page a scale, those rows stay worth 0 (and E4M3's NaN stays NaN)."""
+    d = 64
+    cache = _alloc(kvp, 1, 1, d, 1, 1, fmt)
+    cache.page_table.zero_()
+    x = np.zeros((4, 1, 1, d), np.uint16)
+    x[0, ..., 3], x[0, ..., 4], x[0, ..., 5] = 0x7F80, 0xFF80, 0x8000       # inf, -inf, -0
+    x[1, ..., 7] = 0x7FC0                                                    # NaN
+    x[2:] = _bits(73, (2, 1, 1, d))
+    heads = [[ref.Head(d, fmt)]]
+    flag, st = torch.full((1, 1), -1, dtype=torch.int32, device="cuda"), status_word()
+    for i in range(4):
+        kvp.kvp_append_block8(cache, dev_bf16(x[i]), dev_bf16(x[i]), i, mode=1, flag_step=flag, status=st)
+        w = ref.widen(x[i, 0, 0])
+        heads[0][0].append(w, w, ref.NEVER, i)
+        torch.cuda.synchronize()
+        _check_cache(cache, heads, fmt)
+        k, _ = kvp.kvp_read_block8(cache, 0, 2)
+        assert not k[0, 0].any() and st.item() == 0
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 def test_append_errors_leave_the_head_unchanged(kvp, fmt):
     B, H, d, T = 1, 5, 64, 20
     cache, heads, now = _build(kvp, fmt, 71, B, T, H, d, keep_all=True, reserve=16)
