@@ -784,7 +784,9 @@ KVP_API kvp_status kvp_append_block8_devpos(int fmt, int mode, int batch, int n_
  * KVP_ERR_BOUNDS and its slots give zero rows.
  *
  * k_out, v_out  device bf16, 16-byte aligned; strides in elements, multiples
- *            of 8, and at least head_dim along every dimension longer than 1
+ *            of 8; along a dimension longer than 1 a step clears a row and all
+ *            that the dimensions of smaller strides span, in whatever order
+ *            (rows that overlap are KVP_ERR_INVALID)
  * first_slot, n_slots  >= 0; n_slots 0 does nothing. Slots may lie past the
  *            page table.
  */
@@ -847,10 +849,11 @@ KVP_API kvp_status kvp_decode_attn_block8_devpos(int fmt, int batch, int n_q_hea
  *   i < rot_dim/2, is rotated by the angle pos[t] * inv_freq[i]; values from
  *   rot_dim on are y
  *
- * Everything in fp32, rounded to bf16 once at the end. Angles are exact to
- * about 2^-32 turns at every position: `turns` holds inv_freq[i] / (2 pi) as
- * 64-bit fixed-point fractions of a turn (kvp_rope_turns makes them, on the
- * host), and pos * turns is taken modulo one turn in 64-bit integers.
+ * Everything in fp32, rounded to bf16 once at the end. Angles are as good at
+ * every position (about 2^-26 of a turn, their fp32 form): `turns` holds
+ * inv_freq[i] / (2 pi) as 64-bit fixed-point fractions of a turn
+ * (kvp_rope_turns makes them, on the host), and pos * turns is taken modulo
+ * one turn in 64-bit integers.
  *
  * n_tok      tokens (>= 0; 0 does nothing)
  * n_q_heads, n_k_heads  >= 0, not both 0; q (k) may be NULL when its count is 0
@@ -863,9 +866,9 @@ KVP_API kvp_status kvp_decode_attn_block8_devpos(int fmt, int batch, int n_q_hea
  * wq, wk     device fp32 [head_dim] norm weights, 16-byte aligned, or NULL for no
  *            norm (of queries, of keys)
  * eps        >= 0, finite
- * q_out, k_out  as q, k, strides at least head_dim along every dimension longer
- *            than 1; each may be its input itself (same address and strides),
- *            and may not overlap an input otherwise
+ * q_out, k_out  as q, k, of strides whose rows do not overlap (as
+ *            kvp_read_block8's); each may be its input itself (same address and
+ *            strides), and may not overlap an input otherwise
  */
 KVP_API kvp_status kvp_rope_turns(int n, const double* inv_freq, uint64_t* turns);
 KVP_API kvp_status kvp_qk_norm_rope(int64_t n_tok, int n_q_heads, int n_k_heads, int head_dim, int rot_dim,

@@ -760,10 +760,7 @@ extern "C" kvp_status kvp_read_block8(int fmt, int batch, int n_kv_heads, int he
   if (n_slots == 0) return KVP_OK;
   if (k_out == nullptr || v_out == nullptr) return KVP_ERR_INVALID;
   if (!aligned16(k_out) || !aligned16(v_out) || stride_b % 8 || stride_t % 8 || stride_h % 8) return KVP_ERR_ALIGN;
-  // rows that two slots, heads or sequences share would be written twice
-  if ((batch > 1 && stride_b < head_dim) || (n_slots > 1 && stride_t < head_dim) ||
-      (n_kv_heads > 1 && stride_h < head_dim))
-    return KVP_ERR_INVALID;
+  if (!rows_apart({{{stride_b, batch}, {stride_t, n_slots}, {stride_h, n_kv_heads}}}, head_dim)) return KVP_ERR_INVALID;
   const int pages_each = (first_slot + n_slots - 1) / kPage - first_slot / kPage + 1;
   const int64_t items = static_cast<int64_t>(batch) * n_kv_heads * pages_each;
   const int64_t ctas = (items + kPageWarps - 1) / kPageWarps;

@@ -12,7 +12,10 @@
 // int8's range and lose half a step at every growth.
 #pragma once
 
+#include <algorithm>
+#include <array>
 #include <atomic>
+#include <utility>
 
 #include <cuda_fp16.h>
 
@@ -118,6 +121,20 @@ KVP_DEV uint32_t rescale4(uint32_t w, float ratio) {
   const float2 a = decode2<FMT>(w), b = decode2<FMT>(w >> 16);
   return encode2<FMT>(__fmul_rn(a.x, ratio), __fmul_rn(a.y, ratio)) |
          (encode2<FMT>(__fmul_rn(b.x, ratio), __fmul_rn(b.y, ratio)) << 16);
+}
+
+// Whether rows of `width` values that lie n[i] steps of stride[i] apart along three dimensions never overlap (each
+// dimension's steps clear everything that the dimensions of smaller strides span): a call that writes such rows twice,
+// in an order that nothing fixes, is refused. Dimensions of length 1 have no stride.
+inline bool rows_apart(std::array<std::pair<int64_t, int64_t>, 3> stride_n, int64_t width) {
+  std::sort(stride_n.begin(), stride_n.end());
+  int64_t span = width;
+  for (const auto& [stride, n] : stride_n) {
+    if (n <= 1) continue;
+    if (stride < span || stride > (INT64_MAX - span) / n) return false;
+    span += stride * (n - 1);
+  }
+  return true;
 }
 
 // SM count of the current device, whose number goes to *device (0 when it cannot be asked); asked once per device.

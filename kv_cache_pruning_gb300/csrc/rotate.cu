@@ -314,8 +314,7 @@ extern "C" kvp_status kvp_qk_norm_rope(int64_t n_tok, int n_q_heads, int n_k_hea
       if (s < 0) return KVP_ERR_INVALID;
       if (s % 8 != 0) return KVP_ERR_ALIGN;
     }
-    // rows that two tokens or heads share would be written twice
-    if ((n_tok > 1 && p.yt[i] < head_dim) || (p.heads[i] > 1 && p.yh[i] < head_dim)) return KVP_ERR_INVALID;
+    if (!rows_apart({{{p.yt[i], n_tok}, {p.yh[i], p.heads[i]}, {0, 1}}}, head_dim)) return KVP_ERR_INVALID;
     if (p.x[i] == p.y[i] && ((n_tok > 1 && p.xt[i] != p.yt[i]) || (p.heads[i] > 1 && p.xh[i] != p.yh[i])))
       return KVP_ERR_INVALID;
   }

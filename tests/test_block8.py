@@ -116,6 +116,10 @@ def test_read_refusals(k):
     assert call(first=2**31 - 20, n=4) == k.KVP_ERR_UNSUPPORTED
     assert call(ko=8) == k.KVP_ERR_ALIGN
     assert call(st=132) == k.KVP_ERR_ALIGN
+    # b 2, n 4, h 2 rows of 64: a slot's heads reach into the next slot, a sequence's slots into the next sequence
+    assert call(st=64) == k.KVP_ERR_INVALID
+    assert call(sb=448) == k.KVP_ERR_INVALID
+    assert call(sh=1 << 62) == k.KVP_ERR_INVALID
     assert call(n=0, ko=None) == k.KVP_OK       # nothing to do: nothing is launched
 
 
@@ -176,6 +180,8 @@ def test_rotation_refusals(k):
     assert call(qst=-8) == k.KVP_ERR_INVALID
     assert call(qot=120) == k.KVP_ERR_INVALID        # rows written twice
     assert call(qoh=0) == k.KVP_ERR_INVALID
+    assert call(qot=128) == k.KVP_ERR_INVALID        # a token's second head is the next token's first
+    assert call(qot=128, qoh=384) == k.KVP_ERR_INVALID
     assert call(qo=16, qot=512) == k.KVP_ERR_INVALID  # in place with other strides
     assert call(d=96) == k.KVP_ERR_UNSUPPORTED
     assert call(rot=24) == k.KVP_ERR_UNSUPPORTED
