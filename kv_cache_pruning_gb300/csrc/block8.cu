@@ -2,8 +2,8 @@
 // kvp_read_block8: writing and reading a paged cache held in 8 bits with one
 // scale per page (16 tokens of one (b, h)) for K and one for V.
 //
-// The bulk write runs three passes after zeroing the counts, each launched early
-// behind the one before it. The count pass counts the present entries of every
+// The bulk write of a short prompt is one launch (below); any other runs three
+// passes after zeroing the counts, each launched early behind the one before it. The count pass counts the present entries of every
 // 128-entry segment and (b, h). The list pass, one warp per segment, writes the
 // remapping list, the expire values and the page table, and names each page's
 // owner. The page pass gives one warp a page: it gathers the page's 16 K and V
@@ -18,10 +18,12 @@
 // with the list read page by page, 55 / 337 with owners and positions read ahead,
 // 54 / 329 with cached instead of streaming loads, 51 / 274 with magnitudes on
 // packed pairs and int8 rounded by the multiply-add, 48 / 271 with the passes
-// launched early. Not kept: K and V in separate warps (55 / 343), a third CTA per
-// SM (52 / 306), pages in position order over all heads (no faster reads, a dearer
-// list), and listing and quantising in one pass (61 / 364: its warps idle while
-// they list).
+// launched early, 46 / 263 with the list pass in 32-bit arithmetic. Not kept: K
+// and V in separate warps (55 / 343), a third CTA per SM (52 / 306), pages in
+// position order over all heads (no faster reads, a dearer list), listing and
+// quantising in one pass (61 / 364: its warps idle while they list), and counting
+// by clusters of CTAs, which needs no zeroed counts (47 / 266; 3 to 10 us slower at
+// 131,072 x 8 and 70,000 x 64 positions).
 #include "block8.cuh"
 #include "compact_prep.cuh"
 
