@@ -3,8 +3,9 @@
 // scale per page (16 tokens of one (b, h)) for K and one for V.
 //
 // The bulk write of a short prompt is one launch (below); any other runs three
-// passes after zeroing the counts, each launched early behind the one before it. The count pass counts the present entries of every
-// 128-entry segment and (b, h). The list pass, one warp per segment, writes the
+// passes after zeroing the counts, each launched early behind the one before it.
+// The count pass counts the present entries of every 128-entry segment and (b, h)
+// and leaves a bit for each score. The list pass, one warp per segment, writes the
 // remapping list, the expire values and the page table, and names each page's
 // owner. The page pass gives one warp a page: it gathers the page's 16 K and V
 // rows through the list (all row loads of a lane in flight before the first is
@@ -18,7 +19,8 @@
 // with the list read page by page, 55 / 337 with owners and positions read ahead,
 // 54 / 329 with cached instead of streaming loads, 51 / 274 with magnitudes on
 // packed pairs and int8 rounded by the multiply-add, 48 / 271 with the passes
-// launched early, 46 / 263 with the list pass in 32-bit arithmetic. Not kept: K
+// launched early, 46 / 266 with the list pass in 32-bit arithmetic, 45 / 266 with
+// the count pass's bits for the list pass (scores only). Not kept: K
 // and V in separate warps (55 / 343), a third CTA per SM (52 / 306), pages in
 // position order over all heads (no faster reads, a dearer list), listing and
 // quantising in one pass (61 / 364: its warps idle while they list), and counting
@@ -34,8 +36,10 @@ namespace {
 // then each page's owner: its (b, h), and its index in that (b, h) with the
 // number of its rows in the low 5 bits (an index is below 2^27).
 size_t prep_bytes(int64_t BH, int NS) { return (compact_ws_bytes(BH, NS) + 15) & ~static_cast<size_t>(15); }
+// Then, for the scored mask, a bit for each position: its score reaches the threshold.
+size_t owner_bytes(int n_pages_cap) { return (static_cast<size_t>(n_pages_cap) * sizeof(uint2) + 15) & ~static_cast<size_t>(15); }
 size_t block8_ws_bytes(int64_t BH, int NS, int n_pages_cap) {
-  return prep_bytes(BH, NS) + 16 + static_cast<size_t>(n_pages_cap) * sizeof(uint2);
+  return prep_bytes(BH, NS) + 16 + owner_bytes(n_pages_cap) + static_cast<size_t>(BH) * NS * sizeof(uint4);
 }
 
 // ------------------------------------------------------------------ count pass
@@ -46,10 +50,13 @@ __global__ void __launch_bounds__(1024) zero_counts_kernel(int BH, int32_t* coun
   for (int i = threadIdx.x; i < BH; i += 1024) count[i] = 0;
 }
 
-// Present entries of each 128-entry segment (one warp each), and of each (b, h) (one atomic a CTA).
-__global__ void __launch_bounds__(kWarpsPerCta * 32) count_block8_kernel(MaskedSrc src, int now, int NS,
-                                                                          int32_t* seg_cnt,
-                                                                          int32_t* count) {
+// Present entries of each 128-entry segment, and of each (b, h) (one atomic for every kWarpsPerCta segments). A warp takes a
+// segment of one (b, h): flags lie along its positions. Of scores it leaves a bit each (the score reaches the threshold)
+// for the list pass.
+constexpr int kWords = kSeg / 32;
+template <bool kScores>
+__global__ void __launch_bounds__(kWarpsPerCta * 32) count_segments_kernel(MaskedSrc src, int now, int NS, uint4* high,
+                                                                           int32_t* seg_cnt, int32_t* count) {
   __shared__ int cta_kept[kWarpsPerCta];
   pdl_launch_dependents();
   pdl_wait();
@@ -58,16 +65,27 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32) count_block8_kernel(MaskedS
   const auto sv = src.view(bh);
   const int lo = sg * kSeg, hi = min(lo + kSeg, sv.length());
   int kept = 0;
+  uint32_t word[kWords];
 #pragma unroll
-  for (int u = 0; u < kSeg / 32; ++u) {
+  for (int u = 0; u < kWords; ++u) {
     const int t = lo + u * 32 + lane;
     int64_t row;
-    if (sg < NS && t < hi) kept += sv.keep(sv.expire_row(t, row), now);
+    if constexpr (kScores) {
+      const int32_t e = sg < NS && t < hi ? sv.expire_row(t, row) : now;
+      kept += sv.keep(e, now);
+      word[u] = __ballot_sync(0xffffffffu, e == kNever);
+    } else {
+      if (sg < NS && t < hi) kept += sv.keep(sv.expire_row(t, row), now);
+    }
   }
   kept = __reduce_add_sync(0xffffffffu, kept);
   if (lane == 0) {
     cta_kept[warp] = kept;
-    if (sg < NS) seg_cnt[static_cast<int64_t>(bh) * NS + sg] = kept;
+    if (sg < NS) {
+      const int64_t at = static_cast<int64_t>(bh) * NS + sg;
+      seg_cnt[at] = kept;
+      if constexpr (kScores) high[at] = make_uint4(word[0], word[1], word[2], word[3]);
+    }
   }
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -78,12 +96,60 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32) count_block8_kernel(MaskedS
   }
 }
 
+// The same of scores, which lie along the heads of one position, when there are many: a warp takes 32 positions of up to
+// 32 heads, a head a lane, so that whole lines are read. Measured on a GB300 (us a write on the device, heads of 128, 0.4
+// kept, segments / heads side by side): 4 x 20,000 positions of 12 heads 56.1 / 58.8, of 16 73.4 / 73.3, of 24 105.6 /
+// 104.1; 64 x 1,200 of 16 82.9 / 81.7; 70,000 of 64 242 / 230; 512 x 64 of 32 190 / 179; 16 x 8,192 of 8 61.1 / 64.9.
+constexpr int kManyHeads = 16;
+__global__ void __launch_bounds__(kWarpsPerCta * kWords * 32) count_scores_kernel(MaskedSrc src, int now, int NS,
+                                                                                 uint32_t* high, int32_t* seg_cnt,
+                                                                                 int32_t* count) {
+  __shared__ int kept_s[kWarpsPerCta * kWords][32];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w = warp % kWords;
+  const int chunks = (src.H + 31) / 32, b = blockIdx.x / chunks, h = (blockIdx.x - b * chunks) * 32 + lane;
+  const int bh = b * src.H + h, sg = blockIdx.y * kWarpsPerCta + warp / kWords, t0 = sg * kSeg + w * 32;
+  const bool live = h < src.H && sg < NS;
+  int kept = 0;
+  if (live) {
+    const float* sc = src.scores + (static_cast<int64_t>(b) * src.n + t0) * src.H + h;
+    const float th = src.tau[bh];
+    const int n = min(src.n - t0, 32);
+    float x[32];
+#pragma unroll
+    for (int u = 0; u < 32; ++u) x[u] = u < n ? sc[static_cast<int64_t>(u) * src.H] : 0.f;
+    uint32_t word = 0;
+#pragma unroll
+    for (int u = 0; u < 32; ++u) {
+      const int32_t e = expire_kvzap(x[u], th, t0 + u, src.window);
+      word |= (e == kNever ? 1u : 0u) << u;
+      kept += u < n && now < e;
+    }
+    high[(static_cast<int64_t>(bh) * NS + sg) * kWords + w] = word;
+  }
+  kept_s[warp][lane] = kept;
+  __syncthreads();
+  if (w == 0) {  // the segment's words
+#pragma unroll
+    for (int i = 1; i < kWords; ++i) kept += kept_s[warp + i][lane];
+    if (live) seg_cnt[static_cast<int64_t>(bh) * NS + sg] = kept;
+    kept_s[warp][lane] = kept;
+  }
+  __syncthreads();
+  if (warp == 0 && h < src.H) {
+#pragma unroll
+    for (int i = 1; i < kWarpsPerCta; ++i) kept += kept_s[i * kWords][lane];
+    if (kept) atomicAdd(&count[bh], kept);
+  }
+}
+
 // ------------------------------------------------------------------ list pass
-template <bool kFused>
+template <bool kFused, bool kScores>
 __global__ void __launch_bounds__(kWarpsPerCta * 32) list_kernel(
     MaskedSrc src, int now, int NS, int table_share, int reserve, int max_pages, int n_pages_cap, int BH, CompactWs ws,
     const int32_t* count, int32_t* status, int32_t* expire_pool, int32_t* page_table, int32_t* remap, int32_t* n_used,
-    uint2* owner) {
+    uint2* owner, const uint4* high) {
   pdl_launch_dependents();
   pdl_wait();
   const int bh = blockIdx.x;  // pairs vary fastest: CTAs resident together read the same positions of all heads
@@ -96,12 +162,19 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32) list_kernel(
   const auto sv = src.view(bh);
   const int n = sv.length();
   const int lo = sg * kSeg, hi = min(lo + kSeg, n);
-  int32_t exps[kSeg / 32];
+  int32_t exps[kWords];
+  if constexpr (kScores) {
+    const uint4 x = live ? high[static_cast<int64_t>(bh) * NS + sg] : make_uint4(0, 0, 0, 0);
+    const uint32_t word[kWords] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-  for (int u = 0; u < kSeg / 32; ++u) {
-    const int t = lo + u * 32 + lane;
-    int64_t row;
-    exps[u] = live && t < hi ? sv.expire_row(t, row) : 0;
+    for (int u = 0; u < kWords; ++u) exps[u] = (word[u] >> lane) & 1u ? kNever : lo + u * 32 + lane + src.window;
+  } else {
+#pragma unroll
+    for (int u = 0; u < kWords; ++u) {
+      const int t = lo + u * 32 + lane;
+      int64_t row;
+      exps[u] = live && t < hi ? sv.expire_row(t, row) : 0;
+    }
   }
   int slot0 = 0;
   if (live)
@@ -160,7 +233,7 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32) list_kernel(
 
   int nk = 0;
 #pragma unroll
-  for (int u = 0; u < kSeg / 32; ++u) {
+  for (int u = 0; u < kWords; ++u) {
     const int t = lo + u * 32 + lane;
     const int32_t e = exps[u];
     const bool keep = t < hi && sv.keep(e, now);
@@ -590,21 +663,25 @@ kvp_status launch_compact(const MaskedSrc& src, int BH, int NS, int now, int res
   const int segs = (NS + kWarpsPerCta - 1) / kWarpsPerCta;
   zero_counts_kernel<<<1, 1024, 0, st>>>(BH, count);
   if (cudaGetLastError() != cudaSuccess) return KVP_ERR_CUDA;
-  if (launch_pdl(count_block8_kernel, dim3(BH, segs), dim3(kWarpsPerCta * 32), 0, st, src, now, NS, ws.seg_cnt, count) !=
-      cudaSuccess)
-    return KVP_ERR_CUDA;
+  uint4* high = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(owner) + owner_bytes(n_pages_cap));
+  const bool scores = src.mode == KVP_MASK_KVZAP;
+  const dim3 warps(kWarpsPerCta * 32);
+  const cudaError_t counted =
+      scores && src.H >= kManyHeads
+          ? launch_pdl(count_scores_kernel, dim3(BH / src.H * ((src.H + 31) / 32), segs), dim3(kWarpsPerCta * kWords * 32), 0,
+                       st, src, now, NS, reinterpret_cast<uint32_t*>(high), ws.seg_cnt, count)
+          : launch_pdl(scores ? count_segments_kernel<true> : count_segments_kernel<false>, dim3(BH, segs), warps, 0, st, src,
+                       now, NS, high, ws.seg_cnt, count);
+  if (counted != cudaSuccess) return KVP_ERR_CUDA;
   const int32_t* cnt = count;
-  const int share = (max_pages + NS - 1) / NS;
-  if (BH <= kFusedBH) {
-    if (launch_pdl(list_kernel<true>, dim3(BH, segs), dim3(kWarpsPerCta * 32), 0, st, src, now, NS, share, reserve, max_pages,
-                   n_pages_cap, BH, ws, cnt, status, expire_pool, page_table, remap, n_used, owner) != cudaSuccess)
-      return KVP_ERR_CUDA;
-  } else {
-    base_kernel<<<1, 1024, 0, st>>>(BH, reserve, max_pages, n_pages_cap, ws, cnt, status);
-    if (launch_pdl(list_kernel<false>, dim3(BH, segs), dim3(kWarpsPerCta * 32), 0, st, src, now, NS, share, reserve, max_pages,
-                   n_pages_cap, BH, ws, cnt, status, expire_pool, page_table, remap, n_used, owner) != cudaSuccess)
-      return KVP_ERR_CUDA;
-  }
+  const bool fused = BH <= kFusedBH;
+  if (!fused) base_kernel<<<1, 1024, 0, st>>>(BH, reserve, max_pages, n_pages_cap, ws, cnt, status);
+  const auto list = fused ? (scores ? list_kernel<true, true> : list_kernel<true, false>)
+                          : (scores ? list_kernel<false, true> : list_kernel<false, false>);
+  if (launch_pdl(list, dim3(BH, segs), warps, 0, st, src, now, NS, (max_pages + NS - 1) / NS, reserve, max_pages,
+                 n_pages_cap, BH, ws, cnt, status, expire_pool, page_table, remap, n_used, owner,
+                 static_cast<const uint4*>(high)) != cudaSuccess)
+    return KVP_ERR_CUDA;
   // at most one page for each 16 positions and reserved slots: small calls take a small grid
   const int64_t most = static_cast<int64_t>(BH) * ((static_cast<int64_t>(src.n) + reserve + kPage - 1) / kPage);
   const int64_t need = (most < n_pages_cap ? most : n_pages_cap) / kPageWarps + 1;

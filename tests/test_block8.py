@@ -60,8 +60,8 @@ def test_compact_refusals(k):
     assert call(wsb=ws - 1) == k.KVP_ERR_WORKSPACE
     assert call(wsp=None) == k.KVP_ERR_WORKSPACE
     assert L.kvp_compact_block8_workspace_bytes(0, 3, 16, 4) == 0
-    # the other compactions' words, 16-byte rounded, the page count, 8 bytes a page
-    assert ws == (L.kvp_compact_workspace_bytes(2, 3, 16) + 15) // 16 * 16 + 16 + 4 * 8
+    # the other compactions' words, 16-byte rounded, the page count, 8 bytes a page, a bit for each of a segment's 128 positions
+    assert ws == (L.kvp_compact_workspace_bytes(2, 3, 16) + 15) // 16 * 16 + 16 + 4 * 8 + 2 * 3 * 16
 
 
 def test_append_refusals(k):

@@ -142,6 +142,10 @@ def _compare(out, lse, heads, q, now, scale, G):
     (1, 1, 1025, 3, 64, 30, 5, 40),      # a position more: the passes
     (0, 129, 110, 1, 64, 20, 0, 0),      # a (b, h) more: the passes
     (1, 2, 1537, 5, 128, 0, 0, 17),
+    (0, 2, 1100, 15, 64, 60, 0, 3),      # heads one by one ..
+    (0, 2, 1111, 16, 64, 200, 0, 3),     # .. and side by side: half a warp of them
+    (0, 1, 1057, 33, 64, 5, 0, 0),       # a warp and one
+    (0, 33, 31, 70, 64, 8, 0, 1),        # the same with the page-base pass
 ])
 def test_bulk_write_is_bit_exact(kvp, fmt, mode, B, T, H, d, window, delay, reserve):
     now = T - 1
@@ -171,6 +175,25 @@ def test_bulk_write_is_bit_exact(kvp, fmt, mode, B, T, H, d, window, delay, rese
     for a, b in ((cache.count, bf.count), (cache.page_table, bf.page_table), (cache.remap, bf.remap)):
         assert torch.equal(a, b)
     assert torch.equal(cache.expire_pool[:used], bf.expire_pool[:used])
+
+
+@pytest.mark.parametrize("H", [3, 18])
+@pytest.mark.parametrize("window", [0, 100])
+def test_bulk_write_of_unusual_scores(kvp, H, window):
+    """Scores and thresholds that are NaN, infinite, zeros of both signs, or equal."""
+    T, d, fmt = 1090, 64, ref.E4M3
+    odd = np.array([np.nan, np.inf, -np.inf, 0.0, -0.0, 0.5, np.float32(2**-149), -1.0], np.float32)
+    scores = odd[(np.abs(syn.normal_f32(81, 331, (1, T, H))) * 1000).astype(int) % 8]
+    tau = odd[np.arange(H) % 8][None]
+    x = _bits(82, (1, T, H, d))
+    cache = _alloc(kvp, 1, H, d, 69 * H, 69, fmt)
+    st = status_word()
+    kvp.kvp_compact_block8(dev_bf16(x), dev_bf16(x), T - 1, 0, cache, mode=0, scores=dev_f32(scores), tau=dev_f32(tau),
+                           window=window, status=st)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    w = ref.widen(x)
+    _check_cache(cache, ref.compact(fmt, 0, w, w, T - 1, window, 0, scores, tau), fmt, 0)
 
 
 @pytest.mark.parametrize("fmt", FMTS)
