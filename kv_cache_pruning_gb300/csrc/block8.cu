@@ -3,10 +3,10 @@
 // scale per page (16 tokens of one (b, h)) for K and one for V.
 //
 // The bulk write of a short prompt is one launch (below); any other runs three
-// passes after zeroing the counts, each launched early behind the one before it.
-// The count pass counts the present entries of every 128-entry segment and (b, h)
-// and leaves a bit for each score. The list pass, one warp per segment, writes the
-// remapping list, the expire values and the page table, and names each page's
+// passes (after zeroing the counts, unless they are few), each launched early
+// behind the one before it. The count pass counts the present entries
+// of every 128-entry segment and (b, h) and leaves a bit for each score. The list
+// pass, one warp per segment, writes the remapping list, the expire values and the page table, and names each page's
 // owner. The page pass gives one warp a page: it gathers the page's 16 K and V
 // rows through the list (all row loads of a lane in flight before the first is
 // used), takes the two largest magnitudes, and writes codes and scales, so every
@@ -37,7 +37,9 @@ namespace {
 // number of its rows in the low 5 bits (an index is below 2^27).
 size_t prep_bytes(int64_t BH, int NS) { return (compact_ws_bytes(BH, NS) + 15) & ~static_cast<size_t>(15); }
 // Then, for the scored mask, a bit for each position: its score reaches the threshold.
-size_t owner_bytes(int n_pages_cap) { return (static_cast<size_t>(n_pages_cap) * sizeof(uint2) + 15) & ~static_cast<size_t>(15); }
+size_t owner_bytes(int n_pages_cap) {
+  return (static_cast<size_t>(n_pages_cap) * sizeof(uint2) + 15) & ~static_cast<size_t>(15);
+}
 size_t block8_ws_bytes(int64_t BH, int NS, int n_pages_cap) {
   return prep_bytes(BH, NS) + 16 + owner_bytes(n_pages_cap) + static_cast<size_t>(BH) * NS * sizeof(uint4);
 }
@@ -50,13 +52,27 @@ __global__ void __launch_bounds__(1024) zero_counts_kernel(int BH, int32_t* coun
   for (int i = threadIdx.x; i < BH; i += 1024) count[i] = 0;
 }
 
-// Present entries of each 128-entry segment, and of each (b, h) (one atomic for every kWarpsPerCta segments). A warp takes a
+// A CTA's entries of a (b, h): to its place among the sums that the list pass's CTAs all add up (the CTA's blockIdx.y of
+// [.., BH]), or, where those would be too many, to the (b, h)'s count, which a launch of its own has zeroed. Measured on a
+// GB300 (us a write, on the device in brackets; heads of 128, 0.4 kept; sums / zeroed counts): 1 x 1,500 positions of 8 heads
+// 16.2 (7.4) / 19.6 (7.9), 4 x 4,096 of 8 14.5 (12.2) / 17.9 (12.3), 8 x 2,048 of 16 25.2 (24.4) / 27.5 (24.7); more (b, h)s:
+// 16 x 4,096 of 8 35.8 (34.9) / 37.8 (34.6), 64 x 1,100 of 5 31.4 (30.6) / 32.6 (28.9); more sums of each: 1 x 8,192 of 8
+// 16.1 (9.9) / 19.7 (9.6), 1 x 131,072 of 8 85 (84) / 65 (61).
+constexpr int kMostSums = 512;     // in all
+constexpr int kMostSumsEach = 8;   // of a (b, h)
+KVP_DEV void add_count(int32_t* part, int32_t* count, int BH, int bh, int kept) {
+  if (part != nullptr) part[static_cast<int64_t>(blockIdx.y) * BH + bh] = kept;
+  else if (kept) atomicAdd(&count[bh], kept);
+}
+
+// Present entries of each 128-entry segment, and of each (b, h) in kWarpsPerCta of them. A warp takes a
 // segment of one (b, h): flags lie along its positions. Of scores it leaves a bit each (the score reaches the threshold)
 // for the list pass.
 constexpr int kWords = kSeg / 32;
 template <bool kScores>
 __global__ void __launch_bounds__(kWarpsPerCta * 32) count_segments_kernel(MaskedSrc src, int now, int NS, uint4* high,
-                                                                           int32_t* seg_cnt, int32_t* count) {
+                                                                           int32_t* seg_cnt, int32_t* part,
+                                                                           int32_t* count) {
   __shared__ int cta_kept[kWarpsPerCta];
   pdl_launch_dependents();
   pdl_wait();
@@ -92,7 +108,7 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32) count_segments_kernel(Maske
     int t = 0;
 #pragma unroll
     for (int w = 0; w < kWarpsPerCta; ++w) t += cta_kept[w];
-    if (t) atomicAdd(&count[bh], t);
+    add_count(part, count, gridDim.x, bh, t);
   }
 }
 
@@ -102,8 +118,8 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32) count_segments_kernel(Maske
 // 104.1; 64 x 1,200 of 16 82.9 / 81.7; 70,000 of 64 242 / 230; 512 x 64 of 32 190 / 179; 16 x 8,192 of 8 61.1 / 64.9.
 constexpr int kManyHeads = 16;
 __global__ void __launch_bounds__(kWarpsPerCta * kWords * 32) count_scores_kernel(MaskedSrc src, int now, int NS,
-                                                                                 uint32_t* high, int32_t* seg_cnt,
-                                                                                 int32_t* count) {
+                                                                                 int BH, uint32_t* high, int32_t* seg_cnt,
+                                                                                 int32_t* part, int32_t* count) {
   __shared__ int kept_s[kWarpsPerCta * kWords][32];
   pdl_launch_dependents();
   pdl_wait();
@@ -140,7 +156,7 @@ __global__ void __launch_bounds__(kWarpsPerCta * kWords * 32) count_scores_kerne
   if (warp == 0 && h < src.H) {
 #pragma unroll
     for (int i = 1; i < kWarpsPerCta; ++i) kept += kept_s[i * kWords][lane];
-    if (kept) atomicAdd(&count[bh], kept);
+    add_count(part, count, BH, bh, kept);
   }
 }
 
@@ -148,8 +164,8 @@ __global__ void __launch_bounds__(kWarpsPerCta * kWords * 32) count_scores_kerne
 template <bool kFused, bool kScores>
 __global__ void __launch_bounds__(kWarpsPerCta * 32) list_kernel(
     MaskedSrc src, int now, int NS, int table_share, int reserve, int max_pages, int n_pages_cap, int BH, CompactWs ws,
-    const int32_t* count, int32_t* status, int32_t* expire_pool, int32_t* page_table, int32_t* remap, int32_t* n_used,
-    uint2* owner, const uint4* high) {
+    const int32_t* part, int32_t* count, int32_t* status, int32_t* expire_pool, int32_t* page_table, int32_t* remap,
+    int32_t* n_used, uint2* owner, const uint4* high) {
   pdl_launch_dependents();
   pdl_wait();
   const int bh = blockIdx.x;  // pairs vary fastest: CTAs resident together read the same positions of all heads
@@ -180,13 +196,23 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32) list_kernel(
   if (live)
     for (int c0 = 0; c0 < sg; c0 += 32)
       slot0 += c0 + lane < sg ? ws.seg_cnt[static_cast<int64_t>(bh) * NS + c0 + lane] : 0;
-  int base;
+  int base, cnt;
   if constexpr (kFused) {
     // (page sums stay below 2^31: checked on the host)
     __shared__ int3 red_s[kWarpsPerCta];
+    __shared__ int cnt_s;
     int before = 0, total = 0, most = 0;
     for (int i = threadIdx.x; i < BH; i += kWarpsPerCta * 32) {
-      const int pg = (count[i] + reserve + kPage - 1) / kPage;
+      int c = 0;
+      if (part != nullptr) {
+#pragma unroll 8
+        for (int y = 0; y < static_cast<int>(gridDim.y); ++y) c += part[y * BH + i];
+        if (i == bh && blockIdx.y == 0) count[bh] = c;
+      } else {
+        c = count[i];
+      }
+      if (i == bh) cnt_s = c;
+      const int pg = (c + reserve + kPage - 1) / kPage;
       before += i < bh ? pg : 0;
       total += pg;
       most = max(most, pg);
@@ -210,16 +236,17 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32) list_kernel(
     }
     if (!ok) return;
     base = before;
+    cnt = cnt_s;
   } else {
     const bool ok = ws.ok[0] != 0;
     if (first_cta && threadIdx.x == 0)
       *n_used = ok ? ws.base[BH - 1] + (count[BH - 1] + reserve + kPage - 1) / kPage : 0;
     if (!ok) return;
     base = ws.base[bh];
+    cnt = count[bh];
   }
   if (!live) return;
   slot0 = __reduce_add_sync(0xffffffffu, slot0);
-  const int cnt = count[bh];
   const int pages = (cnt + reserve + kPage - 1) / kPage;
   int32_t* remap_bh = remap + static_cast<int64_t>(bh) * max_pages * kPage;
   // this segment's share of the page-table row, the owners and the remap tail: table_share pages and their slots
@@ -661,7 +688,9 @@ kvp_status launch_compact(const MaskedSrc& src, int BH, int NS, int now, int res
   const int sms = current_sms(&device);
   if (sms == 0) return KVP_ERR_CUDA;
   const int segs = (NS + kWarpsPerCta - 1) / kWarpsPerCta;
-  zero_counts_kernel<<<1, 1024, 0, st>>>(BH, count);
+  const bool fused = BH <= kFusedBH;
+  int32_t* part = segs <= kMostSumsEach && BH * segs <= kMostSums ? ws.seg_off : nullptr;
+  if (part == nullptr) zero_counts_kernel<<<1, 1024, 0, st>>>(BH, count);
   if (cudaGetLastError() != cudaSuccess) return KVP_ERR_CUDA;
   uint4* high = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(owner) + owner_bytes(n_pages_cap));
   const bool scores = src.mode == KVP_MASK_KVZAP;
@@ -669,18 +698,16 @@ kvp_status launch_compact(const MaskedSrc& src, int BH, int NS, int now, int res
   const cudaError_t counted =
       scores && src.H >= kManyHeads
           ? launch_pdl(count_scores_kernel, dim3(BH / src.H * ((src.H + 31) / 32), segs), dim3(kWarpsPerCta * kWords * 32), 0,
-                       st, src, now, NS, reinterpret_cast<uint32_t*>(high), ws.seg_cnt, count)
+                       st, src, now, NS, BH, reinterpret_cast<uint32_t*>(high), ws.seg_cnt, part, count)
           : launch_pdl(scores ? count_segments_kernel<true> : count_segments_kernel<false>, dim3(BH, segs), warps, 0, st, src,
-                       now, NS, high, ws.seg_cnt, count);
+                       now, NS, high, ws.seg_cnt, part, count);
   if (counted != cudaSuccess) return KVP_ERR_CUDA;
-  const int32_t* cnt = count;
-  const bool fused = BH <= kFusedBH;
-  if (!fused) base_kernel<<<1, 1024, 0, st>>>(BH, reserve, max_pages, n_pages_cap, ws, cnt, status);
+  if (!fused) base_kernel<<<1, 1024, 0, st>>>(BH, reserve, max_pages, n_pages_cap, ws, count, status);
   const auto list = fused ? (scores ? list_kernel<true, true> : list_kernel<true, false>)
                           : (scores ? list_kernel<false, true> : list_kernel<false, false>);
   if (launch_pdl(list, dim3(BH, segs), warps, 0, st, src, now, NS, (max_pages + NS - 1) / NS, reserve, max_pages,
-                 n_pages_cap, BH, ws, cnt, status, expire_pool, page_table, remap, n_used, owner,
-                 static_cast<const uint4*>(high)) != cudaSuccess)
+                 n_pages_cap, BH, ws, static_cast<const int32_t*>(part), count, status, expire_pool, page_table, remap,
+                 n_used, owner, static_cast<const uint4*>(high)) != cudaSuccess)
     return KVP_ERR_CUDA;
   // at most one page for each 16 positions and reserved slots: small calls take a small grid
   const int64_t most = static_cast<int64_t>(BH) * ((static_cast<int64_t>(src.n) + reserve + kPage - 1) / kPage);

@@ -70,7 +70,7 @@ struct MaskedSrc {
 };
 
 // Workspace layout (int32): segment counts [BH*NS], a second [BH*NS] block
-// kept for the layout's stability, page base [BH], flag [1] (1 = budget ok);
+// (the block-scaled write's sums of several segments), page base [BH], flag [1] (1 = budget ok);
 // base and flag are used only above kFusedBH pairs.
 struct CompactWs {
   int32_t* seg_cnt;

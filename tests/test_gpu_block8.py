@@ -146,6 +146,10 @@ def _compare(out, lse, heads, q, now, scale, G):
     (0, 2, 1111, 16, 64, 200, 0, 3),     # .. and side by side: half a warp of them
     (0, 1, 1057, 33, 64, 5, 0, 0),       # a warp and one
     (0, 33, 31, 70, 64, 8, 0, 1),        # the same with the page-base pass
+    (0, 1, 4096, 3, 64, 128, 0, 2),      # the most positions whose counts need no zeroing
+    (0, 1, 4097, 3, 64, 128, 0, 2),      # a position more
+    (1, 2, 4200, 2, 64, 128, 9, 0),
+    (1, 57, 1030, 3, 64, 40, 9, 0),      # a (b, h) more: 513 sums
 ])
 def test_bulk_write_is_bit_exact(kvp, fmt, mode, B, T, H, d, window, delay, reserve):
     now = T - 1
@@ -300,7 +304,7 @@ def test_steps_back_to_back_give_the_bits_of_steps_apart(kvp, fmt):
         assert torch.equal(a, b)
 
 
-@pytest.mark.parametrize("B,T", [(2, 100), (2, 1100), (600, 20)])     # one launch, the passes, the page-base pass
+@pytest.mark.parametrize("B,T", [(2, 100), (2, 1100), (2, 4200), (600, 20)])   # one launch, the passes, the page-base pass
 def test_bulk_write_records_a_full_pool(kvp, B, T):
     H, d = 2, 64
     each = (T + 15) // 16
