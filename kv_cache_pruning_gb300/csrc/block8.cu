@@ -4,14 +4,15 @@
 //
 // The bulk write of a short prompt is one launch (below); any other runs three
 // passes (after zeroing the counts, unless they are few), each launched early
-// behind the one before it. The count pass counts the present entries
-// of every 128-entry segment and (b, h) and leaves a bit for each score. The list
-// pass, one warp per segment, writes the remapping list, the expire values and the page table, and names each page's
-// owner. The page pass gives one warp a page: it gathers the page's 16 K and V
-// rows through the list (all row loads of a lane in flight before the first is
-// used), takes the two largest magnitudes, and writes codes and scales, so every
-// row is read once and every code written once. Pages are dealt out by their ids
-// over a persistent grid, which keeps the warps even whatever the counts are.
+// behind the one before it. The count pass counts the present entries of every
+// 128-entry segment and (b, h) and leaves a bit for each score. The list pass, one
+// warp per segment, writes the remapping list, the expire values and the page
+// table, and names each page's owner. The page pass gives one warp a page: it
+// gathers the page's 16 K and V rows through the list (all row loads of a lane in
+// flight before the first is used), takes the two largest magnitudes, and writes
+// codes and scales, so every row is read once and every code written once. Pages
+// are dealt out by their ids over a persistent grid, which keeps the warps even
+// whatever the counts are.
 //
 // The page pass is bound by memory (a row's 4 D bytes in, 2 D out) with the
 // conversions close behind. Measured on a GB300, 16 x 8192 x 8 heads of 128,
@@ -20,12 +21,12 @@
 // 54 / 329 with cached instead of streaming loads, 51 / 274 with magnitudes on
 // packed pairs and int8 rounded by the multiply-add, 48 / 271 with the passes
 // launched early, 46 / 266 with the list pass in 32-bit arithmetic, 45 / 266 with
-// the count pass's bits for the list pass (scores only). Not kept: K
-// and V in separate warps (55 / 343), a third CTA per SM (52 / 306), pages in
-// position order over all heads (no faster reads, a dearer list), listing and
-// quantising in one pass (61 / 364: its warps idle while they list), and counting
-// by clusters of CTAs, which needs no zeroed counts (47 / 266; 3 to 10 us slower at
-// 131,072 x 8 and 70,000 x 64 positions).
+// the count pass's bits for the list pass (scores only). Not kept: K and V in
+// separate warps (55 / 343), a third CTA per SM (52 / 306), pages in position order
+// over all heads (no faster reads, a dearer list), listing and quantising in one
+// pass (61 / 364: its warps idle while they list), and counting by clusters of CTAs,
+// which needs no zeroed counts (47 / 266; 3 to 10 us slower at 131,072 x 8 and
+// 70,000 x 64 positions).
 #include "block8.cuh"
 #include "compact_prep.cuh"
 
@@ -65,9 +66,8 @@ KVP_DEV void add_count(int32_t* part, int32_t* count, int BH, int bh, int kept) 
   else if (kept) atomicAdd(&count[bh], kept);
 }
 
-// Present entries of each 128-entry segment, and of each (b, h) in kWarpsPerCta of them. A warp takes a
-// segment of one (b, h): flags lie along its positions. Of scores it leaves a bit each (the score reaches the threshold)
-// for the list pass.
+// Present entries of each 128-entry segment, and of each (b, h) in kWarpsPerCta of them. A warp takes a segment of one (b, h):
+// flags lie along its positions. Of scores it leaves a bit each (the score reaches the threshold) for the list pass.
 constexpr int kWords = kSeg / 32;
 template <bool kScores>
 __global__ void __launch_bounds__(kWarpsPerCta * 32) count_segments_kernel(MaskedSrc src, int now, int NS, uint4* high,
@@ -690,8 +690,10 @@ kvp_status launch_compact(const MaskedSrc& src, int BH, int NS, int now, int res
   const int segs = (NS + kWarpsPerCta - 1) / kWarpsPerCta;
   const bool fused = BH <= kFusedBH;
   int32_t* part = segs <= kMostSumsEach && BH * segs <= kMostSums ? ws.seg_off : nullptr;
-  if (part == nullptr) zero_counts_kernel<<<1, 1024, 0, st>>>(BH, count);
-  if (cudaGetLastError() != cudaSuccess) return KVP_ERR_CUDA;
+  if (part == nullptr) {
+    zero_counts_kernel<<<1, 1024, 0, st>>>(BH, count);
+    if (cudaGetLastError() != cudaSuccess) return KVP_ERR_CUDA;
+  }
   uint4* high = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(owner) + owner_bytes(n_pages_cap));
   const bool scores = src.mode == KVP_MASK_KVZAP;
   const dim3 warps(kWarpsPerCta * 32);
