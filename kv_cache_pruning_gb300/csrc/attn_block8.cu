@@ -22,15 +22,21 @@
 //
 // Precision: q is scaled by a power of two per head and turned into fp16
 // exactly (but for elements 2^-28 of the largest). The weights
-// (at most 2^15; the largest of a row is 2^12 or more) enter the second product
+// (at most 2^15; the largest of a row is 2^12 or more, 1 or more at logits whose
+// steps in fp32 are 8 and more) enter the second product
 // as an fp16 pair hi + lo: 22 bits, and never further off than 2^-25, 2^-37 of
-// the row's sum. With at most 4 heads per kv head the pair fills the 8 columns of one product
+// the row's sum (2^-25 at such logits). With at most 4 heads per kv head the pair fills the 8 columns of one product
 // (hi in columns 0..3, lo in 4..7), with 5 to 8 it takes two. A page's product
 // starts from zero and is added to the fp32 accumulators with the V scale by
 // fused multiply-adds.
 //
-// The running maximum is lazy: it moves only when a logit exceeds it by more
-// than 2^3 (a vote per page), so most pages need no shuffles and no rescaling.
+// The running reference is lazy: it is 12 below the largest base-2 logit when it
+// moves (rounded up, so that logits of any size stay within 12 above it), and
+// moves only when a logit is more than 15 above it (a vote per page), so most
+// pages need no shuffles and no rescaling. A logit is compared with the
+// reference by their difference, which is exact where it matters: a sum of the
+// reference and 15 rounds by more than that at logits of 2^25, where a weight
+// would leave fp16's range.
 //
 // Work split: all pages of all (b, h) form one list (b-major, h-minor, page
 // order), cut evenly over the CTAs and, within a CTA, over its warps. Partial
@@ -48,8 +54,8 @@ constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxBH = 4096;     // (b, h) pairs whose page prefix fits in shared memory
 constexpr int kMaxCtas = 512;    // grid bound used to size the workspace
-constexpr float kLazy = 3.f;     // how far a base-2 logit may pass the reference before it moves
-constexpr float kBias = 12.f;    // weights are 2^(x - m + kBias): at most 2^(kLazy + kBias) in fp16
+constexpr float kBelow = 12.f;   // the reference's distance from the largest base-2 logit when it moves
+constexpr float kAbove = 15.f;   // how far a logit may be above it: weights 2^(x - m) are at most 2^15 in fp16
 constexpr int kFewPieces = 8;    // CTAs whose partial results of one (b, h) are merged in one round trip
 constexpr int kOwnExtra = 96;    // pages by which the longest (b, h) may pass an even share to have a CTA of its own
 constexpr int kCtaPages = 2 * kWarps;  // fewest pages of an even share: more CTAs would have more to merge
@@ -193,7 +199,7 @@ __host__ __device__ constexpr size_t smem_bytes(int BH, int G) {
 
 // A row's log-sum-exp from its reference and sum (0 for a row without slots; NaN passes through).
 KVP_DEV void write_lse(const Params& p, int64_t row, float m, float l) {
-  if (p.lse != nullptr) p.lse[row] = l > 0.f ? (m - kBias + log2f(l)) * 0.69314718055994531f : (l == 0.f ? -INFINITY : l);
+  if (p.lse != nullptr) p.lse[row] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : (l == 0.f ? -INFINITY : l);
 }
 
 // kDup: at most 4 heads per kv head, hi and lo weights in one product.
@@ -414,17 +420,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block8_kernel(const Params p
         x[1] = in0 ? x[1] * f1 : -INFINITY;
         x[2] = in1 ? x[2] * f0 : -INFINITY;
         x[3] = in1 ? x[3] * f1 : -INFINITY;
-        // a reference that has fallen behind (or none yet) moves to the page's maximum
+        // a reference that has fallen behind (or none yet, -inf) moves up to 12 below the page's maximum
         const float top0 = fmaxf(x[0], x[2]), top1 = fmaxf(x[1], x[3]);
-        if (__any_sync(0xffffffffu, top0 > s.m[0] + kLazy || top1 > s.m[1] + kLazy)) {
+        if (__any_sync(0xffffffffu, top0 - s.m[0] > kAbove || top1 - s.m[1] > kAbove)) {
           float m0 = top0, m1 = top1;
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) {
             m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
             m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
           }
-          m0 = fmaxf(m0, s.m[0]);
-          m1 = fmaxf(m1, s.m[1]);
+          m0 = fmaxf(__fsub_ru(m0, kBelow), s.m[0]);
+          m1 = fmaxf(__fsub_ru(m1, kBelow), s.m[1]);
           const float r0 = m0 == s.m[0] ? 1.f : ex2_approx(s.m[0] - m0), r1 = m1 == s.m[1] ? 1.f : ex2_approx(s.m[1] - m1);
           s.m[0] = m0;
           s.m[1] = m1;
@@ -439,9 +445,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block8_kernel(const Params p
           }
         }
         // a head whose reference is still -inf has only -inf logits: weight 0, not NaN
-        const float c0 = s.m[0] == -INFINITY ? 0.f : kBias - s.m[0], c1 = s.m[1] == -INFINITY ? 0.f : kBias - s.m[1];
-        const float w0 = ex2_approx(x[0] + c0), w1 = ex2_approx(x[1] + c1);
-        const float w2 = ex2_approx(x[2] + c0), w3 = ex2_approx(x[3] + c1);
+        const float c0 = s.m[0] == -INFINITY ? 0.f : s.m[0], c1 = s.m[1] == -INFINITY ? 0.f : s.m[1];
+        const float w0 = ex2_approx(x[0] - c0), w1 = ex2_approx(x[1] - c1);
+        const float w2 = ex2_approx(x[2] - c0), w3 = ex2_approx(x[3] - c1);
         s.l[0] += w0 + w2;
         s.l[1] += w1 + w3;
         const uint32_t h0 = pack_half2(w0, w1), h1 = pack_half2(w2, w3);
