@@ -805,7 +805,11 @@ KVP_API kvp_status kvp_read_block8(int fmt, int batch, int n_kv_heads, int head_
  * over the slots i < count[b, h] of kv head h = j / (Hq / H) whose expire is
  * greater than `now`; an empty set gives a zero row and lse -inf. K and V are
  * the codes' exact values; products run on the tensor cores (fp16 operands,
- * fp32 accumulation; the weights as an fp16 pair, about 22 bits).
+ * fp32 accumulation; the weights as an fp16 pair, about 22 bits). Values may be
+ * of any size: an output overflows only if the magnitudes of its channel's
+ * values add up to more than 2^135 (256 slots of bf16's largest number). Logits
+ * have to be fp32 numbers: scale times a row's largest |q| times a page's largest
+ * |k| times head_dim below 2^127.
  *
  * Hq a multiple of H, Hq/H from 1 to 8, B*H <= 4096. q device bf16
  * [B, Hq, head_dim], 16-byte aligned. scale > 0, or 0 for 1/sqrt(head_dim).

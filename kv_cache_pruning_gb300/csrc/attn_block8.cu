@@ -28,7 +28,10 @@
 // the row's sum (2^-25 at such logits). With at most 4 heads per kv head the pair fills the 8 columns of one product
 // (hi in columns 0..3, lo in 4..7), with 5 to 8 it takes two. A page's product
 // starts from zero and is added to the fp32 accumulators with the V scale by
-// fused multiply-adds.
+// fused multiply-adds. They hold 2^-23 of the weighted sums, which are up to 2^15
+// a slot larger than the values: no sum of values whose magnitudes add up to less
+// than 2^135 overflows, and the smallest scale, 2^-126, still is a number (a power of
+// two, so that nothing else changes).
 //
 // The running reference is lazy: it is 12 below the largest base-2 logit when it
 // moves (rounded up, so that logits of any size stay within 12 above it), and
@@ -56,6 +59,7 @@ constexpr int kMaxBH = 4096;     // (b, h) pairs whose page prefix fits in share
 constexpr int kMaxCtas = 512;    // grid bound used to size the workspace
 constexpr float kBelow = 12.f;   // the reference's distance from the largest base-2 logit when it moves
 constexpr float kAbove = 15.f;   // how far a logit may be above it: weights 2^(x - m) are at most 2^15 in fp16
+constexpr float kDown = 1.f / 8388608.f;  // the accumulators' share of the weighted sums, 2^-23
 constexpr int kFewPieces = 8;    // CTAs whose partial results of one (b, h) are merged in one round trip
 constexpr int kOwnExtra = 96;    // pages by which the longest (b, h) may pass an even share to have a CTA of its own
 constexpr int kCtaPages = 2 * kWarps;  // fewest pages of an even share: more CTAs would have more to merge
@@ -196,6 +200,9 @@ __host__ __device__ constexpr size_t smem_bytes(int BH, int G) {
   return prefix_bytes(BH) + static_cast<size_t>(kWarps) * 2 * part_floats<D>(G) * 4 +
          static_cast<size_t>(G) * kMaxCtas * 8 + kThreads * 16;
 }
+
+// What takes a row's accumulators to its output, from its sum of weights (0 for a row without slots).
+KVP_DEV float out_factor(float l) { return l == 0.f ? 0.f : (1.f / kDown) / l; }
 
 // A row's log-sum-exp from its reference and sum (0 for a row without slots; NaN passes through).
 KVP_DEV void write_lse(const Params& p, int64_t row, float m, float l) {
@@ -415,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block8_kernel(const Params p
         for (int c = 0; c < 4; ++c) x[c] += x2[c];
         const int id_next = i + 1 < n ? id_of(i + 1) : -1;
         if (i + 1 < n) request_k(id_next);
-        const float f0 = qs[0] * sc.x, f1 = qs[1] * sc.x;
+        const float f0 = qs[0] * sc.x, f1 = qs[1] * sc.x, fv = sc.y * kDown;
         x[0] = in0 ? x[0] * f0 : -INFINITY;
         x[1] = in0 ? x[1] * f1 : -INFINITY;
         x[2] = in1 ? x[2] * f0 : -INFINITY;
@@ -487,13 +494,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block8_kernel(const Params p
           mma_f16_zero(y, a0, a1, a2, a3, b0, b1);
           if constexpr (!kDup) mma_f16_16816(y, a0, a1, a2, a3, d0, d1);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) s.acc[2 * w][c] = fmaf(y[c], sc.y, s.acc[2 * w][c]);
+          for (int c = 0; c < 4; ++c) s.acc[2 * w][c] = fmaf(y[c], fv, s.acc[2 * w][c]);
           codes_to_f16<FMT>(ab1, a0, a1);
           codes_to_f16<FMT>(cd1, a2, a3);
           mma_f16_zero(y, a0, a1, a2, a3, b0, b1);
           if constexpr (!kDup) mma_f16_16816(y, a0, a1, a2, a3, d0, d1);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) s.acc[2 * w + 1][c] = fmaf(y[c], sc.y, s.acc[2 * w + 1][c]);
+          for (int c = 0; c < 4; ++c) s.acc[2 * w + 1][c] = fmaf(y[c], fv, s.acc[2 * w + 1][c]);
         }
         if (i + 1 < n) {
           request_v(id_next);
@@ -527,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block8_kernel(const Params p
         const int head = 2 * t + hh;
         if (head < G && (!kDup || t < 2)) {
           float* dst = whole ? p.out + (static_cast<int64_t>(u) * G + head) * D : part + head * D;
-          const float inv = whole ? (s.l[hh] == 0.f ? 0.f : 1.f / s.l[hh]) : 1.f;
+          const float inv = whole ? out_factor(s.l[hh]) : 1.f;
 #pragma unroll
           for (int j = 0; j < D / 32; ++j)
             reinterpret_cast<float4*>(dst + g * (D / 8))[j] =
@@ -604,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block8_kernel(const Params p
       }
       const float2 ml = merged_ml[head];
       if (whole) {
-        const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;
+        const float inv = out_factor(ml.y);
         reinterpret_cast<float4*>(p.out + static_cast<int64_t>(u) * G * D)[i] =
             make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
         if (i % (D / 4) == 0) write_lse(p, static_cast<int64_t>(u) * G + head, ml.x, ml.y);
@@ -667,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block8_kernel(const Params p
           a.z = fmaf(w, x[c].z, a.z);
           a.w = fmaf(w, x[c].w, a.w);
         }
-        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const float inv = out_factor(l);
         reinterpret_cast<float4*>(p.out + static_cast<int64_t>(u) * G * D)[i] =
             make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
         if (i % (D / 4) == 0) write_lse(p, static_cast<int64_t>(u) * G + head, m, l);
@@ -722,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block8_kernel(const Params p
         a.w += x.w;
       }
       const float2 ml = merged_ml[head];
-      const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;
+      const float inv = out_factor(ml.y);
       reinterpret_cast<float4*>(p.out + static_cast<int64_t>(u) * G * D)[i] =
           make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
       if (i % (D / 4) == 0) write_lse(p, static_cast<int64_t>(u) * G + head, ml.x, ml.y);

@@ -1,4 +1,5 @@
-"""The 8-bit cache's attention at the ends of the number range."""
+"""The 8-bit cache's attention at the ends of the number range: logits of millions, values near bf16's largest and
+smallest numbers."""
 import math
 
 import numpy as np
@@ -77,3 +78,52 @@ def test_logits_that_tell_one_token_apart(kvp, fmt):
                 # the others are 2^(e - 3) log2(e) or more below: weight 0. Equal weights, as above, and a page's add
                 off = np.abs(out[0, j].double().cpu().numpy() - v[top].mean(0))
                 assert (off <= (16 + T / 16) * 2.0**-23 * np.abs(v[top]).mean(0)).all(), (e, j)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G", [2, 5])
+def test_values_near_the_largest_numbers(kvp, fmt, d, G):
+    """Values up to bf16's largest number: their weighted mean is finite, so the output is. Slots enough for partial
+    results of several warps and CTAs, one page of one sign and of the largest magnitude among smaller ones."""
+    B, T, H = 1, 150, 2
+    v = syn.normal_f32(511, 1, (B, T, H, d)).astype(np.float64) * 2.0**100
+    v[0, 32:48] = np.sign(v[0, 32:48]) * 2.0**116
+    v[0, 64:80] = np.abs(v[0, 64:80]) * 2.0**24                  # up to about 2^126, all positive
+    v[0, 70] = 2.0**127
+    kb, vb = syn.f32_to_bf16_bits(syn.normal_f32(512, 1, (B, T, H, d))), syn.f32_to_bf16_bits(v.astype(np.float32))
+    cache, heads = _written(kvp, fmt, kb, vb)
+    assert max(heads[0][0].scales[1]) >= 2.0**118
+    q = syn.normal_bf16(513, 1, (B, H * G, d))
+    for limit in (0, 1, 3):
+        out = kvp.kvp_decode_attn_block8(dev_bf16(q), cache, T - 1, grid_limit=limit)
+        torch.cuda.synchronize()
+        got = out.double().cpu().numpy()
+        for h in range(H):
+            sl = slice(h * G, (h + 1) * G)
+            want, _, size_abs, size = heads[0][h].attend(ref.widen(q)[0, sl], T - 1, 1 / math.sqrt(d))
+            tol, _ = ref.attention_bounds(d, T, size_abs, size)
+            assert np.isfinite(got[0, sl]).all() and (np.abs(got[0, sl] - want) <= tol).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("G", [3, 8])
+def test_values_near_the_smallest_numbers(kvp, fmt, G):
+    """Pages whose scale is the smallest, 2^-126, beside one another: nothing of their values is lost but fp32's own
+    subnormal steps."""
+    T, d = 150, 64
+    kb = syn.f32_to_bf16_bits(syn.normal_f32(521, 1, (1, T, 1, d)))
+    vb = syn.f32_to_bf16_bits((syn.normal_f32(522, 1, (1, T, 1, d)).astype(np.float64) * 2.0**-121).astype(np.float32))
+    cache, heads = _written(kvp, fmt, kb, vb)
+    assert max(heads[0][0].scales[1]) <= 2.0**-124
+    q = syn.normal_bf16(523, 1, (1, G, d))
+    for limit in (0, 2):
+        out = kvp.kvp_decode_attn_block8(dev_bf16(q), cache, T - 1, grid_limit=limit)
+        torch.cuda.synchronize()
+        want, _, size_abs, size = heads[0][0].attend(ref.widen(q)[0], T - 1, 1 / 8)
+        tol, _ = ref.attention_bounds(d, T, size_abs, size)
+        # the bounds without their allowance for this range, 1e-37; instead half of fp32's smallest step (2^-150) at each
+        # of a sum's T / 16 + 40 additions, 2^11 of the output's units in one of the sum's (weights are 2^12 and more,
+        # values enter scaled down by 2^23 at most), and one at the end
+        tol = tol - 1e-37 + (T / 16 + 40) * 2.0**-139 + 2.0**-149
+        assert (np.abs(out.double().cpu().numpy()[0] - want) <= tol).all()
