@@ -806,8 +806,14 @@ def kvp_decode_attn_mla(q, cache: LatentPagedKV, now, *, scale=0.0, out=None, n_
 # These calls are made once a layer and step, often on little work, so their checks are written to be cheap: a device
 # is its index, a handle checks its buffers when it is made and keeps their sizes (they cannot be replaced in it).
 
-_raw_stream = torch._C._cuda_getCurrentRawStream   # the current stream of a device, without a Stream object
-_current_device = torch._C._cuda_getDevice
+# (the names are looked up when called: torch builds without CUDA lack them, and the package imports there, too)
+def _raw_stream(dev):
+    """The current stream of a device, without a Stream object."""
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _current_device():
+    return torch._C._cuda_getDevice()
 
 
 def _refuse(t, dtype, name, dev, shape=None):
