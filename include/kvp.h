@@ -855,9 +855,11 @@ KVP_API kvp_status kvp_decode_attn_block8_devpos(int fmt, int batch, int n_q_hea
  *
  * Everything in fp32, rounded to bf16 once at the end. Angles are as good at
  * every position (about 2^-26 of a turn, their fp32 form): `turns` holds
- * inv_freq[i] / (2 pi) as 64-bit fixed-point fractions of a turn
- * (kvp_rope_turns makes them, on the host), and pos * turns is taken modulo
- * one turn in 64-bit integers.
+ * inv_freq[i] / (2 pi) as 64-bit fixed-point fractions of a turn, right to their
+ * last bit (kvp_rope_turns makes them, on the host, from inv_freq of magnitude up
+ * to 2^32; larger ones and NaN are KVP_ERR_INVALID), and pos * turns is taken
+ * modulo one turn in 64-bit integers: 2^-33 of a turn off at most before its fp32
+ * form.
  *
  * n_tok      tokens (>= 0; 0 does nothing)
  * n_q_heads, n_k_heads  >= 0, not both 0; q (k) may be NULL when its count is 0

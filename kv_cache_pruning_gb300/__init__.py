@@ -1092,7 +1092,7 @@ def kvp_decode_attn_block8_devpos(q, cache: Block8PagedKV, now_dev, *, scale=0.0
 # --------------------------------------------------------------------------- norm and rotation of queries and keys
 
 def kvp_rope_turns(inv_freq, *, device=None):
-    """inv_freq (radians per position, a sequence or tensor; float64 keeps far positions exact) as the table that
+    """inv_freq (radians per position, a sequence or tensor of magnitudes up to 2^32; taken as float64) as the table that
     kvp_qk_norm_rope takes: 64-bit fractions of a turn, an int64 tensor on `device` (inv_freq's, if it is on a GPU)."""
     f = torch.as_tensor(inv_freq, dtype=torch.float64)
     if device is None:

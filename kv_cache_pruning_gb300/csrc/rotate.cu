@@ -270,10 +270,17 @@ extern "C" kvp_status kvp_rope_turns(int n, const double* inv_freq, uint64_t* tu
   if (n < 0) return KVP_ERR_INVALID;
   if (n == 0) return KVP_OK;
   if (inv_freq == nullptr || turns == nullptr) return KVP_ERR_INVALID;
+  // 1 / (2 pi) as the sum of two doubles, and the quotient as the sum of two with it (the product's own rounding error by
+  // a fused multiply-add): a position multiplies the quotient's error by up to 2^31, so one double's 2^-53 of it would
+  // show at far positions. Below 2^32 radians the sum is within 2^-74 of a turn.
+  constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57, kOne = 18446744073709551616.0;  // 2^64
   for (int i = 0; i < n; ++i) {
-    if (!std::isfinite(inv_freq[i])) return KVP_ERR_INVALID;
-    const double t = std::fabs(inv_freq[i]) / 6.283185307179586476925;
-    const uint64_t u = static_cast<uint64_t>((t - std::floor(t)) * 18446744073709551616.0);  // exact: t - floor(t) < 1
+    const double f = std::fabs(inv_freq[i]);
+    if (!(f <= 4294967296.0)) return KVP_ERR_INVALID;
+    const double hi = f * kHi, lo = std::fma(f, kHi, -hi) + f * kLo;
+    const double x = (hi - std::floor(hi)) * kOne, whole = std::floor(x);  // both exact
+    const uint64_t u = static_cast<uint64_t>(whole) +
+                       static_cast<uint64_t>(static_cast<int64_t>(std::floor(x - whole + lo * kOne + 0.5)));
     turns[i] = inv_freq[i] < 0 ? 0 - u : u;
   }
   return KVP_OK;
