@@ -690,10 +690,8 @@ kvp_status launch_compact(const MaskedSrc& src, int BH, int NS, int now, int res
   const int segs = (NS + kWarpsPerCta - 1) / kWarpsPerCta;
   const bool fused = BH <= kFusedBH;
   int32_t* part = segs <= kMostSumsEach && BH * segs <= kMostSums ? ws.seg_off : nullptr;
-  if (part == nullptr) {
-    zero_counts_kernel<<<1, 1024, 0, st>>>(BH, count);
-    if (cudaGetLastError() != cudaSuccess) return KVP_ERR_CUDA;
-  }
+  if (part == nullptr && launch_after(zero_counts_kernel, dim3(1), dim3(1024), st, BH, count) != cudaSuccess)
+    return KVP_ERR_CUDA;
   uint4* high = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(owner) + owner_bytes(n_pages_cap));
   const bool scores = src.mode == KVP_MASK_KVZAP;
   const dim3 warps(kWarpsPerCta * 32);
@@ -704,7 +702,9 @@ kvp_status launch_compact(const MaskedSrc& src, int BH, int NS, int now, int res
           : launch_pdl(scores ? count_segments_kernel<true> : count_segments_kernel<false>, dim3(BH, segs), warps, 0, st, src,
                        now, NS, high, ws.seg_cnt, part, count);
   if (counted != cudaSuccess) return KVP_ERR_CUDA;
-  if (!fused) base_kernel<<<1, 1024, 0, st>>>(BH, reserve, max_pages, n_pages_cap, ws, count, status);
+  if (!fused && launch_after(base_kernel, dim3(1), dim3(1024), st, BH, reserve, max_pages, n_pages_cap, ws,
+                             static_cast<const int32_t*>(count), status) != cudaSuccess)
+    return KVP_ERR_CUDA;
   const auto list = fused ? (scores ? list_kernel<true, true> : list_kernel<true, false>)
                           : (scores ? list_kernel<false, true> : list_kernel<false, false>);
   if (launch_pdl(list, dim3(BH, segs), warps, 0, st, src, now, NS, (max_pages + NS - 1) / NS, reserve, max_pages,
@@ -720,7 +720,7 @@ kvp_status launch_compact(const MaskedSrc& src, int BH, int NS, int now, int res
                  static_cast<const int32_t*>(remap), kq_pool, vq_pool, reinterpret_cast<float2*>(scale_pool),
                  expire_pool) != cudaSuccess)
     return KVP_ERR_CUDA;
-  return cudaGetLastError() == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
+  return KVP_OK;
 }
 
 kvp_status append_block8_impl(int fmt, int mode, int batch, int n_kv_heads, int head_dim, int pos,

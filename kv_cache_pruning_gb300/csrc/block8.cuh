@@ -137,6 +137,19 @@ inline bool rows_apart(std::array<std::pair<int64_t, int64_t>, 3> stride_n, int6
   return true;
 }
 
+// Launches kern<<<grid, block, 0, st>>>(args...), which starts when the launch before it has ended. Its error is this
+// launch's own: what an earlier call of the caller's has left pending is neither reported here nor taken away.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_after(void (*kern)(KArgs...), dim3 grid, dim3 block, cudaStream_t st, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = st;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+  if (e != cudaSuccess) (void)cudaGetLastError();
+  return e;
+}
+
 // SM count of the current device, whose number goes to *device (0 when it cannot be asked); asked once per device.
 inline int current_sms(int* device) {
   static std::atomic<int> known[64];
