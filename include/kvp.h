@@ -871,7 +871,10 @@ KVP_API kvp_status kvp_decode_attn_block8_devpos(int fmt, int batch, int n_q_hea
  * turns      device uint64 [rot_dim / 2], 8-byte aligned (NULL when rot_dim is 0)
  * wq, wk     device fp32 [head_dim] norm weights, 16-byte aligned, or NULL for no
  *            norm (of queries, of keys)
- * eps        >= 0, finite
+ * eps        >= 0, finite. The mean of a normed row's squares, plus eps, is an fp32
+ *            number: it has to be 2^-100 or more (below, what underflows of the
+ *            squares shows), and the squares have to sum to less than 2^128
+ *            (values up to 2^60 always do; past it the row comes out as zeros)
  * q_out, k_out  as q, k, of strides whose rows do not overlap (as
  *            kvp_read_block8's); each may be its input itself (same address and
  *            strides), and may not overlap an input otherwise

@@ -16,7 +16,10 @@
 // streaming loads, 210 (0.94 of measured HBM) with the weights in shared memory
 // instead, which leaves the registers of 32 warps an SM without spills to speak of.
 // Not kept: the next step's rows requested before this one's arithmetic (264), one
-// step or three in flight instead of two (239, 241).
+// step or three in flight instead of two (239, 241); scaling rows whose squares leave
+// fp32's range by a power of two, behind a vote a row (214, 218 interleaved; 131,072 x
+// 5 heads 82.5 against 80.4), after the other rows (215, 84.5), or in a function of its
+// own (218, 82.6).
 //
 // An angle is a 64-bit product: turns[i] = inv_freq[i] / (2 pi) as a 64-bit
 // fraction of a turn, times the position modulo one turn (the integer wraps
