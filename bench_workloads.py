@@ -19,9 +19,10 @@ runs measure the rest of the path on the shapes it is quoted for:
                  inverse of the kept fraction
   prune_sweep_long  the same sweep on one layer of the 65B-shaped MHA stack
                  (64 heads, 131,072 cached tokens, batch 1)
-  block8_decode  the same layer with its cache in 8 bits, a scale for each page: the
-                 prompt written, 64 steps of norm and rotation, append and
-                 attention, the cache read back; beside the same steps in bf16
+  block8_decode  four Llama-3-8B-shaped layers in turn (more than L2 holds) with their
+                 caches in 8 bits, a scale for each page: the prompt written, 64
+                 steps of norm and rotation, append and attention, the cache read
+                 back; beside the same steps in bf16
 
 Decode loops are captured once in a CUDA graph (the C-ABI calls only enqueue
 work on the current stream) and replayed for timing, so host launch overhead
@@ -632,19 +633,21 @@ def quant_decode(kvp, dev, peaks, seed=0, steps=64, reps=3):
             "one_tier": res[1], "two_tier": res[2]}
 
 
-def block8_decode(kvp, dev, peaks, seed=0, steps=64, reps=3):
-    """The 8-bit cache with a scale for each page on the Llama-3-8B-shaped layer (batch 16, 8,192-token prompt, 32 q / 8
+def block8_decode(kvp, dev, peaks, seed=0, steps=64, layers=4, reps=3):
+    """The 8-bit cache with a scale for each page on Llama-3-8B-shaped layers (batch 16, 8,192-token prompt, 32 q / 8
     kv heads, head_dim 128), a quarter of the prompt kept (tau at each head's 75th-percentile score, 128-token window),
     in both formats and, beside them, in bf16. The prompt's keys are normed and rotated (kvp_qk_norm_rope) and written
     (kvp_compact_block8); each of 64 decode steps norms and rotates its queries and keys from one projection's output,
-    appends and attends (one CUDA graph, positions in device memory); the cache is read back at the end."""
+    appends and attends (one CUDA graph, positions in device memory); the cache is read back at the end. Four layers take
+    turns, so that a layer's cache (71 MB in 8 bits) is no longer in L2 when its turn comes again; figures are a layer's.
+    The bf16 append takes contiguous rows only: they are laid out before the steps are timed."""
     B, T, H, Hq, d, W = 16, 8192, 8, 32, 128, 128
-    G = Hq // H
     g = torch.Generator(device=dev)
     g.manual_seed(seed)
     K = _randn_bf16((B * T, H, d), g, dev)
     V = _randn_bf16((B, T, H, d), g, dev)
     qkv = _randn_bf16((steps, B, Hq + 2 * H, d), g, dev)
+    v_rows = qkv[:, :, Hq + H:].contiguous()
     s = torch.randn((B, T, H), generator=g, device=dev)
     s_new = torch.randn((steps, B, H), generator=g, device=dev)
     st = torch.zeros(1, dtype=torch.int32, device=dev)
@@ -668,52 +671,54 @@ def block8_decode(kvp, dev, peaks, seed=0, steps=64, reps=3):
     res = {}
     for name, fmt in (("bf16", None), ("e4m3", kvp.KVP_BLOCK8_E4M3), ("int8", kvp.KVP_BLOCK8_INT8)):
         if fmt is None:
-            c = kvp.PagedKV.allocate(B, H, d, cap, mp, device=dev)
+            caches = [kvp.PagedKV.allocate(B, H, d, cap, mp, device=dev) for _ in range(layers)]
             ws_c = torch.empty(kvp.kvp_compact_workspace_bytes(B, H, T), dtype=torch.uint8, device=dev)
             ws_a = torch.zeros(kvp.kvp_decode_attn_workspace_bytes(B, Hq, H, d), dtype=torch.uint8, device=dev)
             row_bytes = 2 * 2 * d + 4
         else:
-            c = kvp.Block8PagedKV.allocate(B, H, d, cap, mp, fmt=fmt, device=dev)
+            caches = [kvp.Block8PagedKV.allocate(B, H, d, cap, mp, fmt=fmt, device=dev) for _ in range(layers)]
             ws_c = torch.empty(kvp.kvp_compact_block8_workspace_bytes(B, H, T, cap), dtype=torch.uint8, device=dev)
             ws_a = torch.zeros(kvp.kvp_decode_attn_block8_workspace_bytes(B, Hq, H, d), dtype=torch.uint8, device=dev)
             row_bytes = 2 * d + 4 + 8 / 16
 
         def prefill():
             fn = kvp.kvp_compact_masked if fmt is None else kvp.kvp_compact_block8
-            fn(Kr, V, T - 1, steps, c, mode=kvp.KVP_MASK_KVZAP, scores=s, tau=tau, window=W, status=st, workspace=ws_c)
+            for c in caches:
+                fn(Kr, V, T - 1, steps, c, mode=kvp.KVP_MASK_KVZAP, scores=s, tau=tau, window=W, status=st, workspace=ws_c)
 
-        def step(i):
+        def step(i, c):
             kvp.kvp_qk_norm_rope(qkv[i, :, :Hq], qkv[i, :, Hq:Hq + H], pos, turns, q_weight=w[0], k_weight=w[1], q_out=q,
                                  k_out=k)
-            v = qkv[i, :, Hq + H:]
             kw = dict(mode=kvp.KVP_MASK_KVZAP, score=s_new[i], tau=tau, window=W, status=st)
             if fmt is None:
-                kvp.kvp_append_devpos(c, k, v.contiguous(), pos[:1], **kw)
+                kvp.kvp_append_devpos(c, k, v_rows[i], pos[:1], **kw)
                 kvp.kvp_decode_attn_devpos(q, c, pos[:1], out=out, workspace=ws_a, status=st)
             else:
-                kvp.kvp_append_block8_devpos(c, k, v, pos[:1], **kw)
+                kvp.kvp_append_block8_devpos(c, k, qkv[i, :, Hq + H:], pos[:1], **kw)
                 kvp.kvp_decode_attn_block8_devpos(q, c, pos[:1], out=out, workspace=ws_a, status=st)
 
         def loop():
             pos.fill_(T - 1)
             for i in range(steps):
                 pos.add_(1)
-                step(i)
+                for c in caches:
+                    step(i, c)
 
-        ms_write = _time(_graph(prefill), reps=reps)
+        ms_write = _time(_graph(prefill), reps=reps) / layers
         torch.cuda.synchronize()
-        kept = int(c.count.sum().item())
+        kept = int(caches[0].count.sum().item())
 
         def attend():
             for _ in range(steps):
-                if fmt is None:
-                    kvp.kvp_decode_attn(q, c, T - 1, out=out, workspace=ws_a, status=st)
-                else:
-                    kvp.kvp_decode_attn_block8(q, c, T - 1, out=out, workspace=ws_a, status=st)
+                for c in caches:
+                    if fmt is None:
+                        kvp.kvp_decode_attn(q, c, T - 1, out=out, workspace=ws_a, status=st)
+                    else:
+                        kvp.kvp_decode_attn_block8(q, c, T - 1, out=out, workspace=ws_a, status=st)
 
-        step(0)                        # queries of a first step; the prompt's cache again for the measurements
+        step(0, caches[0])             # queries of a first step; the prompt's cache again for the measurements
         prefill()
-        ms_attn = _time(_graph(attend), reps=reps) / steps
+        ms_attn = _time(_graph(attend), reps=reps) / (steps * layers)
         torch.cuda.synchronize()
         gr = torch.cuda.CUDAGraph()
         with torch.cuda.graph(gr):
@@ -723,20 +728,25 @@ def block8_decode(kvp, dev, peaks, seed=0, steps=64, reps=3):
             prefill()                  # the loop appends: start every replay from the prompt's cache
             torch.cuda.synchronize()
             best = min(best, _time(gr.replay))
+        best /= steps * layers
         res[name] = {"prompt_write_us": ms_write * 1e3, "attention_us": ms_attn * 1e3, "attention_bytes": kept * row_bytes,
                      "attention_frac_of_hbm": kept * row_bytes / (ms_attn * 1e-3) / 1e9 / peaks[0],
-                     "us_per_step": best / steps * 1e3, "decode_tokens_per_s": B / (best / steps * 1e-3),
-                     "slots": int(c.count.sum().item())}
+                     "us_per_step_and_layer": best * 1e3, "slots": int(caches[0].count.sum().item())}
         if fmt is not None:
-            rows = c.count.max().item()
+            rows = caches[0].count.max().item()
             ko = torch.empty(B, rows, H, d, dtype=torch.bfloat16, device=dev)
             vo = torch.empty_like(ko)
-            res[name]["read_back_us"] = 1e3 * _time(
-                _graph(lambda: kvp.kvp_read_block8(c, 0, rows, k_out=ko, v_out=vo, status=st)), reps=reps)
+
+            def read_back():
+                for c in caches:
+                    kvp.kvp_read_block8(c, 0, rows, k_out=ko, v_out=vo, status=st)
+
+            res[name]["read_back_us"] = 1e3 * _time(_graph(read_back), reps=reps) / layers
         assert st.item() == 0, kvp.status_string(st.item())
-    return {"workload": "block8_decode: Llama-3-8B layer, batch 16, 8192-token prompt, tau at the 75th percentile, window "
-                        "128, + 64 decode steps of norm and rotation, append, attention; one CUDA graph; the cache in "
-                        "bf16, and in 8 bits with a scale for each page",
+    return {"workload": "block8_decode: Llama-3-8B layers, batch 16, 8192-token prompt, tau at the 75th percentile, window "
+                        "128, + 64 decode steps of norm and rotation, append, attention; one CUDA graph; four layers in "
+                        "turn (more than L2 holds), figures of one; the cache in bf16, and in 8 bits with a scale for "
+                        "each page",
             "prompt_keys_rotation_us": ms_rot * 1e3, **res}
 
 
