@@ -775,10 +775,12 @@ KVP_API kvp_status kvp_append_block8_devpos(int fmt, int mode, int batch, int n_
                                             int32_t* status, void* stream);
 
 /* kvp_read_block8 - slots first_slot .. first_slot + n_slots - 1 of every
- * (b, h) back as bf16 rows (to pass a cache on, or to compact it anew from
- * its remap and expire values): slot s goes to element
+ * (b, h) back as bf16 rows (to pass them on to what takes rows; their positions
+ * are the remap list's): slot s goes to element
  * b*stride_b + (s - first_slot)*stride_t + h*stride_h of k_out and v_out, as
- * code * scale rounded to bf16 (exact unless it is a bf16 subnormal). Slots at
+ * code * scale rounded to bf16 (exact unless it is a bf16 subnormal, or 2^128,
+ * which bf16 holds as infinity: E4M3 rounds magnitudes from 2^128 - 2^123 up to
+ * it, int8 those from 2^128 - 2^121). Slots at
  * or past count[b, h] (clamped to max_pages*16) give zero rows. Expired slots
  * are read like the others. A page id outside [0, n_pages_cap) records
  * KVP_ERR_BOUNDS and its slots give zero rows.

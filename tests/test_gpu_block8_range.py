@@ -127,3 +127,21 @@ def test_values_near_the_smallest_numbers(kvp, fmt, G):
         # values enter scaled down by 2^23 at most), and one at the end
         tol = tol - 1e-37 + (T / 16 + 40) * 2.0**-139 + 2.0**-149
         assert (np.abs(out.double().cpu().numpy()[0] - want) <= tol).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_the_largest_numbers_read_back(kvp, fmt):
+    """Codes whose value is 2^128 read as infinity, those below as themselves."""
+    d = 64
+    rows = [0x7F77, 0x7F7D, 0x7F7F, 0xFF7F]       # 2^128 (1 - 9 / 256), (1 - 3 / 256), (1 - 1 / 256), and its negative
+    kb = np.zeros((1, len(rows), 1, d), np.uint16)
+    kb[0, :, 0, 3] = rows
+    cache, heads = _written(kvp, fmt, kb, kb)
+    k, v = kvp.kvp_read_block8(cache, 0, len(rows))
+    torch.cuda.synchronize()
+    want = heads[0][0].values(0)
+    top = want.max()
+    assert top == 2.0**128 and (np.abs(want[:, 3]) == top).tolist() == [False, fmt == ref.E4M3, True, True]
+    want = np.where(np.abs(want) == top, np.copysign(np.inf, want), want)
+    for got in (k, v):
+        np.testing.assert_array_equal(got[0, :, 0].double().cpu().numpy(), want)
