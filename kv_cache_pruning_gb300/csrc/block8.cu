@@ -249,7 +249,11 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32) list_kernel(
   slot0 = __reduce_add_sync(0xffffffffu, slot0);
   const int pages = (cnt + reserve + kPage - 1) / kPage;
   int32_t* remap_bh = remap + static_cast<int64_t>(bh) * max_pages * kPage;
-  // this segment's share of the page-table row, the owners and the remap tail: table_share pages and their slots
+  // this segment's share of the page-table row, the owners and the remap tail: table_share pages and their slots. A table
+  // wider than the prompt is cleared to its end all the same. Measured on a GB300 (us on the device, heads of 128, half
+  // kept; tables of the prompt's pages / of 8,192): 1 x 100 positions of 8 heads 4.8 / 14.6 (short_kernel), 4 x 1,100 of 8
+  // 8.5 / 12.7, 64 x 128 of 8 11.8 / 63.7 (a warp clears 512 KB; all of it is 268 MB, 40 us at the copy rate), 16 x 8,192
+  // of 8 59.9 / 69.6 (67 MB, 10 us).
   const int p_lo = static_cast<int>(min(static_cast<int64_t>(sg) * table_share, static_cast<int64_t>(max_pages)));
   const int p_hi = p_lo + min(table_share, max_pages - p_lo);
   for (int p = p_lo + lane; p < p_hi; p += 32) {
