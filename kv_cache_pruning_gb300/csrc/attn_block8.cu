@@ -67,7 +67,8 @@ constexpr int kFewPieces = 8;    // CTAs whose partial results of one (b, h) are
 // 11.4, 64 (b, h) 14.7 / 16.1, 17.7 / 18.1, 20.2 / 19.3, 128 (b, h) 42.6 / 46.2, 54.3 / 58.0, 66.7 / 69.7; int8 of 128, 8
 // (b, h) 10.7 / 11.7, 12.9 / 12.0, 14.6 / 11.8, 64 (b, h) 16.0 / 16.7, 19.8 / 18.6, 22.7 / 20.1; E4M3 of 64, 8 (b, h) 7.5 /
 // 9.8, 8.8 / 10.2, 9.8 / 10.1, 64 (b, h) 11.4 / 13.2, 13.8 / 14.5, 15.6 / 15.4; int8 of 64, 64 (b, h) 11.8 / 13.5, 14.4 /
-// 14.9, 16.4 / 15.7. The two are level at 80 (int8 of 128, few (b, h)) to 140 (E4M3 of 64), later with more (b, h).
+// 14.9, 16.4 / 15.7. With 8 and 64 (b, h) the two are level at 80 (int8 of 128) to 140 (E4M3 of 64); with 128, which HBM
+// bounds, at 108 (E4M3 of 64), 155 (int8 of 128) and past 200 (E4M3 of 128), so that right above 96 they lose a little.
 constexpr int kOwnExtra = 96;
 constexpr int kCtaPages = 2 * kWarps;  // fewest pages of an even share: more CTAs would have more to merge
 constexpr int kAhead = 1;        // pages whose lines are brought into L2 before their loads
