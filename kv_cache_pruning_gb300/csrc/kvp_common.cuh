@@ -5,6 +5,9 @@
 // Written from the PTX ISA's descriptions of these instructions.
 #pragma once
 
+#include <algorithm>
+#include <array>
+#include <atomic>
 #include <cstdint>
 #include <mutex>
 #include <utility>
@@ -479,6 +482,51 @@ KVP_DEV uint32_t cvt_f32x2_to_e4m3x2(float lo, float hi) {
 // ---------------------------------------------------------------- bf16 helpers
 KVP_DEV float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 KVP_DEV float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// ---------------------------------------------------------------- host: argument checks, launches, devices
+// Whether rows of `width` values that lie n[i] steps of stride[i] apart along three dimensions never overlap (each
+// dimension's steps clear everything that the dimensions of smaller strides span): a call that writes such rows twice,
+// in an order that nothing fixes, is refused. Dimensions of length 1 have no stride.
+inline bool rows_apart(std::array<std::pair<int64_t, int64_t>, 3> stride_n, int64_t width) {
+  std::sort(stride_n.begin(), stride_n.end());
+  int64_t span = width;
+  for (const auto& [stride, n] : stride_n) {
+    if (n <= 1) continue;
+    if (stride < span || stride > (INT64_MAX - span) / n) return false;
+    span += stride * (n - 1);
+  }
+  return true;
+}
+
+// Launches kern<<<grid, block, 0, st>>>(args...), which starts when the launch before it has ended. Its error is this
+// launch's own: what an earlier call of the caller's has left pending is neither reported here nor taken away.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_after(void (*kern)(KArgs...), dim3 grid, dim3 block, cudaStream_t st, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = st;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+  if (e != cudaSuccess) (void)cudaGetLastError();
+  return e;
+}
+
+// SM count of the current device, whose number goes to *device (0 when it cannot be asked); asked once per device.
+inline int current_sms(int* device) {
+  static std::atomic<int> known[64];
+  int n = 0;
+  if (cudaGetDevice(device) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return 0;
+  }
+  if (*device < 64 && (n = known[*device].load(std::memory_order_relaxed)) != 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, *device) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return 0;
+  }
+  if (*device < 64) known[*device].store(n, std::memory_order_relaxed);
+  return n;
+}
 
 // ---------------------------------------------------------------- host: TMA descriptors
 inline PFN_cuTensorMapEncodeTiled_v12000 tmap_encode_fn() {
