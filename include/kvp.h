@@ -889,6 +889,196 @@ KVP_API kvp_status kvp_qk_norm_rope(int64_t n_tok, int n_q_heads, int n_k_heads,
                                     int64_t qo_stride_t, int64_t qo_stride_h, void* k_out, int64_t ko_stride_t,
                                     int64_t ko_stride_h, void* stream);
 
+/* ------------------------------------------------------------------------ */
+/* Attention over whole prompts, and eviction by what it pays. The cache of the
+ * calls above is pruned by a score for each entry (KVzap summary, "실제 적용") or
+ * a flag (DMS article); the calls below make such a score from the model's own
+ * attention: the weight that an entry has received so far, summed over queries
+ * and over the query heads that share it. The pages name the attention only
+ * (DMS article, "DMS 작동 방식" step 5); keeping the entries of most accumulated
+ * weight is this library's addition beside the keep rules that it had.
+ *
+ *   kvp_prompt_attn      a prompt's attention, with each row's log-sum-exp
+ *   kvp_prompt_weights   from it, the weight that each entry received
+ *   kvp_evict            a prompt's entries within a budget, as the expire
+ *                        values that kvp_compact takes (or scores: laid out by
+ *                        token, the sums are what kvp_threshold and
+ *                        kvp_compact_masked take for scores)
+ *   kvp_decode_attn_acc  a decode step's attention, its weights added to the sums
+ *   kvp_evict_paged      a paged cache's entries within a budget
+ */
+
+/* kvp_prompt_attn - causal attention of every token of several packed prompts
+ * (sequences) over its own sequence:
+ *
+ *   out[t, j] = sum_{t' <= t} softmax_t'(scale * q[t, j] . k[t', h]) v[t', h]
+ *   lse[j, t] = ln sum_{t' <= t} exp(scale * q[t, j] . k[t', h])
+ *
+ * with h = j / (Hq / H), t and t' rows of the same sequence. Sequence s is rows
+ * seq_start[s] .. seq_start[s] + len - 1, len = seq_len[s], or
+ * seq_start[s + 1] - seq_start[s] without seq_len (a padded batch: starts a
+ * fixed step apart, with lengths). Rows of no sequence are neither read for a
+ * result nor written. A masked key or value never touches a row, whatever it
+ * holds (infinities, NaN); a visible NaN makes its row (a value: its column of
+ * the row) NaN, a visible infinite value an infinity or NaN there. A row whose
+ * logits are all -inf comes out zero with lse -inf.
+ *
+ * Sums, maxima and products accumulate in fp32. The softmax weights enter the
+ * product with V as bf16 (relative error <= 2^-8 each; the normaliser sums the
+ * unrounded ones), and out is rounded to bf16 once. Weights are carried at
+ * 2^-28 or less, so that sums of any bf16 values stay in range; values below
+ * 2^-98 lose precision.
+ *
+ * n_seqs     >= 0;  n_tok rows in all, 0 .. 2^31 - 1
+ * n_q_heads  a multiple of n_kv_heads, any quotient; head_dim 64 or 128
+ * q, k, v    device bf16, head h of row t at t*stride_t + h*stride_h elements
+ *            (each tensor its own; multiples of 8, not 0 along a dimension
+ *            longer than 1), 16-byte aligned: views of one projection's output
+ *            need no copy
+ * seq_start  device int32 [n_seqs + 1], ascending from 0 or more to n_tok or less
+ * seq_len    device int32 [n_seqs], 0 .. seq_start[s + 1] - seq_start[s], or NULL.
+ *            A sequence that breaks this records KVP_ERR_BOUNDS in `status` (may
+ *            be NULL) and is left out.
+ * scale      > 0, finite, or 0 for 1/sqrt(head_dim)
+ * out        device bf16, strides as q's, rows that do not overlap (as
+ *            kvp_read_block8's); it may not overlap an input
+ * lse        device fp32 [n_q_heads, n_tok] (output; a head's rows side by side),
+ *            or NULL
+ */
+KVP_API kvp_status kvp_prompt_attn(int n_seqs, int64_t n_tok, int n_q_heads, int n_kv_heads, int head_dim,
+                                   const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k,
+                                   int64_t k_stride_t, int64_t k_stride_h, const void* v, int64_t v_stride_t,
+                                   int64_t v_stride_h, const int32_t* seq_start, const int32_t* seq_len, float scale,
+                                   void* out, int64_t out_stride_t, int64_t out_stride_h, float* lse, int32_t* status,
+                                   void* stream);
+
+/* kvp_prompt_weights - the attention weight that every key of packed prompts
+ * received:
+ *
+ *   acc[t', h] = sum_j sum_{t >= t'} exp(scale * q[t, j] . k[t', h] - lse[j, t])
+ *
+ * over the query heads j of kv head h and the rows t of the same sequence, all
+ * of them, or the last n_last of each sequence (what the end of a prompt looks
+ * at). A query whose lse is -inf pays nothing. Written, not added to, for every
+ * row of every sequence; rows of no sequence are left as they were. Sums are
+ * fp32, of partial sums over 128 queries at most, in a fixed order. A weight is
+ * as good as its lse: |lse| 2^-24 relative.
+ *
+ * n_last     0 for all, or >= 1
+ * lse        device fp32 [n_q_heads, n_tok], as kvp_prompt_attn writes it
+ * acc        device fp32 (output), row t' of sequence s and kv head h at
+ *            s*acc_stride_s + t'*acc_stride_t + h*acc_stride_h elements, t'
+ *            counted from the sequence's start and below acc_len (a longer
+ *            sequence records KVP_ERR_BOUNDS, its rows past acc_len are not
+ *            written); or, with acc_stride_s -1, by token: at
+ *            (seq_start[s] + t')*acc_stride_t + h*acc_stride_h, acc_len unused.
+ *            Elements do not overlap (as kvp_read_block8's rows).
+ * Everything else: as kvp_prompt_attn.
+ */
+KVP_API kvp_status kvp_prompt_weights(int n_seqs, int64_t n_tok, int n_q_heads, int n_kv_heads, int head_dim,
+                                      const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k,
+                                      int64_t k_stride_t, int64_t k_stride_h, const int32_t* seq_start,
+                                      const int32_t* seq_len, const float* lse, float scale, int n_last, float* acc,
+                                      int64_t acc_stride_s, int64_t acc_stride_t, int64_t acc_stride_h, int acc_len,
+                                      int32_t* status, void* stream);
+
+/* kvp_decode_attn_acc - kvp_decode_attn_lse that adds the weights it pays to
+ * running sums by position:
+ *
+ *   acc[b, h, remap[b, h, i]] += sum_j exp(scale * q[b, j] . k_i - lse[b, j])
+ *
+ * over the present slots i of (b, h) and the query heads j of kv head h; sums
+ * of slots that are not present stay as they are. By position, so that they
+ * outlive the slots: a compaction moves entries and their sums stay where they
+ * are. A position outside [0, acc_len) records KVP_ERR_BOUNDS in `status` and
+ * nothing is added for it.
+ *
+ * remap      device int32 [B, H, max_pages*16], as kvp_compact writes it
+ * acc        device fp32, position p of (b, h) at b*acc_stride_b + h*acc_stride_h
+ *            + p elements (strides whose rows of acc_len do not overlap)
+ * lse        device fp32 [B, Hq] (output), or NULL
+ * workspace  as kvp_decode_attn's (zero-filled before its first use; its first
+ *            bytes serve kvp_decode_attn calls of the same sizes as well), of
+ *            kvp_decode_attn_acc_workspace_bytes(...): it also holds a call's
+ *            logits, 4 bytes for each query head and slot
+ * Everything else: as kvp_decode_attn.
+ */
+KVP_API size_t kvp_decode_attn_acc_workspace_bytes(int batch, int n_q_heads, int n_kv_heads, int head_dim,
+                                                   int max_pages);
+KVP_API kvp_status kvp_decode_attn_acc(int batch, int n_q_heads, int n_kv_heads, int head_dim, const void* q,
+                                       const void* k_pool, const void* v_pool, const int32_t* expire_pool,
+                                       int n_pages_cap, const int32_t* page_table, int max_pages,
+                                       const int32_t* remap, const int32_t* count, int now, float scale, float* out,
+                                       float* lse, float* acc, int64_t acc_stride_b, int64_t acc_stride_h,
+                                       int acc_len, int grid_limit, void* workspace, size_t workspace_bytes,
+                                       int32_t* status, void* stream);
+
+/* kvp_decode_attn_acc_devpos - the same with the decode position read from
+ * device memory, as kvp_decode_attn_devpos's.
+ */
+KVP_API kvp_status kvp_decode_attn_acc_devpos(int batch, int n_q_heads, int n_kv_heads, int head_dim, const void* q,
+                                              const void* k_pool, const void* v_pool, const int32_t* expire_pool,
+                                              int n_pages_cap, const int32_t* page_table, int max_pages,
+                                              const int32_t* remap, const int32_t* count, const int32_t* now_dev,
+                                              float scale, float* out, float* lse, float* acc, int64_t acc_stride_b,
+                                              int64_t acc_stride_h, int acc_len, int grid_limit, void* workspace,
+                                              size_t workspace_bytes, int32_t* status, void* stream);
+
+/* kvp_evict - which of a prompt's entries stay within a budget: of each (b, h)
+ * the recent ones (positions t > now - recent), and of the others the
+ * budget - (number of recent ones) of largest acc, the first of equal ones
+ * (-0 equals 0, NaN ranks below -inf). Recent entries stay even where they alone
+ * are more than the budget.
+ *
+ *   expire[b, h, t] = KVP_EXPIRE_NEVER if it stays, now if it goes
+ *
+ * is what kvp_compact takes at step now.
+ *
+ * acc        device fp32, position t of (b, h) at b*stride_b + t*stride_t +
+ *            h*stride_h elements (>= 0)
+ * budget     >= 0;  recent >= 0;  now 0 .. KVP_EXPIRE_NEVER - 1
+ * expire     device int32 [B, H, n_pos] (output)
+ * count      device int32 [B, H] (output or NULL): entries that stay
+ * B*H at most 2^24; n_pos at most 2^31 - 2^16
+ */
+KVP_API kvp_status kvp_evict(int batch, int n_kv_heads, int n_pos, const float* acc, int64_t stride_b,
+                             int64_t stride_t, int64_t stride_h, int budget, int recent, int now, int32_t* expire,
+                             int32_t* count, void* stream);
+
+/* kvp_evict_paged - the same for a paged cache in use (kvp_compact's, or any
+ * other with its tables: 8-bit, or latent with n_kv_heads 1): of the present
+ * slots of each (b, h) (slot < count, expire > now) those whose position is
+ * above now - recent stay, and the budget - (their number) heaviest of the
+ * others, by acc[b, h, position], the first slots of equal ones. A slot that
+ * goes gets expire = now: it is gone for every call at this step or later, and
+ * the next kvp_compact_paged drops it. The other slots' expire values stay.
+ *
+ * acc        device fp32, position p of (b, h) at b*acc_stride_b +
+ *            h*acc_stride_h + p elements (>= 0), as kvp_decode_attn_acc's
+ * kept       device int32 [B, H] (output or NULL): present slots that stay
+ * expire_pool (changed), n_pages_cap, page_table, max_pages, remap, count: as
+ *            kvp_compact writes them; count is clamped to max_pages*16. A page id
+ *            outside [0, n_pages_cap), or a present slot's position outside
+ *            [0, acc_len), records KVP_ERR_BOUNDS in `status` (may be NULL) and
+ *            the slot is left alone, as if it were not present.
+ * B*H at most 2^24
+ */
+KVP_API kvp_status kvp_evict_paged(int batch, int n_kv_heads, const float* acc, int64_t acc_stride_b,
+                                   int64_t acc_stride_h, int acc_len, int32_t* expire_pool, int n_pages_cap,
+                                   const int32_t* page_table, int max_pages, const int32_t* remap,
+                                   const int32_t* count, int budget, int recent, int now, int32_t* kept,
+                                   int32_t* status, void* stream);
+
+/* kvp_evict_paged_devpos - the same with the step read from device memory
+ * (now_dev a device int32, 4-byte aligned). A step below 0, or of
+ * KVP_EXPIRE_NEVER, records KVP_ERR_INVALID in `status` and nothing is changed.
+ */
+KVP_API kvp_status kvp_evict_paged_devpos(int batch, int n_kv_heads, const float* acc, int64_t acc_stride_b,
+                                          int64_t acc_stride_h, int acc_len, int32_t* expire_pool, int n_pages_cap,
+                                          const int32_t* page_table, int max_pages, const int32_t* remap,
+                                          const int32_t* count, int budget, int recent, const int32_t* now_dev,
+                                          int32_t* kept, int32_t* status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

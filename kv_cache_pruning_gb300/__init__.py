@@ -125,6 +125,17 @@ _SIGS = {
     "kvp_rope_turns": (_I, [_I, _P, _P]),
     "kvp_qk_norm_rope": (_I, [_L, _I, _I, _I, _I, _I, _P, _L, _L, _P, _L, _L, _P, _P, _P, _P, _F, _P, _L, _L, _P, _L, _L,
                               _P]),
+    "kvp_prompt_attn": (_I, [_I, _L, _I, _I, _I, _P, _L, _L, _P, _L, _L, _P, _L, _L, _P, _P, _F, _P, _L, _L, _P, _P, _P]),
+    "kvp_prompt_weights": (_I, [_I, _L, _I, _I, _I, _P, _L, _L, _P, _L, _L, _P, _P, _P, _F, _I, _P, _L, _L, _L, _I, _P,
+                                _P]),
+    "kvp_decode_attn_acc_workspace_bytes": (_S, [_I, _I, _I, _I, _I]),
+    "kvp_decode_attn_acc": (_I, [_I, _I, _I, _I, _P, _P, _P, _P, _I, _P, _I, _P, _P, _I, _F, _P, _P, _P, _L, _L, _I, _I,
+                                 _P, _S, _P, _P]),
+    "kvp_decode_attn_acc_devpos": (_I, [_I, _I, _I, _I, _P, _P, _P, _P, _I, _P, _I, _P, _P, _P, _F, _P, _P, _P, _L, _L,
+                                        _I, _I, _P, _S, _P, _P]),
+    "kvp_evict": (_I, [_I, _I, _I, _P, _L, _L, _L, _I, _I, _I, _P, _P, _P]),
+    "kvp_evict_paged": (_I, [_I, _I, _P, _L, _L, _I, _P, _I, _P, _I, _P, _P, _I, _I, _I, _P, _P, _P]),
+    "kvp_evict_paged_devpos": (_I, [_I, _I, _P, _L, _L, _I, _P, _I, _P, _I, _P, _P, _I, _I, _P, _P, _P, _P]),
     "kvp_decode_attn_mla_workspace_bytes": (_S, [_I, _I, _I]),
     "kvp_decode_attn_mla": (_I, [_I, _I, _I, _I, _P, _P, _P, _I, _P, _I, _P, _I, _F, _P, _I, _P, _S, _P, _P]),
 }
@@ -1144,6 +1155,172 @@ def kvp_qk_norm_rope(q, k, pos, turns, *, q_weight=None, k_weight=None, eps=1e-6
           _on(q_weight, _F32, "q_weight", dev, (d,)), _on(k_weight, _F32, "k_weight", dev, (d,)), eps, qo, qo0, qo1, ko,
           ko0, ko1)
     return q_out, k_out
+
+
+# --------------------------------------------------------------------------- attention over prompts, eviction by its weights
+#
+# Tensors are checked as in the two sections above: on one CUDA device, which need not be the current one.
+
+def _device_of(t, name):
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return dev
+
+
+def _seqs(seq_start, seq_len, dev):
+    """(number of sequences, pointer of the starts, pointer of the lengths or None)."""
+    n = seq_start.numel() - 1
+    if n < 0 or seq_start.dim() != 1:
+        raise ValueError("seq_start must be [n_seqs + 1]")
+    return n, _on(seq_start, _I32, "seq_start", dev), _on(seq_len, _I32, "seq_len", dev, (n,))
+
+
+def kvp_prompt_attn(q, k, v, seq_start, *, seq_len=None, scale=0.0, out=None, lse=None, status=None, stream=None):
+    """out [n_tok, Hq, d] bf16 = causal attention of q [n_tok, Hq, d] over k, v [n_tok, H, d] (bf16, any strides with d
+    contiguous: views of one projection need no copy), each packed sequence over itself: rows seq_start[s] ..
+    seq_start[s + 1] - 1 (int32 [n_seqs + 1]), or the first seq_len[s] of them (int32 [n_seqs]). lse (fp32 [Hq, n_tok],
+    if given) receives each row's log-sum-exp, for kvp_prompt_weights."""
+    dev = _device_of(q, "q")
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q and k must be [n_tok, heads, d]")
+    (n, hq, d), h = q.shape, k.shape[1]
+    qp, qs = _rows(q, "q", dev)
+    kp, ks = _rows(k, "k", dev, (n, h, d))
+    vp, vs = _rows(v, "v", dev, (n, h, d))
+    if out is None:
+        out = _new(torch.empty, (n, hq, d), _BF16, dev, stream)
+    op, os_ = _rows(out, "out", dev, (n, hq, d))
+    n_seqs, sp, lp = _seqs(seq_start, seq_len, dev)
+    _call(_lib.kvp_prompt_attn, dev, stream, n_seqs, n, hq, h, d, qp, *qs, kp, *ks, vp, *vs, sp, lp, scale, op, *os_,
+          _on(lse, _F32, "lse", dev, (hq, n)), _status(status, dev))
+    return out
+
+
+def kvp_prompt_weights(q, k, seq_start, lse, *, seq_len=None, scale=0.0, n_last=0, acc=None, status=None, stream=None):
+    """acc fp32: the weight that each key of k [n_tok, H, d] received from the queries q [n_tok, Hq, d] of its sequence
+    (the last n_last of each sequence, 0: all), given kvp_prompt_attn's lse [Hq, n_tok]. acc is [n_tok, H] (the scores
+    that kvp_threshold and kvp_compact_masked take, where sequences are of one length) or [n_seqs, H, T] (the sums by
+    position that kvp_evict and kvp_decode_attn_acc take, T at least the longest sequence), of any strides; None: a new
+    [n_tok, H], zero in rows of no sequence."""
+    dev = _device_of(q, "q")
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q and k must be [n_tok, heads, d]")
+    (n, hq, d), h = q.shape, k.shape[1]
+    qp, qs = _rows(q, "q", dev)
+    kp, ks = _rows(k, "k", dev, (n, h, d))
+    n_seqs, sp, lp = _seqs(seq_start, seq_len, dev)
+    if acc is None:
+        acc = _new(torch.zeros, (n, h), _F32, dev, stream)
+    by_token = acc.dim() == 2
+    if acc.shape != (n, h) if by_token else acc.dim() != 3 or acc.shape[:2] != (n_seqs, h):
+        raise ValueError("acc must be [n_tok, H] or [n_seqs, H, T]")
+    if acc.dtype is not _F32 or acc.get_device() != dev:
+        _refuse(acc, _F32, "acc", dev)
+    st = acc.stride()
+    strides = (-1, st[0], st[1], 0) if by_token else (st[0], st[2], st[1], acc.shape[2])
+    _call(_lib.kvp_prompt_weights, dev, stream, n_seqs, n, hq, h, d, qp, *qs, kp, *ks, sp, lp,
+          _on(lse, _F32, "lse", dev, (hq, n)), scale, n_last, acc.data_ptr(), *strides, _status(status, dev))
+    return acc
+
+
+def _sums(acc, dev, b, h):
+    """(pointer, stride of b, stride of h, length) of weight sums [B, H, T] whose positions lie side by side."""
+    if acc.dim() != 3 or acc.shape[:2] != (b, h):
+        raise ValueError("acc must be [B, H, T]")
+    st, t = acc.stride(), acc.shape[2]
+    if acc.dtype is not _F32 or acc.get_device() != dev or (st[2] != 1 and t > 1):
+        _refuse(acc, _F32, "acc", dev)
+    return acc.data_ptr(), st[0] if b > 1 else 0, st[1] if h > 1 else 0, t
+
+
+def kvp_decode_attn_acc_workspace_bytes(batch, n_q_heads, n_kv_heads, head_dim, max_pages) -> int:
+    return _lib.kvp_decode_attn_acc_workspace_bytes(batch, n_q_heads, n_kv_heads, head_dim, max_pages)
+
+
+def _attn_acc(fn, q, cache, now, acc, scale, out, lse, grid_limit, workspace, status, stream):
+    dev, shape = _device_of(q, "q"), q.shape
+    cap, d = cache.k_pool.shape[0], cache.k_pool.shape[-1]
+    b, h, width = cache.page_table.shape
+    if len(shape) != 3 or shape[0] != b or shape[2] != d:
+        raise ValueError("q must be [B, Hq, d] of the cache's batch and head_dim")
+    hq, pool = shape[1], (cap, PAGE, d)
+    if out is None:
+        out = _new(torch.empty, shape, _F32, dev, stream)
+    ws, ws_bytes = _space(_lib.kvp_decode_attn_acc_workspace_bytes(b, hq, h, d, width), workspace, dev, stream,
+                          torch.zeros)
+    _call(fn, dev, stream, b, hq, h, d, _on(q, _BF16, "q", dev), _on(cache.k_pool, _BF16, "k_pool", dev, pool),
+          _on(cache.v_pool, _BF16, "v_pool", dev, pool), _on(cache.expire_pool, _I32, "expire_pool", dev, (cap, PAGE)),
+          cap, _on(cache.page_table, _I32, "page_table", dev), width,
+          _on(cache.remap, _I32, "remap", dev, (b, h, width * PAGE)), _on(cache.count, _I32, "count", dev, (b, h)), now,
+          scale, _on(out, _F32, "out", dev, shape), _on(lse, _F32, "lse", dev, (b, hq)), *_sums(acc, dev, b, h),
+          grid_limit, ws.data_ptr(), ws_bytes, _status(status, dev))
+    return out
+
+
+def kvp_decode_attn_acc(q, cache: PagedKV, now, acc, *, scale=0.0, out=None, lse=None, grid_limit=0, workspace=None,
+                        status=None, stream=None):
+    """kvp_decode_attn_lse (lse optional) that adds the weights it pays, over the query heads of a kv head, to
+    acc[b, h, position] (fp32 [B, H, T], positions side by side; zeros where none has been paid yet). A caller-provided
+    workspace must be zero-filled before its first use (torch.zeros)."""
+    return _attn_acc(_lib.kvp_decode_attn_acc, q, cache, now, acc, scale, out, lse, grid_limit, workspace, status, stream)
+
+
+def kvp_decode_attn_acc_devpos(q, cache: PagedKV, now_dev, acc, *, scale=0.0, out=None, lse=None, grid_limit=0,
+                               workspace=None, status=None, stream=None):
+    """kvp_decode_attn_acc with the decode position taken from now_dev (a device int32 tensor of one element) when the
+    call runs on the stream."""
+    now = _on(now_dev, _I32, "now_dev", _device_of(q, "q"))
+    return _attn_acc(_lib.kvp_decode_attn_acc_devpos, q, cache, now, acc, scale, out, lse, grid_limit, workspace, status,
+                     stream)
+
+
+def kvp_evict(acc, now, *, budget, recent=WINDOW, expire=None, count=None, stream=None):
+    """(expire int32 [B, H, T], count int32 [B, H]) from weight sums acc (fp32 [B, H, T], any strides): of each (b, h)
+    the last `recent` positions stay, and of the others the heaviest that `budget` leaves room for (the first of equal
+    ones). expire is EXPIRE_NEVER for those and `now` for the rest: kvp_compact at step `now` drops them."""
+    dev = _device_of(acc, "acc")
+    if acc.dim() != 3:
+        raise ValueError("acc must be [B, H, T]")
+    if acc.dtype is not _F32:
+        _refuse(acc, _F32, "acc", dev)
+    b, h, t = acc.shape
+    if expire is None:
+        expire = _new(torch.empty, (b, h, t), _I32, dev, stream)
+    if count is None:
+        count = _new(torch.empty, (b, h), _I32, dev, stream)
+    st = acc.stride()
+    _call(_lib.kvp_evict, dev, stream, b, h, t, acc.data_ptr(), st[0], st[2], st[1], budget, recent, now,
+          _on(expire, _I32, "expire", dev, (b, h, t)), _on(count, _I32, "count", dev, (b, h)))
+    return expire, count
+
+
+def _evict_paged(fn, cache, acc, now, dev, budget, recent, kept, status, stream):
+    table = cache.page_table
+    b, h, width = table.shape if table.dim() == 3 else (table.shape[0], 1, table.shape[1])   # (a latent cache has no heads)
+    cap = cache.expire_pool.shape[0]
+    heads = table.shape[:-1]
+    _call(fn, dev, stream, b, h, *_sums(acc, dev, b, h), _on(cache.expire_pool, _I32, "expire_pool", dev, (cap, PAGE)), cap,
+          _on(table, _I32, "page_table", dev), width, _on(cache.remap, _I32, "remap", dev, (*heads, width * PAGE)),
+          _on(cache.count, _I32, "count", dev, heads), budget, recent, now, _per_head(kept, _I32, "kept", dev, b * h),
+          _status(status, dev))
+    return cache
+
+
+def kvp_evict_paged(cache, acc, now, *, budget, recent=WINDOW, kept=None, status=None, stream=None):
+    """Entries of a paged cache in use (PagedKV, Block8PagedKV or LatentPagedKV) beyond the budget: of each (b, h)'s
+    present slots those of the last `recent` positions stay, and of the others the heaviest by acc[b, h, position]
+    (fp32 [B, H, T], positions side by side) that `budget` leaves room for; the rest expire at `now`. kept (int32
+    [B, H], if given) receives how many stay."""
+    return _evict_paged(_lib.kvp_evict_paged, cache, acc, now, _device_of(acc, "acc"), budget, recent, kept, status, stream)
+
+
+def kvp_evict_paged_devpos(cache, acc, now_dev, *, budget, recent=WINDOW, kept=None, status=None, stream=None):
+    """kvp_evict_paged with the step taken from now_dev (a device int32 tensor of one element) when the call runs on the
+    stream."""
+    dev = _device_of(acc, "acc")
+    return _evict_paged(_lib.kvp_evict_paged_devpos, cache, acc, _on(now_dev, _I32, "now_dev", dev), dev, budget, recent,
+                        kept, status, stream)
 
 
 __all__ = [n for n in dir() if n.startswith(("kvp_", "KVP_", "PagedKV", "QuantPagedKV", "LatentPagedKV",

@@ -89,11 +89,21 @@ struct AttnParams {
   int max_pages_q, n_pages_cap_q;
   const int32_t* now_dev;  // device int32 holding the decode position, or null: `now` is used
   float* lse;              // [B, Hq]: ln of the sum of exp(scaled logits) of each row, or null
+  // accumulating kernels only
+  float* logits;           // [B*H, max_pages, 16, G]: each slot's base-2 logits, -inf where it is not present
+  float2* row_ml;          // [B, Hq]: each row's base-2 reference and its sum
 };
 
 // A row's natural log-sum-exp from its base-2 reference m2 and its sum
 // l = sum 2^(x - m2) of the base-2 logits x (-inf when the row is empty).
 KVP_DEV float row_lse(float m2, float l) { return l > 0.f ? (m2 + log2f(l)) * 0.69314718055994531f : -INFINITY; }
+
+// A finished row's log-sum-exp, and for the accumulating kernels (kA) what its weights are worked out from.
+template <bool kA>
+KVP_DEV void put_row(const AttnParams& p, size_t row, float m2, float l) {
+  if (!kA || p.lse != nullptr) p.lse[row] = row_lse(m2, l);
+  if constexpr (kA) p.row_ml[row] = make_float2(m2, l);
+}
 
 // Eight E4M3 codes (bytes of x then y, element 0 in the lowest byte) to fp32,
 // exactly (every E4M3 value is an fp16 value).
@@ -187,7 +197,7 @@ KVP_DEV int slice_of(int g, int bh, int nw, int64_t c_end) {
 // bring every piece into the ring in one round trip; otherwise the lanes load
 // them from L2 (the staged path holds one piece per lane: npc <= 32). Returns
 // false if a bounded wait gave up.
-template <int D, int G>
+template <int D, int G, bool kA>
 KVP_DEV bool merge_pieces(const AttnParams& p, int cbh, int npc, size_t s0, bool staged, uint8_t* ring,
                           uint64_t* mbar, uint32_t& merge_par, int lane) {
   // every piece of this (b, h) is written: merge them. Lanes take
@@ -239,7 +249,7 @@ KVP_DEV bool merge_pieces(const AttnParams& p, int cbh, int npc, size_t s0, bool
       for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
       L[i] = l;
     }
-    if (p.lse != nullptr && lane < G) {
+    if ((kA || p.lse != nullptr) && lane < G) {
       float mm = M[0], ll = L[0];
 #pragma unroll
       for (int i = 1; i < G; ++i)
@@ -247,7 +257,7 @@ KVP_DEV bool merge_pieces(const AttnParams& p, int cbh, int npc, size_t s0, bool
           mm = M[i];
           ll = L[i];
         }
-      p.lse[static_cast<size_t>(cbh) * G + lane] = row_lse(mm, ll);
+      put_row<kA>(p, static_cast<size_t>(cbh) * G + lane, mm, ll);
     }
     float4 A[FPL];
 #pragma unroll
@@ -367,7 +377,7 @@ KVP_DEV bool merge_pieces(const AttnParams& p, int cbh, int npc, size_t s0, bool
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) L[i] += __shfl_xor_sync(0xffffffffu, L[i], o);
   }
-  if (p.lse != nullptr && lane < G) {
+  if ((kA || p.lse != nullptr) && lane < G) {
     float mm = M[0], ll = L[0];
 #pragma unroll
     for (int i = 1; i < G; ++i)
@@ -375,7 +385,7 @@ KVP_DEV bool merge_pieces(const AttnParams& p, int cbh, int npc, size_t s0, bool
         mm = M[i];
         ll = L[i];
       }
-    p.lse[static_cast<size_t>(cbh) * G + lane] = row_lse(mm, ll);
+    put_row<kA>(p, static_cast<size_t>(cbh) * G + lane, mm, ll);
   }
 #pragma unroll
   for (int k = 0; k < FPL; ++k) {
@@ -401,7 +411,10 @@ KVP_DEV bool merge_pieces(const AttnParams& p, int cbh, int npc, size_t s0, bool
 // columns it covers in a bf16 row, the K row scale multiplies the lane's
 // partial dot product and the V row scale multiplies p in the P.V update (the
 // softmax sum takes p itself); a slot of that tier counts once now >= start.
-template <int D, int G, bool kQ>
+//
+// kA: the accumulating kernel (one tier). Each slot's logits and each finished
+// row's reference and sum go to the workspace, for acc_kernel below.
+template <int D, int G, bool kQ, bool kA>
 __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const AttnParams p) {
   using C = AttnCfg<D, G>;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -780,6 +793,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const AttnPara
     for (int u = 0; u < C::VL; ++u) {
       const float pv = exp2f(x[u] - mh);
       if (s % C::DUP == 0) p_s[rowsel * G * C::RS + idx_base + u] = pv;
+      if constexpr (kA) {
+        const int r = ((idx_base + u) % C::RS) * C::RPS + rowsel;
+        if (s % C::DUP == 0)
+          p.logits[((static_cast<size_t>(cbh) * p.max_pages + li) * kPage + r) * G + (idx_base + u) / C::RS] = x[u];
+      }
     }
     __syncwarp();
 
@@ -817,7 +835,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const AttnPara
       }
       const bool whole = pref[cbh] >= r0 && pref[cbh + 1] <= r1;
       if (whole) {
-        if (p.lse != nullptr && lane < G) {
+        if ((kA || p.lse != nullptr) && lane < G) {
           float mm = m_run[0], ll = lt[0];
 #pragma unroll
           for (int i = 1; i < G; ++i)
@@ -825,7 +843,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const AttnPara
               mm = m_run[i];
               ll = lt[i];
             }
-          p.lse[static_cast<size_t>(cbh) * G + lane] = row_lse(mm, ll);
+          put_row<kA>(p, static_cast<size_t>(cbh) * G + lane, mm, ll);
         }
         if (rowsel == 0) {
 #pragma unroll
@@ -871,7 +889,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const AttnPara
           constexpr int kRingPieces = (kNst * C::STAGE_BYTES - 32) / (kAccB + kMlB);
           constexpr int kStaged = kRingPieces < 32 ? kRingPieces : 32;
           const int npc = w_last - w_first + 1;
-          if (!merge_pieces<D, G>(p, cbh, npc, static_cast<size_t>(w_first) + cbh, g + 1 == r1 && npc <= kStaged,
+          if (!merge_pieces<D, G, kA>(p, cbh, npc, static_cast<size_t>(w_first) + cbh, g + 1 == r1 && npc <= kStaged,
                                   ring, &bars[kNst], merge_par, lane))
             return;
         }
@@ -965,7 +983,9 @@ KVP_DEV uint32_t bf16x2_to_f16x2(uint32_t w) {
 // K row scale applies to S; the V row scale is folded into p, which enters
 // the product as one fp16 value (11 bits; the bf16 pages take p as a bf16
 // hi + lo pair).
-template <int D, int G, bool kQ>
+//
+// kA: the accumulating kernel (one tier), as attn_decode_kernel's.
+template <int D, int G, bool kQ, bool kA>
 __global__ void __launch_bounds__(kThreads, 1) attn_mma_kernel(const AttnParams p,
                                                                const __grid_constant__ CUtensorMap tmK,
                                                                const __grid_constant__ CUtensorMap tmV,
@@ -1390,6 +1410,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_mma_kernel(const AttnParams 
     x[1] = v0 ? sacc[1] * sc0 : -INFINITY;
     x[2] = v1 ? sacc[2] * sc1 : -INFINITY;
     x[3] = v1 ? sacc[3] * sc1 : -INFINITY;
+    if constexpr (kA) {  // tokens g and g + 8, heads 2t and 2t + 1: two heads a store
+      static_assert(G % 2 == 0, "heads in pairs");
+      if (2 * tq < G) {
+        float* at = p.logits + ((static_cast<size_t>(cbh) * p.max_pages + li) * kPage + gq) * G + 2 * tq;
+        *reinterpret_cast<float2*>(at) = make_float2(x[0], x[1]);
+        *reinterpret_cast<float2*>(at + 8 * G) = make_float2(x[2], x[3]);
+      }
+    }
     const bool grow = x[0] > m2[0] + kLazyRescale || x[2] > m2[0] + kLazyRescale || x[1] > m2[1] + kLazyRescale ||
                       x[3] > m2[1] + kLazyRescale;
     if (__any_sync(0xffffffffu, grow)) {
@@ -1493,9 +1521,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_mma_kernel(const AttnParams 
       if (whole) {
         const float i0 = lt0 > 0.f ? 1.f / lt0 : 0.f, i1 = lt1 > 0.f ? 1.f / lt1 : 0.f;
         float* ob = p.out + static_cast<size_t>(cbh) * G * D;
-        if (p.lse != nullptr && gq == 0) {
-          if (h0 < G) p.lse[static_cast<size_t>(cbh) * G + h0] = row_lse(m2[0], lt0);
-          if (h1 < G) p.lse[static_cast<size_t>(cbh) * G + h1] = row_lse(m2[1], lt1);
+        if ((kA || p.lse != nullptr) && gq == 0) {
+          if (h0 < G) put_row<kA>(p, static_cast<size_t>(cbh) * G + h0, m2[0], lt0);
+          if (h1 < G) put_row<kA>(p, static_cast<size_t>(cbh) * G + h1, m2[1], lt1);
         }
 #pragma unroll
         for (int mt = 0; mt < KS; ++mt) {
@@ -1546,7 +1574,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_mma_kernel(const AttnParams 
           constexpr int kRingPieces = (kNst * C::STAGE_BYTES - 32) / (kAccB + kMlB);
           constexpr int kStaged = kRingPieces < 32 ? kRingPieces : 32;
           const int npc = w_last - w_first + 1;
-          if (!merge_pieces<D, G>(p, cbh, npc, static_cast<size_t>(w_first) + cbh, g + 1 == r1 && npc <= kStaged,
+          if (!merge_pieces<D, G, kA>(p, cbh, npc, static_cast<size_t>(w_first) + cbh, g + 1 == r1 && npc <= kStaged,
                                   ring, &bars[kNst], merge_par, lane))
             return;
         }
@@ -1579,11 +1607,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_mma_kernel(const AttnParams 
 
 // Grid of the persistent kernel on this process's device: one CTA per SM
 // times the CTAs an SM holds, computed once (with the shared-memory opt-in).
-template <int D, int G, bool kQ>
+template <int D, int G, bool kQ, bool kA>
 int attn_grid() {
   static const int grid = [] {
     using C = AttnCfg<D, G>;
-    auto kern = attn_decode_kernel<D, G, kQ>;
+    auto kern = attn_decode_kernel<D, G, kQ, kA>;
     int dev = 0, nsm = 0, occ = 0;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess ||
         cudaGetDevice(&dev) != cudaSuccess ||
@@ -1595,22 +1623,22 @@ int attn_grid() {
   return grid;
 }
 
-template <int D, int G, bool kQ>
+template <int D, int G, bool kQ, bool kA>
 kvp_status launch_attn(const AttnParams& p, int grid_limit, cudaStream_t st) {
   using C = AttnCfg<D, G>;
-  int grid = attn_grid<D, G, kQ>();
+  int grid = attn_grid<D, G, kQ, kA>();
   if (grid <= 0) return KVP_ERR_CUDA;
   if (grid_limit > 0 && grid > grid_limit) grid = grid_limit;
-  if (launch_pdl(attn_decode_kernel<D, G, kQ>, dim3(grid), dim3(kThreads), C::SMEM, st, p) != cudaSuccess)
+  if (launch_pdl(attn_decode_kernel<D, G, kQ, kA>, dim3(grid), dim3(kThreads), C::SMEM, st, p) != cudaSuccess)
     return KVP_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
 }
 
-template <int D, int G, bool kQ>
+template <int D, int G, bool kQ, bool kA>
 int attn_mma_grid() {
   static const int grid = [] {
     using C = MmaCfg<D>;
-    auto kern = attn_mma_kernel<D, G, kQ>;
+    auto kern = attn_mma_kernel<D, G, kQ, kA>;
     int dev = 0, nsm = 0, occ = 0;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess ||
         cudaGetDevice(&dev) != cudaSuccess ||
@@ -1622,23 +1650,24 @@ int attn_mma_grid() {
   return grid;
 }
 
-template <int D, int G, bool kQ>
+template <int D, int G, bool kQ, bool kA>
 kvp_status launch_attn_mma(const AttnParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV,
                            const CUtensorMap& tmKq, const CUtensorMap& tmVq, int grid_limit, cudaStream_t st) {
   using C = MmaCfg<D>;
-  int grid = attn_mma_grid<D, G, kQ>();
+  int grid = attn_mma_grid<D, G, kQ, kA>();
   if (grid <= 0) return KVP_ERR_CUDA;
   if (grid_limit > 0 && grid > grid_limit) grid = grid_limit;
-  if (launch_pdl(attn_mma_kernel<D, G, kQ>, dim3(grid), dim3(kThreads), C::SMEM, st, p, tmK, tmV, tmKq, tmVq) !=
+  if (launch_pdl(attn_mma_kernel<D, G, kQ, kA>, dim3(grid), dim3(kThreads), C::SMEM, st, p, tmK, tmV, tmKq, tmVq) !=
       cudaSuccess)
     return KVP_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
 }
 
-template <int D, bool kQ>
+template <int D, bool kQ, bool kA>
 kvp_status dispatch_mma(const AttnParams& p, int G, int grid_limit, cudaStream_t st) {
   CUtensorMap tmK, tmV;
-  const int64_t rows = static_cast<int64_t>(p.n_pages_cap) * kPage;
+  // (a pool without pages takes no copy: its map stands for one row that is never read)
+  const int64_t rows = p.n_pages_cap > 0 ? static_cast<int64_t>(p.n_pages_cap) * kPage : 1;
   if (!make_tmap_bf16(&tmK, p.k_pool, rows, D, D, kPage, 64) || !make_tmap_bf16(&tmV, p.v_pool, rows, D, D, kPage, 64))
     return KVP_ERR_CUDA;
   // the fp8 tier's K and V codes, 16 rows a box (a pool with no pages takes no copy: the bf16 maps stand in)
@@ -1648,23 +1677,90 @@ kvp_status dispatch_mma(const AttnParams& p, int G, int grid_limit, cudaStream_t
       (!make_tmap_u8_rows(&tmKq, p.kq_pool, rows_q, D, kPage) || !make_tmap_u8_rows(&tmVq, p.vq_pool, rows_q, D, kPage)))
     return KVP_ERR_CUDA;
   if constexpr (kQ) {
-    if (G == 1) return launch_attn_mma<D, 1, kQ>(p, tmK, tmV, tmKq, tmVq, grid_limit, st);
-    if (G == 2) return launch_attn_mma<D, 2, kQ>(p, tmK, tmV, tmKq, tmVq, grid_limit, st);
+    if (G == 1) return launch_attn_mma<D, 1, kQ, false>(p, tmK, tmV, tmKq, tmVq, grid_limit, st);
+    if (G == 2) return launch_attn_mma<D, 2, kQ, false>(p, tmK, tmV, tmKq, tmVq, grid_limit, st);
   }
-  if (G == 4) return launch_attn_mma<D, 4, kQ>(p, tmK, tmV, tmKq, tmVq, grid_limit, st);
+  if (G == 4) return launch_attn_mma<D, 4, kQ, kA>(p, tmK, tmV, tmKq, tmVq, grid_limit, st);
   if (G != 8) return KVP_ERR_UNSUPPORTED;
-  return launch_attn_mma<D, 8, kQ>(p, tmK, tmV, tmKq, tmVq, grid_limit, st);
+  return launch_attn_mma<D, 8, kQ, kA>(p, tmK, tmV, tmKq, tmVq, grid_limit, st);
 }
 
 template <int D, bool kQ>
 kvp_status dispatch_g(const AttnParams& p, int G, int grid_limit, cudaStream_t st) {
   switch (G) {
-    case 1: return launch_attn<D, 1, kQ>(p, grid_limit, st);
-    case 2: return launch_attn<D, 2, kQ>(p, grid_limit, st);
-    case 4: return launch_attn<D, 4, kQ>(p, grid_limit, st);
-    case 8: return launch_attn<D, 8, kQ>(p, grid_limit, st);
+    case 1: return launch_attn<D, 1, kQ, false>(p, grid_limit, st);
+    case 2: return launch_attn<D, 2, kQ, false>(p, grid_limit, st);
+    case 4: return launch_attn<D, 4, kQ, false>(p, grid_limit, st);
+    case 8: return launch_attn<D, 8, kQ, false>(p, grid_limit, st);
     default: return KVP_ERR_UNSUPPORTED;
   }
+}
+
+// Accumulating calls of 1 and 2 query heads per kv head (from 4 on they go to the tensor-core kernel).
+template <int D>
+kvp_status dispatch_acc(const AttnParams& p, int G, int grid_limit, cudaStream_t st) {
+  switch (G) {
+    case 1: return launch_attn<D, 1, false, true>(p, grid_limit, st);
+    case 2: return launch_attn<D, 2, false, true>(p, grid_limit, st);
+    default: return KVP_ERR_UNSUPPORTED;
+  }
+}
+
+// Where an accumulating call's weights go.
+struct AccArgs {
+  float* logits;          // workspace
+  float2* row_ml;
+  const int32_t* remap;   // [B, H, max_pages * 16]: position of a slot
+  float* acc;             // weight sums by position
+  int64_t stride_b, stride_h;
+  int acc_len;
+};
+
+// acc[b, h, position of slot i] += sum over the kv head's G query heads of
+// 2^(x_i - m) / l, from the logits x and each row's (m, l) that the attention
+// kernel left: the softmax weights themselves, once the whole row is known.
+// One thread a slot, so that a sum takes its one addition a call in a fixed
+// order, without atomics. A slot that was not present has x = -inf and is left
+// alone. Reads 4 G + 4 bytes of logits and position and reads and writes 4 of
+// the sum, where the attention before it reads 4 D + 4: at D = 128 and G = 4
+// 5 % more bytes, most of them out of L2.
+constexpr int kAccThreads = 256;
+template <int G>
+__global__ void __launch_bounds__(kAccThreads) acc_kernel(const AttnParams p, const AccArgs a) {
+  pdl_wait();
+  const int bh = blockIdx.y;
+  const int slot = blockIdx.x * kAccThreads + threadIdx.x;
+  if (slot >= clamp_count(p.count, bh, p.max_pages)) return;
+  const size_t at = static_cast<size_t>(bh) * p.max_pages * kPage + slot;
+  float x[G];
+#pragma unroll
+  for (int i = 0; i < G; ++i) x[i] = __ldcg(p.logits + at * G + i);
+  float w = 0.f;
+  bool present = false;
+#pragma unroll
+  for (int i = 0; i < G; ++i) {
+    const float2 ml = __ldcg(p.row_ml + static_cast<size_t>(bh) * G + i);
+    present |= !(x[i] == -INFINITY);
+    if (ml.y != 0.f) w += exp2f(x[i] - ml.x) / ml.y;  // 0: a row without a finite logit pays nothing
+  }
+  if (!present) return;
+  const int pos = a.remap[at];
+  if (pos < 0 || pos >= a.acc_len) {
+    record_error(p.status, KVP_ERR_BOUNDS);
+    return;
+  }
+  float* sum = a.acc + (bh / p.H) * a.stride_b + (bh % p.H) * a.stride_h + pos;
+  *sum += w;
+}
+
+kvp_status launch_acc(const AttnParams& p, int G, const AccArgs& a, cudaStream_t st) {
+  const int64_t slots = static_cast<int64_t>(p.max_pages) * kPage;
+  if (slots == 0) return KVP_OK;
+  const dim3 grid(static_cast<unsigned>((slots + kAccThreads - 1) / kAccThreads), static_cast<unsigned>(p.B * p.H));
+  auto go = [&](auto kern) {
+    return launch_pdl(kern, grid, dim3(kAccThreads), 0, st, p, a) == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
+  };
+  return G == 1 ? go(acc_kernel<1>) : G == 2 ? go(acc_kernel<2>) : G == 4 ? go(acc_kernel<4>) : go(acc_kernel<8>);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -1716,7 +1812,8 @@ kvp_status decode_attn_impl(int batch, int n_q_heads, int n_kv_heads, int head_d
                             const void* v_pool, const int32_t* expire_pool, int n_pages_cap,
                             const int32_t* page_table, int max_pages, const int32_t* count, const QuantTier* qt,
                             int now, const int32_t* now_dev, float scale, float* out, float* lse, int grid_limit,
-                            void* workspace, size_t workspace_bytes, int32_t* status, void* stream) {
+                            void* workspace, size_t workspace_bytes, int32_t* status, void* stream,
+                            const AccArgs* ac = nullptr) {
   if (batch <= 0 || n_q_heads <= 0 || n_kv_heads <= 0 || max_pages < 0 || grid_limit < 0 || n_pages_cap < 0)
     return KVP_ERR_INVALID;
   if (n_q_heads % n_kv_heads != 0) return KVP_ERR_INVALID;
@@ -1779,7 +1876,21 @@ kvp_status decode_attn_impl(int batch, int n_q_heads, int n_kv_heads, int head_d
                qt ? qt->max_pages : 0,
                qt ? qt->n_pages_cap : 0,
                now_dev,
-               lse};
+               lse,
+               ac ? ac->logits : nullptr,
+               ac ? ac->row_ml : nullptr};
+  if (ac != nullptr) {
+    // as below: pools of 2^31 rows and more do not fit the device
+    if (static_cast<int64_t>(n_pages_cap) * kPage > 0x7fffffff) return KVP_ERR_UNSUPPORTED;
+    kvp_status r;
+    if (G >= 4) {
+      r = head_dim == 128 ? dispatch_mma<128, false, true>(p, G, grid_limit, st)
+                          : dispatch_mma<64, false, true>(p, G, grid_limit, st);
+    } else {
+      r = head_dim == 128 ? dispatch_acc<128>(p, G, grid_limit, st) : dispatch_acc<64>(p, G, grid_limit, st);
+    }
+    return r == KVP_OK ? launch_acc(p, G, *ac, st) : r;
+  }
   // Eight query heads per kv head go to the tensor-core kernel: with the
   // CUDA-core page math a page takes twice the multiply-adds of G = 4 and the
   // kernel is bound by instruction issue (measured on a GB300, Llama-3-8B
@@ -1797,11 +1908,11 @@ kvp_status decode_attn_impl(int batch, int n_q_heads, int n_kv_heads, int head_d
                    static_cast<int64_t>(n_pages_cap) * kPage <= 0x7fffffff;
   if (qt != nullptr) {
     if (mma)
-      return head_dim == 128 ? dispatch_mma<128, true>(p, G, grid_limit, st) : dispatch_mma<64, true>(p, G, grid_limit, st);
+      return head_dim == 128 ? dispatch_mma<128, true, false>(p, G, grid_limit, st) : dispatch_mma<64, true, false>(p, G, grid_limit, st);
     return head_dim == 128 ? dispatch_g<128, true>(p, G, grid_limit, st) : dispatch_g<64, true>(p, G, grid_limit, st);
   }
   if (mma)
-    return head_dim == 128 ? dispatch_mma<128, false>(p, G, grid_limit, st) : dispatch_mma<64, false>(p, G, grid_limit, st);
+    return head_dim == 128 ? dispatch_mma<128, false, false>(p, G, grid_limit, st) : dispatch_mma<64, false, false>(p, G, grid_limit, st);
   return head_dim == 128 ? dispatch_g<128, false>(p, G, grid_limit, st) : dispatch_g<64, false>(p, G, grid_limit, st);
 }
 }  // namespace
@@ -1852,6 +1963,68 @@ extern "C" kvp_status kvp_decode_attn_two_tier(int batch, int n_q_heads, int n_k
   return decode_attn_impl(batch, n_q_heads, n_kv_heads, head_dim, q, k_pool, v_pool, expire_pool, n_pages_cap,
                           page_table, max_pages, count, &qt, now, nullptr, scale, out, nullptr, grid_limit,
                           workspace, workspace_bytes, status, stream);
+}
+
+// ---------------------------------------------------------------- adding the weights up
+namespace {
+// workspace of an accumulating call: kvp_decode_attn's (its counters first), then each row's (m, l), then the logits
+size_t acc_ws_rows(int batch, int n_q_heads) { return round16(static_cast<size_t>(batch) * n_q_heads * sizeof(float2)); }
+
+kvp_status decode_attn_acc_impl(int batch, int n_q_heads, int n_kv_heads, int head_dim, const void* q,
+                                const void* k_pool, const void* v_pool, const int32_t* expire_pool, int n_pages_cap,
+                                const int32_t* page_table, int max_pages, const int32_t* remap, const int32_t* count,
+                                int now, const int32_t* now_dev, float scale, float* out, float* lse, float* acc,
+                                int64_t acc_stride_b, int64_t acc_stride_h, int acc_len, int grid_limit,
+                                void* workspace, size_t workspace_bytes, int32_t* status, void* stream) {
+  if (remap == nullptr || acc == nullptr) return KVP_ERR_INVALID;
+  if (acc_len < 0 || acc_stride_b < 0 || acc_stride_h < 0) return KVP_ERR_INVALID;
+  if ((reinterpret_cast<uintptr_t>(acc) & 3u) != 0) return KVP_ERR_ALIGN;
+  if (!rows_apart({{{acc_stride_b, batch}, {acc_stride_h, n_kv_heads}, {0, 1}}}, acc_len)) return KVP_ERR_INVALID;
+  const size_t need = kvp_decode_attn_acc_workspace_bytes(batch, n_q_heads, n_kv_heads, head_dim, max_pages);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return KVP_ERR_WORKSPACE;
+  if (need > 0 && !aligned16(workspace)) return KVP_ERR_ALIGN;
+  const size_t base = round16(kvp_decode_attn_workspace_bytes(batch, n_q_heads, n_kv_heads, head_dim));
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const AccArgs ac{reinterpret_cast<float*>(ws + base + acc_ws_rows(batch, n_q_heads)),
+                   reinterpret_cast<float2*>(ws + base), remap, acc, acc_stride_b, acc_stride_h, acc_len};
+  return decode_attn_impl(batch, n_q_heads, n_kv_heads, head_dim, q, k_pool, v_pool, expire_pool, n_pages_cap,
+                          page_table, max_pages, count, nullptr, now, now_dev, scale, out, lse, grid_limit, workspace,
+                          workspace_bytes, status, stream, &ac);
+}
+}  // namespace
+
+extern "C" size_t kvp_decode_attn_acc_workspace_bytes(int batch, int n_q_heads, int n_kv_heads, int head_dim,
+                                                      int max_pages) {
+  const size_t base = kvp_decode_attn_workspace_bytes(batch, n_q_heads, n_kv_heads, head_dim);
+  if (base == 0 || max_pages < 0) return 0;
+  return round16(base) + acc_ws_rows(batch, n_q_heads) +
+         static_cast<size_t>(batch) * n_q_heads * max_pages * kPage * sizeof(float);
+}
+
+extern "C" kvp_status kvp_decode_attn_acc(int batch, int n_q_heads, int n_kv_heads, int head_dim, const void* q,
+                                          const void* k_pool, const void* v_pool, const int32_t* expire_pool,
+                                          int n_pages_cap, const int32_t* page_table, int max_pages,
+                                          const int32_t* remap, const int32_t* count, int now, float scale, float* out,
+                                          float* lse, float* acc, int64_t acc_stride_b, int64_t acc_stride_h,
+                                          int acc_len, int grid_limit, void* workspace, size_t workspace_bytes,
+                                          int32_t* status, void* stream) {
+  return decode_attn_acc_impl(batch, n_q_heads, n_kv_heads, head_dim, q, k_pool, v_pool, expire_pool, n_pages_cap,
+                              page_table, max_pages, remap, count, now, nullptr, scale, out, lse, acc, acc_stride_b,
+                              acc_stride_h, acc_len, grid_limit, workspace, workspace_bytes, status, stream);
+}
+
+extern "C" kvp_status kvp_decode_attn_acc_devpos(int batch, int n_q_heads, int n_kv_heads, int head_dim, const void* q,
+                                                 const void* k_pool, const void* v_pool, const int32_t* expire_pool,
+                                                 int n_pages_cap, const int32_t* page_table, int max_pages,
+                                                 const int32_t* remap, const int32_t* count, const int32_t* now_dev,
+                                                 float scale, float* out, float* lse, float* acc,
+                                                 int64_t acc_stride_b, int64_t acc_stride_h, int acc_len,
+                                                 int grid_limit, void* workspace, size_t workspace_bytes,
+                                                 int32_t* status, void* stream) {
+  if (now_dev == nullptr) return KVP_ERR_INVALID;
+  return decode_attn_acc_impl(batch, n_q_heads, n_kv_heads, head_dim, q, k_pool, v_pool, expire_pool, n_pages_cap,
+                              page_table, max_pages, remap, count, 0, now_dev, scale, out, lse, acc, acc_stride_b,
+                              acc_stride_h, acc_len, grid_limit, workspace, workspace_bytes, status, stream);
 }
 
 // ---------------------------------------------------------------- merging partial attention
