@@ -59,15 +59,16 @@ KVP_DEV int seq_rows(const Seqs& s, int i, int& start) {
   return len;
 }
 
-// Tile number `idx` of all sequences' (a whole warp calls this); false past the last.
-KVP_DEV bool find_tile(const Seqs& s, int idx, Tile& t) {
+// Number `idx` of all sequences' tiles of `tile` rows, each sequence's last tile first (a whole warp calls this); false
+// past the last.
+KVP_DEV bool find_tile(const Seqs& s, int tile, int idx, Tile& t) {
   const int lane = threadIdx.x & 31;
   int before = 0;
   for (int base = 0; base < s.n; base += 32) {
     const int i = base + lane;
     int start = 0;
     const int len = i < s.n ? seq_rows(s, i, start) : 0;
-    const int tiles = (len + kTile - 1) / kTile;
+    const int tiles = (len + tile - 1) / tile;
     int incl = tiles;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -80,7 +81,7 @@ KVP_DEV bool find_tile(const Seqs& s, int idx, Tile& t) {
       t.seq = base + src;
       t.start = __shfl_sync(0xffffffffu, start, src);
       t.len = __shfl_sync(0xffffffffu, len, src);
-      t.r = idx - before - __shfl_sync(0xffffffffu, incl - tiles, src);
+      t.r = before + __shfl_sync(0xffffffffu, incl, src) - 1 - idx;
       return true;
     }
     before += __shfl_sync(0xffffffffu, incl, 31);
@@ -104,36 +105,490 @@ KVP_DEV float dot(const float (&a)[D / 32], const float (&b)[D / 32]) {
   return s;
 }
 
+// ---------------------------------------------------------------- attention
+// S = Q K^T and O += P V on tcgen05, 128 query rows x 128 keys a step, two such
+// query tiles (A and B) a CTA so that the tensor cores work on one while the
+// softmax of the other runs. The tiles share their K and V: they are two query
+// heads of one kv head over the same 128 rows (G even), or 256 rows of one head
+// (G odd; the second may be past the end). Tensor memory holds S and O of both
+// (512 columns at D = 128); P, rounded to bf16, overwrites its S.
+//
+// Warps 0-3 and 4-7 are the softmax of A and B: a thread owns a row, so that
+// maxima and sums need no exchange. Warp 8 issues the products, warp 9 the
+// copies: K and V tiles of 128 rows through one ring. Tiles and key blocks start
+// with the sequence, so only a tile's last block is masked.
+//
+// The reference M of a row's weights 2^(x c - M), c = scale log2 e, is its first
+// block's maximum and moves only when a later one passes it by 2^8; then the
+// softmax warps rescale O themselves (a block's S is complete only after the
+// products of the block before).
+//
+// A masked weight is 0, but 0 times an infinite or NaN value is NaN: before the
+// products of the masked block its V tile is searched, such values are zeroed,
+// and the first row that holds one is noted for each column, for the rows that
+// do see it.
 template <int D>
-__global__ void __launch_bounds__(kPWarps * 32) prompt_attn_kernel(const PromptParams p) {
-  pdl_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int j = blockIdx.y, h = j / p.G;
-  Tile t;
-  if (!find_tile(p.seqs, blockIdx.x, t)) return;
-  for (int r = t.r * kTile + warp; r < min(t.len, (t.r + 1) * kTile); r += kPWarps) {
-    const int64_t row = t.start + r;
-    float q[D / 32], o[D / 32] = {}, m = -INFINITY, l = 0.f;
-    load_row<D>(p.q + row * p.qt + j * p.qh, q);
-    for (int c = 0; c <= r; ++c) {
-      float k[D / 32], v[D / 32];
-      load_row<D>(p.k + (t.start + c) * p.kt + h * p.kh, k);
-      load_row<D>(p.v + (t.start + c) * p.vt + h * p.vh, v);
-      const float x = dot<D>(q, k) * p.qscale;
-      const float mn = fmaxf(m, x), ref = mn == -INFINITY ? 0.f : mn;
-      const float al = exp2f(m - ref), w = exp2f(x - ref - kHeadroom);
-      m = mn;
-      l = l * al + w;
+struct AttnCfg {
+  static constexpr int kBoxes = D / 64;
+  static constexpr int kBoxBytes = kTile * 128;          // 128 rows x 64 columns
+  static constexpr int kTileBytes = kBoxes * kBoxBytes;  // one tile of Q, K or V
+  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kQOff = 0;
+  static constexpr int kRingOff = 2 * kTileBytes;
+  static constexpr int kBadOff = kRingOff + kStages * kTileBytes;  // first row with +inf, -inf, NaN of each column
+  static constexpr int kBarOff = kBadOff + 3 * D * 4;
+  static constexpr int kBars = 1 + 2 * kStages + 2 + 2 + 2 + 1;
+  static constexpr int kSmem = 1024 + kBarOff + kBars * 8 + 32;
+  static_assert(kSmem <= 232448, "shared memory budget");
+  static_assert(kBarOff % 8 == 0, "alignment");
+};
+constexpr int kSoftWarps = 8, kMmaWarp = 8, kCopyWarp = 9;
+constexpr int kAttnThreads = 384;             // warps 10 and 11 only give their registers away
+// A row's 128 logits stay in registers: the softmax warps take 232 each and the
+// others 40, of the 168 a thread that the block is launched with:
+// 256 x 232 + 128 x 40 = 384 x 168.
+constexpr int kRegsSoft = 232, kRegsRest = 40;
+constexpr uint32_t kSCol = 0, kOCol = 256;  // S (and P) of A, B at 0, 128; O at 256, 384
+constexpr uint32_t kTmemCols = 512;
+constexpr float kLazy = 8.f;                // how far a row's maximum may pass its reference (base 2)
+constexpr float kBig = 268435456.f;         // from references of 2^28 on, x c - M is taken as (x - max) c
+
+// Two fp32 values as one register pair: packed arithmetic of sm_100 and later.
+KVP_DEV uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+KVP_DEV void unpack2(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+KVP_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+KVP_DEV uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+KVP_DEV uint32_t bf16x2(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// Searches the V tile of 128 rows at `tile` (swizzled boxes) for infinities and NaN (128 threads call this, thread t
+// row t): they become zeros, and rows below `rows` note their position in bad[kind][column].
+template <int D>
+KVP_DEV void clear_bad_values(uint8_t* tile, int t, int pos, bool inside, int* bad) {
+  using C = AttnCfg<D>;
+#pragma unroll 4
+  for (int c = 0; c < D / 8; ++c) {
+    uint4* at = reinterpret_cast<uint4*>(tile + (c >> 3) * C::kBoxBytes + t * 128 + (((c & 7) ^ (t & 7)) << 4));
+    const uint4 w = *at;
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+    bool any = false;
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) o[i] = fmaf(w, v[i], o[i] * al);
+    for (int i = 0; i < 4; ++i) any |= (x[i] & 0x7F80u) == 0x7F80u || (x[i] & 0x7F800000u) == 0x7F800000u;
+    if (!any) continue;
+    uint32_t y[4];
+    for (int i = 0; i < 4; ++i) {
+      y[i] = x[i];
+      for (int half = 0; half < 2; ++half) {
+        const uint32_t v = (x[i] >> (16 * half)) & 0xFFFFu;
+        if ((v & 0x7F80u) != 0x7F80u) continue;
+        y[i] &= half ? 0x0000FFFFu : 0xFFFF0000u;
+        const int kind = (v & 0x7Fu) != 0 ? 2 : (v >> 15);
+        if (inside) atomicMin(&bad[kind * D + c * 8 + 2 * i + half], pos);
+      }
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i)
-      p.out[row * p.ot + j * p.oh + i * 32 + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(o[i] * inv));
-    if (p.lse != nullptr && lane == 0)
-      p.lse[j * p.seqs.n_tok + row] = l == 0.f ? -INFINITY : (m + kHeadroom + log2f(l)) * kLn2;
+    *at = make_uint4(y[0], y[1], y[2], y[3]);
   }
+}
+
+struct AttnMaps {
+  CUtensorMap q, k, v;  // [D, heads, rows], boxes of 64 x 1 x 128
+};
+
+template <int D>
+__global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const PromptParams p,
+                                                                      const __grid_constant__ AttnMaps maps) {
+  using C = AttnCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int* bad = reinterpret_cast<int*>(smem + C::kBadOff);
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
+  uint64_t* full = q_full + 1;
+  uint64_t* empty = full + C::kStages;
+  uint64_t* s_full = empty + C::kStages;  // [A, B]
+  uint64_t* p_full = s_full + 2;
+  uint64_t* o_full = p_full + 2;
+  uint64_t* fin = o_full + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(fin + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* s_tile = reinterpret_cast<int*>(tmem_slot + 2);  // start, length, first tile (-1: none)
+
+  if (tid == 0) {
+    mbar_init(q_full, 1);
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&s_full[x], 1);
+      mbar_init(&p_full[x], 4);
+      mbar_init(&o_full[x], 1);
+    }
+    mbar_init(fin, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&maps.q);
+    prefetch_tmap(&maps.k);
+    prefetch_tmap(&maps.v);
+  }
+  for (int i = tid; i < 3 * D; i += kAttnThreads) bad[i] = INT32_MAX;
+  if (warp == kMmaWarp) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  const bool by_head = p.G % 2 == 0;
+  const int cols = by_head ? p.Hq / 2 : p.Hq;  // work items of one tile
+  const int item = blockIdx.x / cols, col = blockIdx.x % cols;
+  if (warp == 0) {
+    Tile t;
+    const bool some = find_tile(p.seqs, by_head ? kTile : 2 * kTile, item, t);
+    if (lane == 0) {
+      s_tile[0] = some ? t.start : 0;
+      s_tile[1] = some ? t.len : 0;
+      s_tile[2] = some ? (by_head ? t.r : 2 * t.r) : -1;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int start = s_tile[0], len = s_tile[1], tile0 = s_tile[2];
+  if (tile0 >= 0) {
+    // head and tile of A and B, and the key blocks of each
+    const int hA = by_head ? 2 * col : col, hB = by_head ? 2 * col + 1 : col;
+    const int tA = tile0, tB = by_head ? tile0 : tile0 + 1;
+    const int nA = tA + 1, nB = tB * kTile < len ? tB + 1 : 0;
+    const int n = max(nA, nB);
+    const int kv = hA / p.G;
+
+    if (warp >= kSoftWarps) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+    if (warp == kCopyWarp) {
+      // ------------------------------------------------------------ copies
+      if (lane == 0) {
+        auto load = [&](const CUtensorMap* m, uint8_t* dst, int head, int row, uint64_t* bar) {
+#pragma unroll
+          for (int b = 0; b < C::kBoxes; ++b) tma_load_3d(dst + b * C::kBoxBytes, m, 64 * b, head, row, bar);
+        };
+        mbar_arrive_expect_tx(q_full, (nB > 0 ? 2 : 1) * C::kTileBytes);
+        load(&maps.q, smem + C::kQOff, hA, start + tA * kTile, q_full);
+        if (nB > 0) load(&maps.q, smem + C::kQOff + C::kTileBytes, hB, start + tB * kTile, q_full);
+        int i = 0;
+        bool ok = true;
+        for (; i < 2 * n; ++i) {  // K of block 0, V of block 0, K of block 1, ...
+          const int st = i % C::kStages;
+          if (i >= C::kStages) ok = mbar_wait(&empty[st], (i / C::kStages - 1) & 1, abort_flag, p.seqs.status);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&full[st], C::kTileBytes);
+          load((i & 1) ? &maps.v : &maps.k, smem + C::kRingOff + st * C::kTileBytes, kv, start + (i >> 1) * kTile,
+               &full[st]);
+        }
+        if (!ok) {
+          record_error(p.seqs.status, KVP_ERR_TIMEOUT);
+          *abort_flag = 1;
+          // what was issued lands before the shared memory can go to another CTA (each wait bounded again)
+          (void)mbar_wait(q_full, 0);
+          for (int k = max(0, i - C::kStages); k < i; ++k) (void)mbar_wait(&full[k % C::kStages], (k / C::kStages) & 1);
+        }
+      }
+      __syncwarp();
+    } else if (warp == kMmaWarp) {
+      // ------------------------------------------------------------ products
+      if (lane == 0) {
+        constexpr uint32_t idS = idesc_bf16_f32(kTile, kTile);
+        constexpr uint32_t idO = idesc_bf16_f32(kTile, D) | kIdescBMnMajor;
+        const uint32_t q0 = smem_u32(smem + C::kQOff), ring = smem_u32(smem + C::kRingOff);
+        auto landed = [&](int i) {
+          return mbar_wait(&full[i % C::kStages], (i / C::kStages) & 1, abort_flag, p.seqs.status);
+        };
+        auto issue_s = [&](int x, int j) {  // S of tile x, key block j
+          const uint64_t a = sw128_kmajor_desc(q0 + x * C::kTileBytes);
+          const uint64_t b = sw128_kmajor_desc(ring + (2 * j % C::kStages) * C::kTileBytes);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t off = static_cast<uint64_t>(((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4);
+            umma_bf16(tmem + kSCol + x * kTile, a + off, b + off, idS, kk > 0);
+          }
+          umma_commit(&s_full[x]);
+        };
+        // a stage is given back only if a later copy takes it: no arrival is left on its way when the CTA ends
+        auto release = [&](int i) {
+          if (i + C::kStages < 2 * n) umma_commit(&empty[i % C::kStages]);
+        };
+        bool ok = mbar_wait(q_full, 0, abort_flag, p.seqs.status) && landed(0);
+        if (ok) {
+          tc_fence_after();
+          issue_s(0, 0);
+          if (nB > 0) issue_s(1, 0);
+          release(0);
+        }
+        for (int j = 0; ok && j < n; ++j) {
+          ok = landed(2 * j + 1) && (j + 1 >= n || landed(2 * j + 2));
+          for (int x = 0; ok && x < 2; ++x) {
+            const int nx = x == 0 ? nA : nB;
+            if (j >= nx) continue;
+            ok = mbar_wait(&p_full[x], j & 1, abort_flag, p.seqs.status);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t v0 = ring + ((2 * j + 1) % C::kStages) * C::kTileBytes;
+#pragma unroll
+            for (int ks = 0; ks < kTile / 16; ++ks)
+              umma_bf16_tmem_a(tmem + kOCol + x * 128, tmem + kSCol + x * kTile + ks * 8,
+                               sw128_mnmajor_desc(v0 + ks * 2048, C::kBoxBytes, 1024), idO, j > 0 || ks > 0);
+            if (j == nx - 1) umma_commit(&o_full[x]);
+            if (j + 1 < nx) issue_s(x, j + 1);
+          }
+          if (!ok) break;
+          release(2 * j + 1);
+          if (j + 1 < n) release(2 * j + 2);
+        }
+        if (!ok) {
+          record_error(p.seqs.status, KVP_ERR_TIMEOUT);
+          *abort_flag = 1;
+        }
+        umma_commit(fin);
+        (void)mbar_wait(fin, 0);  // every product has completed before tensor and shared memory go
+      }
+      __syncwarp();
+    }
+    } else {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
+      // ------------------------------------------------------------ softmax
+      const int x = warp >> 2, row = (warp & 3) * 32 + lane;
+      const int nx = x == 0 ? nA : nB, tile = x == 0 ? tA : tB, head = x == 0 ? hA : hB;
+      const int pos = tile * kTile + row;  // in the sequence; past its end: nothing is stored
+      const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+      const uint32_t scol = trow + kSCol + x * kTile, ocol = trow + kOCol + x * 128;
+      const float c = p.qscale;
+      float M = -INFINITY, m = -INFINITY, l = 0.f;
+      bool ok = true;
+      for (int j = 0; j < nx; ++j) {
+        ok = mbar_wait(&s_full[x], j & 1, abort_flag, p.seqs.status);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        float s[kTile];
+        tmem_ld_cols(scol, s);
+        if (j == nx - 1) {
+#pragma unroll
+          for (int i = 0; i < kTile; ++i)
+            if (i > row) s[i] = -INFINITY;
+        }
+        float mx0 = fmaxf(s[0], s[1]), mx1 = fmaxf(s[2], s[3]);
+#pragma unroll
+        for (int i = 4; i < kTile; i += 4) {
+          mx0 = fmaxf(mx0, fmaxf(s[i], s[i + 1]));
+          mx1 = fmaxf(mx1, fmaxf(s[i + 2], s[i + 3]));
+        }
+        const float mx = fmaxf(mx0, mx1);
+        bool big = fabsf(M) >= kBig && M != -INFINITY;
+        const bool grow = big ? (mx - m) * c > kLazy : fmaf(mx, c, -M) > kLazy - kHeadroom;
+        if (__any_sync(0xffffffffu, grow)) {
+          const float M_new = fmaf(mx, c, kHeadroom);
+          const bool big_new = fabsf(M_new) >= kBig;
+          float al = 1.f;
+          if (grow) {
+            const float e = big_new ? (big ? (m - mx) * c : fmaf(-mx, c, M) - kHeadroom)
+                                    : (big ? fmaf(m, c, kHeadroom - M_new) : M - M_new);
+            al = M == -INFINITY ? 0.f : ex2_approx(e);
+            M = M_new;
+            m = mx;
+            big = big_new;
+            l *= al;
+          }
+          if (j > 0) {
+#pragma unroll 1
+            for (int o = 0; o < D; o += 32) {
+              float v[32];
+              tmem_ld32(ocol + o, v);
+              uint32_t w[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(v[i] * al);
+              tmem_st32(ocol + o, w);
+            }
+          }
+        }
+        uint64_t sum[2] = {0, 0};
+        if (!__any_sync(0xffffffffu, big)) {
+          const float Ms = M == -INFINITY ? 0.f : -M;
+          const uint64_t c2 = pack2(c, c), M2 = pack2(Ms, Ms);
+#pragma unroll
+          for (int part = 0; part < kTile; part += 64) {
+            uint32_t w[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              float a, b;
+              unpack2(fma2(pack2(s[part + 2 * i], s[part + 2 * i + 1]), c2, M2), a, b);
+              a = ex2_approx(a);
+              b = ex2_approx(b);
+              sum[i & 1] = add2(sum[i & 1], pack2(a, b));
+              w[i] = bf16x2(a, b);
+            }
+            tmem_st32(scol + part / 2, w);
+          }
+        } else {  // logits whose differences are lost beside the reference's rounding, in some row of the warp
+          const float Ms = M == -INFINITY ? 0.f : M;
+#pragma unroll 1
+          for (int part = 0; part < kTile; part += 64) {
+            uint32_t w[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              float e[2];
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const float y = part == 0 ? s[2 * i + k] : s[64 + 2 * i + k];
+                e[k] = ex2_approx(big ? fmaf(y - m, c, -kHeadroom) : fmaf(y, c, -Ms));
+              }
+              sum[i & 1] = add2(sum[i & 1], pack2(e[0], e[1]));
+              w[i] = bf16x2(e[0], e[1]);
+            }
+            tmem_st32(scol + part / 2, w);
+          }
+        }
+        float l0, l1, l2, l3;
+        unpack2(sum[0], l0, l1);
+        unpack2(sum[1], l2, l3);
+        l += (l0 + l1) + (l2 + l3);
+        if (j == nx - 1) {
+          const int i = 2 * j + 1;
+          ok = mbar_wait(&full[i % C::kStages], (i / C::kStages) & 1, abort_flag, p.seqs.status);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+          clear_bad_values<D>(smem + C::kRingOff + (i % C::kStages) * C::kTileBytes, row, pos, pos < len, bad);
+          fence_proxy_async();
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[x]);
+      }
+      // what the other warps noted in `bad` is visible from here on (of two tiles of one head, also the other tile's)
+      named_bar_sync(by_head ? 1 + x : 3, by_head ? 128 : 256);
+      if (ok && nx > 0) {
+        ok = mbar_wait(&o_full[x], 0, abort_flag, p.seqs.status);
+        ok = __all_sync(0xffffffffu, ok);
+        tc_fence_after();
+      }
+      if (!ok) {
+        if (lane == 0) {
+          record_error(p.seqs.status, KVP_ERR_TIMEOUT);
+          *abort_flag = 1;
+        }
+      } else if (nx > 0) {
+        const bool mine = pos < len;
+        const int64_t r = start + pos;
+        uint16_t* out = p.out + r * p.ot + head * p.oh;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+        for (int o = 0; o < D; o += 32) {
+          float v[32];
+          tmem_ld32(ocol + o, v);
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            v[i] *= inv;
+            if (l == 0.f) v[i] = 0.f;
+          }
+          bool some = false;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const int b = min(bad[o + i], min(bad[D + o + i], bad[2 * D + o + i]));
+            some |= b <= pos;
+          }
+          if (some) {
+            for (int i = 0; i < 32; ++i) {
+              const bool up = bad[o + i] <= pos, down = bad[D + o + i] <= pos, nan = bad[2 * D + o + i] <= pos;
+              if (up) v[i] += INFINITY;
+              if (down) v[i] -= INFINITY;
+              if (nan) v[i] = NAN;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) w[i] = bf16x2(v[2 * i], v[2 * i + 1]);
+          if (mine) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              reinterpret_cast<uint4*>(out + o)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+          }
+        }
+        if (mine && p.lse != nullptr) {
+          // the reference and the sum's logarithm; a big one as it was taken
+          const float ref = fabsf(M) >= kBig ? m * c + kHeadroom : M;
+          p.lse[head * p.seqs.n_tok + r] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Rows of bf16 [rows, heads, D] with the given strides as a tensor map whose boxes are 128 rows x 64 columns of a head.
+template <int D>
+bool make_tmap_heads(CUtensorMap* m, const void* base, int64_t rows, int64_t st, int heads, int64_t sh) {
+  auto fn = tmap_encode_fn();
+  if (fn == nullptr) return false;
+  if (heads == 1) sh = D;
+  if (rows == 1) st = D;
+  const cuuint64_t dims[3] = {D, static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(sh) * 2, static_cast<cuuint64_t>(st) * 2};
+  const cuuint32_t box[3] = {64, 1, kTile};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+kvp_status launch_attn(const PromptParams& p, int n_kv_heads, cudaStream_t st) {
+  using C = AttnCfg<D>;
+  AttnMaps maps;
+  if (!make_tmap_heads<D>(&maps.q, p.q, p.seqs.n_tok, p.qt, p.Hq, p.qh) ||
+      !make_tmap_heads<D>(&maps.k, p.k, p.seqs.n_tok, p.kt, n_kv_heads, p.kh) ||
+      !make_tmap_heads<D>(&maps.v, p.v, p.seqs.n_tok, p.vt, n_kv_heads, p.vh))
+    return KVP_ERR_CUDA;
+  static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is raised
+  int device = 0;
+  if (current_sms(&device) == 0) return KVP_ERR_CUDA;
+  if (device > 63 || (ready.load(std::memory_order_relaxed) >> device & 1u) == 0) {
+    if (cudaFuncSetAttribute(prompt_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) !=
+        cudaSuccess) {
+      (void)cudaGetLastError();
+      return KVP_ERR_CUDA;
+    }
+    if (device <= 63) ready.fetch_or(uint64_t{1} << device, std::memory_order_relaxed);
+  }
+  const bool by_head = p.G % 2 == 0;
+  const int tile = by_head ? kTile : 2 * kTile;
+  const int64_t ctas = (p.seqs.n_tok / tile + p.seqs.n) * (by_head ? p.Hq / 2 : p.Hq);
+  if (ctas > 0x7fffffff) return KVP_ERR_UNSUPPORTED;
+  return launch_pdl(prompt_attn_kernel<D>, dim3(static_cast<unsigned>(ctas)), dim3(kAttnThreads), C::kSmem, st, p,
+                    maps) == cudaSuccess
+             ? KVP_OK
+             : KVP_ERR_CUDA;
 }
 
 template <int D>
@@ -142,7 +597,7 @@ __global__ void __launch_bounds__(kPWarps * 32) prompt_weights_kernel(const Prom
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int h = blockIdx.y;
   Tile t;
-  if (!find_tile(p.seqs, blockIdx.x, t)) return;
+  if (!find_tile(p.seqs, kTile, blockIdx.x, t)) return;
   const int first = p.n_last > 0 ? max(0, t.len - p.n_last) : 0;
   for (int c = t.r * kTile + warp; c < min(t.len, (t.r + 1) * kTile); c += kPWarps) {
     float k[D / 32], total = 0.f;
@@ -224,15 +679,8 @@ extern "C" kvp_status kvp_prompt_attn(int n_seqs, int64_t n_tok, int n_q_heads, 
   p.Hq = n_q_heads, p.G = n_q_heads / n_kv_heads;
   p.qscale = (scale > 0.f ? scale : 1.f / sqrtf(static_cast<float>(head_dim))) * kLog2e;
   p.lse = lse;
-  const int64_t tiles = n_tok / kTile + n_seqs;
-  if (tiles > 0x7fffffff) return KVP_ERR_UNSUPPORTED;
-  const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(n_q_heads));
-  auto go = [&](auto kern) {
-    return launch_pdl(kern, grid, dim3(kPWarps * 32), 0, static_cast<cudaStream_t>(stream), p) == cudaSuccess
-               ? KVP_OK
-               : KVP_ERR_CUDA;
-  };
-  return head_dim == 128 ? go(prompt_attn_kernel<128>) : go(prompt_attn_kernel<64>);
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  return head_dim == 128 ? launch_attn<128>(p, n_kv_heads, cs) : launch_attn<64>(p, n_kv_heads, cs);
 }
 
 extern "C" kvp_status kvp_prompt_weights(int n_seqs, int64_t n_tok, int n_q_heads, int n_kv_heads, int head_dim,
