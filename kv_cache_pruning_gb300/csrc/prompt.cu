@@ -144,13 +144,14 @@ struct AttnCfg {
 };
 constexpr int kSoftWarps = 8, kMmaWarp = 8, kCopyWarp = 9;
 constexpr int kAttnThreads = 384;             // warps 10 and 11 only give their registers away
-// A row's 128 logits stay in registers: the softmax warps take 232 each and the
-// others 40, of the 168 a thread that the block is launched with:
-// 256 x 232 + 128 x 40 = 384 x 168.
-constexpr int kRegsSoft = 232, kRegsRest = 40;
+// A row's 128 logits stay in registers: the softmax warps take 216 each and the
+// others 72, of the 168 a thread that the block is launched with:
+// 256 x 216 + 128 x 72 = 384 x 168.
+constexpr int kRegsSoft = 216, kRegsRest = 72;
 constexpr uint32_t kSCol = 0, kOCol = 256;  // S (and P) of A, B at 0, 128; O at 256, 384
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLazy = 8.f;                // how far a row's maximum may pass its reference (base 2)
+constexpr float kMostSum = 1.f / 8192;      // 128 weights of 2^(kLazy - kHeadroom)
 constexpr float kBig = 268435456.f;         // from references of 2^28 on, x c - M is taken as (x - max) c
 
 // Two fp32 values as one register pair: packed arithmetic of sm_100 and later.
@@ -173,6 +174,43 @@ KVP_DEV uint64_t add2(uint64_t a, uint64_t b) {
 KVP_DEV uint32_t bf16x2(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// Loads 128 consecutive fp32 columns of this warp's 32 TMEM lanes (one row per thread) in one round and waits for them,
+// in one asm block so that no use can move above the wait.
+KVP_DEV void tmem_ld128(uint32_t taddr, float (&v)[128]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%128];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%129];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,"
+      "%80,%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95}, [%130];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,%111,"
+      "%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127}, [%131];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
+        "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
+        "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31]),
+        "=f"(v[32]), "=f"(v[33]), "=f"(v[34]), "=f"(v[35]), "=f"(v[36]), "=f"(v[37]), "=f"(v[38]), "=f"(v[39]),
+        "=f"(v[40]), "=f"(v[41]), "=f"(v[42]), "=f"(v[43]), "=f"(v[44]), "=f"(v[45]), "=f"(v[46]), "=f"(v[47]),
+        "=f"(v[48]), "=f"(v[49]), "=f"(v[50]), "=f"(v[51]), "=f"(v[52]), "=f"(v[53]), "=f"(v[54]), "=f"(v[55]),
+        "=f"(v[56]), "=f"(v[57]), "=f"(v[58]), "=f"(v[59]), "=f"(v[60]), "=f"(v[61]), "=f"(v[62]), "=f"(v[63]),
+        "=f"(v[64]), "=f"(v[65]), "=f"(v[66]), "=f"(v[67]), "=f"(v[68]), "=f"(v[69]), "=f"(v[70]), "=f"(v[71]),
+        "=f"(v[72]), "=f"(v[73]), "=f"(v[74]), "=f"(v[75]), "=f"(v[76]), "=f"(v[77]), "=f"(v[78]), "=f"(v[79]),
+        "=f"(v[80]), "=f"(v[81]), "=f"(v[82]), "=f"(v[83]), "=f"(v[84]), "=f"(v[85]), "=f"(v[86]), "=f"(v[87]),
+        "=f"(v[88]), "=f"(v[89]), "=f"(v[90]), "=f"(v[91]), "=f"(v[92]), "=f"(v[93]), "=f"(v[94]), "=f"(v[95]),
+        "=f"(v[96]), "=f"(v[97]), "=f"(v[98]), "=f"(v[99]), "=f"(v[100]), "=f"(v[101]), "=f"(v[102]), "=f"(v[103]),
+        "=f"(v[104]), "=f"(v[105]), "=f"(v[106]), "=f"(v[107]), "=f"(v[108]), "=f"(v[109]), "=f"(v[110]), "=f"(v[111]),
+        "=f"(v[112]), "=f"(v[113]), "=f"(v[114]), "=f"(v[115]), "=f"(v[116]), "=f"(v[117]), "=f"(v[118]), "=f"(v[119]),
+        "=f"(v[120]), "=f"(v[121]), "=f"(v[122]), "=f"(v[123]), "=f"(v[124]), "=f"(v[125]), "=f"(v[126]), "=f"(v[127])
+      : "r"(taddr), "r"(taddr + 32), "r"(taddr + 64), "r"(taddr + 96)
+      : "memory");
 }
 
 // Searches the V tile of 128 rows at `tile` (swizzled boxes) for infinities and NaN (128 threads call this, thread t
@@ -204,6 +242,39 @@ KVP_DEV void clear_bad_values(uint8_t* tile, int t, int pos, bool inside, int* b
   }
 }
 
+// One lane of a converged warp, and products and commits that this lane issues (`leader` nonzero there alone).
+KVP_DEV uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
+}
+KVP_DEV void mma_ss(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)), "r"(leader)
+      : "memory");
+}
+KVP_DEV void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)), "r"(leader)
+      : "memory");
+}
+KVP_DEV void commit_to(uint32_t leader, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(leader)
+      : "memory");
+}
+
 struct AttnMaps {
   CUtensorMap q, k, v;  // [D, heads, rows], boxes of 64 x 1 x 128
 };
@@ -214,7 +285,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
   using C = AttnCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // the same in every lane, as the compiler can see
   int* bad = reinterpret_cast<int*>(smem + C::kBadOff);
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
   uint64_t* full = q_full + 1;
@@ -309,61 +381,66 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
       __syncwarp();
     } else if (warp == kMmaWarp) {
       // ------------------------------------------------------------ products
-      if (lane == 0) {
-        constexpr uint32_t idS = idesc_bf16_f32(kTile, kTile);
-        constexpr uint32_t idO = idesc_bf16_f32(kTile, D) | kIdescBMnMajor;
-        const uint32_t q0 = smem_u32(smem + C::kQOff), ring = smem_u32(smem + C::kRingOff);
-        auto landed = [&](int i) {
-          return mbar_wait(&full[i % C::kStages], (i / C::kStages) & 1, abort_flag, p.seqs.status);
-        };
-        auto issue_s = [&](int x, int j) {  // S of tile x, key block j
-          const uint64_t a = sw128_kmajor_desc(q0 + x * C::kTileBytes);
-          const uint64_t b = sw128_kmajor_desc(ring + (2 * j % C::kStages) * C::kTileBytes);
+      // The whole warp runs this, on the same values, and one elected lane issues: so the descriptors stay in uniform
+      // registers. (With the loop on one lane alone each product's operands were moved there one by one: 75 to 115
+      // cycles a product, where it runs for 64.)
+      constexpr uint32_t idS = idesc_bf16_f32(kTile, kTile);
+      constexpr uint32_t idO = idesc_bf16_f32(kTile, D) | kIdescBMnMajor;
+      const uint32_t leader = elect_one();
+      const uint32_t q0 = smem_u32(smem + C::kQOff), ring = smem_u32(smem + C::kRingOff);
+      auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.seqs.status)) != 0;
+      };
+      auto landed = [&](int i) { return wait_all(&full[i % C::kStages], (i / C::kStages) & 1); };
+      auto issue_s = [&](int x, int j) {  // S of tile x, key block j
+        const uint64_t a = sw128_kmajor_desc(q0 + x * C::kTileBytes);
+        const uint64_t b = sw128_kmajor_desc(ring + (2 * j % C::kStages) * C::kTileBytes);
+        const uint32_t d = tmem + kSCol + x * kTile;
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint64_t off = static_cast<uint64_t>(((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4);
-            umma_bf16(tmem + kSCol + x * kTile, a + off, b + off, idS, kk > 0);
-          }
-          umma_commit(&s_full[x]);
-        };
-        // a stage is given back only if a later copy takes it: no arrival is left on its way when the CTA ends
-        auto release = [&](int i) {
-          if (i + C::kStages < 2 * n) umma_commit(&empty[i % C::kStages]);
-        };
-        bool ok = mbar_wait(q_full, 0, abort_flag, p.seqs.status) && landed(0);
-        if (ok) {
-          tc_fence_after();
-          issue_s(0, 0);
-          if (nB > 0) issue_s(1, 0);
-          release(0);
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint64_t off = static_cast<uint64_t>(((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4);
+          mma_ss(leader, d, a + off, b + off, idS, kk > 0);
         }
-        for (int j = 0; ok && j < n; ++j) {
-          ok = landed(2 * j + 1) && (j + 1 >= n || landed(2 * j + 2));
-          for (int x = 0; ok && x < 2; ++x) {
-            const int nx = x == 0 ? nA : nB;
-            if (j >= nx) continue;
-            ok = mbar_wait(&p_full[x], j & 1, abort_flag, p.seqs.status);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t v0 = ring + ((2 * j + 1) % C::kStages) * C::kTileBytes;
-#pragma unroll
-            for (int ks = 0; ks < kTile / 16; ++ks)
-              umma_bf16_tmem_a(tmem + kOCol + x * 128, tmem + kSCol + x * kTile + ks * 8,
-                               sw128_mnmajor_desc(v0 + ks * 2048, C::kBoxBytes, 1024), idO, j > 0 || ks > 0);
-            if (j == nx - 1) umma_commit(&o_full[x]);
-            if (j + 1 < nx) issue_s(x, j + 1);
-          }
-          if (!ok) break;
-          release(2 * j + 1);
-          if (j + 1 < n) release(2 * j + 2);
-        }
-        if (!ok) {
-          record_error(p.seqs.status, KVP_ERR_TIMEOUT);
-          *abort_flag = 1;
-        }
-        umma_commit(fin);
-        (void)mbar_wait(fin, 0);  // every product has completed before tensor and shared memory go
+        commit_to(leader, &s_full[x]);
+      };
+      // a stage is given back only if a later copy takes it: no arrival is left on its way when the CTA ends
+      auto release = [&](int i) {
+        if (i + C::kStages < 2 * n) commit_to(leader, &empty[i % C::kStages]);
+      };
+      bool ok = wait_all(q_full, 0) && landed(0);
+      if (ok) {
+        tc_fence_after();
+        issue_s(0, 0);
+        if (nB > 0) issue_s(1, 0);
+        release(0);
       }
+      for (int j = 0; ok && j < n; ++j) {
+        ok = landed(2 * j + 1) && (j + 1 >= n || landed(2 * j + 2));
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int nx = x == 0 ? nA : nB;
+          if (!ok || j >= nx) continue;
+          ok = wait_all(&p_full[x], j & 1);
+          if (!ok) continue;
+          tc_fence_after();
+          const uint64_t v0 = sw128_mnmajor_desc(ring + ((2 * j + 1) % C::kStages) * C::kTileBytes, C::kBoxBytes, 1024);
+#pragma unroll
+          for (int ks = 0; ks < kTile / 16; ++ks)
+            mma_ts(leader, tmem + kOCol + x * 128, tmem + kSCol + x * kTile + ks * 8, v0 + ((ks * 2048) >> 4), idO,
+                   j > 0 || ks > 0);
+          if (j == nx - 1) commit_to(leader, &o_full[x]);
+          if (j + 1 < nx) issue_s(x, j + 1);
+        }
+        if (!ok) break;
+        release(2 * j + 1);
+        if (j + 1 < n) release(2 * j + 2);
+      }
+      if (!ok && lane == 0) {
+        record_error(p.seqs.status, KVP_ERR_TIMEOUT);
+        *abort_flag = 1;
+      }
+      commit_to(leader, fin);
+      (void)mbar_wait(fin, 0);  // every product has completed before tensor and shared memory go
       __syncwarp();
     }
     } else {
@@ -385,22 +462,48 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
         }
         tc_fence_after();
         float s[kTile];
-        tmem_ld_cols(scol, s);
+        tmem_ld128(scol, s);
         if (j == nx - 1) {
 #pragma unroll
           for (int i = 0; i < kTile; ++i)
             if (i > row) s[i] = -INFINITY;
         }
-        float mx0 = fmaxf(s[0], s[1]), mx1 = fmaxf(s[2], s[3]);
+        uint32_t w[kTile / 2];
+        uint64_t sum[4];
+        auto weigh = [&]() {
+          const uint64_t c2 = pack2(c, c), M2 = pack2(-M, -M);
+          sum[0] = sum[1] = sum[2] = sum[3] = 0;
 #pragma unroll
-        for (int i = 4; i < kTile; i += 4) {
-          mx0 = fmaxf(mx0, fmaxf(s[i], s[i + 1]));
-          mx1 = fmaxf(mx1, fmaxf(s[i + 2], s[i + 3]));
+          for (int i = 0; i < kTile / 2; ++i) {
+            float e, f;
+            unpack2(fma2(pack2(s[2 * i], s[2 * i + 1]), c2, M2), e, f);
+            e = ex2_approx(e);
+            f = ex2_approx(f);
+            sum[i & 3] = add2(sum[i & 3], pack2(e, f));
+            w[i] = bf16x2(e, f);
+          }
+        };
+        // With the reference as it is: no maximum is taken. If a row's sum says that some weight may have passed it by
+        // 2^8 (or is no number, or the row has no reference yet), the block is taken again below.
+        bool again = M == -INFINITY || fabsf(M) >= kBig;
+        if (!__any_sync(0xffffffffu, again)) {
+          weigh();
+          float e, f;
+          unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), e, f);
+          again = !(e + f <= kMostSum);
         }
-        const float mx = fmaxf(mx0, mx1);
-        bool big = fabsf(M) >= kBig && M != -INFINITY;
-        const bool grow = big ? (mx - m) * c > kLazy : fmaf(mx, c, -M) > kLazy - kHeadroom;
-        if (__any_sync(0xffffffffu, grow)) {
+        if (__any_sync(0xffffffffu, again)) {
+          float mx = -INFINITY;
+#pragma unroll 1
+          for (int o = 0; o < kTile; o += 32) {  // S is still there
+            float v[32];
+            tmem_ld32(scol + o, v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (j < nx - 1 || o + i <= row) mx = fmaxf(mx, v[i]);
+          }
+          bool big = fabsf(M) >= kBig && M != -INFINITY;
+          const bool grow = big ? (mx - m) * c > kLazy : fmaf(mx, c, -M) > kLazy - kHeadroom;
           const float M_new = fmaf(mx, c, kHeadroom);
           const bool big_new = fabsf(M_new) >= kBig;
           float al = 1.f;
@@ -413,59 +516,33 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
             big = big_new;
             l *= al;
           }
-          if (j > 0) {
+          if (j > 0 && __any_sync(0xffffffffu, grow)) {
 #pragma unroll 1
             for (int o = 0; o < D; o += 32) {
               float v[32];
               tmem_ld32(ocol + o, v);
-              uint32_t w[32];
+              uint32_t y[32];
 #pragma unroll
-              for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(v[i] * al);
-              tmem_st32(ocol + o, w);
+              for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(v[i] * al);
+              tmem_st32(ocol + o, y);
             }
+          }
+          // 2^(x c - M); where a reference is so large that its rounding counts, 2^((x - max) c - headroom)
+          const float ref = M == -INFINITY ? 0.f : M;
+          sum[0] = sum[1] = sum[2] = sum[3] = 0;
+#pragma unroll
+          for (int i = 0; i < kTile / 2; ++i) {
+            const float a0 = s[2 * i], a1 = s[2 * i + 1];
+            const float e = ex2_approx(big ? fmaf(a0 - m, c, -kHeadroom) : fmaf(a0, c, -ref));
+            const float f = ex2_approx(big ? fmaf(a1 - m, c, -kHeadroom) : fmaf(a1, c, -ref));
+            sum[i & 3] = add2(sum[i & 3], pack2(e, f));
+            w[i] = bf16x2(e, f);
           }
         }
-        uint64_t sum[2] = {0, 0};
-        if (!__any_sync(0xffffffffu, big)) {
-          const float Ms = M == -INFINITY ? 0.f : -M;
-          const uint64_t c2 = pack2(c, c), M2 = pack2(Ms, Ms);
-#pragma unroll
-          for (int part = 0; part < kTile; part += 64) {
-            uint32_t w[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              float a, b;
-              unpack2(fma2(pack2(s[part + 2 * i], s[part + 2 * i + 1]), c2, M2), a, b);
-              a = ex2_approx(a);
-              b = ex2_approx(b);
-              sum[i & 1] = add2(sum[i & 1], pack2(a, b));
-              w[i] = bf16x2(a, b);
-            }
-            tmem_st32(scol + part / 2, w);
-          }
-        } else {  // logits whose differences are lost beside the reference's rounding, in some row of the warp
-          const float Ms = M == -INFINITY ? 0.f : M;
-#pragma unroll 1
-          for (int part = 0; part < kTile; part += 64) {
-            uint32_t w[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              float e[2];
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const float y = part == 0 ? s[2 * i + k] : s[64 + 2 * i + k];
-                e[k] = ex2_approx(big ? fmaf(y - m, c, -kHeadroom) : fmaf(y, c, -Ms));
-              }
-              sum[i & 1] = add2(sum[i & 1], pack2(e[0], e[1]));
-              w[i] = bf16x2(e[0], e[1]);
-            }
-            tmem_st32(scol + part / 2, w);
-          }
-        }
-        float l0, l1, l2, l3;
-        unpack2(sum[0], l0, l1);
-        unpack2(sum[1], l2, l3);
-        l += (l0 + l1) + (l2 + l3);
+        tmem_st_cols(scol, w);
+        float l0, l1;
+        unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), l0, l1);
+        l += l0 + l1;
         if (j == nx - 1) {
           const int i = 2 * j + 1;
           ok = mbar_wait(&full[i % C::kStages], (i / C::kStages) & 1, abort_flag, p.seqs.status);
