@@ -137,7 +137,8 @@ struct AttnCfg {
   static constexpr int kRingOff = 2 * kTileBytes;
   static constexpr int kBadOff = kRingOff + kStages * kTileBytes;  // first row with +inf, -inf, NaN of each column
   static constexpr int kBarOff = kBadOff + 3 * D * 4;
-  static constexpr int kBars = 1 + 2 * kStages + 2 + 2 + 2 + 1;
+  static constexpr int kPairs = 8;                       // ring of barriers that give stages back
+  static constexpr int kBars = 1 + kStages + kPairs + 2 + 2 + 2 + 1;
   static constexpr int kSmem = 1024 + kBarOff + kBars * 8 + 32;
   static_assert(kSmem <= 232448, "shared memory budget");
   static_assert(kBarOff % 8 == 0, "alignment");
@@ -211,6 +212,39 @@ KVP_DEV void tmem_ld128(uint32_t taddr, float (&v)[128]) {
         "=f"(v[120]), "=f"(v[121]), "=f"(v[122]), "=f"(v[123]), "=f"(v[124]), "=f"(v[125]), "=f"(v[126]), "=f"(v[127])
       : "r"(taddr), "r"(taddr + 32), "r"(taddr + 64), "r"(taddr + 96)
       : "memory");
+}
+
+// The weights 2^(s c + ref) of a row's 128 logits: to tensor memory as bf16 pairs, and their sums (of the unrounded ones)
+// in four pairs. One warp a scheduler does this at a time, so its order counts: the exponential of one value takes the
+// special-function unit four cycles, and the products, conversions and sums of other values are placed in between.
+KVP_DEV void weigh_block(const float (&s)[kTile], float c, float ref, uint32_t taddr, uint64_t (&sum)[4]) {
+  constexpr int kAhead = 4, kBehind = 4;
+  const uint64_t c2 = pack2(c, c), r2 = pack2(ref, ref);
+  uint64_t t[kTile / 2];
+  float e[kTile];
+  uint32_t w[kTile / 2];
+  sum[0] = sum[1] = sum[2] = sum[3] = 0;
+  auto scale = [&](int i) {
+    asm volatile("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(t[i]) : "l"(pack2(s[2 * i], s[2 * i + 1])), "l"(c2), "l"(r2));
+  };
+  auto finish = [&](int i) {
+    asm volatile("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(e[2 * i + 1]), "f"(e[2 * i]));
+    asm volatile("add.rn.f32x2 %0, %0, %1;" : "+l"(sum[i & 3]) : "l"(pack2(e[2 * i], e[2 * i + 1])));
+    if (i % 16 == 15) tmem_st16(taddr + (i & ~15), w + (i & ~15));
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) scale(i);
+#pragma unroll
+  for (int i = 0; i < kTile / 2; ++i) {
+    float a, b;
+    unpack2(t[i], a, b);
+    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(e[2 * i]) : "f"(a));
+    if (i + kAhead < kTile / 2) scale(i + kAhead);
+    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(e[2 * i + 1]) : "f"(b));
+    if (i >= kBehind) finish(i - kBehind);
+  }
+#pragma unroll
+  for (int i = kTile / 2 - kBehind; i < kTile / 2; ++i) finish(i);
 }
 
 // Searches the V tile of 128 rows at `tile` (swizzled boxes) for infinities and NaN (128 threads call this, thread t
@@ -291,7 +325,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
   uint64_t* full = q_full + 1;
   uint64_t* empty = full + C::kStages;
-  uint64_t* s_full = empty + C::kStages;  // [A, B]
+  uint64_t* s_full = empty + C::kPairs;  // [A, B]
   uint64_t* p_full = s_full + 2;
   uint64_t* o_full = p_full + 2;
   uint64_t* fin = o_full + 2;
@@ -301,10 +335,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
 
   if (tid == 0) {
     mbar_init(q_full, 1);
-    for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
-    }
+    for (int i = 0; i < C::kStages; ++i) mbar_init(&full[i], 1);
+    for (int i = 0; i < C::kPairs; ++i) mbar_init(&empty[i], 1);
     for (int x = 0; x < 2; ++x) {
       mbar_init(&s_full[x], 1);
       mbar_init(&p_full[x], 4);
@@ -364,7 +396,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
         bool ok = true;
         for (; i < 2 * n; ++i) {  // K of block 0, V of block 0, K of block 1, ...
           const int st = i % C::kStages;
-          if (i >= C::kStages) ok = mbar_wait(&empty[st], (i / C::kStages - 1) & 1, abort_flag, p.seqs.status);
+          if (i >= C::kStages) {  // tile i - kStages is given back with the pair (V of a block, K of the next) that it is of
+            const int pair = (i - C::kStages + 1) / 2;
+            ok = mbar_wait(&empty[pair % C::kPairs], (pair / C::kPairs) & 1, abort_flag, p.seqs.status);
+          }
           if (!ok) break;
           mbar_arrive_expect_tx(&full[st], C::kTileBytes);
           load((i & 1) ? &maps.v : &maps.k, smem + C::kRingOff + st * C::kTileBytes, kv, start + (i >> 1) * kTile,
@@ -391,10 +426,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
       auto wait_all = [&](uint64_t* bar, uint32_t parity) {
         return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.seqs.status)) != 0;
       };
-      auto landed = [&](int i) { return wait_all(&full[i % C::kStages], (i / C::kStages) & 1); };
-      auto issue_s = [&](int x, int j) {  // S of tile x, key block j
+      int st = 0;                    // ring stage and phase of the tile to land next
+      uint32_t ph = 0;
+      auto landed = [&]() {
+        const bool r = wait_all(&full[st], ph);
+        if (++st == C::kStages) {
+          st = 0;
+          ph ^= 1;
+        }
+        return r;
+      };
+      auto issue_s = [&](int x, int stage) {  // S of tile x with the K in `stage`
         const uint64_t a = sw128_kmajor_desc(q0 + x * C::kTileBytes);
-        const uint64_t b = sw128_kmajor_desc(ring + (2 * j % C::kStages) * C::kTileBytes);
+        const uint64_t b = sw128_kmajor_desc(ring + stage * C::kTileBytes);
         const uint32_t d = tmem + kSCol + x * kTile;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
@@ -403,37 +447,44 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
         }
         commit_to(leader, &s_full[x]);
       };
-      // a stage is given back only if a later copy takes it: no arrival is left on its way when the CTA ends
-      auto release = [&](int i) {
-        if (i + C::kStages < 2 * n) commit_to(leader, &empty[i % C::kStages]);
+      // stages are given back only if a later copy takes one: no arrival is left on its way when the CTA ends
+      auto release = [&](int pair) {
+        if (2 * pair - 1 + C::kStages < 2 * n) commit_to(leader, &empty[pair % C::kPairs]);
       };
-      bool ok = wait_all(q_full, 0) && landed(0);
+      int vst = 1, kst = 2;          // stages of V of block j and K of block j + 1
+      bool ok = wait_all(q_full, 0) && landed();
       if (ok) {
         tc_fence_after();
         issue_s(0, 0);
         if (nB > 0) issue_s(1, 0);
         release(0);
+        ok = landed() && (n < 2 || landed());
       }
       for (int j = 0; ok && j < n; ++j) {
-        ok = landed(2 * j + 1) && (j + 1 >= n || landed(2 * j + 2));
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const int nx = x == 0 ? nA : nB;
-          if (!ok || j >= nx) continue;
-          ok = wait_all(&p_full[x], j & 1);
-          if (!ok) continue;
-          tc_fence_after();
-          const uint64_t v0 = sw128_mnmajor_desc(ring + ((2 * j + 1) % C::kStages) * C::kTileBytes, C::kBoxBytes, 1024);
+          if (ok && j < nx) {
+            ok = wait_all(&p_full[x], j & 1);
+            if (ok) {
+              tc_fence_after();
+              const uint64_t v0 = sw128_mnmajor_desc(ring + vst * C::kTileBytes, C::kBoxBytes, 1024);
 #pragma unroll
-          for (int ks = 0; ks < kTile / 16; ++ks)
-            mma_ts(leader, tmem + kOCol + x * 128, tmem + kSCol + x * kTile + ks * 8, v0 + ((ks * 2048) >> 4), idO,
-                   j > 0 || ks > 0);
-          if (j == nx - 1) commit_to(leader, &o_full[x]);
-          if (j + 1 < nx) issue_s(x, j + 1);
+              for (int ks = 0; ks < kTile / 16; ++ks)
+                mma_ts(leader, tmem + kOCol + x * 128, tmem + kSCol + x * kTile + ks * 8, v0 + ((ks * 2048) >> 4), idO,
+                       j > 0 || ks > 0);
+              if (j == nx - 1) commit_to(leader, &o_full[x]);
+              if (j + 1 < nx) issue_s(x, kst);
+            }
+          }
+          // while A's products run: the tiles of the next step
+          if (x == 0 && ok && j + 1 < n) ok = landed() && (j + 2 >= n || landed());
         }
-        if (!ok) break;
-        release(2 * j + 1);
-        if (j + 1 < n) release(2 * j + 2);
+        release(j + 1);
+        vst += 2;
+        if (vst >= C::kStages) vst -= C::kStages;
+        kst += 2;
+        if (kst >= C::kStages) kst -= C::kStages;
       }
       if (!ok && lane == 0) {
         record_error(p.seqs.status, KVP_ERR_TIMEOUT);
@@ -468,40 +519,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
           for (int i = 0; i < kTile; ++i)
             if (i > row) s[i] = -INFINITY;
         }
-        uint32_t w[kTile / 2];
         uint64_t sum[4];
-        auto weigh = [&]() {
-          const uint64_t c2 = pack2(c, c), M2 = pack2(-M, -M);
-          sum[0] = sum[1] = sum[2] = sum[3] = 0;
-#pragma unroll
-          for (int i = 0; i < kTile / 2; ++i) {
-            float e, f;
-            unpack2(fma2(pack2(s[2 * i], s[2 * i + 1]), c2, M2), e, f);
-            e = ex2_approx(e);
-            f = ex2_approx(f);
-            sum[i & 3] = add2(sum[i & 3], pack2(e, f));
-            w[i] = bf16x2(e, f);
-          }
-        };
         // With the reference as it is: no maximum is taken. If a row's sum says that some weight may have passed it by
         // 2^8 (or is no number, or the row has no reference yet), the block is taken again below.
         bool again = M == -INFINITY || fabsf(M) >= kBig;
         if (!__any_sync(0xffffffffu, again)) {
-          weigh();
+          weigh_block(s, c, -M, scol, sum);
           float e, f;
           unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), e, f);
           again = !(e + f <= kMostSum);
         }
         if (__any_sync(0xffffffffu, again)) {
           float mx = -INFINITY;
-#pragma unroll 1
-          for (int o = 0; o < kTile; o += 32) {  // S is still there
-            float v[32];
-            tmem_ld32(scol + o, v);
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (j < nx - 1 || o + i <= row) mx = fmaxf(mx, v[i]);
-          }
+          for (int i = 0; i < kTile; ++i) mx = fmaxf(mx, s[i]);
           bool big = fabsf(M) >= kBig && M != -INFINITY;
           const bool grow = big ? (mx - m) * c > kLazy : fmaf(mx, c, -M) > kLazy - kHeadroom;
           const float M_new = fmaf(mx, c, kHeadroom);
@@ -531,15 +562,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
           const float ref = M == -INFINITY ? 0.f : M;
           sum[0] = sum[1] = sum[2] = sum[3] = 0;
 #pragma unroll
-          for (int i = 0; i < kTile / 2; ++i) {
-            const float a0 = s[2 * i], a1 = s[2 * i + 1];
-            const float e = ex2_approx(big ? fmaf(a0 - m, c, -kHeadroom) : fmaf(a0, c, -ref));
-            const float f = ex2_approx(big ? fmaf(a1 - m, c, -kHeadroom) : fmaf(a1, c, -ref));
-            sum[i & 3] = add2(sum[i & 3], pack2(e, f));
-            w[i] = bf16x2(e, f);
+          for (int o = 0; o < kTile; o += 32) {
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float a0 = s[o + 2 * i], a1 = s[o + 2 * i + 1];
+              const float e = ex2_approx(big ? fmaf(a0 - m, c, -kHeadroom) : fmaf(a0, c, -ref));
+              const float f = ex2_approx(big ? fmaf(a1 - m, c, -kHeadroom) : fmaf(a1, c, -ref));
+              sum[i & 3] = add2(sum[i & 3], pack2(e, f));
+              w[i] = bf16x2(e, f);
+            }
+            tmem_st16(scol + o / 2, w);
           }
         }
-        tmem_st_cols(scol, w);
         float l0, l1;
         unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), l0, l1);
         l += l0 + l1;
