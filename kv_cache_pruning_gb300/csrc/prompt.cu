@@ -276,6 +276,34 @@ KVP_DEV void clear_bad_values(uint8_t* tile, int t, int pos, bool inside, int* b
   }
 }
 
+// mbar_wait for warps that wait while others of their scheduler compute: a probe may suspend the warp for a microsecond
+// (it wakes when the phase completes), so that a waiting warp takes no issue slots, and the flag that ends all waits is
+// looked at after a failed probe only.
+KVP_DEV bool wait_quietly(uint64_t* bar, uint32_t parity, const volatile int* abort, const volatile int32_t* status) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 0;; ++i) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(1000u)
+        : "memory");
+    if (done) return true;
+    if ((i & 63u) == 63u) {
+      if (*abort) return false;
+      if (status != nullptr && *status == KVP_ERR_TIMEOUT) return false;
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) {
+        t0 = now;
+      } else if (now - t0 > kWaitLimitNs) {
+        return false;
+      }
+    }
+  }
+}
+
 // One lane of a converged warp, and products and commits that this lane issues (`leader` nonzero there alone).
 KVP_DEV uint32_t elect_one() {
   uint32_t r;
@@ -398,7 +426,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
           const int st = i % C::kStages;
           if (i >= C::kStages) {  // tile i - kStages is given back with the pair (V of a block, K of the next) that it is of
             const int pair = (i - C::kStages + 1) / 2;
-            ok = mbar_wait(&empty[pair % C::kPairs], (pair / C::kPairs) & 1, abort_flag, p.seqs.status);
+            ok = wait_quietly(&empty[pair % C::kPairs], (pair / C::kPairs) & 1, abort_flag, p.seqs.status);
           }
           if (!ok) break;
           mbar_arrive_expect_tx(&full[st], C::kTileBytes);
@@ -424,7 +452,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
       const uint32_t leader = elect_one();
       const uint32_t q0 = smem_u32(smem + C::kQOff), ring = smem_u32(smem + C::kRingOff);
       auto wait_all = [&](uint64_t* bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.seqs.status)) != 0;
+        return __all_sync(0xffffffffu, wait_quietly(bar, parity, abort_flag, p.seqs.status)) != 0;
       };
       int st = 0;                    // ring stage and phase of the tile to land next
       uint32_t ph = 0;
@@ -474,11 +502,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
                 mma_ts(leader, tmem + kOCol + x * 128, tmem + kSCol + x * kTile + ks * 8, v0 + ((ks * 2048) >> 4), idO,
                        j > 0 || ks > 0);
               if (j == nx - 1) commit_to(leader, &o_full[x]);
-              if (j + 1 < nx) issue_s(x, kst);
+              // the next step's tiles, while these products run: V here, K beside the second tile's
+              if (x == 0 && j + 1 < n) ok = landed();
+              if (x == 1 && j + 2 < n) ok = landed();
+              if (ok && j + 1 < nx) issue_s(x, kst);
             }
+          } else if (ok && x == 1 ? j + 2 < n : j + 1 < n) {
+            ok = ok && landed();
           }
-          // while A's products run: the tiles of the next step
-          if (x == 0 && ok && j + 1 < n) ok = landed() && (j + 2 >= n || landed());
         }
         release(j + 1);
         vst += 2;
@@ -506,7 +537,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
       float M = -INFINITY, m = -INFINITY, l = 0.f;
       bool ok = true;
       for (int j = 0; j < nx; ++j) {
-        ok = mbar_wait(&s_full[x], j & 1, abort_flag, p.seqs.status);
+        ok = wait_quietly(&s_full[x], j & 1, abort_flag, p.seqs.status);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
@@ -580,7 +611,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
         l += l0 + l1;
         if (j == nx - 1) {
           const int i = 2 * j + 1;
-          ok = mbar_wait(&full[i % C::kStages], (i / C::kStages) & 1, abort_flag, p.seqs.status);
+          ok = wait_quietly(&full[i % C::kStages], (i / C::kStages) & 1, abort_flag, p.seqs.status);
           if (!__all_sync(0xffffffffu, ok)) {
             ok = false;
             break;
@@ -596,7 +627,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
       // what the other warps noted in `bad` is visible from here on (of two tiles of one head, also the other tile's)
       named_bar_sync(by_head ? 1 + x : 3, by_head ? 128 : 256);
       if (ok && nx > 0) {
-        ok = mbar_wait(&o_full[x], 0, abort_flag, p.seqs.status);
+        ok = wait_quietly(&o_full[x], 0, abort_flag, p.seqs.status);
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
       }
