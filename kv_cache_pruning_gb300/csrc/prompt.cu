@@ -89,6 +89,70 @@ KVP_DEV bool find_tile(const Seqs& s, int tile, int idx, Tile& t) {
   return false;
 }
 
+// The sequences' tiles of `tile` rows from the longest work to the shortest: by their number in their sequence, the last
+// ones first, and sequence by sequence among equal ones (a whole warp calls these).
+struct TileOrder {
+  const Seqs& s;
+  int tile, total, most;
+  int mine, my_start, my_len;  // with 32 sequences at most: this lane's
+  KVP_DEV TileOrder(const Seqs& seqs, int tile_) : s(seqs), tile(tile_) {
+    int sum = 0, top = 0;
+    const int lane = threadIdx.x & 31;
+    for (int i = lane; i < s.n; i += 32) {
+      my_len = seq_rows(s, i, my_start);
+      mine = (my_len + tile - 1) / tile;
+      sum += mine;
+      top = max(top, mine);
+    }
+    if (lane >= s.n) mine = my_len = my_start = 0;
+    total = __reduce_add_sync(0xffffffffu, sum);
+    most = __reduce_max_sync(0xffffffffu, top);
+  }
+  KVP_DEV int tiles(int i, int& start, int& len) const {
+    if (s.n <= 32) {
+      start = my_start;
+      len = my_len;
+      return mine;
+    }
+    len = i < s.n ? seq_rows(s, i, start) : 0;
+    return (len + tile - 1) / tile;
+  }
+  // tiles of number r and above in their sequences
+  KVP_DEV int from(int r) const {
+    int sum = 0, start, len;
+    for (int i = threadIdx.x & 31; i < (s.n + 31) / 32 * 32; i += 32) sum += max(0, tiles(i, start, len) - r);
+    return __reduce_add_sync(0xffffffffu, sum);
+  }
+  KVP_DEV Tile find(int idx) const {  // idx < total
+    int lo = 0, hi = most, above = 0;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2, f = from(mid);
+      if (f > idx) {
+        lo = mid;
+      } else {
+        hi = mid;
+        above = f;
+      }
+    }
+    Tile t{0, 0, 0, lo};
+    int left = idx - above;
+    const int lane = threadIdx.x & 31;
+    for (int base = 0; base < s.n; base += 32) {
+      int start = 0, len = 0;
+      const uint32_t has = __ballot_sync(0xffffffffu, tiles(base + lane, start, len) > lo);
+      if (left < __popc(has)) {
+        const int src = __fns(has, 0, left + 1);
+        t.seq = base + src;
+        t.start = __shfl_sync(0xffffffffu, start, src);
+        t.len = __shfl_sync(0xffffffffu, len, src);
+        break;
+      }
+      left -= __popc(has);
+    }
+    return t;
+  }
+};
+
 template <int D>
 KVP_DEV void load_row(const uint16_t* p, float (&x)[D / 32]) {
   const int lane = threadIdx.x & 31;
@@ -124,27 +188,35 @@ KVP_DEV float dot(const float (&a)[D / 32], const float (&b)[D / 32]) {
 // products of the block before).
 //
 // A masked weight is 0, but 0 times an infinite or NaN value is NaN: before the
-// products of the masked block its V tile is searched, such values are zeroed,
-// and the first row that holds one is noted for each column, for the rows that
-// do see it.
+// products of a masked block its V tile is searched and such values are zeroed.
+// Only then do the rows look them up in memory again, and add those they see.
+//
+// One CTA an SM takes work items in turn (warp 11 works them out one ahead): the
+// next item's Q, K and V are on their way, and its first S is there, while the
+// softmax warps still write the last one's rows. Items go out from the longest
+// to the shortest, forwards and backwards over the CTAs by turns.
+constexpr int kInfo = 2;                    // work items ahead
+constexpr int kFlags = 4;                   // items whose flags are apart: no warp is three items ahead of another
 template <int D>
 struct AttnCfg {
   static constexpr int kBoxes = D / 64;
   static constexpr int kBoxBytes = kTile * 128;          // 128 rows x 64 columns
   static constexpr int kTileBytes = kBoxes * kBoxBytes;  // one tile of Q, K or V
-  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kStages = D == 128 ? 5 : 8;       // ring of K and V tiles
+  static constexpr int kPairs = 8;                       // ring of barriers that give stages back
   static constexpr int kQOff = 0;
   static constexpr int kRingOff = 2 * kTileBytes;
-  static constexpr int kBadOff = kRingOff + kStages * kTileBytes;  // first row with +inf, -inf, NaN of each column
-  static constexpr int kBarOff = kBadOff + 3 * D * 4;
-  static constexpr int kPairs = 8;                       // ring of barriers that give stages back
-  static constexpr int kBars = 1 + kStages + kPairs + 2 + 2 + 2 + 1;
-  static constexpr int kSmem = 1024 + kBarOff + kBars * 8 + 32;
+  static constexpr int kBarOff = kRingOff + kStages * kTileBytes;
+  static constexpr int kBars = 2 + kStages + kPairs + 3 * 2 + 1 + 2 * kInfo;
+  static constexpr int kInfoOff = (kBarOff + kBars * 8 + 15) / 16 * 16;  // [slot]{first row, length, tile, column}
+  static constexpr int kFlagOff = kInfoOff + kInfo * 16;           // tensor memory's address, abort, bad values
+  static constexpr int kSmem = 1024 + kFlagOff + 8 + 8 * kFlags;
   static_assert(kSmem <= 232448, "shared memory budget");
-  static_assert(kBarOff % 8 == 0, "alignment");
+  static_assert(kRingOff % 1024 == 0 && kBarOff % 8 == 0 && kInfoOff % 16 == 0 && kFlagOff % 4 == 0,
+                "alignment");
 };
-constexpr int kSoftWarps = 8, kMmaWarp = 8, kCopyWarp = 9;
-constexpr int kAttnThreads = 384;             // warps 10 and 11 only give their registers away
+constexpr int kSoftWarps = 8, kMmaWarp = 8, kCopyWarp = 9, kPlanWarp = 11;
+constexpr int kAttnThreads = 384;             // warp 10 only gives its registers away
 // A row's 128 logits stay in registers: the softmax warps take 216 each and the
 // others 72, of the 168 a thread that the block is launched with:
 // 256 x 216 + 128 x 72 = 384 x 168.
@@ -247,32 +319,51 @@ KVP_DEV void weigh_block(const float (&s)[kTile], float c, float ref, uint32_t t
   for (int i = kTile / 2 - kBehind; i < kTile / 2; ++i) finish(i);
 }
 
-// Searches the V tile of 128 rows at `tile` (swizzled boxes) for infinities and NaN (128 threads call this, thread t
-// row t): they become zeros, and rows below `rows` note their position in bad[kind][column].
+// Searches row t of a V tile (swizzled boxes) for infinities and NaN (exponents of ones), and makes them zeros; if the row
+// is one of the sequence (`inside`), both tiles' flags get `tag` first.
 template <int D>
-KVP_DEV void clear_bad_values(uint8_t* tile, int t, int pos, bool inside, int* bad) {
+KVP_DEV void clear_bad_values(uint8_t* tile, int t, bool inside, volatile int* flags, int tag) {
   using C = AttnCfg<D>;
-#pragma unroll 4
+  auto at = [&](int c) {
+    return reinterpret_cast<uint4*>(tile + (c >> 3) * C::kBoxBytes + t * 128 + (((c & 7) ^ (t & 7)) << 4));
+  };
+  uint32_t found = 0;
+#pragma unroll 8
   for (int c = 0; c < D / 8; ++c) {
-    uint4* at = reinterpret_cast<uint4*>(tile + (c >> 3) * C::kBoxBytes + t * 128 + (((c & 7) ^ (t & 7)) << 4));
-    const uint4 w = *at;
-    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-    bool any = false;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) any |= (x[i] & 0x7F80u) == 0x7F80u || (x[i] & 0x7F800000u) == 0x7F800000u;
-    if (!any) continue;
-    uint32_t y[4];
+    const uint4 w = *at(c);
+    found |= ((w.x & 0x7F807F80u) + 0x00800080u) | ((w.y & 0x7F807F80u) + 0x00800080u) |
+             ((w.z & 0x7F807F80u) + 0x00800080u) | ((w.w & 0x7F807F80u) + 0x00800080u);
+  }
+  if ((found & 0x80008000u) == 0u) return;
+  if (inside) {
+    flags[0] = tag;
+    flags[1] = tag;
+    __threadfence_block();
+  }
+  for (int c = 0; c < D / 8; ++c) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(at(c));
     for (int i = 0; i < 4; ++i) {
-      y[i] = x[i];
-      for (int half = 0; half < 2; ++half) {
-        const uint32_t v = (x[i] >> (16 * half)) & 0xFFFFu;
-        if ((v & 0x7F80u) != 0x7F80u) continue;
-        y[i] &= half ? 0x0000FFFFu : 0xFFFF0000u;
-        const int kind = (v & 0x7Fu) != 0 ? 2 : (v >> 15);
-        if (inside) atomicMin(&bad[kind * D + c * 8 + 2 * i + half], pos);
+      if ((w[i] & 0x7F80u) == 0x7F80u) w[i] &= 0xFFFF0000u;
+      if ((w[i] & 0x7F800000u) == 0x7F800000u) w[i] &= 0x0000FFFFu;
+    }
+  }
+}
+
+// Adds the infinities and NaN of 32 columns of V that clear_bad_values took out, from memory: rows 0 .. last, `stride`
+// values apart.
+KVP_DEV void add_bad_values(float (&v)[32], const uint16_t* rows, int64_t stride, int last) {
+#pragma unroll 1
+  for (int r = 0; r <= last; ++r) {
+#pragma unroll
+    for (int k = 0; k < 32; k += 8) {
+      const uint4 q = *reinterpret_cast<const uint4*>(rows + r * stride + k);
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if ((w[i] & 0x7F80u) == 0x7F80u) v[k + 2 * i] += bf16_lo(w[i]);
+        if ((w[i] & 0x7F800000u) == 0x7F800000u) v[k + 2 * i + 1] += bf16_hi(w[i]);
       }
     }
-    *at = make_uint4(y[0], y[1], y[2], y[3]);
   }
 }
 
@@ -349,20 +440,24 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // the same in every lane, as the compiler can see
-  int* bad = reinterpret_cast<int*>(smem + C::kBadOff);
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
-  uint64_t* full = q_full + 1;
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* full = q_empty + 1;
   uint64_t* empty = full + C::kStages;
   uint64_t* s_full = empty + C::kPairs;  // [A, B]
   uint64_t* p_full = s_full + 2;
   uint64_t* o_full = p_full + 2;
   uint64_t* fin = o_full + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(fin + 1);
+  uint64_t* info_full = fin + 1;
+  uint64_t* info_empty = info_full + kInfo;
+  int4* info = reinterpret_cast<int4*>(smem + C::kInfoOff);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kFlagOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* s_tile = reinterpret_cast<int*>(tmem_slot + 2);  // start, length, first tile (-1: none)
+  volatile int* bad_values = abort_flag + 1;  // [item % kFlags][A, B]: item + 1 if masked blocks hold some
 
   if (tid == 0) {
     mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
     for (int i = 0; i < C::kStages; ++i) mbar_init(&full[i], 1);
     for (int i = 0; i < C::kPairs; ++i) mbar_init(&empty[i], 1);
     for (int x = 0; x < 2; ++x) {
@@ -371,74 +466,135 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
       mbar_init(&o_full[x], 1);
     }
     mbar_init(fin, 1);
+    for (int i = 0; i < kInfo; ++i) {
+      mbar_init(&info_full[i], 1);
+      mbar_init(&info_empty[i], kSoftWarps + 2);
+    }
     *abort_flag = 0;
+    for (int i = 0; i < 2 * kFlags; ++i) bad_values[i] = 0;
     fence_mbar_init();
     prefetch_tmap(&maps.q);
     prefetch_tmap(&maps.k);
     prefetch_tmap(&maps.v);
   }
-  for (int i = tid; i < 3 * D; i += kAttnThreads) bad[i] = INT32_MAX;
   if (warp == kMmaWarp) {
     tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish();
   }
   pdl_wait();
-  const bool by_head = p.G % 2 == 0;
-  const int cols = by_head ? p.Hq / 2 : p.Hq;  // work items of one tile
-  const int item = blockIdx.x / cols, col = blockIdx.x % cols;
-  if (warp == 0) {
-    Tile t;
-    const bool some = find_tile(p.seqs, by_head ? kTile : 2 * kTile, item, t);
-    if (lane == 0) {
-      s_tile[0] = some ? t.start : 0;
-      s_tile[1] = some ? t.len : 0;
-      s_tile[2] = some ? (by_head ? t.r : 2 * t.r) : -1;
-    }
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int start = s_tile[0], len = s_tile[1], tile0 = s_tile[2];
-  if (tile0 >= 0) {
-    // head and tile of A and B, and the key blocks of each
-    const int hA = by_head ? 2 * col : col, hB = by_head ? 2 * col + 1 : col;
-    const int tA = tile0, tB = by_head ? tile0 : tile0 + 1;
-    const int nA = tA + 1, nB = tB * kTile < len ? tB + 1 : 0;
-    const int n = max(nA, nB);
-    const int kv = hA / p.G;
+  const bool by_head = p.G % 2 == 0;
+  const int cols = by_head ? p.Hq / 2 : p.Hq;  // work items of one tile
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_quietly(bar, parity, abort_flag, p.seqs.status); };
+  auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+  auto gave_up = [&]() {
+    if (lane == 0) {
+      record_error(p.seqs.status, KVP_ERR_TIMEOUT);
+      *abort_flag = 1;
+    }
+  };
+  // A work item: A and B are heads hA, hB over tiles tA, tB of rows from `start` on, with nA and nB key blocks.
+  struct Item {
+    int start, len, tA, tB, hA, hB, nA, nB;
+  };
+  // Item number i of this CTA, as warp 11 leaves it (a whole warp calls this); false: there are no more, or a wait gave up.
+  auto next_item = [&](int i, Item& t, bool& ok) {
+    const int slot = i % kInfo;
+    ok = wait_all(&info_full[slot], (i / kInfo) & 1);
+    if (!ok) return false;
+    const int4 v = info[slot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&info_empty[slot]);
+    if (v.z < 0) return false;
+    t.start = v.x;
+    t.len = v.y;
+    t.tA = v.z;
+    t.tB = by_head ? v.z : v.z + 1;
+    t.hA = by_head ? 2 * v.w : v.w;
+    t.hB = by_head ? 2 * v.w + 1 : v.w;
+    t.nA = t.tA + 1;
+    t.nB = t.tB * kTile < t.len ? t.tB + 1 : 0;
+    return true;
+  };
+  Item t;
+  bool ok = true;
 
-    if (warp >= kSoftWarps) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
-    if (warp == kCopyWarp) {
-      // ------------------------------------------------------------ copies
-      if (lane == 0) {
-        auto load = [&](const CUtensorMap* m, uint8_t* dst, int head, int row, uint64_t* bar) {
-#pragma unroll
-          for (int b = 0; b < C::kBoxes; ++b) tma_load_3d(dst + b * C::kBoxBytes, m, 64 * b, head, row, bar);
-        };
-        mbar_arrive_expect_tx(q_full, (nB > 0 ? 2 : 1) * C::kTileBytes);
-        load(&maps.q, smem + C::kQOff, hA, start + tA * kTile, q_full);
-        if (nB > 0) load(&maps.q, smem + C::kQOff + C::kTileBytes, hB, start + tB * kTile, q_full);
-        int i = 0;
-        bool ok = true;
-        for (; i < 2 * n; ++i) {  // K of block 0, V of block 0, K of block 1, ...
-          const int st = i % C::kStages;
-          if (i >= C::kStages) {  // tile i - kStages is given back with the pair (V of a block, K of the next) that it is of
-            const int pair = (i - C::kStages + 1) / 2;
-            ok = wait_quietly(&empty[pair % C::kPairs], (pair / C::kPairs) & 1, abort_flag, p.seqs.status);
-          }
-          if (!ok) break;
-          mbar_arrive_expect_tx(&full[st], C::kTileBytes);
-          load((i & 1) ? &maps.v : &maps.k, smem + C::kRingOff + st * C::kTileBytes, kv, start + (i >> 1) * kTile,
-               &full[st]);
+  if (warp >= kSoftWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+    if (warp == kPlanWarp) {
+      // ------------------------------------------------------------ work items
+      const TileOrder order(p.seqs, by_head ? kTile : 2 * kTile);
+      const int64_t items = static_cast<int64_t>(order.total) * cols;
+      for (int i = 0;; ++i) {
+        const int64_t at = static_cast<int64_t>(i) * gridDim.x + ((i & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        int4 v = make_int4(0, 0, -1, 0);
+        if (at < items) {
+          const Tile f = order.find(static_cast<int>(at / cols));
+          v = make_int4(f.start, f.len, by_head ? f.r : 2 * f.r, static_cast<int>(at % cols));
         }
+        const int slot = i % kInfo;
+        if (i >= kInfo) ok = wait_all(&info_empty[slot], (i / kInfo - 1) & 1);
         if (!ok) {
-          record_error(p.seqs.status, KVP_ERR_TIMEOUT);
-          *abort_flag = 1;
-          // what was issued lands before the shared memory can go to another CTA (each wait bounded again)
-          (void)mbar_wait(q_full, 0);
-          for (int k = max(0, i - C::kStages); k < i; ++k) (void)mbar_wait(&full[k % C::kStages], (k / C::kStages) & 1);
+          gave_up();
+          break;
+        }
+        if (lane == 0) {
+          info[slot] = v;
+          mbar_arrive(&info_full[slot]);
+        }
+        __syncwarp();
+        if (v.z < 0) break;
+      }
+    } else if (warp == kCopyWarp) {
+      // ------------------------------------------------------------ copies
+      int g = 0, i = 0, nq = 0;  // tiles, items and pairs of query tiles so far
+      auto load = [&](const CUtensorMap* m, uint8_t* dst, int head, int row, uint64_t* bar) {
+#pragma unroll
+        for (int b = 0; b < C::kBoxes; ++b) tma_load_3d(dst + b * C::kBoxBytes, m, 64 * b, head, row, bar);
+      };
+      for (; next_item(i, t, ok); ++i) {
+        const int kv = t.hA / p.G, n = max(t.nA, t.nB);
+        if (lane == 0) {
+          for (int k = 0; ok && k < 2 * n; ++k) {  // K of block 0, V of block 0, K of block 1, ...
+            const int st = g % C::kStages;
+            if (g >= C::kStages) {  // tile g - kStages is given back with the pair (V of a block, K of the next) that it is of
+              const int pair = (g - C::kStages + 1) / 2;
+              ok = wait(&empty[pair % C::kPairs], (pair / C::kPairs) & 1);
+              if (!ok) break;
+            }
+            mbar_arrive_expect_tx(&full[st], C::kTileBytes);
+            load((k & 1) ? &maps.v : &maps.k, smem + C::kRingOff + st * C::kTileBytes, kv, t.start + (k >> 1) * kTile,
+                 &full[st]);
+            ++g;
+            if (k == 1) {  // the queries, once the last item's products with its own are done
+              if (i > 0) ok = wait(q_empty, (i - 1) & 1);
+              if (!ok) break;
+              ++nq;
+              mbar_arrive_expect_tx(q_full, (t.nB > 0 ? 2 : 1) * C::kTileBytes);
+              load(&maps.q, smem + C::kQOff, t.hA, t.start + t.tA * kTile, q_full);
+              if (t.nB > 0) load(&maps.q, smem + C::kQOff + C::kTileBytes, t.hB, t.start + t.tB * kTile, q_full);
+            }
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) {
+          gave_up();
+          break;
+        }
+      }
+      if (lane == 0 && g > 0) {
+        if (ok) {  // no arrival is left on its way when the CTA ends
+          ok = wait(q_empty, (i - 1) & 1);
+          for (int pair = max(0, (g - C::kStages + 1) / 2); ok && pair <= g / 2; ++pair)
+            ok = wait(&empty[pair % C::kPairs], (pair / C::kPairs) & 1);
+        }
+        // what was issued lands before the shared memory can go to another CTA (each wait bounded again)
+        if (!ok) {
+          if (nq > 0) (void)mbar_wait(q_full, (nq - 1) & 1);
+          for (int k = max(0, g - C::kStages); k < g; ++k) (void)mbar_wait(&full[k % C::kStages], (k / C::kStages) & 1);
         }
       }
       __syncwarp();
@@ -451,9 +607,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
       constexpr uint32_t idO = idesc_bf16_f32(kTile, D) | kIdescBMnMajor;
       const uint32_t leader = elect_one();
       const uint32_t q0 = smem_u32(smem + C::kQOff), ring = smem_u32(smem + C::kRingOff);
-      auto wait_all = [&](uint64_t* bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, wait_quietly(bar, parity, abort_flag, p.seqs.status)) != 0;
-      };
       int st = 0;                    // ring stage and phase of the tile to land next
       uint32_t ph = 0;
       auto landed = [&]() {
@@ -475,80 +628,84 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
         }
         commit_to(leader, &s_full[x]);
       };
-      // stages are given back only if a later copy takes one: no arrival is left on its way when the CTA ends
-      auto release = [&](int pair) {
-        if (2 * pair - 1 + C::kStages < 2 * n) commit_to(leader, &empty[pair % C::kPairs]);
+      int pair = 0;                  // V of an item's last block is given back with K of the next item's first
+      auto release = [&]() {
+        commit_to(leader, &empty[pair % C::kPairs]);
+        ++pair;
       };
-      int vst = 1, kst = 2;          // stages of V of block j and K of block j + 1
-      bool ok = wait_all(q_full, 0) && landed();
-      if (ok) {
+      uint32_t pph[2] = {0, 0};      // phases of p_full
+      int kst = 0;                   // ring stage of the K to use next; a V's is the one after its block's K
+      auto after = [&](int stage, int k) { return stage + k >= C::kStages ? stage + k - C::kStages : stage + k; };
+      int i = 0;
+      for (; next_item(i, t, ok); ++i) {
+        const int nA = t.nA, nB = t.nB, n = max(nA, nB);
+        ok = landed() && wait_all(q_full, i & 1);
+        if (!ok) break;
         tc_fence_after();
-        issue_s(0, 0);
-        if (nB > 0) issue_s(1, 0);
-        release(0);
+        // S and P of the last item's tiles are used up: its products come first in the pipe
+        issue_s(0, kst);
+        if (nB > 0) issue_s(1, kst);
+        release();
+        if (n == 1) commit_to(leader, q_empty);
         ok = landed() && (n < 2 || landed());
-      }
-      for (int j = 0; ok && j < n; ++j) {
+        for (int j = 0; ok && j < n; ++j) {
+          const int vst = after(kst, 1), nst = after(kst, 2);
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int nx = x == 0 ? nA : nB;
-          if (ok && j < nx) {
-            ok = wait_all(&p_full[x], j & 1);
-            if (ok) {
-              tc_fence_after();
-              const uint64_t v0 = sw128_mnmajor_desc(ring + vst * C::kTileBytes, C::kBoxBytes, 1024);
+          for (int x = 0; x < 2; ++x) {
+            const int nx = x == 0 ? nA : nB;
+            if (ok && j < nx) {
+              ok = wait_all(&p_full[x], pph[x]);
+              pph[x] ^= 1;
+              if (ok) {
+                tc_fence_after();
+                const uint64_t v0 = sw128_mnmajor_desc(ring + vst * C::kTileBytes, C::kBoxBytes, 1024);
 #pragma unroll
-              for (int ks = 0; ks < kTile / 16; ++ks)
-                mma_ts(leader, tmem + kOCol + x * 128, tmem + kSCol + x * kTile + ks * 8, v0 + ((ks * 2048) >> 4), idO,
-                       j > 0 || ks > 0);
-              if (j == nx - 1) commit_to(leader, &o_full[x]);
-              // the next step's tiles, while these products run: V here, K beside the second tile's
-              if (x == 0 && j + 1 < n) ok = landed();
-              if (x == 1 && j + 2 < n) ok = landed();
-              if (ok && j + 1 < nx) issue_s(x, kst);
+                for (int ks = 0; ks < kTile / 16; ++ks)
+                  mma_ts(leader, tmem + kOCol + x * 128, tmem + kSCol + x * kTile + ks * 8, v0 + ((ks * 2048) >> 4), idO,
+                         j > 0 || ks > 0);
+                if (j == nx - 1) commit_to(leader, &o_full[x]);
+              }
             }
-          } else if (ok && x == 1 ? j + 2 < n : j + 1 < n) {
-            ok = ok && landed();
+            // the next step's tiles, while these products run: V here, K beside the second tile's
+            if (ok && j + 1 + x < n) ok = landed();
+            if (ok && j + 1 < nx) issue_s(x, nst);
           }
+          if (j + 1 < n) release();
+          if (j + 2 == n) commit_to(leader, q_empty);
+          kst = nst;
         }
-        release(j + 1);
-        vst += 2;
-        if (vst >= C::kStages) vst -= C::kStages;
-        kst += 2;
-        if (kst >= C::kStages) kst -= C::kStages;
+        if (!ok) break;
       }
-      if (!ok && lane == 0) {
-        record_error(p.seqs.status, KVP_ERR_TIMEOUT);
-        *abort_flag = 1;
-      }
+      if (ok && i > 0) release();    // V of the last item's last block
+      if (!ok) gave_up();
       commit_to(leader, fin);
       (void)mbar_wait(fin, 0);  // every product has completed before tensor and shared memory go
-      __syncwarp();
     }
-    } else {
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
-      // ------------------------------------------------------------ softmax
-      const int x = warp >> 2, row = (warp & 3) * 32 + lane;
-      const int nx = x == 0 ? nA : nB, tile = x == 0 ? tA : tB, head = x == 0 ? hA : hB;
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
+    // ------------------------------------------------------------ softmax
+    const int x = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t scol = trow + kSCol + x * kTile, ocol = trow + kOCol + x * 128;
+    const float c = p.qscale;
+    uint32_t sph = 0, oph = 0;  // phases of s_full and o_full
+    uint32_t g = 0;             // tiles of K and V before this item
+    for (int i = 0; next_item(i, t, ok); ++i) {
+      const int nx = x == 0 ? t.nA : t.nB, tile = x == 0 ? t.tA : t.tB, head = x == 0 ? t.hA : t.hB;
       const int pos = tile * kTile + row;  // in the sequence; past its end: nothing is stored
-      const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-      const uint32_t scol = trow + kSCol + x * kTile, ocol = trow + kOCol + x * 128;
-      const float c = p.qscale;
+      volatile int* flags = bad_values + i % kFlags * 2;
       float M = -INFINITY, m = -INFINITY, l = 0.f;
-      bool ok = true;
       for (int j = 0; j < nx; ++j) {
-        ok = wait_quietly(&s_full[x], j & 1, abort_flag, p.seqs.status);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
+        ok = wait_all(&s_full[x], sph);
+        sph ^= 1;
+        if (!ok) break;
         tc_fence_after();
         float s[kTile];
         tmem_ld128(scol, s);
         if (j == nx - 1) {
 #pragma unroll
-          for (int i = 0; i < kTile; ++i)
-            if (i > row) s[i] = -INFINITY;
+          for (int k = 0; k < kTile; ++k)
+            if (k > row) s[k] = -INFINITY;
         }
         uint64_t sum[4];
         // With the reference as it is: no maximum is taken. If a row's sum says that some weight may have passed it by
@@ -609,14 +766,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
         float l0, l1;
         unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), l0, l1);
         l += l0 + l1;
-        if (j == nx - 1) {
-          const int i = 2 * j + 1;
-          ok = wait_quietly(&full[i % C::kStages], (i / C::kStages) & 1, abort_flag, p.seqs.status);
-          if (!__all_sync(0xffffffffu, ok)) {
-            ok = false;
-            break;
-          }
-          clear_bad_values<D>(smem + C::kRingOff + (i % C::kStages) * C::kTileBytes, row, pos, pos < len, bad);
+        // the masked block's values (of two heads the first tile's warps see to them: its products come first)
+        if (j == nx - 1 && (x == 0 || !by_head)) {
+          const uint32_t k = g + 2 * j + 1;
+          ok = wait_all(&full[k % C::kStages], (k / C::kStages) & 1);
+          if (!ok) break;
+          clear_bad_values<D>(smem + C::kRingOff + (k % C::kStages) * C::kTileBytes, row, pos < t.len, flags, i + 1);
           fence_proxy_async();
         }
         tmem_st_wait();
@@ -624,62 +779,42 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[x]);
       }
-      // what the other warps noted in `bad` is visible from here on (of two tiles of one head, also the other tile's)
-      named_bar_sync(by_head ? 1 + x : 3, by_head ? 128 : 256);
-      if (ok && nx > 0) {
-        ok = wait_quietly(&o_full[x], 0, abort_flag, p.seqs.status);
-        ok = __all_sync(0xffffffffu, ok);
-        tc_fence_after();
-      }
-      if (!ok) {
-        if (lane == 0) {
-          record_error(p.seqs.status, KVP_ERR_TIMEOUT);
-          *abort_flag = 1;
-        }
-      } else if (nx > 0) {
-        const bool mine = pos < len;
-        const int64_t r = start + pos;
-        uint16_t* out = p.out + r * p.ot + head * p.oh;
-        const float inv = l == 0.f ? 0.f : 1.f / l;
+      g += 2 * max(t.nA, t.nB);
+      if (!ok) break;
+      if (nx == 0) continue;
+      ok = wait_all(&o_full[x], oph);
+      oph ^= 1;
+      if (!ok) break;
+      tc_fence_after();
+      const bool some = flags[x] == i + 1;
+      const bool mine = pos < t.len;
+      const int64_t r = t.start + pos;
+      uint16_t* out = p.out + r * p.ot + head * p.oh;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
-        for (int o = 0; o < D; o += 32) {
-          float v[32];
-          tmem_ld32(ocol + o, v);
-          uint32_t w[16];
+      for (int o = 0; o < D; o += 32) {
+        float v[32];
+        tmem_ld32(ocol + o, v);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            v[i] *= inv;
-            if (l == 0.f) v[i] = 0.f;
-          }
-          bool some = false;
+        for (int k = 0; k < 32; ++k) v[k] = l == 0.f ? 0.f : v[k] * inv;
+        if (some && mine)
+          add_bad_values(v, p.v + (t.start + t.tA * kTile) * p.vt + head / p.G * p.vh + o, p.vt, pos - t.tA * kTile);
+        if (mine) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int b = min(bad[o + i], min(bad[D + o + i], bad[2 * D + o + i]));
-            some |= b <= pos;
-          }
-          if (some) {
-            for (int i = 0; i < 32; ++i) {
-              const bool up = bad[o + i] <= pos, down = bad[D + o + i] <= pos, nan = bad[2 * D + o + i] <= pos;
-              if (up) v[i] += INFINITY;
-              if (down) v[i] -= INFINITY;
-              if (nan) v[i] = NAN;
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 16; ++i) w[i] = bf16x2(v[2 * i], v[2 * i + 1]);
-          if (mine) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              reinterpret_cast<uint4*>(out + o)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-          }
+          for (int k = 0; k < 32; k += 8)
+            *reinterpret_cast<uint4*>(out + o + k) =
+                make_uint4(bf16x2(v[k], v[k + 1]), bf16x2(v[k + 2], v[k + 3]), bf16x2(v[k + 4], v[k + 5]),
+                           bf16x2(v[k + 6], v[k + 7]));
         }
-        if (mine && p.lse != nullptr) {
-          // the reference and the sum's logarithm; a big one as it was taken
-          const float ref = fabsf(M) >= kBig ? m * c + kHeadroom : M;
-          p.lse[head * p.seqs.n_tok + r] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
-        }
+      }
+      tc_fence_before();  // O has been read: the next item's products may overwrite it once its P is there
+      if (mine && p.lse != nullptr) {
+        // the reference and the sum's logarithm; a big one as it was taken
+        const float ref = fabsf(M) >= kBig ? m * c + kHeadroom : M;
+        p.lse[head * p.seqs.n_tok + r] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
       }
     }
+    if (!ok) gave_up();
   }
   tc_fence_before();
   __syncthreads();
@@ -715,7 +850,8 @@ kvp_status launch_attn(const PromptParams& p, int n_kv_heads, cudaStream_t st) {
     return KVP_ERR_CUDA;
   static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is raised
   int device = 0;
-  if (current_sms(&device) == 0) return KVP_ERR_CUDA;
+  const int sms = current_sms(&device);
+  if (sms == 0) return KVP_ERR_CUDA;
   if (device > 63 || (ready.load(std::memory_order_relaxed) >> device & 1u) == 0) {
     if (cudaFuncSetAttribute(prompt_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) !=
         cudaSuccess) {
@@ -725,11 +861,9 @@ kvp_status launch_attn(const PromptParams& p, int n_kv_heads, cudaStream_t st) {
     if (device <= 63) ready.fetch_or(uint64_t{1} << device, std::memory_order_relaxed);
   }
   const bool by_head = p.G % 2 == 0;
-  const int tile = by_head ? kTile : 2 * kTile;
-  const int64_t ctas = (p.seqs.n_tok / tile + p.seqs.n) * (by_head ? p.Hq / 2 : p.Hq);
-  if (ctas > 0x7fffffff) return KVP_ERR_UNSUPPORTED;
-  return launch_pdl(prompt_attn_kernel<D>, dim3(static_cast<unsigned>(ctas)), dim3(kAttnThreads), C::kSmem, st, p,
-                    maps) == cudaSuccess
+  const int64_t most = (p.seqs.n_tok / (by_head ? kTile : 2 * kTile) + p.seqs.n) * (by_head ? p.Hq / 2 : p.Hq);
+  return launch_pdl(prompt_attn_kernel<D>, dim3(static_cast<unsigned>(std::min<int64_t>(sms, most))), dim3(kAttnThreads),
+                    C::kSmem, st, p, maps) == cudaSuccess
              ? KVP_OK
              : KVP_ERR_CUDA;
 }
