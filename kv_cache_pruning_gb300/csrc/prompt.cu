@@ -1,175 +1,10 @@
-// kvp_prompt_attn, kvp_prompt_weights: causal attention over packed prompts,
-// and the weight that every key received (DMS article, "DMS 작동 방식" step 5:
-// the standard attention, here of a whole prompt).
-//
-// The simplest form of both: a warp a row, its lanes over the head's values, an
-// online softmax key by key.
-#include "kvp_common.cuh"
+// kvp_prompt_attn: causal attention over packed prompts (DMS article, "DMS 작동
+// 방식" step 5: the standard attention, here of a whole prompt).
+#include "prompt.cuh"
 
 namespace kvp {
 namespace {
 
-constexpr int kTile = 128;       // rows of a sequence that a CTA takes
-constexpr int kPWarps = 8;
-constexpr float kLn2 = 0.69314718055994531f;
-constexpr float kLog2e = 1.4426950408889634f;
-// A weight is held as 2^(x - reference - kHeadroom): sums of up to 2^20 values of any bf16 size (the reference may
-// lag by 2^8) stay below 2^128 that way.
-constexpr float kHeadroom = 28.f;
-
-struct Seqs {
-  const int32_t* start;
-  const int32_t* len;
-  int n;
-  int64_t n_tok;
-  int32_t* status;
-};
-
-struct PromptParams {
-  Seqs seqs;
-  const uint16_t* q;
-  const uint16_t* k;
-  const uint16_t* v;
-  int64_t qt, qh, kt, kh, vt, vh, ot, oh;
-  int Hq, G;
-  float qscale;   // scale * log2 e
-  uint16_t* out;
-  float* lse;
-  // weights
-  const float* lse_in;
-  int n_last;
-  float* acc;
-  int64_t as, at, ah;
-  int acc_len;
-};
-
-struct Tile {
-  int seq, start, len, r;  // sequence, its first row and length, tile of it
-};
-
-// A sequence's rows; one that breaks the rules is recorded and has none.
-KVP_DEV int seq_rows(const Seqs& s, int i, int& start) {
-  start = s.start[i];
-  const int end = s.start[i + 1];
-  const int len = s.len != nullptr ? s.len[i] : end - start;
-  if (start < 0 || end < start || end > s.n_tok || len < 0 || len > end - start) {
-    record_error(s.status, KVP_ERR_BOUNDS);
-    return 0;
-  }
-  return len;
-}
-
-// Number `idx` of all sequences' tiles of `tile` rows, each sequence's last tile first (a whole warp calls this); false
-// past the last.
-KVP_DEV bool find_tile(const Seqs& s, int tile, int idx, Tile& t) {
-  const int lane = threadIdx.x & 31;
-  int before = 0;
-  for (int base = 0; base < s.n; base += 32) {
-    const int i = base + lane;
-    int start = 0;
-    const int len = i < s.n ? seq_rows(s, i, start) : 0;
-    const int tiles = (len + tile - 1) / tile;
-    int incl = tiles;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    const uint32_t hit = __ballot_sync(0xffffffffu, idx < before + incl);
-    if (hit != 0) {
-      const int src = __ffs(hit) - 1;
-      t.seq = base + src;
-      t.start = __shfl_sync(0xffffffffu, start, src);
-      t.len = __shfl_sync(0xffffffffu, len, src);
-      t.r = before + __shfl_sync(0xffffffffu, incl, src) - 1 - idx;
-      return true;
-    }
-    before += __shfl_sync(0xffffffffu, incl, 31);
-  }
-  return false;
-}
-
-// The sequences' tiles of `tile` rows from the longest work to the shortest: by their number in their sequence, the last
-// ones first, and sequence by sequence among equal ones (a whole warp calls these).
-struct TileOrder {
-  const Seqs& s;
-  int tile, total, most;
-  int mine, my_start, my_len;  // with 32 sequences at most: this lane's
-  KVP_DEV TileOrder(const Seqs& seqs, int tile_) : s(seqs), tile(tile_) {
-    int sum = 0, top = 0;
-    const int lane = threadIdx.x & 31;
-    for (int i = lane; i < s.n; i += 32) {
-      my_len = seq_rows(s, i, my_start);
-      mine = (my_len + tile - 1) / tile;
-      sum += mine;
-      top = max(top, mine);
-    }
-    if (lane >= s.n) mine = my_len = my_start = 0;
-    total = __reduce_add_sync(0xffffffffu, sum);
-    most = __reduce_max_sync(0xffffffffu, top);
-  }
-  KVP_DEV int tiles(int i, int& start, int& len) const {
-    if (s.n <= 32) {
-      start = my_start;
-      len = my_len;
-      return mine;
-    }
-    len = i < s.n ? seq_rows(s, i, start) : 0;
-    return (len + tile - 1) / tile;
-  }
-  // tiles of number r and above in their sequences
-  KVP_DEV int from(int r) const {
-    int sum = 0, start, len;
-    for (int i = threadIdx.x & 31; i < (s.n + 31) / 32 * 32; i += 32) sum += max(0, tiles(i, start, len) - r);
-    return __reduce_add_sync(0xffffffffu, sum);
-  }
-  KVP_DEV Tile find(int idx) const {  // idx < total
-    int lo = 0, hi = most, above = 0;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2, f = from(mid);
-      if (f > idx) {
-        lo = mid;
-      } else {
-        hi = mid;
-        above = f;
-      }
-    }
-    Tile t{0, 0, 0, lo};
-    int left = idx - above;
-    const int lane = threadIdx.x & 31;
-    for (int base = 0; base < s.n; base += 32) {
-      int start = 0, len = 0;
-      const uint32_t has = __ballot_sync(0xffffffffu, tiles(base + lane, start, len) > lo);
-      if (left < __popc(has)) {
-        const int src = __fns(has, 0, left + 1);
-        t.seq = base + src;
-        t.start = __shfl_sync(0xffffffffu, start, src);
-        t.len = __shfl_sync(0xffffffffu, len, src);
-        break;
-      }
-      left -= __popc(has);
-    }
-    return t;
-  }
-};
-
-template <int D>
-KVP_DEV void load_row(const uint16_t* p, float (&x)[D / 32]) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) x[i] = __uint_as_float(static_cast<uint32_t>(p[i * 32 + lane]) << 16);
-}
-template <int D>
-KVP_DEV float dot(const float (&a)[D / 32], const float (&b)[D / 32]) {
-  float s = 0.f;
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) s = fmaf(a[i], b[i], s);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return s;
-}
-
-// ---------------------------------------------------------------- attention
 // S = Q K^T and O += P V on tcgen05, 128 query rows x 128 keys a step, two such
 // query tiles (A and B) a CTA so that the tensor cores work on one while the
 // softmax of the other runs. The tiles share their K and V: they are two query
@@ -227,63 +62,9 @@ constexpr float kLazy = 8.f;                // how far a row's maximum may pass 
 constexpr float kMostSum = 1.f / 8192;      // 128 weights of 2^(kLazy - kHeadroom)
 constexpr float kBig = 268435456.f;         // from references of 2^28 on, x c - M is taken as (x - max) c
 
-// Two fp32 values as one register pair: packed arithmetic of sm_100 and later.
-KVP_DEV uint64_t pack2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-KVP_DEV void unpack2(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-KVP_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-KVP_DEV uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 KVP_DEV uint32_t bf16x2(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&b);
-}
-
-// Loads 128 consecutive fp32 columns of this warp's 32 TMEM lanes (one row per thread) in one round and waits for them,
-// in one asm block so that no use can move above the wait.
-KVP_DEV void tmem_ld128(uint32_t taddr, float (&v)[128]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%128];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
-      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%129];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,"
-      "%80,%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95}, [%130];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,%111,"
-      "%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127}, [%131];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
-        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
-        "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
-        "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31]),
-        "=f"(v[32]), "=f"(v[33]), "=f"(v[34]), "=f"(v[35]), "=f"(v[36]), "=f"(v[37]), "=f"(v[38]), "=f"(v[39]),
-        "=f"(v[40]), "=f"(v[41]), "=f"(v[42]), "=f"(v[43]), "=f"(v[44]), "=f"(v[45]), "=f"(v[46]), "=f"(v[47]),
-        "=f"(v[48]), "=f"(v[49]), "=f"(v[50]), "=f"(v[51]), "=f"(v[52]), "=f"(v[53]), "=f"(v[54]), "=f"(v[55]),
-        "=f"(v[56]), "=f"(v[57]), "=f"(v[58]), "=f"(v[59]), "=f"(v[60]), "=f"(v[61]), "=f"(v[62]), "=f"(v[63]),
-        "=f"(v[64]), "=f"(v[65]), "=f"(v[66]), "=f"(v[67]), "=f"(v[68]), "=f"(v[69]), "=f"(v[70]), "=f"(v[71]),
-        "=f"(v[72]), "=f"(v[73]), "=f"(v[74]), "=f"(v[75]), "=f"(v[76]), "=f"(v[77]), "=f"(v[78]), "=f"(v[79]),
-        "=f"(v[80]), "=f"(v[81]), "=f"(v[82]), "=f"(v[83]), "=f"(v[84]), "=f"(v[85]), "=f"(v[86]), "=f"(v[87]),
-        "=f"(v[88]), "=f"(v[89]), "=f"(v[90]), "=f"(v[91]), "=f"(v[92]), "=f"(v[93]), "=f"(v[94]), "=f"(v[95]),
-        "=f"(v[96]), "=f"(v[97]), "=f"(v[98]), "=f"(v[99]), "=f"(v[100]), "=f"(v[101]), "=f"(v[102]), "=f"(v[103]),
-        "=f"(v[104]), "=f"(v[105]), "=f"(v[106]), "=f"(v[107]), "=f"(v[108]), "=f"(v[109]), "=f"(v[110]), "=f"(v[111]),
-        "=f"(v[112]), "=f"(v[113]), "=f"(v[114]), "=f"(v[115]), "=f"(v[116]), "=f"(v[117]), "=f"(v[118]), "=f"(v[119]),
-        "=f"(v[120]), "=f"(v[121]), "=f"(v[122]), "=f"(v[123]), "=f"(v[124]), "=f"(v[125]), "=f"(v[126]), "=f"(v[127])
-      : "r"(taddr), "r"(taddr + 32), "r"(taddr + 64), "r"(taddr + 96)
-      : "memory");
 }
 
 // The weights 2^(s c + ref) of a row's 128 logits: to tensor memory as bf16 pairs, and their sums (of the unrounded ones)
@@ -365,67 +146,6 @@ KVP_DEV void add_bad_values(float (&v)[32], const uint16_t* rows, int64_t stride
       }
     }
   }
-}
-
-// mbar_wait for warps that wait while others of their scheduler compute: a probe may suspend the warp for a microsecond
-// (it wakes when the phase completes), so that a waiting warp takes no issue slots, and the flag that ends all waits is
-// looked at after a failed probe only.
-KVP_DEV bool wait_quietly(uint64_t* bar, uint32_t parity, const volatile int* abort, const volatile int32_t* status) {
-  uint64_t t0 = 0;
-  for (uint32_t i = 0;; ++i) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(1000u)
-        : "memory");
-    if (done) return true;
-    if ((i & 63u) == 63u) {
-      if (*abort) return false;
-      if (status != nullptr && *status == KVP_ERR_TIMEOUT) return false;
-      const uint64_t now = globaltimer_ns();
-      if (t0 == 0) {
-        t0 = now;
-      } else if (now - t0 > kWaitLimitNs) {
-        return false;
-      }
-    }
-  }
-}
-
-// One lane of a converged warp, and products and commits that this lane issues (`leader` nonzero there alone).
-KVP_DEV uint32_t elect_one() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-  return r;
-}
-KVP_DEV void mma_ss(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)), "r"(leader)
-      : "memory");
-}
-KVP_DEV void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)), "r"(leader)
-      : "memory");
-}
-KVP_DEV void commit_to(uint32_t leader, uint64_t* bar) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\t"
-      "setp.ne.b32 q, %1, 0;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
-      "r"(leader)
-      : "memory");
 }
 
 struct AttnMaps {
@@ -824,22 +544,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
   }
 }
 
-// Rows of bf16 [rows, heads, D] with the given strides as a tensor map whose boxes are 128 rows x 64 columns of a head.
-template <int D>
-bool make_tmap_heads(CUtensorMap* m, const void* base, int64_t rows, int64_t st, int heads, int64_t sh) {
-  auto fn = tmap_encode_fn();
-  if (fn == nullptr) return false;
-  if (heads == 1) sh = D;
-  if (rows == 1) st = D;
-  const cuuint64_t dims[3] = {D, static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(sh) * 2, static_cast<cuuint64_t>(st) * 2};
-  const cuuint32_t box[3] = {64, 1, kTile};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int D>
 kvp_status launch_attn(const PromptParams& p, int n_kv_heads, cudaStream_t st) {
   using C = AttnCfg<D>;
@@ -866,65 +570,6 @@ kvp_status launch_attn(const PromptParams& p, int n_kv_heads, cudaStream_t st) {
                     C::kSmem, st, p, maps) == cudaSuccess
              ? KVP_OK
              : KVP_ERR_CUDA;
-}
-
-template <int D>
-__global__ void __launch_bounds__(kPWarps * 32) prompt_weights_kernel(const PromptParams p) {
-  pdl_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = blockIdx.y;
-  Tile t;
-  if (!find_tile(p.seqs, kTile, blockIdx.x, t)) return;
-  const int first = p.n_last > 0 ? max(0, t.len - p.n_last) : 0;
-  for (int c = t.r * kTile + warp; c < min(t.len, (t.r + 1) * kTile); c += kPWarps) {
-    float k[D / 32], total = 0.f;
-    load_row<D>(p.k + (t.start + c) * p.kt + h * p.kh, k);
-    for (int r0 = max(first, c) / kTile * kTile; r0 < t.len; r0 += kTile)
-      for (int j = h * p.G; j < (h + 1) * p.G; ++j) {
-        float part = 0.f;
-        for (int r = max(r0, max(first, c)); r < min(t.len, r0 + kTile); ++r) {
-          const int64_t row = t.start + r;
-          float q[D / 32];
-          load_row<D>(p.q + row * p.qt + j * p.qh, q);
-          const float x = dot<D>(q, k) * p.qscale, lse = p.lse_in[j * p.seqs.n_tok + row];
-          if (lse != -INFINITY) part += exp2f(x - lse * kLog2e);
-        }
-        total += part;
-      }
-    if (lane == 0) {
-      if (p.as < 0) {
-        p.acc[(t.start + c) * p.at + h * p.ah] = total;
-      } else if (c < p.acc_len) {
-        p.acc[t.seq * p.as + c * p.at + h * p.ah] = total;
-      } else {
-        record_error(p.seqs.status, KVP_ERR_BOUNDS);
-      }
-    }
-  }
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
-// Strides of an input whose rows are read in place.
-kvp_status check_rows(const void* p, int64_t n_tok, int64_t st, int heads, int64_t sh) {
-  if (p == nullptr) return KVP_ERR_INVALID;
-  if (st < 0 || sh < 0 || (n_tok > 1 && st == 0) || (heads > 1 && sh == 0)) return KVP_ERR_INVALID;
-  if (!aligned16(p) || st % 8 != 0 || sh % 8 != 0) return KVP_ERR_ALIGN;
-  if (st > (int64_t{1} << 38) || sh > (int64_t{1} << 38)) return KVP_ERR_UNSUPPORTED;
-  return KVP_OK;
-}
-
-kvp_status check_prompt(int n_seqs, int64_t n_tok, int n_q_heads, int n_kv_heads, int head_dim,
-                        const int32_t* seq_start, const int32_t* seq_len, float scale) {
-  if (n_seqs < 0 || n_tok < 0 || n_q_heads <= 0 || n_kv_heads <= 0) return KVP_ERR_INVALID;
-  if (!(scale >= 0.f) || scale > 3.402823466e38f) return KVP_ERR_INVALID;
-  if (head_dim != 64 && head_dim != 128) return KVP_ERR_UNSUPPORTED;
-  if (n_q_heads % n_kv_heads != 0) return KVP_ERR_INVALID;
-  if (n_q_heads > 65535 || n_tok > 0x7fffffffll) return KVP_ERR_UNSUPPORTED;
-  if (n_seqs > 0 && n_tok > 0 && seq_start == nullptr) return KVP_ERR_INVALID;
-  if (!aligned4(seq_start) || !aligned4(seq_len)) return KVP_ERR_ALIGN;
-  return KVP_OK;
 }
 
 }  // namespace
@@ -958,45 +603,4 @@ extern "C" kvp_status kvp_prompt_attn(int n_seqs, int64_t n_tok, int n_q_heads, 
   p.lse = lse;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   return head_dim == 128 ? launch_attn<128>(p, n_kv_heads, cs) : launch_attn<64>(p, n_kv_heads, cs);
-}
-
-extern "C" kvp_status kvp_prompt_weights(int n_seqs, int64_t n_tok, int n_q_heads, int n_kv_heads, int head_dim,
-                                         const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k,
-                                         int64_t k_stride_t, int64_t k_stride_h, const int32_t* seq_start,
-                                         const int32_t* seq_len, const float* lse, float scale, int n_last, float* acc,
-                                         int64_t acc_stride_s, int64_t acc_stride_t, int64_t acc_stride_h, int acc_len,
-                                         int32_t* status, void* stream) {
-  kvp_status r = check_prompt(n_seqs, n_tok, n_q_heads, n_kv_heads, head_dim, seq_start, seq_len, scale);
-  if (r != KVP_OK) return r;
-  if (n_last < 0 || acc_stride_s < -1 || acc_stride_t < 0 || acc_stride_h < 0) return KVP_ERR_INVALID;
-  if (acc_stride_s >= 0 && acc_len < 0) return KVP_ERR_INVALID;
-  if (n_seqs == 0 || n_tok == 0) return KVP_OK;
-  if ((r = check_rows(q, n_tok, q_stride_t, n_q_heads, q_stride_h)) != KVP_OK) return r;
-  if ((r = check_rows(k, n_tok, k_stride_t, n_kv_heads, k_stride_h)) != KVP_OK) return r;
-  if (lse == nullptr || acc == nullptr) return KVP_ERR_INVALID;
-  if (!aligned4(lse) || !aligned4(acc)) return KVP_ERR_ALIGN;
-  const bool by_token = acc_stride_s < 0;
-  if (!rows_apart({{{by_token ? 0 : acc_stride_s, by_token ? 1 : n_seqs},
-                    {acc_stride_t, by_token ? n_tok : acc_len},
-                    {acc_stride_h, n_kv_heads}}},
-                  1))
-    return KVP_ERR_INVALID;
-  PromptParams p{};
-  p.seqs = Seqs{seq_start, seq_len, n_seqs, n_tok, status};
-  p.q = static_cast<const uint16_t*>(q), p.qt = q_stride_t, p.qh = q_stride_h;
-  p.k = static_cast<const uint16_t*>(k), p.kt = k_stride_t, p.kh = k_stride_h;
-  p.Hq = n_q_heads, p.G = n_q_heads / n_kv_heads;
-  p.qscale = (scale > 0.f ? scale : 1.f / sqrtf(static_cast<float>(head_dim))) * kLog2e;
-  p.lse_in = lse;
-  p.n_last = n_last;
-  p.acc = acc, p.as = acc_stride_s, p.at = acc_stride_t, p.ah = acc_stride_h, p.acc_len = acc_len;
-  const int64_t tiles = n_tok / kTile + n_seqs;
-  if (tiles > 0x7fffffff) return KVP_ERR_UNSUPPORTED;
-  const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(n_kv_heads));
-  auto go = [&](auto kern) {
-    return launch_pdl(kern, grid, dim3(kPWarps * 32), 0, static_cast<cudaStream_t>(stream), p) == cudaSuccess
-               ? KVP_OK
-               : KVP_ERR_CUDA;
-  };
-  return head_dim == 128 ? go(prompt_weights_kernel<128>) : go(prompt_weights_kernel<64>);
 }

@@ -76,7 +76,8 @@ def weights(q, k, lse, seqs, scale=None, n_last=0):
         a, n = s
         x, err = logits(q[a:a + n], k[a:a + n], scale)
         ls = lse[:, a:a + n].double()
-        w = torch.where(torch.isneginf(ls)[..., None], 0.0, torch.exp(x - ls[..., None]))
+        later = torch.ones(n, n, dtype=torch.bool, device=q.device).triu(1)      # whatever their lse is
+        w = torch.where(torch.isneginf(ls)[..., None] | later, 0.0, torch.exp(x - ls[..., None]))
         rel = err + 2.0 ** -22 * (torch.where(torch.isfinite(ls), ls.abs(), 0.0) + 1)
         if n_last:
             w, rel = w[:, max(0, n - n_last):], rel[:, max(0, n - n_last):]

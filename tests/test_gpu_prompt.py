@@ -376,6 +376,18 @@ def test_weights_of_queries_that_pay_nothing(kvp):
     check_weights(kvp, q, k, [0, 300], lse=lse)
 
 
+@pytest.mark.parametrize("n_last", [0, 20, 200])
+def test_weights_of_rows_that_are_no_number(kvp, n_last):
+    """A NaN normaliser touches the keys that its query sees, not those after it."""
+    q, k, _ = qkv(48, 500, 4, 2, 128)
+    lse = ref.attention(q, k, k, [(0, 500)])[1].float()
+    lse[0, 480], lse[2, 490:495] = math.nan, math.nan
+    check_weights(kvp, q, k, [0, 500], lse=lse, n_last=n_last)
+    got = kvp.kvp_prompt_weights(q, k, i32([0, 500]), lse, n_last=n_last)
+    assert bool(torch.isnan(got[:481, 0]).all()) and not bool(torch.isnan(got[481:, 0]).any())
+    assert bool(torch.isnan(got[:495, 1]).all()) and not bool(torch.isnan(got[495:, 1]).any())
+
+
 def test_weights_short_sums_record_bounds(kvp):
     q, k, _ = qkv(47, 300, 2, 1, 64)
     lse = ref.attention(q, k, k, [(0, 300)])[1].float()
