@@ -17,35 +17,40 @@ namespace {
 //
 // Bound: an exponential and 2 D flops for each (query, key) pair. 128 x 128 pairs
 // take the special-function units 512 cycles and, at D = 128, the tensor cores as
-// many. So S has two buffers for each tile (all 512 columns of tensor memory),
-// and all eight softmax warps work at once, two on each scheduler.
+// many. So S of both tiles has two buffers (all 512 columns of tensor memory),
+// and four warps on each scheduler hide each other's latencies: of a tile's keys
+// each thread sums half the queries, 32 at a time, in a loop short enough to stay
+// in the instruction cache. (Eight warps with 128 logits in registers each: twice
+// as long.)
 //
-// Warps 0-3 and 4-7 sum for A and B, warp 8 issues the products, warp 9 copies,
-// warp 10 brings the normalisers (-inf for columns that do not count: their
-// weight is 0), warp 11 works out items one ahead.
+// Warps 0-7 and 8-15 sum for A and B, warp 16 issues the products, warp 17
+// copies, warp 18 brings the normalisers (-inf for columns that do not count:
+// their weight is 0), warp 19 works out items one ahead.
 template <int D, int QB>
 struct WeightsCfg {
   static constexpr int kHeads = kTile / QB;              // query heads of a tile
   static constexpr int kBoxes = D / 64;
   static constexpr int kBoxBytes = kTile * 128;          // 128 rows x 64 columns
   static constexpr int kTileBytes = kBoxes * kBoxBytes;
-  static constexpr int kStages = D == 128 ? 3 : 6;       // ring of query tiles and their normalisers
-  static constexpr int kKOff = 0;                        // keys of A and B, of this item and the next
-  static constexpr int kRingOff = 4 * kTileBytes;
-  static constexpr int kLseOff = kRingOff + kStages * kTileBytes;
-  static constexpr int kBarOff = kLseOff + kStages * kTile * 4;
-  static constexpr int kBars = 2 * kStages + 4 + 8 + 1 + 4;
+  // A window is one query tile or two an item: there the next item's keys come while this one's are used. Else the
+  // room goes to query tiles.
+  static constexpr int kKeyBufs = QB < kTile ? 2 : 1;
+  static constexpr int kStages = (D == 128 ? 6 : 12) - 2 * kKeyBufs;  // ring of query tiles
+  static constexpr int kKOff = 0;                        // keys of A and B
+  static constexpr int kRingOff = 2 * kKeyBufs * kTileBytes;
+  static constexpr int kLseOff = kRingOff + kStages * kTileBytes;  // normalisers of each buffer of S
+  static constexpr int kXchOff = kLseOff + 2 * kTile * 4;          // a sum for each key
+  static constexpr int kBarOff = kXchOff + 2 * kTile * 4;
+  static constexpr int kBars = 2 * kStages + 2 * kKeyBufs + 6 + 1 + 4;
   static constexpr int kInfoOff = (kBarOff + kBars * 8 + 15) / 16 * 16;  // [slot]{sequence, first row, length, head}, {pair}
   static constexpr int kFlagOff = kInfoOff + 2 * 32;                     // tensor memory's address, abort
   static constexpr int kSmem = 1024 + kFlagOff + 8;
   static_assert(kSmem <= 232448, "shared memory budget");
   static_assert(kRingOff % 1024 == 0 && kLseOff % 16 == 0 && kBarOff % 8 == 0 && kInfoOff % 16 == 0, "alignment");
 };
-constexpr int kSumWarps = 8, kMmaWarp = 8, kCopyWarp = 9, kLseWarp = 10, kPlanWarp = 11;
-constexpr int kWeightsThreads = 384;
+constexpr int kSumWarps = 16, kMmaWarp = 16, kCopyWarp = 17, kLseWarp = 18, kPlanWarp = 19;
+constexpr int kWeightsThreads = 640;
 constexpr int kUsers = kSumWarps + 3;  // warps that read a work item
-// A key's 128 logits stay in registers: 256 x 216 + 128 x 72 = 384 x 168.
-constexpr int kRegsSum = 216, kRegsRest = 72;
 constexpr int kWindowRows = 32;        // rows of a query tile where at most twice as many count: heads share a tile
 
 struct WeightsMaps {
@@ -62,11 +67,12 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) prompt_weights_kernel(cons
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // the same in every lane, as the compiler can see
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
   uint64_t* empty = full + C::kStages;
-  uint64_t* k_full = empty + C::kStages;   // [item's parity]
-  uint64_t* k_empty = k_full + 2;
-  uint64_t* s_full = k_empty + 2;          // [A, B][buffer]
-  uint64_t* s_empty = s_full + 4;
-  uint64_t* fin = s_empty + 4;
+  uint64_t* k_full = empty + C::kStages;       // [item % kKeyBufs]
+  uint64_t* k_empty = k_full + C::kKeyBufs;
+  uint64_t* s_full = k_empty + C::kKeyBufs;    // [buffer]: S of A and B
+  uint64_t* s_empty = s_full + 2;              // ... and its normalisers have been used
+  uint64_t* lse_full = s_empty + 2;
+  uint64_t* fin = lse_full + 2;
   uint64_t* info_full = fin + 1;
   uint64_t* info_empty = info_full + 2;
   int4* info = reinterpret_cast<int4*>(smem + C::kInfoOff);
@@ -75,18 +81,19 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) prompt_weights_kernel(cons
 
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(&full[i], 2);               // the tile's bytes, and its normalisers
-      mbar_init(&empty[i], 1 + kSumWarps);  // its products are done, its normalisers read
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < C::kKeyBufs; ++i) {
       mbar_init(&k_full[i], 1);
       mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_empty[i], kSumWarps);
+      mbar_init(&lse_full[i], 1);
       mbar_init(&info_full[i], 1);
       mbar_init(&info_empty[i], kUsers);
-    }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(&s_full[i], 1);
-      mbar_init(&s_empty[i], 4);
     }
     mbar_init(fin, 1);
     *abort_flag = 0;
@@ -146,7 +153,6 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) prompt_weights_kernel(cons
   bool ok = true;
 
   if (warp >= kSumWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
     if (warp == kPlanWarp) {
       // ------------------------------------------------------------ work items
       const TileOrder order(p.seqs, 2 * kTile);
@@ -180,9 +186,10 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) prompt_weights_kernel(cons
       int g = 0, i = 0, nk = 0;  // query tiles, items and pairs of key tiles so far
       for (; next_item(i, t, ok); ++i) {
         if (lane == 0) {
-          const int kb = i & 1;
-          if (i >= 2) ok = wait(&k_empty[kb], ((i >> 1) - 1) & 1);
-          if (ok) {
+          auto keys = [&]() {  // once the item that has used their room before is done
+            const int kb = i % C::kKeyBufs;
+            if (i >= C::kKeyBufs) ok = wait(&k_empty[kb], (i / C::kKeyBufs - 1) & 1);
+            if (!ok) return;
             ++nk;
             const int tiles = t.k0 + kTile < t.len ? 2 : 1;
             mbar_arrive_expect_tx(&k_full[kb], tiles * C::kTileBytes);
@@ -191,7 +198,7 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) prompt_weights_kernel(cons
               for (int b = 0; b < C::kBoxes; ++b)
                 tma_load_3d(smem + C::kKOff + (2 * kb + x) * C::kTileBytes + b * C::kBoxBytes, &maps.k, 64 * b, t.h,
                             t.start + t.k0 + x * kTile, &k_full[kb]);
-          }
+          };
           for (int hg = 0; ok && hg < groups; ++hg) {
             const int heads = min(C::kHeads, p.G - hg * C::kHeads);
             for (int qi = t.i0; ok && qi < t.i1; ++qi) {
@@ -205,6 +212,7 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) prompt_weights_kernel(cons
                   tma_load_3d(smem + C::kRingOff + st * C::kTileBytes + b * C::kBoxBytes + hh * QB * 128, &maps.q, 64 * b,
                               t.h * p.G + hg * C::kHeads + hh, t.start + t.q0(qi), &full[st]);
               ++g;
+              if (hg == 0 && qi == t.i0) keys();  // the first query tile waits for nothing but its stage
             }
           }
         }
@@ -216,11 +224,13 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) prompt_weights_kernel(cons
       }
       if (lane == 0) {
         if (ok) {  // no arrival is left on its way when the CTA ends
-          for (int k = max(0, nk - 2); ok && k < nk; ++k) ok = wait(&k_empty[k & 1], (k >> 1) & 1);
+          for (int k = max(0, nk - C::kKeyBufs); ok && k < nk; ++k)
+            ok = wait(&k_empty[k % C::kKeyBufs], (k / C::kKeyBufs) & 1);
           for (int k = max(0, g - C::kStages); ok && k < g; ++k) ok = wait(&empty[k % C::kStages], (k / C::kStages) & 1);
         }
         if (!ok) {  // what was issued lands before the shared memory can go to another CTA (each wait bounded again)
-          for (int k = max(0, nk - 2); k < nk; ++k) (void)mbar_wait(&k_full[k & 1], (k >> 1) & 1);
+          for (int k = max(0, nk - C::kKeyBufs); k < nk; ++k)
+            (void)mbar_wait(&k_full[k % C::kKeyBufs], (k / C::kKeyBufs) & 1);
           for (int k = max(0, g - C::kStages); k < g; ++k) (void)mbar_wait(&full[k % C::kStages], (k / C::kStages) & 1);
         }
       }
@@ -241,14 +251,14 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) prompt_weights_kernel(cons
                 if (lse != -INFINITY) v[k] = -lse * kLog2e;  // a row without keys pays nothing
               }
             }
-            const int st = g % C::kStages;
-            if (g >= C::kStages) ok = wait_all(&empty[st], (g / C::kStages - 1) & 1);
+            const int buf = g & 1;
+            if (g >= 2) ok = wait_all(&s_empty[buf], ((g >> 1) - 1) & 1);
             if (!ok) break;
-            float* to = reinterpret_cast<float*>(smem + C::kLseOff) + st * kTile;
+            float* to = reinterpret_cast<float*>(smem + C::kLseOff) + buf * kTile;
 #pragma unroll
             for (int k = 0; k < 4; ++k) to[lane + 32 * k] = v[k];
             __syncwarp();
-            if (lane == 0) mbar_arrive(&full[st]);
+            if (lane == 0) mbar_arrive(&lse_full[buf]);
           }
         }
       }
@@ -259,32 +269,31 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) prompt_weights_kernel(cons
       const uint32_t keys = smem_u32(smem + C::kKOff), ring = smem_u32(smem + C::kRingOff);
       int st = 0;                 // ring stage and its phase
       uint32_t ph = 0;
-      uint32_t n_s[2] = {0, 0};   // products of A and B so far: buffer n & 1, its phase n >> 1
+      uint32_t n = 0;             // query tiles so far: buffer n & 1, its phase n >> 1
       int i = 0;
       for (; next_item(i, t, ok); ++i) {
-        const int kb = i & 1;
-        ok = wait_all(&k_full[kb], (i >> 1) & 1);
+        const int kb = i % C::kKeyBufs;
+        ok = wait_all(&k_full[kb], (i / C::kKeyBufs) & 1);
         for (int hg = 0; ok && hg < groups; ++hg) {
           const uint32_t idS = idesc_bf16_f32(kTile, QB * min(C::kHeads, p.G - hg * C::kHeads));
-          for (int qi = t.i0; ok && qi < t.i1; ++qi) {
-            ok = wait_all(&full[st], ph);
+          for (int qi = t.i0; ok && qi < t.i1; ++qi, ++n) {
+            const uint32_t buf = n & 1;
+            // (the normalisers come once the buffer's last logits have been used)
+            ok = wait_all(&full[st], ph) && wait_all(&lse_full[buf], (n >> 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
             const uint64_t b0 = sw128_kmajor_desc(ring + st * C::kTileBytes);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              if (!ok || !t.sees(x, qi)) continue;
-              const uint32_t n = n_s[x]++, buf = n & 1;
-              if (n >= 2) ok = wait_all(&s_empty[2 * x + buf], ((n >> 1) - 1) & 1);
-              if (!ok) continue;
-              tc_fence_after();
+              if (!t.sees(x, qi)) continue;
               const uint64_t a0 = sw128_kmajor_desc(keys + (2 * kb + x) * C::kTileBytes);
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk) {
                 const uint64_t off = static_cast<uint64_t>(((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4);
                 mma_ss(leader, tmem + (2 * x + buf) * kTile, a0 + off, b0 + off, idS, kk > 0);
               }
-              commit_to(leader, &s_full[2 * x + buf]);
             }
-            if (!ok) break;
+            commit_to(leader, &s_full[buf]);
             commit_to(leader, &empty[st]);
             if (++st == C::kStages) {
               st = 0;
@@ -300,60 +309,63 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) prompt_weights_kernel(cons
       (void)mbar_wait(fin, 0);  // every product has completed before tensor and shared memory go
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSum));
     // ------------------------------------------------------------ sums
-    const int x = warp >> 2, row = (warp & 3) * 32 + lane;
-    const uint32_t scol = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 2 * x * kTile;
+    // tile x, key `row`, columns 64 half .. of each query tile
+    const int x = warp >> 3, half = (warp >> 2) & 1, quad = warp & 3, row = quad * 32 + lane;
+    const uint32_t scol = tmem + (static_cast<uint32_t>(quad * 32) << 16) + 2 * x * kTile + half * 64;
+    const float* lse = reinterpret_cast<const float*>(smem + C::kLseOff) + half * 64;
+    float* xch = reinterpret_cast<float*>(smem + C::kXchOff) + x * kTile + row;
     const uint64_t c2 = pack2(p.qscale, p.qscale);
-    int st = 0;
-    uint32_t ph = 0, n = 0;
-    for (int i = 0; next_item(i, t, ok); ++i) {
-      const int pos = t.k0 + x * kTile + row;  // the key's position; past the sequence's end: nothing is stored
-      float total = 0.f, lost = 0.f;           // the sum of the tiles' sums and what its additions rounded off
+    const int pair = 1 + x * 4 + quad;  // named barrier of the two warps of a key, which leave together
+    uint32_t n = 0;
+    for (int i = 0;; ++i) {
+      const bool more = next_item(i, t, ok);
+      if (named_bar_or(pair, 64, !ok)) {
+        ok = false;
+        break;
+      }
+      if (!more) break;
+      const int k0 = t.k0 + x * kTile, pos = k0 + row;  // the key's position; past the sequence's end: nothing is stored
+      float total = 0.f, lost = 0.f;                    // the sum of the tiles' sums and what its additions rounded off
       for (int hg = 0; ok && hg < groups; ++hg) {
-        const int cols = QB * min(C::kHeads, p.G - hg * C::kHeads);
-        for (int qi = t.i0; ok && qi < t.i1; ++qi) {
-          // also of a tile that this one does not see: a stage is given back in its turn
-          ok = wait_all(&full[st], ph);
+        const int cols = QB * min(C::kHeads, p.G - hg * C::kHeads) - half * 64;
+        for (int qi = t.i0; qi < t.i1; ++qi, ++n) {
+          const uint32_t buf = n & 1;
+          ok = wait_all(&s_full[buf], (n >> 1) & 1);
           if (!ok) break;
           if (t.sees(x, qi)) {
-            const uint32_t buf = n & 1;
-            ok = wait_all(&s_full[2 * x + buf], (n >> 1) & 1);
-            if (!ok) break;
-            ++n;
             tc_fence_after();
-            float s[kTile];
-            tmem_ld128(scol + buf * kTile, s);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s_empty[2 * x + buf]);
-            const float* lse = reinterpret_cast<const float*>(smem + C::kLseOff) + st * kTile;
             const int q0 = t.q0(qi);
             uint64_t sum[4] = {0, 0, 0, 0};
             // `cut`: a tile with columns that this key does not see, or that are no query. They count for nothing, whatever
             // their logits and normalisers are.
             auto add_up = [&](auto cut) {
-              const int from = pos - q0, to = t.len - q0;
+#pragma unroll 1
+              for (int o = 0; o < 64; o += 32) {
+                if (o >= cols) break;
+                float s[32];
+                tmem_ld32(scol + buf * kTile + o, s);
+                const float4* to_add = reinterpret_cast<const float4*>(lse + buf * kTile + o);
+                // columns o + k with from <= k < to are queries that see the key
+                const int first = QB == kTile ? half * 64 + o : 0;
+                const int from = pos - q0 - first, to = t.len - q0 - first;
 #pragma unroll
-              for (int part = 0; part < kTile; part += QB) {
-                if (part >= cols) continue;
-#pragma unroll
-                for (int k = part; k < part + QB; k += 4) {
-                  const float4 r = *reinterpret_cast<const float4*>(lse + k);
+                for (int k = 0; k < 32; k += 4) {
+                  const float4 r = to_add[k / 4];
                   float e[4];
                   unpack2(fma2(pack2(s[k], s[k + 1]), c2, pack2(r.x, r.y)), e[0], e[1]);
                   unpack2(fma2(pack2(s[k + 2], s[k + 3]), c2, pack2(r.z, r.w)), e[2], e[3]);
                   if constexpr (decltype(cut)::value) {
 #pragma unroll
-                    for (int o = 0; o < 4; ++o)
-                      if ((k + o) % QB < from || (k + o) % QB >= to) e[o] = -INFINITY;
+                    for (int j = 0; j < 4; ++j)
+                      if (k + j < from || k + j >= to) e[j] = -INFINITY;
                   }
-                  sum[(k / 2) & 3] = add2(sum[(k / 2) & 3], pack2(ex2_approx(e[0]), ex2_approx(e[1])));
+                  sum[k / 2 & 3] = add2(sum[k / 2 & 3], pack2(ex2_approx(e[0]), ex2_approx(e[1])));
                   sum[(k / 2 + 1) & 3] = add2(sum[(k / 2 + 1) & 3], pack2(ex2_approx(e[2]), ex2_approx(e[3])));
                 }
               }
             };
-            if (q0 < t.k0 + x * kTile + kTile - 1 || q0 + QB > t.len) {
+            if (q0 < k0 + kTile - 1 || q0 + QB > t.len) {
               add_up(std::true_type{});
             } else {
               add_up(std::false_type{});
@@ -365,18 +377,21 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) prompt_weights_kernel(cons
             const float both = total + a, back = both - total;
             lost += (total - (both - back)) + (a - back);
             total = both;
+            tc_fence_before();
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&empty[st]);
-          if (++st == C::kStages) {
-            st = 0;
-            ph ^= 1;
-          }
+          if (lane == 0) mbar_arrive(&s_empty[buf]);
         }
       }
-      if (!ok) break;
-      if (pos < t.len) {
-        const float sum = total + (fabsf(lost) < INFINITY ? lost : 0.f);
+      // the two halves of the key's sum meet (the next item's after both have come past its barrier)
+      float sum = total + (fabsf(lost) < INFINITY ? lost : 0.f);
+      if (half == 1) *xch = sum;
+      if (named_bar_or(pair, 64, !ok)) {
+        ok = false;
+        break;
+      }
+      if (half == 0) sum += *xch;
+      if (half == 0 && pos < t.len) {
         if (p.as < 0) {
           p.acc[(t.start + pos) * p.at + t.h * p.ah] = sum;
         } else if (pos < p.acc_len) {
