@@ -26,6 +26,11 @@ namespace {
 // Warps 0-7 and 8-15 sum for A and B, warp 16 issues the products, warp 17
 // copies, warp 18 brings the normalisers (-inf for columns that do not count:
 // their weight is 0), warp 19 works out items one ahead.
+// Work items ahead: the warp that brings the normalisers reads kAhead tiles on, which may be as many items, before it
+// writes the first of them, and no item's place is taken again before every warp has read it.
+constexpr int kItems = 8, kAhead = 4;
+static_assert(kItems > kAhead, "a warp would wait for one that waits for it");
+
 template <int D, int QB>
 struct WeightsCfg {
   static constexpr int kHeads = kTile / QB;              // query heads of a tile
@@ -41,9 +46,9 @@ struct WeightsCfg {
   static constexpr int kLseOff = kRingOff + kStages * kTileBytes;  // normalisers of each buffer of S
   static constexpr int kXchOff = kLseOff + 2 * kTile * 4;          // a sum for each key
   static constexpr int kBarOff = kXchOff + 2 * kTile * 4;
-  static constexpr int kBars = 2 * kStages + 2 * kKeyBufs + 6 + 1 + 4;
+  static constexpr int kBars = 2 * kStages + 2 * kKeyBufs + 6 + 1 + 2 * kItems;
   static constexpr int kInfoOff = (kBarOff + kBars * 8 + 15) / 16 * 16;  // [slot]{sequence, first row, length, head}, {pair}
-  static constexpr int kFlagOff = kInfoOff + 2 * 32;                     // tensor memory's address, abort
+  static constexpr int kFlagOff = kInfoOff + kItems * 32;                // tensor memory's address, abort
   static constexpr int kSmem = 1024 + kFlagOff + 8;
   static_assert(kSmem <= 232448, "shared memory budget");
   static_assert(kRingOff % 1024 == 0 && kLseOff % 16 == 0 && kBarOff % 8 == 0 && kInfoOff % 16 == 0, "alignment");
@@ -74,7 +79,7 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) prompt_weights_kernel(cons
   uint64_t* lse_full = s_empty + 2;
   uint64_t* fin = lse_full + 2;
   uint64_t* info_full = fin + 1;
-  uint64_t* info_empty = info_full + 2;
+  uint64_t* info_empty = info_full + kItems;
   int4* info = reinterpret_cast<int4*>(smem + C::kInfoOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kFlagOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -92,6 +97,8 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) prompt_weights_kernel(cons
       mbar_init(&s_full[i], 1);
       mbar_init(&s_empty[i], kSumWarps);
       mbar_init(&lse_full[i], 1);
+    }
+    for (int i = 0; i < kItems; ++i) {
       mbar_init(&info_full[i], 1);
       mbar_init(&info_empty[i], kUsers);
     }
@@ -131,8 +138,8 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) prompt_weights_kernel(cons
   };
   const int groups = (p.G + C::kHeads - 1) / C::kHeads;
   auto next_item = [&](int i, Item& t, bool& ok) {
-    const int slot = i & 1;
-    ok = wait_all(&info_full[slot], (i >> 1) & 1);
+    const int slot = i % kItems;
+    ok = wait_all(&info_full[slot], (i / kItems) & 1);
     if (!ok) return false;
     const int4 v = info[2 * slot];
     const int pair = info[2 * slot + 1].x;
@@ -167,8 +174,8 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) prompt_weights_kernel(cons
           v = make_int4(f.seq, f.start, f.len, static_cast<int>(at % H));
           pair = (f.len + 2 * kTile - 1) / (2 * kTile) - 1 - f.r;
         }
-        const int slot = i & 1;
-        if (i >= 2) ok = wait_all(&info_empty[slot], ((i >> 1) - 1) & 1);
+        const int slot = i % kItems;
+        if (i >= kItems) ok = wait_all(&info_empty[slot], (i / kItems - 1) & 1);
         if (!ok) {
           gave_up();
           break;
@@ -237,29 +244,55 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) prompt_weights_kernel(cons
       __syncwarp();
     } else if (warp == kLseWarp) {
       // ------------------------------------------------------------ normalisers
-      int g = 0;
-      for (int i = 0; ok && next_item(i, t, ok); ++i) {
-        for (int hg = 0; ok && hg < groups; ++hg) {
-          for (int qi = t.i0; ok && qi < t.i1; ++qi, ++g) {
-            float v[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int col = lane + 32 * k, hh = hg * C::kHeads + col / QB, q = t.q0(qi) + col % QB;
-              v[k] = -INFINITY;
-              if (hh < p.G && q < t.len) {
-                const float lse = p.lse_in[(t.h * p.G + hh) * p.seqs.n_tok + t.start + q];
-                if (lse != -INFINITY) v[k] = -lse * kLog2e;  // a row without keys pays nothing
-              }
-            }
-            const int buf = g & 1;
-            if (g >= 2) ok = wait_all(&s_empty[buf], ((g >> 1) - 1) & 1);
-            if (!ok) break;
-            float* to = reinterpret_cast<float*>(smem + C::kLseOff) + buf * kTile;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) to[lane + 32 * k] = v[k];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&lse_full[buf]);
+      // Loads are issued kAhead tiles before their values are written (one takes as long as a tile's exponentials).
+      int i = 0, hg = groups, qi = 0, g = 0;
+      t.i1 = 0;
+      // lane's columns of the next tile, -inf for those that do not count; false: there is none
+      auto load = [&](float (&v)[4]) {
+        if (qi + 1 < t.i1 && hg < groups) {
+          ++qi;
+        } else {
+          if (++hg >= groups) {
+            if (!next_item(i++, t, ok)) return false;
+            hg = 0;
           }
+          qi = t.i0;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int col = lane + 32 * k, hh = hg * C::kHeads + col / QB, q = t.q0(qi) + col % QB;
+          v[k] = -INFINITY;
+          if (hh < p.G && q < t.len) v[k] = p.lse_in[(t.h * p.G + hh) * p.seqs.n_tok + t.start + q];
+        }
+        return true;
+      };
+      auto write = [&](const float (&v)[4]) {
+        const int buf = g & 1;
+        if (g >= 2) ok = wait_all(&s_empty[buf], ((g >> 1) - 1) & 1);
+        if (!ok) return;
+        float* to = reinterpret_cast<float*>(smem + C::kLseOff) + buf * kTile;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) to[lane + 32 * k] = v[k] == -INFINITY ? v[k] : -v[k] * kLog2e;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&lse_full[buf]);
+        ++g;
+      };
+      float v[kAhead][4];
+      int left = 0;  // tiles loaded and not written
+      bool more = true;
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        more = more && load(v[k]);
+        left += more;
+      }
+      while (ok && left > 0) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          if (!ok || left == 0) break;
+          write(v[k]);
+          --left;
+          more = more && ok && load(v[k]);
+          left += more;
         }
       }
       if (!ok) gave_up();
