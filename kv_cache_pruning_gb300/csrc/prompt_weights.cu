@@ -46,7 +46,7 @@ struct WeightsCfg {
   static constexpr int kLseOff = kRingOff + kStages * kTileBytes;  // normalisers of each buffer of S
   static constexpr int kXchOff = kLseOff + 2 * kTile * 4;          // a sum for each key
   static constexpr int kBarOff = kXchOff + 2 * kTile * 4;
-  static constexpr int kBars = 2 * kStages + 2 * kKeyBufs + 6 + 1 + 2 * kItems;
+  static constexpr int kBars = 2 * kStages + 2 * kKeyBufs + 8 + 1 + 2 * kItems;
   static constexpr int kInfoOff = (kBarOff + kBars * 8 + 15) / 16 * 16;  // [slot]{sequence, first row, length, head}, {pair}
   static constexpr int kFlagOff = kInfoOff + kItems * 32;                // tensor memory's address, abort
   static constexpr int kSmem = 1024 + kFlagOff + 8;
@@ -74,8 +74,8 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) prompt_weights_kernel(cons
   uint64_t* empty = full + C::kStages;
   uint64_t* k_full = empty + C::kStages;       // [item % kKeyBufs]
   uint64_t* k_empty = k_full + C::kKeyBufs;
-  uint64_t* s_full = k_empty + C::kKeyBufs;    // [buffer]: S of A and B
-  uint64_t* s_empty = s_full + 2;              // ... and its normalisers have been used
+  uint64_t* s_full = k_empty + C::kKeyBufs;    // [A, B][buffer]
+  uint64_t* s_empty = s_full + 4;              // [buffer]: S of A and B and the normalisers have been used
   uint64_t* lse_full = s_empty + 2;
   uint64_t* fin = lse_full + 2;
   uint64_t* info_full = fin + 1;
@@ -93,8 +93,8 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) prompt_weights_kernel(cons
       mbar_init(&k_full[i], 1);
       mbar_init(&k_empty[i], 1);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(&s_full[i], 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&s_full[i], 1);
       mbar_init(&s_empty[i], kSumWarps);
       mbar_init(&lse_full[i], 1);
     }
@@ -318,15 +318,16 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) prompt_weights_kernel(cons
             const uint64_t b0 = sw128_kmajor_desc(ring + st * C::kTileBytes);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              if (!t.sees(x, qi)) continue;
-              const uint64_t a0 = sw128_kmajor_desc(keys + (2 * kb + x) * C::kTileBytes);
+              if (t.sees(x, qi)) {
+                const uint64_t a0 = sw128_kmajor_desc(keys + (2 * kb + x) * C::kTileBytes);
 #pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
-                const uint64_t off = static_cast<uint64_t>(((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4);
-                mma_ss(leader, tmem + (2 * x + buf) * kTile, a0 + off, b0 + off, idS, kk > 0);
+                for (int kk = 0; kk < D / 16; ++kk) {
+                  const uint64_t off = static_cast<uint64_t>(((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4);
+                  mma_ss(leader, tmem + (2 * x + buf) * kTile, a0 + off, b0 + off, idS, kk > 0);
+                }
               }
+              commit_to(leader, &s_full[2 * x + buf]);
             }
-            commit_to(leader, &s_full[buf]);
             commit_to(leader, &empty[st]);
             if (++st == C::kStages) {
               st = 0;
@@ -364,7 +365,7 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) prompt_weights_kernel(cons
         const int cols = QB * min(C::kHeads, p.G - hg * C::kHeads) - half * 64;
         for (int qi = t.i0; qi < t.i1; ++qi, ++n) {
           const uint32_t buf = n & 1;
-          ok = wait_all(&s_full[buf], (n >> 1) & 1);
+          ok = wait_all(&s_full[2 * x + buf], (n >> 1) & 1);
           if (!ok) break;
           if (t.sees(x, qi)) {
             tc_fence_after();
