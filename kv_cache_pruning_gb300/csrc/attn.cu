@@ -936,7 +936,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const AttnPara
 // hi + lo pair (two products, about 16 bits of p), to become the second
 // product's B operand. A thread owns heads 2t and 2t+1 of both
 // results, so its softmax state and its output columns coincide.
-template <int D>
+template <int D, bool kA = false>
 struct MmaCfg {
   static constexpr int NBOX = D / 64;                    // 64-column boxes per page of K (or V)
   static constexpr int BOX_BYTES = kPage * 128;          // 16 rows x 128 bytes
@@ -948,7 +948,8 @@ struct MmaCfg {
   // per warp: P^T hi and lo, 8 heads x 16 tokens, bf16; a head's row padded to kPtRow halves so that the
   // stores (lanes 4 apart in heads) and the 32-bit reads (8 heads x 4 token pairs) fall on distinct banks
   static constexpr int kPtRow = 24;
-  static constexpr int PT_BYTES = kWarps * 2 * 8 * kPtRow * 2;
+  static constexpr int kPlanes = kA ? 3 : 2;  // the accumulating kernel keeps 24 bits of p: hi, lo and the rest
+  static constexpr int PT_BYTES = kWarps * kPlanes * 8 * kPtRow * 2;
   static constexpr int BAR_BYTES = kWarps * (kNst + 1) * 8;
   static constexpr int PREF_BYTES = (kMaxBH + 1) * 4;
   static constexpr int SMEM = 1024 + RING_BYTES + REC_BYTES + PT_BYTES + BAR_BYTES + PREF_BYTES;
@@ -991,7 +992,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_mma_kernel(const AttnParams 
                                                                const __grid_constant__ CUtensorMap tmV,
                                                                const __grid_constant__ CUtensorMap tmKq,
                                                                const __grid_constant__ CUtensorMap tmVq) {
-  using C = MmaCfg<D>;
+  using C = MmaCfg<D, kA>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   pdl_launch_dependents();
@@ -1001,7 +1002,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_mma_kernel(const AttnParams 
   const int BH = p.B * p.H;
   uint8_t* ring = smem + warp * kNst * C::STAGE_BYTES;
   int32_t* exp_s = reinterpret_cast<int32_t*>(smem + C::RING_BYTES) + warp * kNst * C::REC_WORDS;
-  uint16_t* pt_s = reinterpret_cast<uint16_t*>(smem + C::RING_BYTES + C::REC_BYTES) + warp * 2 * 8 * C::kPtRow;
+  uint16_t* pt_s = reinterpret_cast<uint16_t*>(smem + C::RING_BYTES + C::REC_BYTES) + warp * C::kPlanes * 8 * C::kPtRow;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::RING_BYTES + C::REC_BYTES + C::PT_BYTES) + warp * (kNst + 1);
   int* pref = reinterpret_cast<int*>(smem + C::RING_BYTES + C::REC_BYTES + C::PT_BYTES + C::BAR_BYTES);
   if (tid == 0) {
@@ -1461,6 +1462,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_mma_kernel(const AttnParams 
         const __nv_bfloat16 lo = __float2bfloat16_rn(pf[i] - __bfloat162float(hi));
         pt_s[(2 * tq + (i & 1)) * C::kPtRow + tok[i]] = __bfloat16_as_ushort(hi);
         pt_s[8 * C::kPtRow + (2 * tq + (i & 1)) * C::kPtRow + tok[i]] = __bfloat16_as_ushort(lo);
+        if constexpr (kA) {
+          const float rest = pf[i] - __bfloat162float(hi) - __bfloat162float(lo);
+          pt_s[16 * C::kPtRow + (2 * tq + (i & 1)) * C::kPtRow + tok[i]] = __bfloat16_as_ushort(__float2bfloat16_rn(rest));
+        }
       }
     }
     __syncwarp();
@@ -1470,6 +1475,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_mma_kernel(const AttnParams 
     if (!isq) {
       pl0 = *reinterpret_cast<const uint32_t*>(pt_s + 8 * C::kPtRow + gq * C::kPtRow + 2 * tq);
       pl1 = *reinterpret_cast<const uint32_t*>(pt_s + 8 * C::kPtRow + gq * C::kPtRow + 8 + 2 * tq);
+    }
+    uint32_t pr0 = 0u, pr1 = 0u;
+    if constexpr (kA) {
+      pr0 = *reinterpret_cast<const uint32_t*>(pt_s + 16 * C::kPtRow + gq * C::kPtRow + 2 * tq);
+      pr1 = *reinterpret_cast<const uint32_t*>(pt_s + 16 * C::kPtRow + gq * C::kPtRow + 8 + 2 * tq);
     }
 
     // ---- O^T += V^T P^T
@@ -1501,6 +1511,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_mma_kernel(const AttnParams 
         }
         mma_bf16_16816(o[mt], a[0], a[1], a[2], a[3], pb0, pb1);
         mma_bf16_16816(o[mt], a[0], a[1], a[2], a[3], pl0, pl1);
+        if constexpr (kA) mma_bf16_16816(o[mt], a[0], a[1], a[2], a[3], pr0, pr1);
       }
     }
     if constexpr (!kEarly) issue_next();
@@ -1637,7 +1648,7 @@ kvp_status launch_attn(const AttnParams& p, int grid_limit, cudaStream_t st) {
 template <int D, int G, bool kQ, bool kA>
 int attn_mma_grid() {
   static const int grid = [] {
-    using C = MmaCfg<D>;
+    using C = MmaCfg<D, kA>;
     auto kern = attn_mma_kernel<D, G, kQ, kA>;
     int dev = 0, nsm = 0, occ = 0;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess ||
@@ -1653,7 +1664,7 @@ int attn_mma_grid() {
 template <int D, int G, bool kQ, bool kA>
 kvp_status launch_attn_mma(const AttnParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV,
                            const CUtensorMap& tmKq, const CUtensorMap& tmVq, int grid_limit, cudaStream_t st) {
-  using C = MmaCfg<D>;
+  using C = MmaCfg<D, kA>;
   int grid = attn_mma_grid<D, G, kQ, kA>();
   if (grid <= 0) return KVP_ERR_CUDA;
   if (grid_limit > 0 && grid > grid_limit) grid = grid_limit;
@@ -1719,44 +1730,71 @@ struct AccArgs {
 // acc[b, h, position of slot i] += sum over the kv head's G query heads of
 // 2^(x_i - m) / l, from the logits x and each row's (m, l) that the attention
 // kernel left: the softmax weights themselves, once the whole row is known.
-// One thread a slot, so that a sum takes its one addition a call in a fixed
-// order, without atomics. A slot that was not present has x = -inf and is left
+// A thread owns its slots, so that a sum takes its one addition a call in a
+// fixed order, without atomics. A slot that was not present has x = -inf and is left
 // alone. Reads 4 G + 4 bytes of logits and position and reads and writes 4 of
 // the sum, where the attention before it reads 4 D + 4: at D = 128 and G = 4
 // 5 % more bytes, most of them out of L2.
-constexpr int kAccThreads = 256;
+constexpr int kAccThreads = 256, kAccSlots = 4;  // slots a thread, their loads in flight at once
 template <int G>
 __global__ void __launch_bounds__(kAccThreads) acc_kernel(const AttnParams p, const AccArgs a) {
   pdl_wait();
   const int bh = blockIdx.y;
-  const int slot = blockIdx.x * kAccThreads + threadIdx.x;
-  if (slot >= clamp_count(p.count, bh, p.max_pages)) return;
-  const size_t at = static_cast<size_t>(bh) * p.max_pages * kPage + slot;
-  float x[G];
-#pragma unroll
-  for (int i = 0; i < G; ++i) x[i] = __ldcg(p.logits + at * G + i);
-  float w = 0.f;
-  bool present = false;
+  const int first = blockIdx.x * (kAccThreads * kAccSlots) + threadIdx.x;
+  const int n = clamp_count(p.count, bh, p.max_pages);
+  if (first - static_cast<int>(threadIdx.x) >= n) return;
+  float m[G], inv[G];
 #pragma unroll
   for (int i = 0; i < G; ++i) {
     const float2 ml = __ldcg(p.row_ml + static_cast<size_t>(bh) * G + i);
-    present |= !(x[i] == -INFINITY);
-    if (ml.y != 0.f) w += exp2f(x[i] - ml.x) / ml.y;  // 0: a row without a finite logit pays nothing
+    m[i] = ml.x;
+    inv[i] = ml.y != 0.f ? 1.f / ml.y : 0.f;  // 0: a row without a finite logit pays nothing
   }
-  if (!present) return;
-  const int pos = a.remap[at];
-  if (pos < 0 || pos >= a.acc_len) {
-    record_error(p.status, KVP_ERR_BOUNDS);
-    return;
+  const size_t base = static_cast<size_t>(bh) * p.max_pages * kPage;
+  float* sums = a.acc + (bh / p.H) * a.stride_b + (bh % p.H) * a.stride_h;
+  float x[kAccSlots][G], old[kAccSlots];
+  int pos[kAccSlots];
+#pragma unroll
+  for (int k = 0; k < kAccSlots; ++k) {
+    const int slot = first + k * kAccThreads;
+    pos[k] = slot < n ? a.remap[base + slot] : -1;
+    const float* at = p.logits + (base + slot) * G;
+    if constexpr (G % 4 == 0) {
+#pragma unroll
+      for (int i = 0; i < G; i += 4) {
+        const float4 v = slot < n ? __ldcg(reinterpret_cast<const float4*>(at + i)) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        x[k][i] = v.x, x[k][i + 1] = v.y, x[k][i + 2] = v.z, x[k][i + 3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < G; ++i) x[k][i] = slot < n ? __ldcg(at + i) : -INFINITY;
+    }
   }
-  float* sum = a.acc + (bh / p.H) * a.stride_b + (bh % p.H) * a.stride_h + pos;
-  *sum += w;
+#pragma unroll
+  for (int k = 0; k < kAccSlots; ++k) old[k] = pos[k] >= 0 && pos[k] < a.acc_len ? sums[pos[k]] : 0.f;
+#pragma unroll
+  for (int k = 0; k < kAccSlots; ++k) {
+    float w = 0.f;
+    bool present = false;
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      present |= !(x[k][i] == -INFINITY);
+      if (inv[i] != 0.f) w = fmaf(exp2f(x[k][i] - m[i]), inv[i], w);
+    }
+    if (!present) continue;
+    if (pos[k] < 0 || pos[k] >= a.acc_len) {
+      record_error(p.status, KVP_ERR_BOUNDS);
+    } else {
+      sums[pos[k]] = old[k] + w;
+    }
+  }
 }
 
 kvp_status launch_acc(const AttnParams& p, int G, const AccArgs& a, cudaStream_t st) {
   const int64_t slots = static_cast<int64_t>(p.max_pages) * kPage;
   if (slots == 0) return KVP_OK;
-  const dim3 grid(static_cast<unsigned>((slots + kAccThreads - 1) / kAccThreads), static_cast<unsigned>(p.B * p.H));
+  constexpr int kCta = kAccThreads * kAccSlots;
+  const dim3 grid(static_cast<unsigned>((slots + kCta - 1) / kCta), static_cast<unsigned>(p.B * p.H));
   auto go = [&](auto kern) {
     return launch_pdl(kern, grid, dim3(kAccThreads), 0, st, p, a) == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
   };

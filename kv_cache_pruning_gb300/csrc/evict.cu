@@ -1,11 +1,17 @@
 // kvp_evict, kvp_evict_paged: which entries stay within a budget, by the
 // attention weight that they have received.
 //
-// Of one (b, h) with n entries: the recent ones stay; of the c others the
-// m = min(c, max(0, budget - recent ones)) heaviest, the first of equal ones.
-// With order-preserving 32-bit keys (-0 = 0, NaN lowest) the m-th largest key T
-// is found by radix selection, 8 bits a pass from the top, and the entries kept
-// are those above T and the first m - #{> T} of those equal to it.
+// Of one (b, h) with n entries: the recent ones stay; of the c others (the
+// candidates) the m = min(c, max(0, budget - recent ones)) heaviest, the first of
+// equal ones. With order-preserving 32-bit keys (-0 = 0, NaN lowest) the m-th
+// largest key T is found by radix selection, 11, 11 and 10 bits from the top, and
+// the entries kept are those above T and the first m - #{> T} of those equal to it.
+//
+// A cluster of CTAs takes a (b, h), each a run of its entries, whose keys it keeps
+// in shared memory: so an entry is read once, whatever the passes. Each pass counts
+// into a histogram of each CTA, and after a cluster barrier every CTA adds them all
+// up (through distributed shared memory) and comes to the same digit. How many
+// entries equal to T the CTAs before it have is in their last histograms.
 #include "kvp_common.cuh"
 
 namespace kvp {
@@ -13,37 +19,40 @@ namespace {
 
 constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
+constexpr int kBins = 2048;                 // 11 bits
+constexpr int kKeysCap = 24576;             // keys that a CTA keeps (96 KB); those of longer runs are made anew
+constexpr uint32_t kNoKey = 0xFFFFFFFFu;    // not a candidate: above the key of any weight
 
-enum Kind { kAbsent = 0, kRecent = 1, kCandidate = 2 };
-
-// fp32 to a key whose unsigned order is the values': NaN 0, -inf 0x007fffff, zeros 0x80000000.
+// fp32 to a key whose unsigned order is the values': NaN 0, -inf 0x007fffff, zeros 0x80000000, inf 0xff800000.
 KVP_DEV uint32_t weight_key(float x) {
   if (x != x) return 0u;
   const uint32_t u = __float_as_uint(x == 0.f ? 0.f : x);
   return u ^ ((u >> 31) != 0u ? 0xFFFFFFFFu : 0x80000000u);
 }
 
+// The entries of a prompt: positions 0 .. n_pos - 1, the recent ones last.
 struct DenseEvict {
   const float* acc;
   int64_t stride_b, stride_t, stride_h;
   int H, n_pos, recent, now;
   int32_t* expire;
-  int32_t* kept;
   const float* row;
   int32_t* out;
-  KVP_DEV void open(int bh, int /*now*/) {
+  int old;  // entries that are not recent
+  KVP_DEV void open(int bh, int /*step*/) {
     row = acc + (bh / H) * stride_b + (bh % H) * stride_h;
     out = expire + static_cast<int64_t>(bh) * n_pos;
+    old = static_cast<int>(min(static_cast<int64_t>(n_pos), max(int64_t{0}, static_cast<int64_t>(now) - recent + 1)));
   }
   KVP_DEV int size() const { return n_pos; }
-  KVP_DEV Kind get(int i, uint32_t& key) const {
-    if (i > static_cast<int64_t>(now) - recent) return kRecent;
-    key = weight_key(row[i * stride_t]);
-    return kCandidate;
+  KVP_DEV uint32_t key(int i, uint32_t& is_recent) const {
+    is_recent = i >= old;
+    return i < old ? weight_key(row[i * stride_t]) : kNoKey;
   }
-  KVP_DEV void put(int i, bool stays) const { out[i] = stays ? kNever : now; }
+  KVP_DEV void put(int i, bool candidate, bool stays) const { out[i] = !candidate || stays ? kNever : now; }
 };
 
+// The present slots of a paged cache.
 struct PagedEvict {
   const float* acc;
   int64_t stride_b, stride_h;
@@ -54,8 +63,6 @@ struct PagedEvict {
   const int32_t* remap;
   const int32_t* count;
   int recent, now;
-  const int32_t* now_dev;
-  int32_t* kept;
   int32_t* status;
   const float* row;
   const int32_t* pages;
@@ -69,102 +76,218 @@ struct PagedEvict {
     n = min(max(count[bh], 0), max_pages * kPage);
   }
   KVP_DEV int size() const { return n; }
-  KVP_DEV Kind get(int i, uint32_t& key) const {
-    const int page = pages[i / kPage];
+  KVP_DEV uint32_t key(int i, uint32_t& is_recent) const {
+    is_recent = 0;
+    const int page = pages[i / kPage], at = pos[i];
     if (page < 0 || page >= n_pages_cap) {
       record_error(status, KVP_ERR_BOUNDS);
-      return kAbsent;
+      return kNoKey;
     }
-    if (expire_pool[static_cast<int64_t>(page) * kPage + i % kPage] <= now) return kAbsent;
-    const int at = pos[i];
-    if (at < 0 || at >= acc_len) {
+    // (the weight is asked for beside the expire value: most slots are present)
+    const bool inside = at >= 0 && at < acc_len;
+    const float w = inside ? row[at] : 0.f;
+    if (expire_pool[static_cast<int64_t>(page) * kPage + i % kPage] <= now) return kNoKey;
+    if (!inside) {
       record_error(status, KVP_ERR_BOUNDS);
-      return kAbsent;
+      return kNoKey;
     }
-    if (at > static_cast<int64_t>(now) - recent) return kRecent;
-    key = weight_key(row[at]);
-    return kCandidate;
+    is_recent = at > static_cast<int64_t>(now) - recent;
+    return is_recent ? kNoKey : weight_key(w);
   }
-  KVP_DEV void put(int i, bool stays) const {
-    if (!stays) expire_pool[static_cast<int64_t>(pages[i / kPage]) * kPage + i % kPage] = now;
+  KVP_DEV void put(int i, bool candidate, bool stays) const {
+    if (candidate && !stays) expire_pool[static_cast<int64_t>(pages[i / kPage]) * kPage + i % kPage] = now;
   }
 };
 
-// One CTA a (b, h), every pass over its entries from memory.
+// The word at `local`'s offset in the shared memory of CTA `rank` of the cluster.
+KVP_DEV uint32_t cluster_address(const void* local, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(local)), "r"(rank));
+  return r;
+}
+KVP_DEV uint4 load_cluster4(uint32_t address) {
+  uint4 r;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "r"(address)
+               : "memory");
+  return r;
+}
+KVP_DEV uint32_t load_cluster(uint32_t address) {
+  uint32_t r;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(r) : "r"(address) : "memory");
+  return r;
+}
+
+struct EvictShared {
+  uint32_t hist[3][kBins];        // one a pass: no CTA clears what another may still read
+  uint32_t recent;
+  uint32_t warp_sum[kEvictWarps];
+  uint32_t digit, left, equal, before;
+};
+
 template <class Src>
-__global__ void __launch_bounds__(kEvictThreads) evict_kernel(Src src, int budget, const int32_t* now_dev, int now,
-                                                             int32_t* kept, int32_t* status) {
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t warp_sum[kEvictWarps];
-  __shared__ uint32_t s_recent, s_cand, s_digit, s_left;
+__global__ void __launch_bounds__(kEvictThreads) evict_kernel(Src src, int cluster, int budget, const int32_t* now_dev,
+                                                             int now, int32_t* kept, int32_t* status) {
+  extern __shared__ uint4 evict_smem[];
+  EvictShared& sh = *reinterpret_cast<EvictShared*>(evict_smem);
+  uint32_t* keys = reinterpret_cast<uint32_t*>(evict_smem + (sizeof(EvictShared) + 15) / 16);
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int bh = blockIdx.x;
+  const int bh = blockIdx.x / cluster, rank = blockIdx.x % cluster;
   if (now_dev != nullptr) {
     now = *now_dev;
-    if (now < 0 || now == kNever) {
+    if (now < 0 || now == kNever) {  // the whole grid
       if (tid == 0) record_error(status, KVP_ERR_INVALID);
       return;
     }
   }
+  for (int i = tid; i < 3 * kBins; i += kEvictThreads) sh.hist[0][i] = 0;
+  if (tid == 0) sh.recent = 0;
   src.open(bh, now);
   const int n = src.size();
-  uint32_t prefix = 0, mask = 0, left = 0;
-  if (tid == 0) s_recent = s_cand = 0;
-  for (int pass = 0; pass < 4; ++pass) {
-    const int shift = 24 - 8 * pass;
-    for (int i = tid; i < 256; i += kEvictThreads) hist[i] = 0;
-    __syncthreads();
-    uint32_t recent = 0, cand = 0;
-    for (int i = tid; i < n; i += kEvictThreads) {
-      uint32_t key = 0;
-      const Kind kind = src.get(i, key);
-      recent += kind == kRecent;
-      if (kind != kCandidate) continue;
-      ++cand;
-      if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & 255u], 1u);
+  // this CTA's run of entries, in multiples of 32
+  const int run = static_cast<int>((static_cast<int64_t>(n) + 32 * cluster - 1) / (32 * cluster)) * 32;
+  const int e0 = min(static_cast<int64_t>(n), static_cast<int64_t>(rank) * run), e1 = min(n - e0, run) + e0;
+  const bool cached = run <= kKeysCap;
+  __syncthreads();
+
+  uint32_t prefix = 0, mask = 0, left = 0, m = 0, cand = 0, recents = 0, before = 0;
+  bool all = false;
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const uint32_t bins = pass == 2 ? 1024 : kBins;
+    uint32_t mine = 0;
+#pragma unroll 4
+    for (int i = e0 + tid; i < e1; i += kEvictThreads) {
+      uint32_t is_recent = 0, key;
+      if (pass == 0 || !cached) {
+        key = src.key(i, is_recent);
+        if (cached) keys[i - e0] = key;
+        mine += is_recent;
+      } else {
+        key = keys[i - e0];
+      }
+      if (key != kNoKey && (key & mask) == prefix) atomicAdd(&sh.hist[pass][(key >> shift) & (bins - 1)], 1u);
     }
     if (pass == 0) {
-      atomicAdd(&s_recent, recent);
-      atomicAdd(&s_cand, cand);
+      mine = __reduce_add_sync(0xffffffffu, mine);
+      if (lane == 0 && mine != 0) atomicAdd(&sh.recent, mine);
     }
-    __syncthreads();
-    if (pass == 0) left = min(s_cand, static_cast<uint32_t>(max(budget - static_cast<int64_t>(s_recent), int64_t{0})));
-    if (left == 0 || (pass == 0 && left == s_cand)) break;  // none or all of the others stay
-    if (tid == 0) {
-      uint32_t above = 0;
-      int d = 255;
-      while (above + hist[d] < left) above += hist[d--];
-      s_digit = d;
-      s_left = left - above;
+    if (cluster > 1) cluster_sync(); else __syncthreads();
+    // all CTAs' counts of bins 4 tid ..
+    uint32_t c[4] = {0, 0, 0, 0}, equal_before[4] = {0, 0, 0, 0};
+    if (4u * tid < bins) {
+      for (int r = 0; r < cluster; ++r) {
+        const uint4 v = cluster > 1 ? load_cluster4(cluster_address(&sh.hist[pass][4 * tid], r))
+                                    : *reinterpret_cast<const uint4*>(&sh.hist[pass][4 * tid]);
+        c[0] += v.x, c[1] += v.y, c[2] += v.z, c[3] += v.w;
+        if (r < rank) equal_before[0] += v.x, equal_before[1] += v.y, equal_before[2] += v.z, equal_before[3] += v.w;
+      }
     }
+    // entries in this thread's bins and in all above: a scan over the threads from the last to the first
+    const uint32_t own = c[0] + c[1] + c[2] + c[3];
+    uint32_t incl = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_down_sync(0xffffffffu, incl, o);
+      if (lane + o < 32) incl += y;
+    }
+    if (lane == 0) sh.warp_sum[warp] = incl;
     __syncthreads();
-    prefix |= s_digit << shift;
-    mask |= 255u << shift;
-    left = s_left;
-  }
-  const uint32_t m = min(s_cand, static_cast<uint32_t>(max(budget - static_cast<int64_t>(s_recent), int64_t{0})));
-  const bool all = m == s_cand, none = m == 0;
-  uint32_t before = 0;  // entries equal to the key so far, in order
-  for (int base = 0; base < n; base += kEvictThreads) {
-    const int i = base + tid;
-    uint32_t key = 0;
-    const Kind kind = i < n ? src.get(i, key) : kAbsent;
-    const bool eq = kind == kCandidate && key == prefix;
-    const uint32_t bits = __ballot_sync(0xffffffffu, eq);
-    if (lane == 0) warp_sum[warp] = __popc(bits);
-    __syncthreads();
-    uint32_t rank = before + __popc(bits & ((1u << lane) - 1u)), total = 0;
+    uint32_t total = 0;
     for (int w = 0; w < kEvictWarps; ++w) {
-      if (w < warp) rank += warp_sum[w];
-      total += warp_sum[w];
+      const uint32_t s = sh.warp_sum[w];
+      if (w > warp) incl += s;
+      total += s;
     }
-    before += total;
+    if (pass == 0) {
+      for (int r = 0; r < cluster; ++r)
+        recents += cluster > 1 ? load_cluster(cluster_address(&sh.recent, r)) : sh.recent;
+      cand = total;
+      const int64_t room = static_cast<int64_t>(budget) - recents;
+      m = room <= 0 ? 0u : room < cand ? static_cast<uint32_t>(room) : cand;
+      left = m;
+      all = m == cand;
+      if (m == 0 || all) break;  // none or all of the candidates stay
+    }
+    uint32_t above = incl - own;
+    if (above < left && incl >= left) {
+#pragma unroll
+      for (int k = 3; k >= 0; --k) {
+        if (above < left && above + c[k] >= left) {
+          sh.digit = 4 * tid + k;
+          sh.left = left - above;
+          sh.equal = c[k];
+          sh.before = equal_before[k];
+        }
+        above += c[k];
+      }
+    }
     __syncthreads();
-    const bool stays = kind == kRecent || all || (!none && (key > prefix || (eq && rank < left)));
-    if (kind != kAbsent) src.put(i, stays);
+    prefix |= sh.digit << shift;
+    mask |= (bins - 1) << shift;
+    left = sh.left;
+    before = sh.before;
   }
-  if (kept != nullptr && tid == 0) kept[bh] = static_cast<int32_t>(s_recent + m);
+  // ---- who stays: the candidates above the key, and of those equal to it the first `left`
+  const bool none = m == 0;
+  const bool ranked = !none && !all && sh.equal != left;
+  __syncthreads();  // sh.equal has been read: what follows uses the same memory
+  for (int base = e0; base < e1; base += kEvictThreads) {
+    const int i = base + tid;
+    uint32_t key = kNoKey, is_recent;
+    if (i < e1) key = cached ? keys[i - e0] : src.key(i, is_recent);
+    const bool eq = key == prefix && key != kNoKey;
+    bool stays = all || (!none && (key > prefix || eq));
+    if (ranked) {
+      const uint32_t bits = __ballot_sync(0xffffffffu, eq);
+      if (lane == 0) sh.warp_sum[warp] = __popc(bits);
+      __syncthreads();
+      uint32_t place = before + __popc(bits & ((1u << lane) - 1u));
+      for (int w = 0; w < kEvictWarps; ++w) {
+        const uint32_t c = sh.warp_sum[w];
+        if (w < warp) place += c;
+        before += c;
+      }
+      if (eq) stays = place < left;
+      __syncthreads();
+    }
+    if (i < e1) src.put(i, key != kNoKey, stays);
+  }
+  if (kept != nullptr && rank == 0 && tid == 0) kept[bh] = static_cast<int32_t>(recents + m);
+  if (cluster > 1) cluster_sync();  // no CTA leaves while another may still read its counts
+}
+
+// CTAs a (b, h): one for each 8,192 entries, up to 8.
+int cluster_for(int64_t n) { return n > 32768 ? 8 : n > 16384 ? 4 : n > 8192 ? 2 : 1; }
+
+template <class Src>
+kvp_status launch_evict(const Src& src, int64_t BH, int64_t most, int budget, const int32_t* now_dev, int now,
+                        int32_t* kept, int32_t* status, void* stream) {
+  const int cluster = cluster_for(most);
+  const int64_t run = (most + 32 * cluster - 1) / (32 * cluster) * 32;
+  constexpr size_t base = (sizeof(EvictShared) + 15) / 16 * 16;
+  const size_t smem = base + static_cast<size_t>(run < kKeysCap ? run : kKeysCap) * 4;
+  static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is raised
+  int device = 0;
+  if (current_sms(&device) == 0) return KVP_ERR_CUDA;
+  if (device > 63 || (ready.load(std::memory_order_relaxed) >> device & 1u) == 0) {
+    if (cudaFuncSetAttribute(evict_kernel<Src>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(base + kKeysCap * 4)) != cudaSuccess) {
+      (void)cudaGetLastError();
+      return KVP_ERR_CUDA;
+    }
+    if (device <= 63) ready.fetch_or(uint64_t{1} << device, std::memory_order_relaxed);
+  }
+  const dim3 grid(static_cast<unsigned>(BH * cluster));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e =
+      cluster > 1 ? launch_pdl_cluster(evict_kernel<Src>, grid, dim3(kEvictThreads), smem, st, cluster, src, cluster,
+                                       budget, now_dev, now, kept, status)
+                  : launch_pdl(evict_kernel<Src>, grid, dim3(kEvictThreads), smem, st, src, cluster, budget, now_dev, now,
+                               kept, status);
+  return e == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
 }
 
 kvp_status evict_paged_impl(int batch, int n_kv_heads, const float* acc, int64_t acc_stride_b, int64_t acc_stride_h,
@@ -183,12 +306,10 @@ kvp_status evict_paged_impl(int batch, int n_kv_heads, const float* acc, int64_t
     if ((reinterpret_cast<uintptr_t>(x) & 3u) != 0) return KVP_ERR_ALIGN;
   const int64_t BH = static_cast<int64_t>(batch) * n_kv_heads;
   if (BH > (1 << 24) || static_cast<int64_t>(max_pages) * kPage > 0x7fff0000) return KVP_ERR_UNSUPPORTED;
-  const PagedEvict src{acc,   acc_stride_b, acc_stride_h, acc_len, n_kv_heads, expire_pool, n_pages_cap, max_pages,
-                       page_table, remap, count, recent, now, now_dev, kept, status, nullptr, nullptr, nullptr, 0};
-  return launch_pdl(evict_kernel<PagedEvict>, dim3(static_cast<unsigned>(BH)), dim3(kEvictThreads), 0,
-                    static_cast<cudaStream_t>(stream), src, budget, now_dev, now, kept, status) == cudaSuccess
-             ? KVP_OK
-             : KVP_ERR_CUDA;
+  const PagedEvict src{acc,        acc_stride_b, acc_stride_h, acc_len, n_kv_heads, expire_pool, n_pages_cap, max_pages,
+                       page_table, remap,        count,        recent,  now,        status,      nullptr,     nullptr,
+                       nullptr,    0};
+  return launch_evict(src, BH, static_cast<int64_t>(max_pages) * kPage, budget, now_dev, now, kept, status, stream);
 }
 
 }  // namespace
@@ -208,12 +329,8 @@ extern "C" kvp_status kvp_evict(int batch, int n_kv_heads, int n_pos, const floa
     if ((reinterpret_cast<uintptr_t>(x) & 3u) != 0) return KVP_ERR_ALIGN;
   const int64_t BH = static_cast<int64_t>(batch) * n_kv_heads;
   if (BH > (1 << 24) || n_pos > 0x7fff0000) return KVP_ERR_UNSUPPORTED;
-  const DenseEvict src{acc, stride_b, stride_t, stride_h, n_kv_heads, n_pos, recent, now, expire, count, nullptr, nullptr};
-  return launch_pdl(evict_kernel<DenseEvict>, dim3(static_cast<unsigned>(BH)), dim3(kEvictThreads), 0,
-                    static_cast<cudaStream_t>(stream), src, budget, nullptr, now, count,
-                    static_cast<int32_t*>(nullptr)) == cudaSuccess
-             ? KVP_OK
-             : KVP_ERR_CUDA;
+  const DenseEvict src{acc, stride_b, stride_t, stride_h, n_kv_heads, n_pos, recent, now, expire, nullptr, nullptr, 0};
+  return launch_evict(src, BH, n_pos, budget, nullptr, now, count, nullptr, stream);
 }
 
 extern "C" kvp_status kvp_evict_paged(int batch, int n_kv_heads, const float* acc, int64_t acc_stride_b,
