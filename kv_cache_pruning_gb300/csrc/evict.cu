@@ -7,11 +7,17 @@
 // largest key T is found by radix selection, 11, 11 and 10 bits from the top, and
 // the entries kept are those above T and the first m - #{> T} of those equal to it.
 //
-// A cluster of CTAs takes a (b, h), each a run of its entries, whose keys it keeps
-// in shared memory: so an entry is read once, whatever the passes. Each pass counts
-// into a histogram of each CTA, and after a cluster barrier every CTA adds them all
-// up (through distributed shared memory) and comes to the same digit. How many
-// entries equal to T the CTAs before it have is in their last histograms.
+// A cluster of CTAs takes a (b, h), each a run of its entries. Each pass counts into
+// a histogram of each CTA, and after a cluster barrier every CTA adds them all up
+// (through distributed shared memory) and comes to the same digit. How many entries
+// equal to T the CTAs before it have is in their last histograms. A thread takes
+// four entries at a time, with 16-byte loads and stores where they lie side by side.
+//
+// Bound: the weights read and the expire values written, 8 bytes an entry, and the
+// counting. Keys of runs up to 8,192 are kept in shared memory (a paged cache's
+// entry is three dependent loads). Those of longer runs are made again from what
+// L2 holds: with the room that they would take, only half as many CTAs run at once
+// (131,072 x 64 weights: 67 us with all keys kept, @@ us so).
 #include "kvp_common.cuh"
 
 namespace kvp {
@@ -20,7 +26,7 @@ namespace {
 constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kBins = 2048;                 // 11 bits
-constexpr int kKeysCap = 24576;             // keys that a CTA keeps (96 KB); those of longer runs are made anew
+constexpr int kKeysCap = 8192;              // keys that a CTA keeps (32 KB)
 constexpr uint32_t kNoKey = 0xFFFFFFFFu;    // not a candidate: above the key of any weight
 
 // fp32 to a key whose unsigned order is the values': NaN 0, -inf 0x007fffff, zeros 0x80000000, inf 0xff800000.
@@ -32,6 +38,7 @@ KVP_DEV uint32_t weight_key(float x) {
 
 // The entries of a prompt: positions 0 .. n_pos - 1, the recent ones last.
 struct DenseEvict {
+  static constexpr bool kExact = true;   // size() is what the call names
   const float* acc;
   int64_t stride_b, stride_t, stride_h;
   int H, n_pos, recent, now;
@@ -39,21 +46,44 @@ struct DenseEvict {
   const float* row;
   int32_t* out;
   int old;  // entries that are not recent
+  bool loads4, stores4;
   KVP_DEV void open(int bh, int /*step*/) {
     row = acc + (bh / H) * stride_b + (bh % H) * stride_h;
     out = expire + static_cast<int64_t>(bh) * n_pos;
     old = static_cast<int>(min(static_cast<int64_t>(n_pos), max(int64_t{0}, static_cast<int64_t>(now) - recent + 1)));
+    loads4 = stride_t == 1 && (reinterpret_cast<uintptr_t>(row) & 15u) == 0;
+    stores4 = (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
   }
   KVP_DEV int size() const { return n_pos; }
-  KVP_DEV uint32_t key(int i, uint32_t& is_recent) const {
-    is_recent = i >= old;
-    return i < old ? weight_key(row[i * stride_t]) : kNoKey;
+  // keys of entries i .. i + 3 (i a multiple of 4; those from e on: kNoKey), and how many of them are recent
+  KVP_DEV uint32_t keys4(int i, int e, uint32_t (&k)[4]) const {
+    const int end = min(old, e);
+    if (loads4 && i + 4 <= end) {
+      const float4 w = *reinterpret_cast<const float4*>(row + i);
+      k[0] = weight_key(w.x), k[1] = weight_key(w.y), k[2] = weight_key(w.z), k[3] = weight_key(w.w);
+      return 0;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) k[j] = i + j < end ? weight_key(row[(i + j) * stride_t]) : kNoKey;
+    return max(0, min(i + 4, e) - max(i, end));
   }
-  KVP_DEV void put(int i, bool candidate, bool stays) const { out[i] = !candidate || stays ? kNever : now; }
+  KVP_DEV void put4(int i, int e, const uint32_t (&k)[4], const bool (&stays)[4]) const {
+    int32_t v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = k[j] == kNoKey || stays[j] ? kNever : now;
+    if (stores4 && i + 4 <= e) {
+      *reinterpret_cast<int4*>(out + i) = make_int4(v[0], v[1], v[2], v[3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (i + j < e) out[i + j] = v[j];
+    }
+  }
 };
 
 // The present slots of a paged cache.
 struct PagedEvict {
+  static constexpr bool kExact = false;  // ... or less
   const float* acc;
   int64_t stride_b, stride_h;
   int acc_len, H;
@@ -76,26 +106,45 @@ struct PagedEvict {
     n = min(max(count[bh], 0), max_pages * kPage);
   }
   KVP_DEV int size() const { return n; }
-  KVP_DEV uint32_t key(int i, uint32_t& is_recent) const {
-    is_recent = 0;
-    const int page = pages[i / kPage], at = pos[i];
+  // (four slots of one page: i is a multiple of 4)
+  KVP_DEV uint32_t keys4(int i, int e, uint32_t (&k)[4]) const {
+    const int page = pages[i / kPage];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) k[j] = kNoKey;
     if (page < 0 || page >= n_pages_cap) {
       record_error(status, KVP_ERR_BOUNDS);
-      return kNoKey;
+      return 0;
     }
-    // (the weight is asked for beside the expire value: most slots are present)
-    const bool inside = at >= 0 && at < acc_len;
-    const float w = inside ? row[at] : 0.f;
-    if (expire_pool[static_cast<int64_t>(page) * kPage + i % kPage] <= now) return kNoKey;
-    if (!inside) {
-      record_error(status, KVP_ERR_BOUNDS);
-      return kNoKey;
+    const int32_t* gone = expire_pool + static_cast<int64_t>(page) * kPage + i % kPage;
+    int at[4], until[4];
+    float w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      at[j] = i + j < e ? pos[i + j] : -1;
+      until[j] = i + j < e ? gone[j] : INT32_MIN;
     }
-    is_recent = at > static_cast<int64_t>(now) - recent;
-    return is_recent ? kNoKey : weight_key(w);
+    // (the weights are asked for beside the expire values: most slots are present)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = at[j] >= 0 && at[j] < acc_len ? row[at[j]] : 0.f;
+    uint32_t recents = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (until[j] <= now) continue;
+      if (at[j] < 0 || at[j] >= acc_len) {
+        record_error(status, KVP_ERR_BOUNDS);
+      } else if (at[j] > static_cast<int64_t>(now) - recent) {
+        ++recents;
+      } else {
+        k[j] = weight_key(w[j]);
+      }
+    }
+    return recents;
   }
-  KVP_DEV void put(int i, bool candidate, bool stays) const {
-    if (candidate && !stays) expire_pool[static_cast<int64_t>(pages[i / kPage]) * kPage + i % kPage] = now;
+  KVP_DEV void put4(int i, int /*e*/, const uint32_t (&k)[4], const bool (&stays)[4]) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (k[j] != kNoKey && !stays[j])
+        expire_pool[static_cast<int64_t>(pages[i / kPage]) * kPage + i % kPage + j] = now;
   }
 };
 
@@ -127,7 +176,7 @@ struct EvictShared {
 };
 
 template <class Src>
-__global__ void __launch_bounds__(kEvictThreads) evict_kernel(Src src, int cluster, int budget, const int32_t* now_dev,
+__global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(Src src, int cluster, int budget, const int32_t* now_dev,
                                                              int now, int32_t* kept, int32_t* status) {
   extern __shared__ uint4 evict_smem[];
   EvictShared& sh = *reinterpret_cast<EvictShared*>(evict_smem);
@@ -158,17 +207,20 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(Src src, int clust
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
     const uint32_t bins = pass == 2 ? 1024 : kBins;
     uint32_t mine = 0;
-#pragma unroll 4
-    for (int i = e0 + tid; i < e1; i += kEvictThreads) {
-      uint32_t is_recent = 0, key;
+#pragma unroll 2
+    for (int i = e0 + 4 * tid; i < e1; i += 4 * kEvictThreads) {
+      uint32_t k[4];
+      uint4* kept_keys = reinterpret_cast<uint4*>(keys + (i - e0));
       if (pass == 0 || !cached) {
-        key = src.key(i, is_recent);
-        if (cached) keys[i - e0] = key;
-        mine += is_recent;
+        mine += src.keys4(i, e1, k);
+        if (cached) *kept_keys = make_uint4(k[0], k[1], k[2], k[3]);
       } else {
-        key = keys[i - e0];
+        const uint4 v = *kept_keys;
+        k[0] = v.x, k[1] = v.y, k[2] = v.z, k[3] = v.w;
       }
-      if (key != kNoKey && (key & mask) == prefix) atomicAdd(&sh.hist[pass][(key >> shift) & (bins - 1)], 1u);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (k[j] != kNoKey && (k[j] & mask) == prefix) atomicAdd(&sh.hist[pass][(k[j] >> shift) & (bins - 1)], 1u);
     }
     if (pass == 0) {
       mine = __reduce_add_sync(0xffffffffu, mine);
@@ -234,44 +286,69 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(Src src, int clust
   const bool none = m == 0;
   const bool ranked = !none && !all && sh.equal != left;
   __syncthreads();  // sh.equal has been read: what follows uses the same memory
-  for (int base = e0; base < e1; base += kEvictThreads) {
-    const int i = base + tid;
-    uint32_t key = kNoKey, is_recent;
-    if (i < e1) key = cached ? keys[i - e0] : src.key(i, is_recent);
-    const bool eq = key == prefix && key != kNoKey;
-    bool stays = all || (!none && (key > prefix || eq));
-    if (ranked) {
-      const uint32_t bits = __ballot_sync(0xffffffffu, eq);
-      if (lane == 0) sh.warp_sum[warp] = __popc(bits);
+#pragma unroll 1
+  for (int base = e0; base < e1; base += 4 * kEvictThreads) {
+    const int i = base + 4 * tid;
+    uint32_t k[4] = {kNoKey, kNoKey, kNoKey, kNoKey};
+    if (i < e1) {
+      if (cached) {
+        const uint4 v = *reinterpret_cast<const uint4*>(keys + (i - e0));
+        k[0] = v.x, k[1] = v.y, k[2] = v.z, k[3] = v.w;
+      } else {
+        (void)src.keys4(i, e1, k);
+      }
+    }
+    bool stays[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) stays[j] = all || (!none && k[j] >= prefix);
+    if (ranked) {  // entries equal to the key, counted in order
+      uint32_t equal = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) equal += k[j] == prefix;
+      uint32_t incl = equal;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      if (lane == 31) sh.warp_sum[warp] = incl;
       __syncthreads();
-      uint32_t place = before + __popc(bits & ((1u << lane) - 1u));
+      uint32_t place = before + incl - equal;
       for (int w = 0; w < kEvictWarps; ++w) {
         const uint32_t c = sh.warp_sum[w];
         if (w < warp) place += c;
         before += c;
       }
-      if (eq) stays = place < left;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (k[j] == prefix) stays[j] = place++ < left;
       __syncthreads();
     }
-    if (i < e1) src.put(i, key != kNoKey, stays);
+    if (i < e1) src.put4(i, e1, k, stays);
   }
   if (kept != nullptr && rank == 0 && tid == 0) kept[bh] = static_cast<int32_t>(recents + m);
   if (cluster > 1) cluster_sync();  // no CTA leaves while another may still read its counts
 }
 
-// CTAs a (b, h): one for each 8,192 entries, up to 8.
-int cluster_for(int64_t n) { return n > 32768 ? 8 : n > 16384 ? 4 : n > 8192 ? 2 : 1; }
+// CTAs a (b, h), up to 8: more while a run is over 4,096 entries and the CTAs fit the device side by side (two an SM).
+int cluster_for(int64_t n, int64_t BH, int sms) {
+  int c = 1;
+  while (c < 8 && n > 4096 * c && BH * c * 2 <= 2 * static_cast<int64_t>(sms)) c *= 2;
+  return c;
+}
 
 template <class Src>
 kvp_status launch_evict(const Src& src, int64_t BH, int64_t most, int budget, const int32_t* now_dev, int now,
                         int32_t* kept, int32_t* status, void* stream) {
-  const int cluster = cluster_for(most);
+  int device = 0;
+  const int sms = current_sms(&device);
+  if (sms == 0) return KVP_ERR_CUDA;
+  const int cluster = cluster_for(most, BH, sms);
   const int64_t run = (most + 32 * cluster - 1) / (32 * cluster) * 32;
   constexpr size_t base = (sizeof(EvictShared) + 15) / 16 * 16;
-  const size_t smem = base + static_cast<size_t>(run < kKeysCap ? run : kKeysCap) * 4;
+  // room for the keys of every run that the kernel keeps: a run is no longer than this one, and shorter only if !kExact
+  const size_t smem = base + (run <= kKeysCap ? static_cast<size_t>(run) * 4 : Src::kExact ? 0 : kKeysCap * 4);
   static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is raised
-  int device = 0;
-  if (current_sms(&device) == 0) return KVP_ERR_CUDA;
   if (device > 63 || (ready.load(std::memory_order_relaxed) >> device & 1u) == 0) {
     if (cudaFuncSetAttribute(evict_kernel<Src>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(base + kKeysCap * 4)) != cudaSuccess) {
