@@ -16,8 +16,9 @@
 // Bound: the weights read and the expire values written, 8 bytes an entry, and the
 // counting. Keys of runs up to 8,192 are kept in shared memory (a paged cache's
 // entry is three dependent loads). Those of longer runs are made again from what
-// L2 holds: with the room that they would take, only half as many CTAs run at once
-// (131,072 x 64 weights: 67 us with all keys kept, @@ us so).
+// L2 holds, but for the last pass's, which the second one lists: with the room that
+// all would take, only half as many CTAs run at once (131,072 x 64 weights: 67 us
+// with all keys kept, @@ us so).
 #include "kvp_common.cuh"
 
 namespace kvp {
@@ -27,13 +28,14 @@ constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kBins = 2048;                 // 11 bits
 constexpr int kKeysCap = 8192;              // keys that a CTA keeps (32 KB)
+constexpr int kListCap = 4096;              // of longer runs: keys with the first pass's digit that it keeps (16 KB)
 constexpr uint32_t kNoKey = 0xFFFFFFFFu;    // not a candidate: above the key of any weight
 
 // fp32 to a key whose unsigned order is the values': NaN 0, -inf 0x007fffff, zeros 0x80000000, inf 0xff800000.
 KVP_DEV uint32_t weight_key(float x) {
-  if (x != x) return 0u;
-  const uint32_t u = __float_as_uint(x == 0.f ? 0.f : x);
-  return u ^ ((u >> 31) != 0u ? 0xFFFFFFFFu : 0x80000000u);
+  const int32_t u = __float_as_int(x + 0.f);  // -0 becomes 0
+  const uint32_t k = static_cast<uint32_t>(u) ^ (static_cast<uint32_t>(u >> 31) | 0x80000000u);
+  return x != x ? 0u : k;
 }
 
 // The entries of a prompt: positions 0 .. n_pos - 1, the recent ones last.
@@ -173,6 +175,7 @@ struct EvictShared {
   uint32_t recent;
   uint32_t warp_sum[kEvictWarps];
   uint32_t digit, left, equal, before;
+  uint32_t listed;                // keys on the list (or more: then it is not used)
 };
 
 template <class Src>
@@ -192,7 +195,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(Src src, int cl
     }
   }
   for (int i = tid; i < 3 * kBins; i += kEvictThreads) sh.hist[0][i] = 0;
-  if (tid == 0) sh.recent = 0;
+  if (tid == 0) sh.recent = sh.listed = 0;
   src.open(bh, now);
   const int n = src.size();
   // this CTA's run of entries, in multiples of 32
@@ -207,8 +210,13 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(Src src, int cl
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
     const uint32_t bins = pass == 2 ? 1024 : kBins;
     uint32_t mine = 0;
+    const bool from_list = pass == 2 && !cached && sh.listed <= kListCap;
+    if (from_list) {
+      for (uint32_t i = tid; i < sh.listed; i += kEvictThreads)
+        if ((keys[i] & mask) == prefix) atomicAdd(&sh.hist[pass][keys[i] & (bins - 1)], 1u);
+    }
 #pragma unroll 2
-    for (int i = e0 + 4 * tid; i < e1; i += 4 * kEvictThreads) {
+    for (int i = from_list ? e1 : e0 + 4 * tid; i < e1; i += 4 * kEvictThreads) {
       uint32_t k[4];
       uint4* kept_keys = reinterpret_cast<uint4*>(keys + (i - e0));
       if (pass == 0 || !cached) {
@@ -219,8 +227,14 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(Src src, int cl
         k[0] = v.x, k[1] = v.y, k[2] = v.z, k[3] = v.w;
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (k[j] != kNoKey && (k[j] & mask) == prefix) atomicAdd(&sh.hist[pass][(k[j] >> shift) & (bins - 1)], 1u);
+      for (int j = 0; j < 4; ++j) {
+        if (k[j] == kNoKey || (k[j] & mask) != prefix) continue;
+        atomicAdd(&sh.hist[pass][(k[j] >> shift) & (bins - 1)], 1u);
+        if (pass == 1 && !cached) {
+          const uint32_t at = atomicAdd(&sh.listed, 1u);
+          if (at < kListCap) keys[at] = k[j];
+        }
+      }
     }
     if (pass == 0) {
       mine = __reduce_add_sync(0xffffffffu, mine);
@@ -347,7 +361,7 @@ kvp_status launch_evict(const Src& src, int64_t BH, int64_t most, int budget, co
   const int64_t run = (most + 32 * cluster - 1) / (32 * cluster) * 32;
   constexpr size_t base = (sizeof(EvictShared) + 15) / 16 * 16;
   // room for the keys of every run that the kernel keeps: a run is no longer than this one, and shorter only if !kExact
-  const size_t smem = base + (run <= kKeysCap ? static_cast<size_t>(run) * 4 : Src::kExact ? 0 : kKeysCap * 4);
+  const size_t smem = base + (run <= kKeysCap ? static_cast<size_t>(run) * 4 : (Src::kExact ? kListCap : kKeysCap) * 4);
   static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is raised
   if (device > 63 || (ready.load(std::memory_order_relaxed) >> device & 1u) == 0) {
     if (cudaFuncSetAttribute(evict_kernel<Src>, cudaFuncAttributeMaxDynamicSharedMemorySize,
