@@ -148,12 +148,15 @@ KVP_DEV void add_bad_values(float (&v)[32], const uint16_t* rows, int64_t stride
   }
 }
 
+// What the two tiles of a work item are: two heads of a kv head, 256 rows of a head; or there is only one.
+enum Tiles { kByHead = 0, kByRow = 1, kOneTile = 2 };
+
 struct AttnMaps {
   CUtensorMap q, k, v;  // [D, heads, rows], boxes of 64 x 1 x 128
 };
 
 template <int D>
-__global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const PromptParams p,
+__global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const PromptParams p, const int tiles,
                                                                       const __grid_constant__ AttnMaps maps) {
   using C = AttnCfg<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -206,8 +209,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const bool by_head = p.G % 2 == 0;
-  const int cols = by_head ? p.Hq / 2 : p.Hq;  // work items of one tile
+  const bool by_head = tiles != kByRow;
+  const int cols = tiles == kByHead ? p.Hq / 2 : p.Hq;  // work items of one tile
   auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_quietly(bar, parity, abort_flag, p.seqs.status); };
   auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
   auto gave_up = [&]() {
@@ -233,10 +236,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
     t.len = v.y;
     t.tA = v.z;
     t.tB = by_head ? v.z : v.z + 1;
-    t.hA = by_head ? 2 * v.w : v.w;
-    t.hB = by_head ? 2 * v.w + 1 : v.w;
+    t.hA = tiles == kByHead ? 2 * v.w : v.w;
+    t.hB = tiles == kByHead ? 2 * v.w + 1 : v.w;
     t.nA = t.tA + 1;
-    t.nB = t.tB * kTile < t.len ? t.tB + 1 : 0;
+    t.nB = tiles != kOneTile && t.tB * kTile < t.len ? t.tB + 1 : 0;
     return true;
   };
   Item t;
@@ -564,10 +567,15 @@ kvp_status launch_attn(const PromptParams& p, int n_kv_heads, cudaStream_t st) {
     }
     if (device <= 63) ready.fetch_or(uint64_t{1} << device, std::memory_order_relaxed);
   }
-  const bool by_head = p.G % 2 == 0;
-  const int64_t most = (p.seqs.n_tok / (by_head ? kTile : 2 * kTile) + p.seqs.n) * (by_head ? p.Hq / 2 : p.Hq);
+  // Two tiles an item, but where even single ones leave SMs idle: then each has less to do (509 tokens, 32/8 heads:
+  // @@ us with pairs, @@ us so).
+  const int64_t singles = (p.seqs.n_tok / kTile + p.seqs.n) * p.Hq;
+  const int tiles = singles <= sms ? kOneTile : p.G % 2 == 0 ? kByHead : kByRow;
+  const int64_t most = tiles == kOneTile  ? singles
+                       : tiles == kByHead ? singles / 2
+                                          : (p.seqs.n_tok / (2 * kTile) + p.seqs.n) * p.Hq;
   return launch_pdl(prompt_attn_kernel<D>, dim3(static_cast<unsigned>(std::min<int64_t>(sms, most))), dim3(kAttnThreads),
-                    C::kSmem, st, p, maps) == cudaSuccess
+                    C::kSmem, st, p, tiles, maps) == cudaSuccess
              ? KVP_OK
              : KVP_ERR_CUDA;
 }
