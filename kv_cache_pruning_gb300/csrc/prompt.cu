@@ -38,11 +38,19 @@ struct AttnCfg {
   static constexpr int kBoxBytes = kTile * 128;          // 128 rows x 64 columns
   static constexpr int kTileBytes = kBoxes * kBoxBytes;  // one tile of Q, K or V
   static constexpr int kStages = D == 128 ? 5 : 8;       // ring of K and V tiles
+  // At D = 64 tensor memory has room for a third S, and the products are short: one warp issues those with K, another
+  // those with V, each block's S as soon as a buffer is free (8,192 tokens, 32/8 heads: 311 us with one warp and two
+  // buffers, where it waited for every signal in turn; @@ us so).
+  static constexpr bool kApart = D == 64;
+  static constexpr int kBufs = kApart ? 3 : 2;           // buffers of S (and then P)
+  static constexpr uint32_t kOCol = kBufs * kTile;       // O of A and B
+  static_assert(kOCol + 2 * D <= 512, "tensor memory");
   static constexpr int kPairs = 8;                       // ring of barriers that give stages back
+  static_assert(!kApart || kPairs == kStages, "one for each stage");
   static constexpr int kQOff = 0;
   static constexpr int kRingOff = 2 * kTileBytes;
   static constexpr int kBarOff = kRingOff + kStages * kTileBytes;
-  static constexpr int kBars = 2 + kStages + kPairs + 3 * 2 + 1 + 2 * kInfo;
+  static constexpr int kBars = 2 + kStages + kPairs + 3 * kBufs + 2 + 2 * kInfo;
   static constexpr int kInfoOff = (kBarOff + kBars * 8 + 15) / 16 * 16;  // [slot]{first row, length, tile, column}
   static constexpr int kFlagOff = kInfoOff + kInfo * 16;           // tensor memory's address, abort, bad values
   static constexpr int kSmem = 1024 + kFlagOff + 8 + 8 * kFlags;
@@ -50,13 +58,12 @@ struct AttnCfg {
   static_assert(kRingOff % 1024 == 0 && kBarOff % 8 == 0 && kInfoOff % 16 == 0 && kFlagOff % 4 == 0,
                 "alignment");
 };
-constexpr int kSoftWarps = 8, kMmaWarp = 8, kCopyWarp = 9, kPlanWarp = 11;
-constexpr int kAttnThreads = 384;             // warp 10 only gives its registers away
+constexpr int kSoftWarps = 8, kMmaWarp = 8, kCopyWarp = 9, kKeysWarp = 10, kPlanWarp = 11;
+constexpr int kAttnThreads = 384;
 // A row's 128 logits stay in registers: the softmax warps take 216 each and the
 // others 72, of the 168 a thread that the block is launched with:
 // 256 x 216 + 128 x 72 = 384 x 168.
 constexpr int kRegsSoft = 216, kRegsRest = 72;
-constexpr uint32_t kSCol = 0, kOCol = 256;  // S (and P) of A, B at 0, 128; O at 256, 384
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLazy = 8.f;                // how far a row's maximum may pass its reference (base 2)
 constexpr float kMostSum = 1.f / 8192;      // 128 weights of 2^(kLazy - kHeadroom)
@@ -167,11 +174,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
   uint64_t* q_empty = q_full + 1;
   uint64_t* full = q_empty + 1;
   uint64_t* empty = full + C::kStages;
-  uint64_t* s_full = empty + C::kPairs;  // [A, B]
-  uint64_t* p_full = s_full + 2;
-  uint64_t* o_full = p_full + 2;
-  uint64_t* fin = o_full + 2;
-  uint64_t* info_full = fin + 1;
+  // [A, B]; where the products are issued apart, [block's number % kBufs], and o_full of every block, not the last alone
+  uint64_t* s_full = empty + C::kPairs;
+  uint64_t* p_full = s_full + C::kBufs;
+  uint64_t* o_full = p_full + C::kBufs;
+  uint64_t* fin = o_full + C::kBufs;
+  uint64_t* info_full = fin + 2;
   uint64_t* info_empty = info_full + kInfo;
   int4* info = reinterpret_cast<int4*>(smem + C::kInfoOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kFlagOff);
@@ -183,15 +191,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
     mbar_init(q_empty, 1);
     for (int i = 0; i < C::kStages; ++i) mbar_init(&full[i], 1);
     for (int i = 0; i < C::kPairs; ++i) mbar_init(&empty[i], 1);
-    for (int x = 0; x < 2; ++x) {
+    for (int x = 0; x < C::kBufs; ++x) {
       mbar_init(&s_full[x], 1);
       mbar_init(&p_full[x], 4);
       mbar_init(&o_full[x], 1);
     }
-    mbar_init(fin, 1);
+    mbar_init(&fin[0], 1);
+    mbar_init(&fin[1], 1);
     for (int i = 0; i < kInfo; ++i) {
       mbar_init(&info_full[i], 1);
-      mbar_init(&info_empty[i], kSoftWarps + 2);
+      mbar_init(&info_empty[i], kSoftWarps + 2 + C::kApart);
     }
     *abort_flag = 0;
     for (int i = 0; i < 2 * kFlags; ++i) bad_values[i] = 0;
@@ -274,6 +283,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
     } else if (warp == kCopyWarp) {
       // ------------------------------------------------------------ copies
       int g = 0, i = 0, nq = 0;  // tiles, items and pairs of query tiles so far
+      // a tile is given back with the pair (V of a block, K of the next) that it is of, or by itself
+      auto given_back = [&](int tile) {
+        const int k = C::kApart ? tile : (tile + 1) / 2;
+        return wait(&empty[k % C::kPairs], (k / C::kPairs) & 1);
+      };
       auto load = [&](const CUtensorMap* m, uint8_t* dst, int head, int row, uint64_t* bar) {
 #pragma unroll
         for (int b = 0; b < C::kBoxes; ++b) tma_load_3d(dst + b * C::kBoxBytes, m, 64 * b, head, row, bar);
@@ -283,9 +297,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
         if (lane == 0) {
           for (int k = 0; ok && k < 2 * n; ++k) {  // K of block 0, V of block 0, K of block 1, ...
             const int st = g % C::kStages;
-            if (g >= C::kStages) {  // tile g - kStages is given back with the pair (V of a block, K of the next) that it is of
-              const int pair = (g - C::kStages + 1) / 2;
-              ok = wait(&empty[pair % C::kPairs], (pair / C::kPairs) & 1);
+            if (g >= C::kStages) {
+              ok = given_back(g - C::kStages);
               if (!ok) break;
             }
             mbar_arrive_expect_tx(&full[st], C::kTileBytes);
@@ -311,8 +324,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
       if (lane == 0 && g > 0) {
         if (ok) {  // no arrival is left on its way when the CTA ends
           ok = wait(q_empty, (i - 1) & 1);
-          for (int pair = max(0, (g - C::kStages + 1) / 2); ok && pair <= g / 2; ++pair)
-            ok = wait(&empty[pair % C::kPairs], (pair / C::kPairs) & 1);
+          for (int k = max(0, g - C::kStages); ok && k < g; ++k) ok = given_back(k);
         }
         // what was issued lands before the shared memory can go to another CTA (each wait bounded again)
         if (!ok) {
@@ -321,6 +333,58 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
         }
       }
       __syncwarp();
+    } else if (C::kApart && (warp == kMmaWarp || warp == kKeysWarp)) {
+      // ------------------------------------------------------------ products, apart
+      // Blocks in the order A 0, B 0, A 1, B 1, ... (those that there are), numbered through all items: block number n is
+      // in buffer n % kBufs, and its S comes once the products of block n - kBufs, which read P from there, are done.
+      const bool keys = warp == kKeysWarp;
+      const uint32_t leader = elect_one();
+      const uint32_t q0 = smem_u32(smem + C::kQOff), ring = smem_u32(smem + C::kRingOff);
+      uint32_t n = 0, g = 0;         // blocks, and tiles of K and V before this item
+      for (int i = 0; next_item(i, t, ok); ++i) {
+        const int blocks = max(t.nA, t.nB);
+        if (keys) ok = wait_all(q_full, i & 1);
+        for (int j = 0; ok && j < blocks; ++j) {
+          const uint32_t k = g + 2 * j + !keys, stage = k % C::kStages;
+          ok = wait_all(&full[stage], (k / C::kStages) & 1);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (!ok || j >= (x == 0 ? t.nA : t.nB)) continue;
+            const uint32_t buf = n % C::kBufs;
+            if (keys) {
+              if (n >= C::kBufs) ok = wait_all(&o_full[buf], (n / C::kBufs - 1) & 1);
+              if (!ok) continue;
+              tc_fence_after();
+              const uint64_t a = sw128_kmajor_desc(q0 + x * C::kTileBytes);
+              const uint64_t b = sw128_kmajor_desc(ring + stage * C::kTileBytes);
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint64_t off = static_cast<uint64_t>(((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4);
+                mma_ss(leader, tmem + buf * kTile, a + off, b + off, idesc_bf16_f32(kTile, kTile), kk > 0);
+              }
+              commit_to(leader, &s_full[buf]);
+            } else {
+              ok = wait_all(&p_full[buf], (n / C::kBufs) & 1);
+              if (!ok) continue;
+              tc_fence_after();
+              const uint64_t v0 = sw128_mnmajor_desc(ring + stage * C::kTileBytes, C::kBoxBytes, 1024);
+#pragma unroll
+              for (int ks = 0; ks < kTile / 16; ++ks)
+                mma_ts(leader, tmem + C::kOCol + x * D, tmem + buf * kTile + ks * 8, v0 + ((ks * 2048) >> 4),
+                       idesc_bf16_f32(kTile, D) | kIdescBMnMajor, j > 0 || ks > 0);
+              commit_to(leader, &o_full[buf]);
+            }
+            ++n;
+          }
+          if (ok) commit_to(leader, &empty[stage]);
+        }
+        if (!ok) break;
+        if (keys) commit_to(leader, q_empty);
+        g += 2 * blocks;
+      }
+      if (!ok) gave_up();
+      commit_to(leader, &fin[keys]);
+      (void)mbar_wait(&fin[keys], 0);  // every product has completed before tensor and shared memory go
     } else if (warp == kMmaWarp) {
       // ------------------------------------------------------------ products
       // The whole warp runs this, on the same values, and one elected lane issues: so the descriptors stay in uniform
@@ -343,7 +407,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
       auto issue_s = [&](int x, int stage) {  // S of tile x with the K in `stage`
         const uint64_t a = sw128_kmajor_desc(q0 + x * C::kTileBytes);
         const uint64_t b = sw128_kmajor_desc(ring + stage * C::kTileBytes);
-        const uint32_t d = tmem + kSCol + x * kTile;
+        const uint32_t d = tmem + x * kTile;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint64_t off = static_cast<uint64_t>(((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4);
@@ -384,7 +448,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
                 const uint64_t v0 = sw128_mnmajor_desc(ring + vst * C::kTileBytes, C::kBoxBytes, 1024);
 #pragma unroll
                 for (int ks = 0; ks < kTile / 16; ++ks)
-                  mma_ts(leader, tmem + kOCol + x * 128, tmem + kSCol + x * kTile + ks * 8, v0 + ((ks * 2048) >> 4), idO,
+                  mma_ts(leader, tmem + C::kOCol + x * D, tmem + x * kTile + ks * 8, v0 + ((ks * 2048) >> 4), idO,
                          j > 0 || ks > 0);
                 if (j == nx - 1) commit_to(leader, &o_full[x]);
               }
@@ -409,20 +473,27 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
     // ------------------------------------------------------------ softmax
     const int x = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t scol = trow + kSCol + x * kTile, ocol = trow + kOCol + x * 128;
+    const uint32_t ocol = trow + C::kOCol + x * D;
     const float c = p.qscale;
-    uint32_t sph = 0, oph = 0;  // phases of s_full and o_full
-    uint32_t g = 0;             // tiles of K and V before this item
+    uint32_t g = 0, n0 = 0;     // tiles of K and V, and blocks, before this item
+    uint32_t blocks = 0, items = 0;  // of this tile
+    // Where the products are issued apart: block `n` has been added to O. (The S of a later block of this tile, or its own,
+    // is there when this is asked, so block n - kBufs has: the barrier's phase is this one or the one before.)
+    auto added = [&](uint32_t n) { return wait_all(&o_full[n % C::kBufs], (n / C::kBufs) & 1); };
     for (int i = 0; next_item(i, t, ok); ++i) {
       const int nx = x == 0 ? t.nA : t.nB, tile = x == 0 ? t.tA : t.tB, head = x == 0 ? t.hA : t.hB;
       const int pos = tile * kTile + row;  // in the sequence; past its end: nothing is stored
       volatile int* flags = bad_values + i % kFlags * 2;
       float M = -INFINITY, m = -INFINITY, l = 0.f;
       for (int j = 0; j < nx; ++j) {
-        ok = wait_all(&s_full[x], sph);
-        sph ^= 1;
+        // the block's number: after those of both tiles before it
+        const auto number = [&](int j) { return n0 + min(j, t.nA) + min(j, t.nB) + (x == 1 && j < t.nA); };
+        const uint32_t buf = C::kApart ? number(j) % C::kBufs : x;
+        ok = wait_all(&s_full[buf], (C::kApart ? number(j) / C::kBufs : blocks) & 1);
         if (!ok) break;
+        ++blocks;
         tc_fence_after();
+        const uint32_t scol = trow + buf * kTile;
         float s[kTile];
         tmem_ld128(scol, s);
         if (j == nx - 1) {
@@ -459,6 +530,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
             l *= al;
           }
           if (j > 0 && __any_sync(0xffffffffu, grow)) {
+            // (else a block's S comes after the products of the tile's block before)
+            if (C::kApart) ok = added(number(j - 1));
+            if (!ok) break;
+            tc_fence_after();
 #pragma unroll 1
             for (int o = 0; o < D; o += 32) {
               float v[32];
@@ -500,13 +575,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[x]);
+        if (lane == 0) mbar_arrive(&p_full[buf]);
       }
-      g += 2 * max(t.nA, t.nB);
       if (!ok) break;
+      const uint32_t last = n0 + min(nx - 1, t.nA) + min(nx - 1, t.nB) + (x == 1 && nx - 1 < t.nA);
+      g += 2 * max(t.nA, t.nB);
+      n0 += t.nA + t.nB;
       if (nx == 0) continue;
-      ok = wait_all(&o_full[x], oph);
-      oph ^= 1;
+      ok = C::kApart ? added(last) : wait_all(&o_full[x], items & 1);
+      ++items;
       if (!ok) break;
       tc_fence_after();
       const bool some = flags[x] == i + 1;
