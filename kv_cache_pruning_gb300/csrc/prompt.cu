@@ -119,10 +119,10 @@ KVP_DEV void clear_bad_values(uint8_t* tile, int t, bool inside, volatile int* f
 #pragma unroll 8
   for (int c = 0; c < D / 8; ++c) {
     const uint4 w = *at(c);
-    found |= ((w.x & 0x7F807F80u) + 0x00800080u) | ((w.y & 0x7F807F80u) + 0x00800080u) |
-             ((w.z & 0x7F807F80u) + 0x00800080u) | ((w.w & 0x7F807F80u) + 0x00800080u);
+    found = __vmaxu2(__vmaxu2(found, w.x & 0x7FFF7FFFu), w.y & 0x7FFF7FFFu);  // the largest magnitudes
+    found = __vmaxu2(__vmaxu2(found, w.z & 0x7FFF7FFFu), w.w & 0x7FFF7FFFu);
   }
-  if ((found & 0x80008000u) == 0u) return;
+  if ((found & 0xFFFFu) < 0x7F80u && (found >> 16) < 0x7F80u) return;
   if (inside) {
     flags[0] = tag;
     flags[1] = tag;
@@ -496,10 +496,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
         const uint32_t scol = trow + buf * kTile;
         float s[kTile];
         tmem_ld128(scol, s);
-        if (j == nx - 1) {
+        if (j == nx - 1) {  // keys after the row's own: those of its own 32 by their lane, those after by the warp
 #pragma unroll
-          for (int k = 0; k < kTile; ++k)
-            if (k > row) s[k] = -INFINITY;
+          for (int o = 0; o < kTile; o += 32) {
+            if (o / 32 < (warp & 3)) continue;
+            const int cut = o / 32 == (warp & 3) ? lane : -1;
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (k > cut) s[o + k] = -INFINITY;
+          }
         }
         uint64_t sum[4];
         // With the reference as it is: no maximum is taken. If a row's sum says that some weight may have passed it by
@@ -512,9 +517,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
           again = !(e + f <= kMostSum);
         }
         if (__any_sync(0xffffffffu, again)) {
-          float mx = -INFINITY;
+          float top[8];
 #pragma unroll
-          for (int i = 0; i < kTile; ++i) mx = fmaxf(mx, s[i]);
+          for (int k = 0; k < 8; ++k) top[k] = fmaxf(s[k], s[8 + k]);
+#pragma unroll
+          for (int k = 16; k < kTile; k += 16)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top[i] = fmaxf(top[i], fmaxf(s[k + i], s[k + 8 + i]));
+          const float mx = fmaxf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])),
+                                 fmaxf(fmaxf(top[4], top[5]), fmaxf(top[6], top[7])));
           bool big = fabsf(M) >= kBig && M != -INFINITY;
           const bool grow = big ? (mx - m) * c > kLazy : fmaf(mx, c, -M) > kLazy - kHeadroom;
           const float M_new = fmaf(mx, c, kHeadroom);
@@ -596,7 +607,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
         float v[32];
         tmem_ld32(ocol + o, v);
 #pragma unroll
-        for (int k = 0; k < 32; ++k) v[k] = l == 0.f ? 0.f : v[k] * inv;
+        for (int k = 0; k < 32; ++k) v[k] *= inv;
+        if (l == 0.f) {  // (a value that is no number counts for nothing here)
+#pragma unroll
+          for (int k = 0; k < 32; ++k) v[k] = 0.f;
+        }
         if (some && mine)
           add_bad_values(v, p.v + (t.start + t.tA * kTile) * p.vt + head / p.G * p.vh + o, p.vt, pos - t.tA * kTile);
         if (mine) {
