@@ -13,12 +13,14 @@
 // equal to T the CTAs before it have is in their last histograms. A thread takes
 // four entries at a time, with 16-byte loads and stores where they lie side by side.
 //
-// Bound: the weights read and the expire values written, 8 bytes an entry, and the
-// counting. Keys of runs up to 8,192 are kept in shared memory (a paged cache's
-// entry is three dependent loads). Those of longer runs are made again from what
-// L2 holds, but for the last pass's, which the second one lists: with the room that
-// all would take, only half as many CTAs run at once (131,072 x 64 weights: 67 us
-// with all keys kept, @@ us so).
+// Bound: the weights read and the expire values written, 8 bytes an entry; what it takes is
+// the passes' latencies, one after the other (131,072 x 64 weights: 29 us, of them 11 for
+// the first pass; issue slots 41 % used). Keys of runs up to 8,192 are kept in shared memory
+// (a paged cache's entry is three dependent loads). Those of longer runs are made again from
+// what L2 holds, but for the keys with the first digit, which the second pass lists: with the
+// room that all would take only half as many CTAs run at once (67 us with all keys kept).
+// Loads of two steps are under way at once: of four, 27.6 us there but 4 % more at runs of
+// 2,048 and 10,007; of one, 32 us.
 #include "kvp_common.cuh"
 
 namespace kvp {
@@ -28,14 +30,16 @@ constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kBins = 2048;                 // 11 bits
 constexpr int kKeysCap = 8192;              // keys that a CTA keeps (32 KB)
-constexpr int kListCap = 4096;              // of longer runs: keys with the first pass's digit that it keeps (16 KB)
-constexpr uint32_t kNoKey = 0xFFFFFFFFu;    // not a candidate: above the key of any weight
+constexpr int kListCap = 4096;              // of longer runs: keys with the first pass's digit (16 KB)
+constexpr int kStep = 4 * kEvictThreads;    // entries of a step of the block's threads, four each
+constexpr int kBatch = 2;                   // steps whose loads a thread has under way
+constexpr uint32_t kNoKey = 0xFFFFFFFFu;    // not a candidate: above the key of any weight, and of a first digit of its own
 
-// fp32 to a key whose unsigned order is the values': NaN 0, -inf 0x007fffff, zeros 0x80000000, inf 0xff800000.
+// fp32 to a key whose unsigned order is the values': -inf 0x00800000, zeros 0x80000001, inf 0xff800001, and NaN, which
+// the sum makes 0x7fffffff whatever its bits were, 0.
 KVP_DEV uint32_t weight_key(float x) {
   const int32_t u = __float_as_int(x + 0.f);  // -0 becomes 0
-  const uint32_t k = static_cast<uint32_t>(u) ^ (static_cast<uint32_t>(u >> 31) | 0x80000000u);
-  return x != x ? 0u : k;
+  return (static_cast<uint32_t>(u) ^ (static_cast<uint32_t>(u >> 31) | 0x80000000u)) + 1u;
 }
 
 // The entries of a prompt: positions 0 .. n_pos - 1, the recent ones last.
@@ -69,10 +73,30 @@ struct DenseEvict {
     for (int j = 0; j < 4; ++j) k[j] = i + j < end ? weight_key(row[(i + j) * stride_t]) : kNoKey;
     return max(0, min(i + 4, e) - max(i, end));
   }
-  KVP_DEV void put4(int i, int e, const uint32_t (&k)[4], const bool (&stays)[4]) const {
+  // the same for entries base + u kStep + 4 thread .. + 3 of each u, loads before what uses them
+  KVP_DEV uint32_t keys_of(int base, int tid, int e, uint32_t (&k)[kBatch][4]) const {
+    uint32_t recents = 0;
+    if (loads4 && base + kBatch * kStep <= min(old, e)) {  // the whole block
+      float4 w[kBatch];
+      const float4* at = reinterpret_cast<const float4*>(row + base) + tid;
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) w[u] = at[u * (kStep / 4)];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        k[u][0] = weight_key(w[u].x), k[u][1] = weight_key(w[u].y);
+        k[u][2] = weight_key(w[u].z), k[u][3] = weight_key(w[u].w);
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) recents += keys4(base + u * kStep + 4 * tid, e, k[u]);
+    }
+    return recents;
+  }
+  KVP_DEV void put4(int i, int e, const bool (&stays)[4]) const {
+    if (i >= e) return;
     int32_t v[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = k[j] == kNoKey || stays[j] ? kNever : now;
+    for (int j = 0; j < 4; ++j) v[j] = stays[j] ? kNever : now;
     if (stores4 && i + 4 <= e) {
       *reinterpret_cast<int4*>(out + i) = make_int4(v[0], v[1], v[2], v[3]);
     } else {
@@ -110,9 +134,10 @@ struct PagedEvict {
   KVP_DEV int size() const { return n; }
   // (four slots of one page: i is a multiple of 4)
   KVP_DEV uint32_t keys4(int i, int e, uint32_t (&k)[4]) const {
-    const int page = pages[i / kPage];
 #pragma unroll
     for (int j = 0; j < 4; ++j) k[j] = kNoKey;
+    if (i >= e) return 0;
+    const int page = pages[i / kPage];
     if (page < 0 || page >= n_pages_cap) {
       record_error(status, KVP_ERR_BOUNDS);
       return 0;
@@ -142,10 +167,16 @@ struct PagedEvict {
     }
     return recents;
   }
-  KVP_DEV void put4(int i, int /*e*/, const uint32_t (&k)[4], const bool (&stays)[4]) const {
+  KVP_DEV uint32_t keys_of(int base, int tid, int e, uint32_t (&k)[kBatch][4]) const {
+    uint32_t recents = 0;
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) recents += keys4(base + u * kStep + 4 * tid, e, k[u]);
+    return recents;
+  }
+  KVP_DEV void put4(int i, int /*e*/, const bool (&stays)[4]) const {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (k[j] != kNoKey && !stays[j])
+      if (!stays[j])
         expire_pool[static_cast<int64_t>(pages[i / kPage]) * kPage + i % kPage + j] = now;
   }
 };
@@ -204,35 +235,61 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(Src src, int cl
   const bool cached = run <= kKeysCap;
   __syncthreads();
 
+  auto kept_keys = [&](int base, uint32_t (&k)[kBatch][4]) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int i = base + u * kStep + 4 * tid;
+      uint4 v = make_uint4(kNoKey, kNoKey, kNoKey, kNoKey);
+      if (i < e1) v = *reinterpret_cast<const uint4*>(keys + (i - e0));
+      k[u][0] = v.x, k[u][1] = v.y, k[u][2] = v.z, k[u][3] = v.w;
+    }
+  };
   uint32_t prefix = 0, mask = 0, left = 0, m = 0, cand = 0, recents = 0, before = 0;
   bool all = false;
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
     const uint32_t bins = pass == 2 ? 1024 : kBins;
     uint32_t mine = 0;
-    const bool from_list = pass == 2 && !cached && sh.listed <= kListCap;
-    if (from_list) {
-      for (uint32_t i = tid; i < sh.listed; i += kEvictThreads)
-        if ((keys[i] & mask) == prefix) atomicAdd(&sh.hist[pass][keys[i] & (bins - 1)], 1u);
-    }
-#pragma unroll 2
-    for (int i = from_list ? e1 : e0 + 4 * tid; i < e1; i += 4 * kEvictThreads) {
-      uint32_t k[4];
-      uint4* kept_keys = reinterpret_cast<uint4*>(keys + (i - e0));
-      if (pass == 0 || !cached) {
-        mine += src.keys4(i, e1, k);
-        if (cached) *kept_keys = make_uint4(k[0], k[1], k[2], k[3]);
-      } else {
-        const uint4 v = *kept_keys;
-        k[0] = v.x, k[1] = v.y, k[2] = v.z, k[3] = v.w;
-      }
+    if (pass == 1 && !cached) {  // the keys with the first digit, as many as there is room for
+      for (int base = e0; base < e1; base += kBatch * kStep) {
+        uint32_t k[kBatch][4], hits = 0;
+        (void)src.keys_of(base, tid, e1, k);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (k[j] == kNoKey || (k[j] & mask) != prefix) continue;
-        atomicAdd(&sh.hist[pass][(k[j] >> shift) & (bins - 1)], 1u);
-        if (pass == 1 && !cached) {
-          const uint32_t at = atomicAdd(&sh.listed, 1u);
-          if (at < kListCap) keys[at] = k[j];
+        for (int j = 0; j < 4 * kBatch; ++j)
+          if (((k[j / 4][j % 4] ^ prefix) & mask) == 0) hits |= 1u << j;
+        if (hits == 0) continue;
+        uint32_t at = atomicAdd(&sh.listed, static_cast<uint32_t>(__popc(hits)));
+        for (; hits != 0 && at < kListCap; hits &= hits - 1) {  // (few: read once more rather than picked from registers)
+          const int j = __ffs(hits) - 1;
+          uint32_t again[4];
+          (void)src.keys4(base + j / 4 * kStep + 4 * tid, e1, again);
+          keys[at++] = (j & 2) != 0 ? (j & 1) != 0 ? again[3] : again[2] : (j & 1) != 0 ? again[1] : again[0];
+        }
+      }
+      __syncthreads();
+    }
+    if (pass > 0 && !cached && sh.listed <= kListCap) {
+      for (uint32_t i = tid; i < sh.listed; i += kEvictThreads)
+        if (((keys[i] ^ prefix) & mask) == 0) atomicAdd(&sh.hist[pass][(keys[i] >> shift) & (bins - 1)], 1u);
+    } else {
+      for (int base = e0; base < e1; base += kBatch * kStep) {
+        uint32_t k[kBatch][4];
+        if (pass == 0 || !cached) mine += src.keys_of(base, tid, e1, k);
+        else kept_keys(base, k);
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const int i = base + u * kStep + 4 * tid;
+          if (base + u * kStep >= e1) break;
+          if (pass == 0) {
+            if (cached && i < e1)
+              *reinterpret_cast<uint4*>(keys + (i - e0)) = make_uint4(k[u][0], k[u][1], k[u][2], k[u][3]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) atomicAdd(&sh.hist[0][k[u][j] >> 21], 1u);
+            continue;
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (((k[u][j] ^ prefix) & mask) == 0) atomicAdd(&sh.hist[pass][(k[u][j] >> shift) & (bins - 1)], 1u);
         }
       }
     }
@@ -251,6 +308,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(Src src, int cl
         if (r < rank) equal_before[0] += v.x, equal_before[1] += v.y, equal_before[2] += v.z, equal_before[3] += v.w;
       }
     }
+    if (pass == 0 && tid == kBins / 4 - 1) c[3] = 0;  // kNoKey's
     // entries in this thread's bins and in all above: a scan over the threads from the last to the first
     const uint32_t own = c[0] + c[1] + c[2] + c[3];
     uint32_t incl = own;
@@ -297,48 +355,46 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(Src src, int cl
     before = sh.before;
   }
   // ---- who stays: the candidates above the key, and of those equal to it the first `left`
-  const bool none = m == 0;
-  const bool ranked = !none && !all && sh.equal != left;
+  const bool ranked = m != 0 && !all && sh.equal != left;
+  const uint32_t least = all ? 0u : m == 0 ? kNoKey : prefix;
   __syncthreads();  // sh.equal has been read: what follows uses the same memory
 #pragma unroll 1
-  for (int base = e0; base < e1; base += 4 * kEvictThreads) {
-    const int i = base + 4 * tid;
-    uint32_t k[4] = {kNoKey, kNoKey, kNoKey, kNoKey};
-    if (i < e1) {
-      if (cached) {
-        const uint4 v = *reinterpret_cast<const uint4*>(keys + (i - e0));
-        k[0] = v.x, k[1] = v.y, k[2] = v.z, k[3] = v.w;
-      } else {
-        (void)src.keys4(i, e1, k);
+  for (int base = e0; base < e1; base += kBatch * kStep) {
+    uint32_t k[kBatch][4];
+    if (cached) kept_keys(base, k);
+    else (void)src.keys_of(base, tid, e1, k);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int i = base + u * kStep + 4 * tid;
+      if (base + u * kStep >= e1) break;
+      bool stays[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) stays[j] = k[u][j] >= least;
+      if (ranked) {  // entries equal to the key, counted in order
+        uint32_t equal = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) equal += k[u][j] == prefix;
+        uint32_t incl = equal;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += y;
+        }
+        if (lane == 31) sh.warp_sum[warp] = incl;
+        __syncthreads();
+        uint32_t place = before + incl - equal;
+        for (int w = 0; w < kEvictWarps; ++w) {
+          const uint32_t c = sh.warp_sum[w];
+          if (w < warp) place += c;
+          before += c;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (k[u][j] == prefix) stays[j] = place++ < left;
+        __syncthreads();
       }
+      src.put4(i, e1, stays);
     }
-    bool stays[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) stays[j] = all || (!none && k[j] >= prefix);
-    if (ranked) {  // entries equal to the key, counted in order
-      uint32_t equal = 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) equal += k[j] == prefix;
-      uint32_t incl = equal;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      if (lane == 31) sh.warp_sum[warp] = incl;
-      __syncthreads();
-      uint32_t place = before + incl - equal;
-      for (int w = 0; w < kEvictWarps; ++w) {
-        const uint32_t c = sh.warp_sum[w];
-        if (w < warp) place += c;
-        before += c;
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (k[j] == prefix) stays[j] = place++ < left;
-      __syncthreads();
-    }
-    if (i < e1) src.put4(i, e1, k, stays);
   }
   if (kept != nullptr && rank == 0 && tid == 0) kept[bh] = static_cast<int32_t>(recents + m);
   if (cluster > 1) cluster_sync();  // no CTA leaves while another may still read its counts

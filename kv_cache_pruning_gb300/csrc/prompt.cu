@@ -9,28 +9,39 @@ namespace {
 // query tiles (A and B) a CTA so that the tensor cores work on one while the
 // softmax of the other runs. The tiles share their K and V: they are two query
 // heads of one kv head over the same 128 rows (G even), or 256 rows of one head
-// (G odd; the second may be past the end). Tensor memory holds S and O of both
-// (512 columns at D = 128); P, rounded to bf16, overwrites its S.
+// (G odd; the second may be past the end); a call with few tiles takes one of them
+// an item. Tensor memory holds S and O of both (512 columns at D = 128); P, rounded
+// to bf16, overwrites its S.
 //
 // Warps 0-3 and 4-7 are the softmax of A and B: a thread owns a row, so that
-// maxima and sums need no exchange. Warp 8 issues the products, warp 9 the
-// copies: K and V tiles of 128 rows through one ring. Tiles and key blocks start
-// with the sequence, so only a tile's last block is masked.
+// maxima and sums need no exchange. Warp 8 issues the products (at D = 64 those with
+// V, and warp 10 those with K), warp 9 the copies: K and V tiles of 128 rows through
+// one ring. Tiles and key blocks start with the sequence, so only a tile's last block
+// is masked.
 //
 // The reference M of a row's weights 2^(x c - M), c = scale log2 e, is its first
 // block's maximum and moves only when a later one passes it by 2^8; then the
-// softmax warps rescale O themselves (a block's S is complete only after the
-// products of the block before).
+// softmax warps rescale O themselves, once the products of the block before are
+// done (at D = 128 a block's S comes after them).
 //
 // A masked weight is 0, but 0 times an infinite or NaN value is NaN: before the
 // products of a masked block its V tile is searched and such values are zeroed.
 // Only then do the rows look them up in memory again, and add those they see.
 //
-// One CTA an SM takes work items in turn (warp 11 works them out one ahead): the
+// One CTA an SM takes work items in turn (warp 11 works them out ahead): the
 // next item's Q, K and V are on their way, and its first S is there, while the
 // softmax warps still write the last one's rows. Items go out from the longest
-// to the shortest, forwards and backwards over the CTAs by turns.
-constexpr int kInfo = 2;                    // work items ahead
+// to the shortest, forwards and backwards over the CTAs by turns. (Handed out as
+// CTAs become free instead, five prompts of 8,192 tokens together: 260 us for 255.)
+//
+// Bound: 4 D flops and an exponential for each (query, key) pair. 128 x 128 pairs
+// take the special-function units 512 cycles, and at D = 128 the tensor cores 512
+// for each of the two products. 16,384 tokens, 32/8 heads of 128: 1.38 ms, 1.59
+// PFLOP/s (84 % of the measured burst rate of a bf16 GEMM, 93 % of its sustained one),
+// at the power limit. Two threads a row with 64 logits each, for twice the warps:
+// 1,858 us for 1,529 at that stage. 8,192 tokens at D = 64: 249 us, bound by the
+// exponentials (144 us at their rate) and what is issued beside them.
+constexpr int kInfo = 2;                    // work items written down ahead of their use
 constexpr int kFlags = 4;                   // items whose flags are apart: no warp is three items ahead of another
 template <int D>
 struct AttnCfg {
@@ -40,7 +51,7 @@ struct AttnCfg {
   static constexpr int kStages = D == 128 ? 5 : 8;       // ring of K and V tiles
   // At D = 64 tensor memory has room for a third S, and the products are short: one warp issues those with K, another
   // those with V, each block's S as soon as a buffer is free (8,192 tokens, 32/8 heads: 311 us with one warp and two
-  // buffers, where it waited for every signal in turn; @@ us so).
+  // buffers, where it waited for every signal in turn; 249 us so).
   static constexpr bool kApart = D == 64;
   static constexpr int kBufs = kApart ? 3 : 2;           // buffers of S (and then P)
   static constexpr uint32_t kOCol = kBufs * kTile;       // O of A and B
@@ -660,7 +671,7 @@ kvp_status launch_attn(const PromptParams& p, int n_kv_heads, cudaStream_t st) {
     if (device <= 63) ready.fetch_or(uint64_t{1} << device, std::memory_order_relaxed);
   }
   // Two tiles an item, but where even single ones leave SMs idle: then each has less to do (509 tokens, 32/8 heads:
-  // @@ us with pairs, @@ us so).
+  // 15.2 us with pairs, 13.4 us so).
   const int64_t singles = (p.seqs.n_tok / kTile + p.seqs.n) * p.Hq;
   const int tiles = singles <= sms ? kOneTile : p.G % 2 == 0 ? kByHead : kByRow;
   const int64_t most = tiles == kOneTile  ? singles

@@ -8,7 +8,7 @@
 namespace kvp {
 namespace {
 
-constexpr int kTile = 128;       // rows of a sequence that a CTA takes
+constexpr int kTile = 128;       // rows of a sequence that one product takes
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.4426950408889634f;
 // A weight is held as 2^(x - reference - kHeadroom): sums of up to 2^20 values of any bf16 size (the reference may
@@ -49,12 +49,12 @@ struct Tile {
 KVP_DEV int seq_rows(const Seqs& s, int i, int& start) {
   start = s.start[i];
   const int end = s.start[i + 1];
-  const int len = s.len != nullptr ? s.len[i] : end - start;
-  if (start < 0 || end < start || end > s.n_tok || len < 0 || len > end - start) {
-    record_error(s.status, KVP_ERR_BOUNDS);
-    return 0;
+  if (start >= 0 && end >= start && end <= s.n_tok) {
+    const int len = s.len != nullptr ? s.len[i] : end - start;
+    if (len >= 0 && len <= end - start) return len;
   }
-  return len;
+  record_error(s.status, KVP_ERR_BOUNDS);
+  return 0;
 }
 
 // The sequences' tiles of `tile` rows from the longest work to the shortest: by their number in their sequence, the last
@@ -272,7 +272,7 @@ kvp_status check_prompt(int n_seqs, int64_t n_tok, int n_q_heads, int n_kv_heads
   if (!(scale >= 0.f) || scale > 3.402823466e38f) return KVP_ERR_INVALID;
   if (head_dim != 64 && head_dim != 128) return KVP_ERR_UNSUPPORTED;
   if (n_q_heads % n_kv_heads != 0) return KVP_ERR_INVALID;
-  if (n_q_heads > 65535 || n_tok > 0x7fffffffll) return KVP_ERR_UNSUPPORTED;
+  if (n_q_heads > 65535 || n_tok > 0x7fff0000ll) return KVP_ERR_UNSUPPORTED;  // (a tile behind the last row is an int)
   if (n_seqs > 0 && n_tok > 0 && seq_start == nullptr) return KVP_ERR_INVALID;
   if (!aligned4(seq_start) || !aligned4(seq_len)) return KVP_ERR_ALIGN;
   return KVP_OK;

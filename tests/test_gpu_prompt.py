@@ -540,6 +540,22 @@ def test_evict_no_numbers_and_infinities(kvp):
     assert torch.equal(expire.cpu(), ref.evict_dense(acc.cpu(), 1000, 50, 800)[0])
 
 
+def test_evict_ranks_every_nan_lowest(kvp):
+    # NaN of both signs and of several payloads, one class, below -inf: the first of them go last
+    bits = i32([0x7F800001, 0x7FFFFFFF, 0x7FC00000, -1, -0x400000, -0x7FFFFF])   # the last three are negative ones
+    for t in (600, 40000):
+        acc = heavy(4, 1, 1, t)
+        at = torch.arange(7, t - 20, 13, device="cuda")
+        acc[0, 0, at] = bits[torch.arange(len(at), device="cuda") % 6].view(torch.float32)
+        acc[0, 0, at + 1] = -math.inf
+        n = t - 10 - len(at)                                                     # candidates that are numbers
+        for budget in (10 + n - 3, 10 + n, 10 + n + 5):
+            expire, count = kvp.kvp_evict(acc, t - 1, budget=budget, recent=10)
+            kept = at[expire[0, 0, at] == NEVER]
+            assert int(count) == budget and int((expire == NEVER).sum()) == budget
+            assert torch.equal(kept, at[:max(0, budget - 10 - n)])
+
+
 @pytest.mark.parametrize("counts", [[[1]], [[0, 40], [700, 16]], [[3000, 5], [17, 2047]], [[9000]], [[70000, 20]]])
 @pytest.mark.parametrize("budget, recent", [(0, 0), (30, 10), (500, 64), (10**6, 5), (2, 10**6)])
 def test_evict_paged(kvp, counts, budget, recent):
