@@ -1002,6 +1002,7 @@ KVP_API kvp_status kvp_prompt_weights(int n_seqs, int64_t n_tok, int n_q_heads, 
  *            bytes serve kvp_decode_attn calls of the same sizes as well), of
  *            kvp_decode_attn_acc_workspace_bytes(...): it also holds a call's
  *            logits, 4 bytes for each query head and slot
+ * max_pages  * 16 at most 2^31 - 2^16, else KVP_ERR_UNSUPPORTED
  * Everything else: as kvp_decode_attn.
  */
 KVP_API size_t kvp_decode_attn_acc_workspace_bytes(int batch, int n_q_heads, int n_kv_heads, int head_dim,
@@ -1040,7 +1041,7 @@ KVP_API kvp_status kvp_decode_attn_acc_devpos(int batch, int n_q_heads, int n_kv
  * budget     >= 0;  recent >= 0;  now 0 .. KVP_EXPIRE_NEVER - 1
  * expire     device int32 [B, H, n_pos] (output)
  * count      device int32 [B, H] (output or NULL): entries that stay
- * B*H at most 2^24; n_pos at most 2^31 - 2^16
+ * Outputs do not overlap acc, nor each other. B*H at most 2^24; n_pos at most 2^31 - 2^16
  */
 KVP_API kvp_status kvp_evict(int batch, int n_kv_heads, int n_pos, const float* acc, int64_t stride_b,
                              int64_t stride_t, int64_t stride_h, int budget, int recent, int now, int32_t* expire,

@@ -1762,7 +1762,8 @@ __global__ void __launch_bounds__(kAccThreads) acc_kernel(const AttnParams p, co
     if constexpr (G % 4 == 0) {
 #pragma unroll
       for (int i = 0; i < G; i += 4) {
-        const float4 v = slot < n ? __ldcg(reinterpret_cast<const float4*>(at + i)) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (slot < n) v = __ldcg(reinterpret_cast<const float4*>(at + i));
         x[k][i] = v.x, x[k][i + 1] = v.y, x[k][i + 2] = v.z, x[k][i + 3] = v.w;
       }
     } else {
@@ -1918,7 +1919,8 @@ kvp_status decode_attn_impl(int batch, int n_q_heads, int n_kv_heads, int head_d
                ac ? ac->logits : nullptr,
                ac ? ac->row_ml : nullptr};
   if (ac != nullptr) {
-    // as below: pools of 2^31 rows and more do not fit the device
+    // a thread's slots past the last one are ints; and as below, pools of 2^31 rows and more do not fit the device
+    if (static_cast<int64_t>(max_pages) * kPage > 0x7fff0000) return KVP_ERR_UNSUPPORTED;
     if (static_cast<int64_t>(n_pages_cap) * kPage > 0x7fffffff) return KVP_ERR_UNSUPPORTED;
     kvp_status r;
     if (G >= 4) {
@@ -1946,11 +1948,13 @@ kvp_status decode_attn_impl(int batch, int n_q_heads, int n_kv_heads, int head_d
                    static_cast<int64_t>(n_pages_cap) * kPage <= 0x7fffffff;
   if (qt != nullptr) {
     if (mma)
-      return head_dim == 128 ? dispatch_mma<128, true, false>(p, G, grid_limit, st) : dispatch_mma<64, true, false>(p, G, grid_limit, st);
+      return head_dim == 128 ? dispatch_mma<128, true, false>(p, G, grid_limit, st)
+                             : dispatch_mma<64, true, false>(p, G, grid_limit, st);
     return head_dim == 128 ? dispatch_g<128, true>(p, G, grid_limit, st) : dispatch_g<64, true>(p, G, grid_limit, st);
   }
   if (mma)
-    return head_dim == 128 ? dispatch_mma<128, false, false>(p, G, grid_limit, st) : dispatch_mma<64, false, false>(p, G, grid_limit, st);
+    return head_dim == 128 ? dispatch_mma<128, false, false>(p, G, grid_limit, st)
+                           : dispatch_mma<64, false, false>(p, G, grid_limit, st);
   return head_dim == 128 ? dispatch_g<128, false>(p, G, grid_limit, st) : dispatch_g<64, false>(p, G, grid_limit, st);
 }
 }  // namespace

@@ -61,7 +61,8 @@ struct AttnCfg {
   static constexpr int kQOff = 0;
   static constexpr int kRingOff = 2 * kTileBytes;
   static constexpr int kBarOff = kRingOff + kStages * kTileBytes;
-  static constexpr int kBars = 2 + kStages + kPairs + 3 * kBufs + 2 + 2 * kInfo;
+  static constexpr int kSignals = kApart ? 2 * kBufs : kBufs;  // barriers that tell of S, and of O
+  static constexpr int kBars = 2 + kStages + kPairs + kBufs + 2 * kSignals + 2 + 2 * kInfo;
   static constexpr int kInfoOff = (kBarOff + kBars * 8 + 15) / 16 * 16;  // [slot]{first row, length, tile, column}
   static constexpr int kFlagOff = kInfoOff + kInfo * 16;           // tensor memory's address, abort, bad values
   static constexpr int kSmem = 1024 + kFlagOff + 8 + 8 * kFlags;
@@ -185,11 +186,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
   uint64_t* q_empty = q_full + 1;
   uint64_t* full = q_empty + 1;
   uint64_t* empty = full + C::kStages;
-  // [A, B]; where the products are issued apart, [block's number % kBufs], and o_full of every block, not the last alone
+  // [A, B], o_full of a tile's last block. Where the products are issued apart, p_full is by buffer and the others, both of
+  // every block, by tile and the number that the block has in it, % kBufs: a tile that has no blocks in some items and a
+  // tile that goes on without it meet no phases of each other's.
   uint64_t* s_full = empty + C::kPairs;
-  uint64_t* p_full = s_full + C::kBufs;
-  uint64_t* o_full = p_full + C::kBufs;
-  uint64_t* fin = o_full + C::kBufs;
+  uint64_t* o_full = s_full + C::kSignals;
+  uint64_t* p_full = o_full + C::kSignals;
+  uint64_t* fin = p_full + C::kBufs;
   uint64_t* info_full = fin + 2;
   uint64_t* info_empty = info_full + kInfo;
   int4* info = reinterpret_cast<int4*>(smem + C::kInfoOff);
@@ -202,11 +205,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
     mbar_init(q_empty, 1);
     for (int i = 0; i < C::kStages; ++i) mbar_init(&full[i], 1);
     for (int i = 0; i < C::kPairs; ++i) mbar_init(&empty[i], 1);
-    for (int x = 0; x < C::kBufs; ++x) {
+    for (int x = 0; x < C::kSignals; ++x) {
       mbar_init(&s_full[x], 1);
-      mbar_init(&p_full[x], 4);
       mbar_init(&o_full[x], 1);
     }
+    for (int x = 0; x < C::kBufs; ++x) mbar_init(&p_full[x], 4);
     mbar_init(&fin[0], 1);
     mbar_init(&fin[1], 1);
     for (int i = 0; i < kInfo; ++i) {
@@ -269,7 +272,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
     if (warp == kPlanWarp) {
       // ------------------------------------------------------------ work items
-      const TileOrder order(p.seqs, by_head ? kTile : 2 * kTile);
+      TileOrder order(p.seqs, by_head ? kTile : 2 * kTile);
       const int64_t items = static_cast<int64_t>(order.total) * cols;
       for (int i = 0;; ++i) {
         const int64_t at = static_cast<int64_t>(i) * gridDim.x + ((i & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
@@ -352,6 +355,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
       const uint32_t leader = elect_one();
       const uint32_t q0 = smem_u32(smem + C::kQOff), ring = smem_u32(smem + C::kRingOff);
       uint32_t n = 0, g = 0;         // blocks, and tiles of K and V before this item
+      uint32_t own[2] = {0, 0};      // blocks of A and of B
+      uint32_t before[3] = {0, 0, 0};  // block n - 1 - i is number before[i] >> 1 of tile before[i] & 1
+      static_assert(!C::kApart || C::kBufs == 3, "before[2] had this block's buffer");
       for (int i = 0; next_item(i, t, ok); ++i) {
         const int blocks = max(t.nA, t.nB);
         if (keys) ok = wait_all(q_full, i & 1);
@@ -363,8 +369,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
             if (!ok || j >= (x == 0 ? t.nA : t.nB)) continue;
             const uint32_t buf = n % C::kBufs;
             if (keys) {
-              if (n >= C::kBufs) ok = wait_all(&o_full[buf], (n / C::kBufs - 1) & 1);
+              const uint32_t last = before[2] >> 1;
+              if (n >= C::kBufs) ok = wait_all(&o_full[(before[2] & 1) * C::kBufs + last % C::kBufs], (last / C::kBufs) & 1);
               if (!ok) continue;
+              before[2] = before[1], before[1] = before[0], before[0] = 2 * own[x] + x;
               tc_fence_after();
               const uint64_t a = sw128_kmajor_desc(q0 + x * C::kTileBytes);
               const uint64_t b = sw128_kmajor_desc(ring + stage * C::kTileBytes);
@@ -373,7 +381,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
                 const uint64_t off = static_cast<uint64_t>(((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4);
                 mma_ss(leader, tmem + buf * kTile, a + off, b + off, idesc_bf16_f32(kTile, kTile), kk > 0);
               }
-              commit_to(leader, &s_full[buf]);
+              commit_to(leader, &s_full[x * C::kBufs + own[x] % C::kBufs]);
             } else {
               ok = wait_all(&p_full[buf], (n / C::kBufs) & 1);
               if (!ok) continue;
@@ -383,9 +391,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
               for (int ks = 0; ks < kTile / 16; ++ks)
                 mma_ts(leader, tmem + C::kOCol + x * D, tmem + buf * kTile + ks * 8, v0 + ((ks * 2048) >> 4),
                        idesc_bf16_f32(kTile, D) | kIdescBMnMajor, j > 0 || ks > 0);
-              commit_to(leader, &o_full[buf]);
+              commit_to(leader, &o_full[x * C::kBufs + own[x] % C::kBufs]);
             }
             ++n;
+            ++own[x];
           }
           if (ok) commit_to(leader, &empty[stage]);
         }
@@ -488,9 +497,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
     const float c = p.qscale;
     uint32_t g = 0, n0 = 0;     // tiles of K and V, and blocks, before this item
     uint32_t blocks = 0, items = 0;  // of this tile
-    // Where the products are issued apart: block `n` has been added to O. (The S of a later block of this tile, or its own,
-    // is there when this is asked, so block n - kBufs has: the barrier's phase is this one or the one before.)
-    auto added = [&](uint32_t n) { return wait_all(&o_full[n % C::kBufs], (n / C::kBufs) & 1); };
+    // Where the products are issued apart: the tile's block number `b` has been added to O. (Its own S, or a later one, is
+    // there when this is asked, so block b - kBufs has: the barrier's phase is this one or the one before.)
+    auto added = [&](uint32_t b) { return wait_all(&o_full[x * C::kBufs + b % C::kBufs], (b / C::kBufs) & 1); };
     for (int i = 0; next_item(i, t, ok); ++i) {
       const int nx = x == 0 ? t.nA : t.nB, tile = x == 0 ? t.tA : t.tB, head = x == 0 ? t.hA : t.hB;
       const int pos = tile * kTile + row;  // in the sequence; past its end: nothing is stored
@@ -500,7 +509,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
         // the block's number: after those of both tiles before it
         const auto number = [&](int j) { return n0 + min(j, t.nA) + min(j, t.nB) + (x == 1 && j < t.nA); };
         const uint32_t buf = C::kApart ? number(j) % C::kBufs : x;
-        ok = wait_all(&s_full[buf], (C::kApart ? number(j) / C::kBufs : blocks) & 1);
+        ok = C::kApart ? wait_all(&s_full[x * C::kBufs + blocks % C::kBufs], (blocks / C::kBufs) & 1)
+                       : wait_all(&s_full[x], blocks & 1);
         if (!ok) break;
         ++blocks;
         tc_fence_after();
@@ -553,7 +563,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
           }
           if (j > 0 && __any_sync(0xffffffffu, grow)) {
             // (else a block's S comes after the products of the tile's block before)
-            if (C::kApart) ok = added(number(j - 1));
+            if (C::kApart) ok = added(blocks - 2);  // (`blocks` counts this one)
             if (!ok) break;
             tc_fence_after();
 #pragma unroll 1
@@ -600,11 +610,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
         if (lane == 0) mbar_arrive(&p_full[buf]);
       }
       if (!ok) break;
-      const uint32_t last = n0 + min(nx - 1, t.nA) + min(nx - 1, t.nB) + (x == 1 && nx - 1 < t.nA);
       g += 2 * max(t.nA, t.nB);
       n0 += t.nA + t.nB;
       if (nx == 0) continue;
-      ok = C::kApart ? added(last) : wait_all(&o_full[x], items & 1);
+      ok = C::kApart ? added(blocks - 1) : wait_all(&o_full[x], items & 1);
       ++items;
       if (!ok) break;
       tc_fence_after();

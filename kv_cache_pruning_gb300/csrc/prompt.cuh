@@ -91,33 +91,40 @@ struct TileOrder {
     for (int i = threadIdx.x & 31; i < (s.n + 31) / 32 * 32; i += 32) sum += max(0, tiles(i, start, len) - r);
     return __reduce_add_sync(0xffffffffu, sum);
   }
-  KVP_DEV Tile find(int idx) const {  // idx < total
-    int lo = 0, hi = most, above = 0;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2, f = from(mid);
-      if (f > idx) {
-        lo = mid;
-      } else {
-        hi = mid;
-        above = f;
+  // Tile idx of the order, idx < total and no less than in the call before: the search goes on from there, so that a
+  // CTA's items together cost one walk over the sequences for each number that its tiles have.
+  int r = 0, above = 0, end = 0;  // tiles of number r are those from `above` to `end` (end 0: no call yet)
+  int base = 0, passed = 0;       // of sequence `base` on: `passed` of them lie before
+  KVP_DEV Tile find(int idx) {
+    if (idx >= end) {
+      int lo = 0, hi = end > 0 ? r : most;
+      above = end;
+      end = total;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2, f = from(mid);
+        if (f > idx) {
+          lo = mid;
+          end = f;
+        } else {
+          hi = mid;
+          above = f;
+        }
       }
+      r = lo;
+      base = passed = 0;
     }
-    Tile t{0, 0, 0, lo};
-    int left = idx - above;
     const int lane = threadIdx.x & 31;
-    for (int base = 0; base < s.n; base += 32) {
+    for (; base < s.n; base += 32) {
       int start = 0, len = 0;
-      const uint32_t has = __ballot_sync(0xffffffffu, tiles(base + lane, start, len) > lo);
+      const uint32_t has = __ballot_sync(0xffffffffu, tiles(base + lane, start, len) > r);
+      const int left = idx - above - passed;
       if (left < __popc(has)) {
         const int src = __fns(has, 0, left + 1);
-        t.seq = base + src;
-        t.start = __shfl_sync(0xffffffffu, start, src);
-        t.len = __shfl_sync(0xffffffffu, len, src);
-        break;
+        return Tile{base + src, __shfl_sync(0xffffffffu, start, src), __shfl_sync(0xffffffffu, len, src), r};
       }
-      left -= __popc(has);
+      passed += __popc(has);
     }
-    return t;
+    return Tile{0, 0, 0, r};
   }
 };
 

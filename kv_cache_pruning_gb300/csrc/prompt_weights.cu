@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) prompt_weights_kernel(cons
   if (warp >= kSumWarps) {
     if (warp == kPlanWarp) {
       // ------------------------------------------------------------ work items
-      const TileOrder order(p.seqs, 2 * kTile);
+      TileOrder order(p.seqs, 2 * kTile);
       const int64_t items = static_cast<int64_t>(order.total) * H;
       for (int i = 0;; ++i) {
         const int64_t at = static_cast<int64_t>(i) * gridDim.x + ((i & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);

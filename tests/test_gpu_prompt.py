@@ -112,6 +112,18 @@ def test_prompt_many_sequences(kvp):
     check_prompt(kvp, q, k, v, start)
 
 
+@pytest.mark.parametrize("d, g", [(128, 2), (64, 3)])
+def test_many_sequences_of_many_lengths(kvp, d, g):
+    gen = torch.Generator().manual_seed(6)
+    lens = (2.0 ** (11 * torch.rand(150, generator=gen))).int().tolist()     # 1 .. 2047, tiles of up to 16 numbers
+    lens[40:75] = [0] * 35                                                   # a whole round of lanes without rows
+    start = starts(lens)
+    q, k, v = qkv(2, start[-1], 2 * g, 2, d)
+    _, lse = check_prompt(kvp, q, k, v, start)
+    check_weights(kvp, q, k, start, lse=lse)
+    check_weights(kvp, q, k, start, lse=lse, n_last=50, by="sequence")
+
+
 @pytest.mark.parametrize("scale", [1e-3, 0.5, 3.0])
 def test_prompt_scales_and_peaks(kvp, scale):
     q, k, v = qkv(21, 500, 4, 2, 128)

@@ -25,8 +25,8 @@ def prompt(L, n_seqs=2, n=10, hq=4, h=2, d=128, q=16, qt=512, qh=128, k=16, kt=2
 @pytest.mark.parametrize("args, name", [
     (dict(n_seqs=-1), "INVALID"), (dict(n=-1), "INVALID"), (dict(hq=0), "INVALID"), (dict(h=0), "INVALID"),
     (dict(hq=5), "INVALID"), (dict(d=96), "UNSUPPORTED"), (dict(hq=65536, h=65536), "UNSUPPORTED"),
-    (dict(n=2**31), "UNSUPPORTED"), (dict(q=None), "INVALID"), (dict(k=None), "INVALID"), (dict(v=None), "INVALID"),
-    (dict(out=None), "INVALID"), (dict(start=None), "INVALID"), (dict(scale=-1.0), "INVALID"),
+    (dict(n=2**31), "UNSUPPORTED"), (dict(n=2**31 - 1), "UNSUPPORTED"), (dict(q=None), "INVALID"),
+    (dict(k=None), "INVALID"), (dict(v=None), "INVALID"), (dict(out=None), "INVALID"), (dict(start=None), "INVALID"), (dict(scale=-1.0), "INVALID"),
     (dict(scale=math.inf), "INVALID"), (dict(scale=math.nan), "INVALID"), (dict(q=8), "ALIGN"), (dict(k=24), "ALIGN"),
     (dict(v=2), "ALIGN"), (dict(out=8), "ALIGN"), (dict(qt=516), "ALIGN"), (dict(kh=4), "ALIGN"), (dict(oh=12), "ALIGN"),
     (dict(vt=0), "INVALID"), (dict(kh=0), "INVALID"), (dict(qh=-128), "INVALID"), (dict(kt=2**39), "UNSUPPORTED"),
@@ -70,7 +70,8 @@ def decode(L, fn="kvp_decode_attn_acc", B=2, hq=8, h=2, d=64, q=16, cap=4, mp=3,
     (dict(q=None), "INVALID"), (dict(remap=None), "INVALID"), (dict(acc=None), "INVALID"), (dict(acc=2), "ALIGN"),
     (dict(al=-1), "INVALID"), (dict(ab=-1), "INVALID"), (dict(ah=99), "INVALID"), (dict(ab=199), "INVALID"),
     (dict(ws=None), "WORKSPACE"), (dict(wsb=100), "WORKSPACE"), (dict(ws=8), "ALIGN"), (dict(q=8), "ALIGN"),
-    (dict(cap=2**27), "UNSUPPORTED"), (dict(B=4097, h=1, hq=1), "UNSUPPORTED"), (dict(scale=math.nan), "INVALID")])
+    (dict(cap=2**27), "UNSUPPORTED"), (dict(mp=2**27 - 1), "UNSUPPORTED"), (dict(B=4097, h=1, hq=1), "UNSUPPORTED"),
+    (dict(scale=math.nan), "INVALID")])
 def test_decode_attn_acc_refuses(L, args, name):
     assert decode(L, **args) == getattr(L, "KVP_ERR_" + name)
 
