@@ -57,8 +57,8 @@ C2 = dict(name="llama3_8b_layer", d_model=4096, n_q_heads=32, n_kv_heads=8, head
 # of layer 0 (147,229 surviving pages): (1,216,819,712 + 3,024,384) B / 147,229,
 # against 8,256 B of K, V and expire values per page. The SHA-256 of attn.cu it
 # was taken on: the figure is reported only while the kernel source is unchanged.
-ATTN_DRAM_BYTES_PER_PAGE = (1216819712 + 3024384) / 147229
-ATTN_SRC_SHA = "433f17596c74514cff7ad12db60d347959b551efb2f918cba549d1a9ab7774d6"
+ATTN_DRAM_BYTES_PER_PAGE = (1216824832 + 3079680) / 147229
+ATTN_SRC_SHA = "f296850ae3d8803ee0d3a64b7130ae990cb77858163296daf1dedb5411000d53"
 
 
 def c5_desc(w=C5):
