@@ -167,16 +167,12 @@ KVP_DEV void add_bad_values(float (&v)[32], const uint16_t* rows, int64_t stride
   }
 }
 
-// Of two lanes B apart the upper one's `lo` and the lower one's `hi` change places.
-template <int B>
-KVP_DEV void swap_parts(uint4& lo, uint4& hi, int lane) {
-  const bool up = (lane & B) != 0;
-  uint4 w = up ? lo : hi;
-  w.x = __shfl_xor_sync(0xffffffffu, w.x, B);
-  w.y = __shfl_xor_sync(0xffffffffu, w.y, B);
-  w.z = __shfl_xor_sync(0xffffffffu, w.z, B);
-  w.w = __shfl_xor_sync(0xffffffffu, w.w, B);
-  if (up) lo = w; else hi = w;
+// 16 bf16 to a 32-byte aligned address, a whole sector in one store (24 prompts, 17,365 rows, 32/8 heads of 128: stores of
+// 16 bytes, for each of which a warp's 32 rows take a pass of their own through L1, made 20 us of 253).
+KVP_DEV void store32(void* to, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
 }
 
 // What the two tiles of a work item are: two heads of a kv head, 256 rows of a head; or there is only one.
@@ -513,6 +509,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
     const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t ocol = trow + C::kOCol + x * D;
     const float c = p.qscale;
+    const bool wide = ((reinterpret_cast<uintptr_t>(p.out) | static_cast<uintptr_t>(p.ot * 2) |
+                        static_cast<uintptr_t>(p.oh * 2)) & 31u) == 0;  // rows of `out` are 32-byte aligned
     uint32_t g = 0, n0 = 0;     // tiles of K and V, and blocks, before this item
     uint32_t blocks = 0, items = 0;  // of this tile
     // Where the products are issued apart: the tile's block number `b` has been added to O. (Its own S, or a later one, is
@@ -595,21 +593,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
             }
           }
           // 2^(x c - M); where a reference is so large that its rounding counts, 2^((x - max) c - headroom)
-          const float ref = M == -INFINITY ? 0.f : M;
-          sum[0] = sum[1] = sum[2] = sum[3] = 0;
+          if (__any_sync(0xffffffffu, big)) {
+            const float off = big ? m : 0.f;
 #pragma unroll
-          for (int o = 0; o < kTile; o += 32) {
-            uint32_t w[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float a0 = s[o + 2 * i], a1 = s[o + 2 * i + 1];
-              const float e = ex2_approx(big ? fmaf(a0 - m, c, -kHeadroom) : fmaf(a0, c, -ref));
-              const float f = ex2_approx(big ? fmaf(a1 - m, c, -kHeadroom) : fmaf(a1, c, -ref));
-              sum[i & 3] = add2(sum[i & 3], pack2(e, f));
-              w[i] = bf16x2(e, f);
-            }
-            tmem_st16(scol + o / 2, w);
+            for (int k = 0; k < kTile; ++k) s[k] -= off;
           }
+          weigh_block(s, c, big ? -kHeadroom : M == -INFINITY ? 0.f : -M, scol, sum);
         }
         float l0, l1;
         unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), l0, l1);
@@ -640,33 +629,45 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
       const int64_t r = t.start + pos;
       uint16_t* out = p.out + r * p.ot + head * p.oh;
       const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll 1
-      for (int o = 0; o < D; o += 32) {
-        float v[32];
-        tmem_ld32(ocol + o, v);
+      if (!__any_sync(0xffffffffu, some || l == 0.f)) {
+        float v[D];
+        if constexpr (D == 128) tmem_ld128(ocol, v); else tmem_ld64(ocol, v);
+        const uint64_t inv2 = pack2(inv, inv);
 #pragma unroll
-        for (int k = 0; k < 32; ++k) v[k] *= inv;
-        if (l == 0.f) {  // (a value that is no number counts for nothing here)
+        for (int k = 0; k < D; k += 16) {
+          uint32_t w[8];
 #pragma unroll
-          for (int k = 0; k < 32; ++k) v[k] = 0.f;
+          for (int i = 0; i < 8; ++i) {
+            float e, f;
+            unpack2(mul2(pack2(v[k + 2 * i], v[k + 2 * i + 1]), inv2), e, f);
+            w[i] = bf16x2(e, f);
+          }
+          if (mine) {
+            if (wide) {
+              store32(out + k, w);
+            } else {
+              *reinterpret_cast<uint4*>(out + k) = make_uint4(w[0], w[1], w[2], w[3]);
+              *reinterpret_cast<uint4*>(out + k + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+          }
         }
-        if (some && mine)
-          add_bad_values(v, p.v + (t.start + t.tA * kTile) * p.vt + head / p.G * p.vh + o, p.vt, pos - t.tA * kTile);
-        // Four lanes trade parts of their rows, so that a store takes 64 bytes of 8 rows rather than 16 of 32, each a line of
-        // its own (24 prompts, 17,365 rows, 32/8 heads of 128: 253 -> 234 us).
-        uint4 u[4];
+      } else {
+#pragma unroll 1
+        for (int o = 0; o < D; o += 32) {
+          float v[32];
+          tmem_ld32(ocol + o, v);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          u[k] = make_uint4(bf16x2(v[8 * k], v[8 * k + 1]), bf16x2(v[8 * k + 2], v[8 * k + 3]),
-                            bf16x2(v[8 * k + 4], v[8 * k + 5]), bf16x2(v[8 * k + 6], v[8 * k + 7]));
-        swap_parts<1>(u[0], u[1], lane);
-        swap_parts<1>(u[2], u[3], lane);
-        swap_parts<2>(u[0], u[2], lane);
-        swap_parts<2>(u[1], u[3], lane);
-        const int part = lane & 3;  // u[k]: this part of the four lanes' row k
+          for (int k = 0; k < 32; ++k) v[k] = l == 0.f ? 0.f : v[k] * inv;  // (a value that is no number counts for nothing)
+          if (some && mine)
+            add_bad_values(v, p.v + (t.start + t.tA * kTile) * p.vt + head / p.G * p.vh + o, p.vt, pos - t.tA * kTile);
+          if (mine) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (pos - part + k < t.len) *reinterpret_cast<uint4*>(out + (k - part) * p.ot + o + 8 * part) = u[k];
+            for (int k = 0; k < 32; k += 8)
+              *reinterpret_cast<uint4*>(out + o + k) =
+                  make_uint4(bf16x2(v[k], v[k + 1]), bf16x2(v[k + 2], v[k + 3]), bf16x2(v[k + 4], v[k + 5]),
+                             bf16x2(v[k + 6], v[k + 7]));
+          }
+        }
       }
       tc_fence_before();  // O has been read: the next item's products may overwrite it once its P is there
       if (mine && p.lse != nullptr) {
