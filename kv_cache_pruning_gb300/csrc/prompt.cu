@@ -119,22 +119,25 @@ KVP_DEV void weigh_block(const float (&s)[kTile], float c, float ref, uint32_t t
   for (int i = kTile / 2 - kBehind; i < kTile / 2; ++i) finish(i);
 }
 
-// Searches row t of a V tile (swizzled boxes) for infinities and NaN (exponents of ones), and makes them zeros; if the row
-// is one of the sequence (`inside`), both tiles' flags get `tag` first.
+// Searches row t of a V tile (swizzled boxes) for infinities and NaN, which times 0 are NaN, and makes them zeros; if the
+// row is one of the sequence (`inside`), both tiles' flags get `tag` first.
 template <int D>
 KVP_DEV void clear_bad_values(uint8_t* tile, int t, bool inside, volatile int* flags, int tag) {
   using C = AttnCfg<D>;
   auto at = [&](int c) {
     return reinterpret_cast<uint4*>(tile + (c >> 3) * C::kBoxBytes + t * 128 + (((c & 7) ^ (t & 7)) << 4));
   };
-  uint32_t found = 0;
-#pragma unroll 8
+  const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+  __nv_bfloat162 found[4] = {zero, zero, zero, zero};
+#pragma unroll
   for (int c = 0; c < D / 8; ++c) {
     const uint4 w = *at(c);
-    found = __vmaxu2(__vmaxu2(found, w.x & 0x7FFF7FFFu), w.y & 0x7FFF7FFFu);  // the largest magnitudes
-    found = __vmaxu2(__vmaxu2(found, w.z & 0x7FFF7FFFu), w.w & 0x7FFF7FFFu);
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) found[i] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x[i]), zero, found[i]);
   }
-  if ((found & 0xFFFFu) < 0x7F80u && (found >> 16) < 0x7F80u) return;
+  const __nv_bfloat162 sum = __hadd2(__hadd2(found[0], found[1]), __hadd2(found[2], found[3]));
+  if (__low2float(sum) == 0.f && __high2float(sum) == 0.f) return;
   if (inside) {
     flags[0] = tag;
     flags[1] = tag;
