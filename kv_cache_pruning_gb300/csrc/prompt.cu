@@ -32,15 +32,15 @@ namespace {
 // next item's Q, K and V are on their way, and its first S is there, while the
 // softmax warps still write the last one's rows. Items go out from the longest
 // to the shortest, forwards and backwards over the CTAs by turns. (Handed out as
-// CTAs become free instead, five prompts of 8,192 tokens together: 260 us for 255.)
+// CTAs become free instead, 24 packed prompts of 17,365 tokens: 260 us for 255.)
 //
 // Bound: 4 D flops and an exponential for each (query, key) pair. 128 x 128 pairs
 // take the special-function units 512 cycles, and at D = 128 the tensor cores 512
-// for each of the two products. 16,384 tokens, 32/8 heads of 128: 1.38 ms, 1.59
-// PFLOP/s (84 % of the measured burst rate of a bf16 GEMM, 93 % of its sustained one),
+// for each of the two products. 16,384 tokens, 32/8 heads of 128: 1.36 ms, 1.62
+// PFLOP/s (86 % of the measured burst rate of a bf16 GEMM, 95 % of its sustained one),
 // at the power limit. Two threads a row with 64 logits each, for twice the warps:
-// 1,858 us for 1,529 at that stage. 8,192 tokens at D = 64: 249 us, bound by the
-// exponentials (144 us at their rate) and what is issued beside them.
+// 1,858 us for 1,529 at that stage. 8,192 tokens at D = 64: 252 us, bound by the chain
+// of a block in its softmax warp (the exponentials alone 112 us at their rate).
 constexpr int kInfo = 2;                    // work items written down ahead of their use
 constexpr int kFlags = 4;                   // items whose flags are apart: no warp is three items ahead of another
 template <int D>
@@ -51,7 +51,7 @@ struct AttnCfg {
   static constexpr int kStages = D == 128 ? 5 : 8;       // ring of K and V tiles
   // At D = 64 tensor memory has room for a third S, and the products are short: one warp issues those with K, another
   // those with V, each block's S as soon as a buffer is free (8,192 tokens, 32/8 heads: 311 us with one warp and two
-  // buffers, where it waited for every signal in turn; 249 us so).
+  // buffers, where it waited for every signal in turn; 252 us so).
   static constexpr bool kApart = D == 64;
   static constexpr int kBufs = kApart ? 3 : 2;           // buffers of S (and then P)
   static constexpr uint32_t kOCol = kBufs * kTile;       // O of A and B
@@ -710,7 +710,7 @@ kvp_status launch_attn(const PromptParams& p, int n_kv_heads, cudaStream_t st) {
     if (device <= 63) ready.fetch_or(uint64_t{1} << device, std::memory_order_relaxed);
   }
   // Two tiles an item, but where even single ones leave SMs idle: then each has less to do (509 tokens, 32/8 heads:
-  // 15.2 us with pairs, 13.4 us so).
+  // 15.2 us with pairs, 12.9 us so).
   const int64_t singles = (p.seqs.n_tok / kTile + p.seqs.n) * p.Hq;
   const int tiles = singles <= sms ? kOneTile : p.G % 2 == 0 ? kByHead : kByRow;
   const int64_t most = tiles == kOneTile  ? singles
