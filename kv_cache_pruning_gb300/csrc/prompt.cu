@@ -636,22 +636,34 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
         float v[D];
         if constexpr (D == 128) tmem_ld128(ocol, v); else tmem_ld64(ocol, v);
         const uint64_t inv2 = pack2(inv, inv);
+        // Two lanes trade halves of 32 columns, so that a store takes 64 bytes of each row (227 -> 222 us with the prompts
+        // named at store32; 2 to 4 % of short calls).
+        const bool odd = (lane & 1) != 0;
+        uint16_t* to = out - (odd ? p.ot - 16 : 0);  // this lane's half, in the row of the even one
+        const int pos0 = pos - odd;
 #pragma unroll
-        for (int k = 0; k < D; k += 16) {
-          uint32_t w[8];
+        for (int k = 0; k < D; k += 32) {
+          uint32_t w[16];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < 16; ++i) {
             float e, f;
             unpack2(mul2(pack2(v[k + 2 * i], v[k + 2 * i + 1]), inv2), e, f);
             w[i] = bf16x2(e, f);
           }
-          if (mine) {
-            if (wide) {
-              store32(out + k, w);
-            } else {
-              *reinterpret_cast<uint4*>(out + k) = make_uint4(w[0], w[1], w[2], w[3]);
-              *reinterpret_cast<uint4*>(out + k + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+          if (wide) {
+            uint32_t y0[8], y1[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? w[i] : w[8 + i], 1);
+              y0[i] = odd ? other : w[i];
+              y1[i] = odd ? w[8 + i] : other;
             }
+            if (pos0 < t.len) store32(to + k, y0);
+            if (pos0 + 1 < t.len) store32(to + p.ot + k, y1);
+          } else if (mine) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+              *reinterpret_cast<uint4*>(out + k + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
           }
         }
       } else {
