@@ -36,8 +36,8 @@ namespace {
 //
 // Bound: 4 D flops and an exponential for each (query, key) pair. 128 x 128 pairs
 // take the special-function units 512 cycles, and at D = 128 the tensor cores 512
-// for each of the two products. 16,384 tokens, 32/8 heads of 128: 1.36 ms, 1.62
-// PFLOP/s (86 % of the measured burst rate of a bf16 GEMM, 95 % of its sustained one),
+// for each of the two products. 16,384 tokens, 32/8 heads of 128: 1.33 ms, 1.66
+// PFLOP/s (88 % of the measured burst rate of a bf16 GEMM, 98 % of its sustained one),
 // at the power limit. Two threads a row with 64 logits each, for twice the warps:
 // 1,858 us for 1,529 at that stage. 8,192 tokens at D = 64: 252 us, bound by the chain
 // of a block in its softmax warp (the exponentials alone 112 us at their rate).
@@ -722,7 +722,7 @@ kvp_status launch_attn(const PromptParams& p, int n_kv_heads, cudaStream_t st) {
     if (device <= 63) ready.fetch_or(uint64_t{1} << device, std::memory_order_relaxed);
   }
   // Two tiles an item, but where even single ones leave SMs idle: then each has less to do (509 tokens, 32/8 heads:
-  // 15.2 us with pairs, 12.9 us so).
+  // 15.2 us with pairs, 12.4 us so).
   const int64_t singles = (p.seqs.n_tok / kTile + p.seqs.n) * p.Hq;
   const int tiles = singles <= sms ? kOneTile : p.G % 2 == 0 ? kByHead : kByRow;
   const int64_t most = tiles == kOneTile  ? singles
