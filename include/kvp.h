@@ -939,7 +939,9 @@ KVP_API kvp_status kvp_qk_norm_rope(int64_t n_tok, int n_q_heads, int n_k_heads,
  * seq_start  device int32 [n_seqs + 1], ascending from 0 or more to n_tok or less
  * seq_len    device int32 [n_seqs], 0 .. seq_start[s + 1] - seq_start[s], or NULL.
  *            A sequence that breaks this records KVP_ERR_BOUNDS in `status` (may
- *            be NULL) and is left out.
+ *            be NULL) and is left out, and so is one whose rows start before the
+ *            end of an earlier one's (whose own numbers are right, be it left
+ *            out for the same reason): no row is written twice.
  * scale      > 0, finite, or 0 for 1/sqrt(head_dim)
  * out        device bf16, strides as q's, rows that do not overlap (as
  *            kvp_read_block8's); it may not overlap an input

@@ -45,7 +45,7 @@ struct Tile {
   int seq, start, len, r;  // sequence, its first row and length, tile of it
 };
 
-// A sequence's rows; one that breaks the rules is recorded and has none.
+// A sequence's rows by its own numbers, or -1 where they break the rules.
 KVP_DEV int seq_rows(const Seqs& s, int i, int& start) {
   start = s.start[i];
   const int end = s.start[i + 1];
@@ -53,8 +53,7 @@ KVP_DEV int seq_rows(const Seqs& s, int i, int& start) {
     const int len = s.len != nullptr ? s.len[i] : end - start;
     if (len >= 0 && len <= end - start) return len;
   }
-  record_error(s.status, KVP_ERR_BOUNDS);
-  return 0;
+  return -1;
 }
 
 // The sequences' tiles of `tile` rows from the longest work to the shortest: by their number in their sequence, the last
@@ -63,38 +62,73 @@ struct TileOrder {
   const Seqs& s;
   int tile, total, most;
   int mine, my_start, my_len;  // with 32 sequences at most: this lane's
+  // Some sequence breaks the rules (recorded). Only then may a later one's rows start before an earlier one's end: without a
+  // step down, starts and ends ascend. So only then is each held against where the rows before it reach.
+  bool broken = false;
   KVP_DEV TileOrder(const Seqs& seqs, int tile_) : s(seqs), tile(tile_) {
-    int sum = 0, top = 0;
     const int lane = threadIdx.x & 31;
+    int sum = 0, top = 0, reach = 0;
+    bool bad = false;
     for (int i = lane; i < s.n; i += 32) {
       my_len = seq_rows(s, i, my_start);
+      bad |= my_len < 0;
       mine = (my_len + tile - 1) / tile;
       sum += mine;
       top = max(top, mine);
     }
     if (lane >= s.n) mine = my_len = my_start = 0;
+    broken = __any_sync(0xffffffffu, bad);
+    if (broken) {
+      if (lane == 0) record_error(s.status, KVP_ERR_BOUNDS);
+      sum = top = 0;
+      for (int base = 0; base < s.n; base += 32) {
+        mine = look_up(base + lane, my_start, my_len, reach);
+        sum += mine;
+        top = max(top, mine);
+      }
+    }
     total = __reduce_add_sync(0xffffffffu, sum);
     most = __reduce_max_sync(0xffffffffu, top);
   }
-  KVP_DEV int tiles(int i, int& start, int& len) const {
+  // Tiles of sequence i, this lane's of a round of 32, whose rows start at `start`: none if it breaks the rules or has rows of
+  // an earlier one's. reach: where the rows of all rounds before end, then those of this one too.
+  KVP_DEV int look_up(int i, int& start, int& len, int& reach) const {
+    start = 0;
+    len = i < s.n ? max(0, seq_rows(s, i, start)) : 0;
+    if (broken) {
+      const int lane = threadIdx.x & 31;
+      int far = len > 0 ? start + len : 0;  // the furthest end up to this lane's
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, far, o);
+        if (lane >= o) far = max(far, y);
+      }
+      int before = __shfl_up_sync(0xffffffffu, far, 1);
+      before = lane == 0 ? reach : max(before, reach);
+      reach = max(reach, __shfl_sync(0xffffffffu, far, 31));
+      if (start < before) len = 0;
+    }
+    return (len + tile - 1) / tile;
+  }
+  KVP_DEV int tiles(int i, int& start, int& len, int& reach) const {
     if (s.n <= 32) {
       start = my_start;
       len = my_len;
       return mine;
     }
-    len = i < s.n ? seq_rows(s, i, start) : 0;
-    return (len + tile - 1) / tile;
+    return look_up(i, start, len, reach);
   }
   // tiles of number r and above in their sequences
   KVP_DEV int from(int r) const {
-    int sum = 0, start, len;
-    for (int i = threadIdx.x & 31; i < (s.n + 31) / 32 * 32; i += 32) sum += max(0, tiles(i, start, len) - r);
+    int sum = 0, start, len, reach = 0;
+    for (int i = threadIdx.x & 31; i < (s.n + 31) / 32 * 32; i += 32) sum += max(0, tiles(i, start, len, reach) - r);
     return __reduce_add_sync(0xffffffffu, sum);
   }
   // Tile idx of the order, idx < total and no less than in the call before: the search goes on from there, so that a
   // CTA's items together cost one walk over the sequences for each number that its tiles have.
   int r = 0, above = 0, end = 0;  // tiles of number r are those from `above` to `end` (end 0: no call yet)
   int base = 0, passed = 0;       // of sequence `base` on: `passed` of them lie before
+  int reached = 0;                // where the rows of those before `base` end
   KVP_DEV Tile find(int idx) {
     if (idx >= end) {
       int lo = 0, hi = end > 0 ? r : most;
@@ -111,18 +145,19 @@ struct TileOrder {
         }
       }
       r = lo;
-      base = passed = 0;
+      base = passed = reached = 0;
     }
     const int lane = threadIdx.x & 31;
     for (; base < s.n; base += 32) {
-      int start = 0, len = 0;
-      const uint32_t has = __ballot_sync(0xffffffffu, tiles(base + lane, start, len) > r);
+      int start = 0, len = 0, next = reached;
+      const uint32_t has = __ballot_sync(0xffffffffu, tiles(base + lane, start, len, next) > r);
       const int left = idx - above - passed;
       if (left < __popc(has)) {
         const int src = __fns(has, 0, left + 1);
         return Tile{base + src, __shfl_sync(0xffffffffu, start, src), __shfl_sync(0xffffffffu, len, src), r};
       }
       passed += __popc(has);
+      reached = next;
     }
     return Tile{0, 0, 0, r};
   }

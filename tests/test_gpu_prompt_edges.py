@@ -1,0 +1,89 @@
+"""Calls over packed prompts at the edges of what they allow, against the restatement in 64 bits (tests/prompt_ref.py)."""
+import math
+
+import pytest
+import torch
+
+import prompt_ref as ref
+from test_gpu_prompt import i32, qkv, status
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------------------- sequences that share rows
+
+def disjoint(start, seq_len, n_tok):
+    """(first row, length) of every sequence that counts; None: its numbers break the rules, or its rows start before the end
+    of an earlier sequence's whose numbers do not."""
+    out, reach = [], 0
+    for s in ref.sequences(start, seq_len, n_tok):
+        if s is not None and s[1] > 0:
+            a, n = s
+            s = s if a >= reach else None
+            reach = max(reach, a + n)
+        out.append(s)
+    return out
+
+
+def stepping(seed, n_seqs, n_tok):
+    """Starts that mostly ascend, some steps down: sequences that break the rules, and later ones that begin in the rows of
+    earlier ones, of the same 32 and of others."""
+    gen = torch.Generator().manual_seed(seed)
+    start, top = [0], 0
+    for i in range(n_seqs):
+        if torch.rand((), generator=gen) < 0.08:
+            start.append(max(0, start[-1] - int(torch.randint(1, 200, (), generator=gen))))
+        elif torch.rand((), generator=gen) < 0.03:
+            start.append(n_tok + 7)
+            top = start[-2]
+        else:
+            at = top if start[-1] > n_tok else start[-1]
+            start.append(min(n_tok, at + int(torch.randint(0, 90, (), generator=gen))))
+    return start
+
+
+SHARED = [([0, 50, 40, 100], None), ([0, 50, 40, 100], [30, 0, 60]), ([0, 50, 40, 100], [45, 0, 60]),
+          ([40, 100, 0, 60, 90], None), ([0, 100, 20, 50, 30, 100], None), ([0, 90, 89, 89, 100], None),
+          ([0, 10, 0, 10, 0, 10], None)]
+
+
+@pytest.mark.parametrize("h, g, d", [(1, 2, 128), (2, 1, 64), (2, 4, 128), (4, 3, 64), (4, 5, 128), (8, 8, 64)])
+@pytest.mark.parametrize("case", range(len(SHARED) + 4))
+def test_no_row_is_written_twice(kvp, h, g, d, case):
+    if case < len(SHARED):
+        (start, seq_len), n = SHARED[case], 100
+    else:
+        n_seqs, n = ((20, 900), (31, 1500), (90, 3000), (400, 9000))[case - len(SHARED)]
+        start, seq_len = stepping(40 + case, n_seqs, n), None
+        if case % 2:
+            seq_len = [max(0, b - a) * 3 // 4 for a, b in zip(start, start[1:])]
+    seqs = disjoint(start, seq_len, n)
+    assert any(s is None for s in seqs)
+    q, k, v = qkv(case, n, h * g, h, d)
+    out, lse = torch.full(q.shape, 3.0, dtype=torch.bfloat16, device="cuda"), torch.full((h * g, n), -7.0, device="cuda")
+    st, lens = status(), None if seq_len is None else i32(seq_len)
+    kvp.kvp_prompt_attn(q, k, v, i32(start), seq_len=lens, out=out, lse=lse, status=st)
+    assert int(st) == kvp.KVP_ERR_BOUNDS
+    mine = torch.zeros(n, dtype=torch.bool, device="cuda")
+    for s in seqs:
+        if s is not None:
+            assert not bool(mine[s[0]:s[0] + s[1]].any())
+            mine[s[0]:s[0] + s[1]] = True
+    want, want_lse, tol, lse_tol = ref.attention(q, k, v, seqs)
+    ref.within(out[mine], want[mine], tol[mine], "out")
+    ref.within(lse[:, mine], want_lse[:, mine], lse_tol[:, mine], "lse")
+    assert bool((out[~mine] == 3.0).all()) and bool((lse[:, ~mine] == -7.0).all())
+    most = max(1, max(s[1] for s in seqs if s is not None))
+    for n_last in (0, 40):
+        want, tol = ref.weights(q, k, lse, seqs, n_last=n_last)
+        acc, by_seq = torch.full((n, h), -5.0, device="cuda"), torch.full((len(seqs), h, most), -5.0, device="cuda")
+        for a in (acc, by_seq):
+            st = status()
+            kvp.kvp_prompt_weights(q, k, i32(start), lse, seq_len=lens, n_last=n_last, acc=a, status=st)
+            assert int(st) == kvp.KVP_ERR_BOUNDS
+        ref.within(acc[mine], want[mine], tol[mine], "sums by token")
+        assert bool((acc[~mine] == -5.0).all())
+        for i, s in enumerate(seqs):
+            a, m = s or (0, 0)
+            ref.within(by_seq[i, :, :m].T, want[a:a + m], tol[a:a + m], f"sums of sequence {i}")
+            assert bool((by_seq[i, :, m:] == -5.0).all())
