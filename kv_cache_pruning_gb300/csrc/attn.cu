@@ -1803,6 +1803,7 @@ kvp_status launch_acc(const AttnParams& p, int G, const AccArgs& a, cudaStream_t
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // workspace: arrival counters [BH], then part_ml [slots, G, 2], then
 // part_acc [slots, G, D], each region starting on 16 bytes; slots = warps of
@@ -1868,7 +1869,7 @@ kvp_status decode_attn_impl(int batch, int n_q_heads, int n_kv_heads, int head_d
     return KVP_ERR_INVALID;
   if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(expire_pool) || !aligned16(out))
     return KVP_ERR_ALIGN;
-  if ((reinterpret_cast<uintptr_t>(lse) & 3u) != 0) return KVP_ERR_ALIGN;
+  if (!aligned4(lse) || !aligned4(page_table) || !aligned4(count)) return KVP_ERR_ALIGN;
   if (qt != nullptr) {
     if (qt->max_pages < 0 || qt->n_pages_cap < 0) return KVP_ERR_INVALID;
     if (static_cast<int64_t>(qt->max_pages) * kPage > 0x7fffffff) return KVP_ERR_UNSUPPORTED;
@@ -1876,6 +1877,7 @@ kvp_status decode_attn_impl(int batch, int n_q_heads, int n_kv_heads, int head_d
         qt->count == nullptr)
       return KVP_ERR_INVALID;
     if (!aligned16(qt->kq_pool) || !aligned16(qt->vq_pool) || !aligned16(qt->meta_pool)) return KVP_ERR_ALIGN;
+    if (!aligned4(qt->page_table) || !aligned4(qt->count)) return KVP_ERR_ALIGN;
   }
   const size_t need = kvp_decode_attn_workspace_bytes(batch, n_q_heads, n_kv_heads, head_dim);
   if (workspace == nullptr || workspace_bytes < need) return KVP_ERR_WORKSPACE;
@@ -2020,7 +2022,7 @@ kvp_status decode_attn_acc_impl(int batch, int n_q_heads, int n_kv_heads, int he
                                 void* workspace, size_t workspace_bytes, int32_t* status, void* stream) {
   if (remap == nullptr || acc == nullptr) return KVP_ERR_INVALID;
   if (acc_len < 0 || acc_stride_b < 0 || acc_stride_h < 0) return KVP_ERR_INVALID;
-  if ((reinterpret_cast<uintptr_t>(acc) & 3u) != 0) return KVP_ERR_ALIGN;
+  if (!aligned4(acc) || !aligned4(remap)) return KVP_ERR_ALIGN;
   if (!rows_apart({{{acc_stride_b, batch}, {acc_stride_h, n_kv_heads}, {0, 1}}}, acc_len)) return KVP_ERR_INVALID;
   const size_t need = kvp_decode_attn_acc_workspace_bytes(batch, n_q_heads, n_kv_heads, head_dim, max_pages);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return KVP_ERR_WORKSPACE;
