@@ -929,7 +929,7 @@ KVP_API kvp_status kvp_qk_norm_rope(int64_t n_tok, int n_q_heads, int n_k_heads,
  * 2^-28 or less, so that sums of any bf16 values stay in range; values below
  * 2^-98 lose precision.
  *
- * n_seqs     >= 0;  n_tok rows in all, 0 .. 2^31 - 2^16
+ * n_seqs     0 .. 2^31 - 2^16;  n_tok rows in all, 0 .. 2^31 - 2^16
  * n_q_heads  a multiple of n_kv_heads, any quotient, 65535 at most; head_dim 64 or
  *            128
  * q, k, v    device bf16, head h of row t at t*stride_t + h*stride_h elements

@@ -340,7 +340,8 @@ kvp_status check_prompt(int n_seqs, int64_t n_tok, int n_q_heads, int n_kv_heads
   if (!(scale >= 0.f) || scale > 3.402823466e38f) return KVP_ERR_INVALID;
   if (head_dim != 64 && head_dim != 128) return KVP_ERR_UNSUPPORTED;
   if (n_q_heads % n_kv_heads != 0) return KVP_ERR_INVALID;
-  if (n_q_heads > 65535 || n_tok > 0x7fff0000ll) return KVP_ERR_UNSUPPORTED;  // (a tile behind the last row is an int)
+  // (a tile behind the last row is an int, and so is a round of sequences behind the last one)
+  if (n_q_heads > 65535 || n_tok > 0x7fff0000ll || n_seqs > 0x7fff0000) return KVP_ERR_UNSUPPORTED;
   if (n_seqs > 0 && n_tok > 0 && seq_start == nullptr) return KVP_ERR_INVALID;
   if (!aligned4(seq_start) || !aligned4(seq_len)) return KVP_ERR_ALIGN;
   return KVP_OK;

@@ -37,3 +37,14 @@ def test_decode_attention_refuses_unaligned_tables(L, which):
     assert lib.kvp_decode_attn_two_tier(2, 8, 2, 64, 16, 16, 16, 16, 4, p["table"], 3, p["count"], 16, 16, 16, 4,
                                         p["table_q"], 3, p["count_q"], 5, 0.0, 16, 0, 16, 1 << 40, None,
                                         None) == L.KVP_ERR_ALIGN
+
+
+# ---------------------------------------------------------------------------- more sequences than the kernels' counters take
+
+@pytest.mark.parametrize("n_seqs", [2**31 - 2**16 + 1, 2**31 - 32, 2**31 - 1])
+def test_prompt_calls_refuse_counts_that_pass_32_bits(L, n_seqs):
+    lib = L.library()
+    assert lib.kvp_prompt_attn(n_seqs, 10, 4, 2, 128, 16, 512, 128, 16, 256, 128, 16, 256, 128, 16, None, 0.0, 16, 512, 128,
+                               None, None, None) == L.KVP_ERR_UNSUPPORTED
+    assert lib.kvp_prompt_weights(n_seqs, 10, 4, 2, 64, 16, 256, 64, 16, 128, 64, 16, None, 16, 0.0, 0, 16, -1, 2, 1, 0,
+                                  None, None) == L.KVP_ERR_UNSUPPORTED
