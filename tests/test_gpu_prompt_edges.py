@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import prompt_ref as ref
-from test_gpu_prompt import i32, qkv, status
+from test_gpu_prompt import cache_of, i32, normal, qkv, status
 
 pytestmark = pytest.mark.gpu
 
@@ -87,3 +87,27 @@ def test_no_row_is_written_twice(kvp, h, g, d, case):
             a, m = s or (0, 0)
             ref.within(by_seq[i, :, :m].T, want[a:a + m], tol[a:a + m], f"sums of sequence {i}")
             assert bool((by_seq[i, :, m:] == -5.0).all())
+
+
+# ---------------------------------------------------------------------------- decode sums of slots that share a position
+
+@pytest.mark.parametrize("g, d", [(1, 128), (2, 64), (4, 128), (8, 64)])
+@pytest.mark.parametrize("share", [2, 3, 1000])
+def test_decode_sums_of_slots_that_share_a_position(kvp, g, d, share):
+    """Neighbouring slots (of one thread's round, of one warp) and slots a thousand apart on one position. A sum of k terms
+    that are all positive rounds k times, each by 2^-24 of at most the whole; the restatement's bound has two of them."""
+    n, b, h = 2600, 1, 2
+    cache = cache_of(kvp, 31 + g, [[n, 1500]], n // 16 + 2, d, h, n + 10)
+    slot = torch.arange(cache.remap.shape[-1], device="cuda", dtype=torch.int32)
+    cache.remap[0, 0] = slot // share
+    cache.remap[0, 1] = slot % (1500 // share + 1)
+    q, acc = normal(3, b, h * g, d), torch.rand(b, h, n + 10, device="cuda")
+    want, tol = ref.decode(q, cache, n + 9, acc)
+    terms = torch.zeros_like(acc).double()
+    for j, m in enumerate((n, 1500)):
+        terms[0, j].index_add_(0, cache.remap[0, j, :m].long(), torch.ones(m, dtype=torch.float64, device="cuda"))
+    st = status()
+    out = kvp.kvp_decode_attn_acc(q, cache, n + 9, acc, status=st)
+    assert int(st) == 0
+    ref.within(out, want[0], tol[0], "out")
+    ref.within(acc, want[2], tol[2] + terms * 2.0 ** -24 * want[2], "acc")
