@@ -996,7 +996,9 @@ KVP_API kvp_status kvp_prompt_weights(int n_seqs, int64_t n_tok, int n_q_heads, 
  * are. A position outside [0, acc_len) records KVP_ERR_BOUNDS in `status` and
  * nothing is added for it. Present slots that share a position (no call here
  * makes such tables) all add to its sum, in no fixed order; else a sum takes
- * one addition a call. A sum below 2^-126 may come out 0.
+ * one addition a call. A sum below 2^-126 may come out 0. After a wait that
+ * gave up (KVP_ERR_TIMEOUT) the sums are as they were before the call, and stay so
+ * in later calls, which record it again, until the workspace is zeroed.
  *
  * remap      device int32 [B, H, max_pages*16], as kvp_compact writes it
  * acc        device fp32, position p of (b, h) at b*acc_stride_b + h*acc_stride_h

@@ -92,6 +92,7 @@ struct AttnParams {
   // accumulating kernels only
   float* logits;           // [B*H, max_pages, 16, G]: each slot's base-2 logits, -inf where it is not present
   float2* row_ml;          // [B, Hq]: each row's base-2 reference and its sum
+  int32_t* unfinished;     // nonzero: a wait gave up since the workspace was zeroed; nothing is added then
 };
 
 // A row's natural log-sum-exp from its base-2 reference m2 and its sum
@@ -103,6 +104,14 @@ template <bool kA>
 KVP_DEV void put_row(const AttnParams& p, size_t row, float m2, float l) {
   if (!kA || p.lse != nullptr) p.lse[row] = row_lse(m2, l);
   if constexpr (kA) p.row_ml[row] = make_float2(m2, l);
+}
+
+// A wait gave up: outputs of this call are unspecified. The sums that an accumulating call adds to are not its outputs
+// alone, so it leaves them as they were (logits and rows in the workspace may be those of a call before).
+template <bool kA>
+KVP_DEV void gave_up(const AttnParams& p) {
+  record_error(p.status, KVP_ERR_TIMEOUT);
+  if constexpr (kA) *static_cast<volatile int32_t*>(p.unfinished) = 1;
 }
 
 // Eight E4M3 codes (bytes of x then y, element 0 in the lowest byte) to fp32,
@@ -229,7 +238,7 @@ KVP_DEV bool merge_pieces(const AttnParams& p, int cbh, int npc, size_t s0, bool
     merge_par ^= 1u;
     if (!__all_sync(0xffffffffu, okm)) {
       if (lane == 0) {
-        record_error(p.status, KVP_ERR_TIMEOUT);
+        gave_up<kA>(p);
         (void)mbar_wait(mbar, merge_par ^ 1u);  // the two copies land before the ring is released (bounded)
       }
       __syncwarp();
@@ -656,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const AttnPara
     const bool ok = mbar_wait(&bars[st], static_cast<uint32_t>((k / kNst) & 1), nullptr, p.status);
     if (!__all_sync(0xffffffffu, ok)) {
       if (lane == 0) {
-        record_error(p.status, KVP_ERR_TIMEOUT);
+        gave_up<kA>(p);
         // let the copies this warp issued land before its shared memory can
         // go to another CTA (each wait bounded again)
         for (int kk = k; kk < n_my && kk < k + kNst; ++kk) (void)mbar_wait(&bars[kk % kNst], (kk / kNst) & 1u);
@@ -1248,7 +1257,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_mma_kernel(const AttnParams 
     const bool ok = mbar_wait(&bars[st], static_cast<uint32_t>((k / kNst) & 1), nullptr, p.status);
     if (!__all_sync(0xffffffffu, ok)) {
       if (lane == 0) {
-        record_error(p.status, KVP_ERR_TIMEOUT);
+        gave_up<kA>(p);
         // let the copies this warp issued land before its shared memory can
         // go to another CTA (each wait bounded again)
         for (int kk = k; kk < n_my && kk < k + kNst; ++kk) (void)mbar_wait(&bars[kk % kNst], (kk / kNst) & 1u);
@@ -1745,6 +1754,7 @@ __global__ void __launch_bounds__(kAccThreads) acc_kernel(const AttnParams p, co
   const int first = blockIdx.x * (kAccThreads * kAccSlots) + threadIdx.x;
   const int n = clamp_count(p.count, bh, p.max_pages);
   if (first - static_cast<int>(threadIdx.x) >= n) return;
+  const bool unfinished = __ldcg(p.unfinished) != 0;
   float m[G], inv[G];
 #pragma unroll
   for (int i = 0; i < G; ++i) {
@@ -1772,6 +1782,10 @@ __global__ void __launch_bounds__(kAccThreads) acc_kernel(const AttnParams p, co
 #pragma unroll
       for (int i = 0; i < G; ++i) x[k][i] = slot < n ? __ldcg(at + i) : -INFINITY;
     }
+  }
+  if (unfinished) {
+    if (threadIdx.x == 0) record_error(p.status, KVP_ERR_TIMEOUT);
+    return;
   }
 #pragma unroll
   for (int k = 0; k < kAccSlots; ++k) {
@@ -1919,7 +1933,9 @@ kvp_status decode_attn_impl(int batch, int n_q_heads, int n_kv_heads, int head_d
                now_dev,
                lse,
                ac ? ac->logits : nullptr,
-               ac ? ac->row_ml : nullptr};
+               ac ? ac->row_ml : nullptr,
+               // (m, l) of the last slot, which no warp has: the last one's, of the largest grid, is the one before
+               ac ? reinterpret_cast<int32_t*>(part_ml + (ws_slots(BH) - 1) * G * 2) : nullptr};
   if (ac != nullptr) {
     // a thread's slots past the last one are ints; and as below, pools of 2^31 rows and more do not fit the device
     if (static_cast<int64_t>(max_pages) * kPage > 0x7fff0000) return KVP_ERR_UNSUPPORTED;
