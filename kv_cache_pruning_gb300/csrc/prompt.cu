@@ -341,11 +341,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
           }
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) {
-          gave_up();
-          break;
-        }
+        if (!ok) break;
       }
+      if (!ok) gave_up();
       if (lane == 0 && g > 0) {
         if (ok) {  // no arrival is left on its way when the CTA ends
           ok = wait(q_empty, (i - 1) & 1);
@@ -691,7 +689,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
         p.lse[head * p.seqs.n_tok + r] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
       }
     }
-    if (!ok) gave_up();
+    if (!ok) {
+      tmem_st_wait();  // weights on their way land before tensor memory goes
+      gave_up();
+    }
   }
   tc_fence_before();
   __syncthreads();

@@ -227,11 +227,9 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) prompt_weights_kernel(cons
           }
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) {
-          gave_up();
-          break;
-        }
+        if (!ok) break;
       }
+      if (!ok) gave_up();
       if (lane == 0) {
         if (ok) {  // no arrival is left on its way when the CTA ends
           for (int k = max(0, nk - C::kKeyBufs); ok && k < nk; ++k)

@@ -120,3 +120,54 @@ def test_decode_sums_stay_where_a_wait_gave_up(kvp, libs, g, counts):
             assert call(-1) == kvp.KVP_ERR_TIMEOUT and torch.equal(acc, first)
     ws.zero_()
     assert call(-1) == 0 and torch.equal(acc, want_acc) and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("h, g, d, lens", [(2, 4, 128, [700, 900, 30]), (2, 3, 128, [900, 130, 700]), (2, 3, 64, [900, 130, 700]),
+                                           (2, 2, 64, [300, 1, 900]), (1, 1, 128, [300]), (1, 2, 64, [500])])
+def test_prompt_calls_end_where_a_wait_gave_up(kvp, libs, h, g, d, lens):
+    """Each call returns and says so (or is right: a wait at a CTA's end, for what is on its way to the CTA itself), and the
+    next one is right. One tile an item and two, of two heads and of two tiles."""
+    lens = lens * (30 if len(lens) > 1 else 1)
+    start = [0]
+    for n in lens:
+        start.append(start[-1] + n)
+    n, hq, start = start[-1], h * g, i32(start)
+    q, k, v = (x.contiguous() for x in qkv(6, n, hq, h, d))
+    want, want_lse = torch.empty_like(q), torch.empty(hq, n, device="cuda")
+    kvp.kvp_prompt_attn(q, k, v, start, out=want, lse=want_lse)
+    st, out, lse = status(), torch.empty_like(q), torch.empty_like(want_lse)
+
+    def attend(at):
+        st.zero_()
+        assert libs["prompt"].set_give_up(at) == 0
+        assert libs["prompt"].kvp_prompt_attn(
+            len(lens), n, hq, h, d, q.data_ptr(), *q.stride()[:2], k.data_ptr(), *k.stride()[:2], v.data_ptr(),
+            *v.stride()[:2], start.data_ptr(), None, 0.0, out.data_ptr(), *out.stride()[:2], lse.data_ptr(), st.data_ptr(),
+            stream()) == kvp.KVP_OK
+        torch.cuda.synchronize()
+        return int(st)
+
+    def weigh(at, n_last, acc):
+        st.zero_()
+        assert libs["prompt_weights"].set_give_up(at) == 0
+        assert libs["prompt_weights"].kvp_prompt_weights(
+            len(lens), n, hq, h, d, q.data_ptr(), *q.stride()[:2], k.data_ptr(), *k.stride()[:2], start.data_ptr(), None,
+            want_lse.data_ptr(), 0.0, n_last, acc.data_ptr(), -1, *acc.stride(), 0, st.data_ptr(), stream()) == kvp.KVP_OK
+        torch.cuda.synchronize()
+        return int(st)
+
+    assert attend(-1) == 0 and torch.equal(out, want) and torch.equal(lse, want_lse)
+    waits = libs["prompt"].get_waits()
+    assert waits > 20
+    for at in [0, 1, 5, waits // 3, waits // 2, 2 * waits // 3, waits - 2, waits - 1]:
+        code = attend(at)
+        assert code == kvp.KVP_ERR_TIMEOUT or at > 0 and code == 0 and torch.equal(out, want) and torch.equal(lse, want_lse), at
+    assert attend(-1) == 0 and torch.equal(out, want) and torch.equal(lse, want_lse)
+    for n_last in (0, 40):
+        want_acc, acc = kvp.kvp_prompt_weights(q, k, start, want_lse, n_last=n_last), torch.zeros(n, h, device="cuda")
+        assert weigh(-1, n_last, acc) == 0 and torch.equal(acc, want_acc)
+        waits = libs["prompt_weights"].get_waits()
+        for at in [0, 1, 5, waits // 3, waits // 2, 2 * waits // 3, waits - 2, waits - 1]:
+            code = weigh(at, n_last, acc.zero_())
+            assert code == kvp.KVP_ERR_TIMEOUT or at > 0 and code == 0 and torch.equal(acc, want_acc), at
+        assert weigh(-1, n_last, acc) == 0 and torch.equal(acc, want_acc)
