@@ -355,6 +355,7 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) prompt_weights_kernel(cons
     uint32_t n = 0;
     for (int i = 0;; ++i) {
       const bool more = next_item(i, t, ok);
+      if (!ok) gave_up();  // before the barrier: the other warp may be waiting for what does not come now
       if (named_bar_or(pair, 64, !ok)) {
         ok = false;
         break;
@@ -421,6 +422,7 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) prompt_weights_kernel(cons
       // the two halves of the key's sum meet (the next item's after both have come past its barrier)
       float sum = total + (fabsf(lost) < INFINITY ? lost : 0.f);
       if (half == 1) *xch = sum;
+      if (!ok) gave_up();
       if (named_bar_or(pair, 64, !ok)) {
         ok = false;
         break;
@@ -436,7 +438,6 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) prompt_weights_kernel(cons
         }
       }
     }
-    if (!ok) gave_up();
   }
   tc_fence_before();
   __syncthreads();

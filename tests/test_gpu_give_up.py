@@ -5,6 +5,7 @@ gave up: no barrier is left without its arrival, and nothing waits for longer th
 import concurrent.futures
 import ctypes
 import subprocess
+import time
 
 import pytest
 import torch
@@ -160,7 +161,9 @@ def test_prompt_calls_end_where_a_wait_gave_up(kvp, libs, h, g, d, lens):
     waits = libs["prompt"].get_waits()
     assert waits > 20
     for at in [0, 1, 5, waits // 3, waits // 2, 2 * waits // 3, waits - 2, waits - 1]:
+        before = time.monotonic()
         code = attend(at)
+        assert time.monotonic() - before < 1.5
         assert code == kvp.KVP_ERR_TIMEOUT or at > 0 and code == 0 and torch.equal(out, want) and torch.equal(lse, want_lse), at
     assert attend(-1) == 0 and torch.equal(out, want) and torch.equal(lse, want_lse)
     for n_last in (0, 40):
@@ -168,6 +171,8 @@ def test_prompt_calls_end_where_a_wait_gave_up(kvp, libs, h, g, d, lens):
         assert weigh(-1, n_last, acc) == 0 and torch.equal(acc, want_acc)
         waits = libs["prompt_weights"].get_waits()
         for at in [0, 1, 5, waits // 3, waits // 2, 2 * waits // 3, waits - 2, waits - 1]:
+            before = time.monotonic()
             code = weigh(at, n_last, acc.zero_())
+            assert time.monotonic() - before < 1.5                # one wait gave up: no other runs to the limit of two seconds
             assert code == kvp.KVP_ERR_TIMEOUT or at > 0 and code == 0 and torch.equal(acc, want_acc), at
         assert weigh(-1, n_last, acc) == 0 and torch.equal(acc, want_acc)
