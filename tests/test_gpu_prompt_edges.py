@@ -111,3 +111,59 @@ def test_decode_sums_of_slots_that_share_a_position(kvp, g, d, share):
     assert int(st) == 0
     ref.within(out, want[0], tol[0], "out")
     ref.within(acc, want[2], tol[2] + terms * 2.0 ** -24 * want[2], "acc")
+
+
+# ---------------------------------------------------------------------------- queries that pay nothing, whatever they hold
+
+def padded_queries(q, lse, rows, bad):
+    """Queries that a caller leaves out, by a log-sum-exp of -inf, and that hold what padding may."""
+    q, lse = q.clone(), lse.clone()
+    q[rows] = bad
+    lse[:, rows] = -math.inf
+    return q, lse
+
+
+@pytest.mark.parametrize("h, g, d", [(2, 4, 128), (1, 3, 64), (3, 1, 128), (1, 7, 64)])
+@pytest.mark.parametrize("n_last", [0, 7, 40, 64, 65, 300])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_queries_that_pay_nothing_may_hold_anything(kvp, h, g, d, n_last, bad):
+    lens = [700, 130, 1, 260]
+    start = [0, 700, 830, 831, 1091]
+    q, k, _ = (x.contiguous() for x in qkv(5, 1091, h * g, h, d))
+    seqs = ref.sequences(start, None, 1091)
+    lse = ref.attention(q, k, k, seqs)[1].float()
+    rows = torch.tensor([3, 127, 128, 300, 301, 302, 690, 699, 828, 829, 900, 1000, 1085], device="cuda")
+    rows = torch.cat([rows, torch.arange(384, 512, device="cuda")])            # a whole tile of queries
+    q2, lse2 = padded_queries(q, lse, rows, bad)
+    # what they pay is 0 by the definition, whatever their logits are: as if they were finite
+    want, tol = ref.weights(q, k, lse2, seqs, n_last=n_last)
+    st, acc = status(), torch.full((1091, h), -5.0, device="cuda")
+    kvp.kvp_prompt_weights(q2, k, i32(start), lse2, n_last=n_last, acc=acc, status=st)
+    assert int(st) == 0
+    ref.within(acc, want, tol, "sums")
+    # one head's query alone, and keys that are no number: those keys' sums are, the others' are not touched
+    lse3, q3, k3 = lse.clone(), q.clone(), k.clone()
+    lse3[0, 699], q3[699, 0], k3[10, 0] = -math.inf, bad, math.nan
+    k3f = k.clone()
+    k3f[10, 0] = 0.0
+    want, tol = ref.weights(q, k3f, lse3, seqs, n_last=n_last)
+    acc = kvp.kvp_prompt_weights(q3, k3, i32(start), lse3, n_last=n_last)
+    paid = torch.arange(700, device="cuda") >= (700 - n_last if n_last else 0)
+    paid[699] = g > 1                                                          # some head's query still looks at key 10
+    assert bool(torch.isnan(acc[10, 0])) == bool(paid[10:].any())
+    other = torch.ones_like(acc, dtype=torch.bool)
+    other[10, 0] = False
+    ref.within(acc[other], want[other], tol[other], "sums beside a key that is no number")
+
+
+def test_an_infinite_normaliser_is_no_mark(kvp):
+    """exp(x - inf) is 0 for a finite logit and no number for a NaN or infinite one: only -inf leaves a query out."""
+    q, k, _ = (x.contiguous() for x in qkv(6, 300, 2, 1, 64))
+    lse = ref.attention(q, k, k, [(0, 300)])[1].float()
+    lse[:, 200] = math.inf
+    want, tol = ref.weights(q, k, lse, [(0, 300)])
+    ref.within(kvp.kvp_prompt_weights(q, k, i32([0, 300]), lse), want, tol, "sums")
+    q[200, 0] = math.nan
+    got = kvp.kvp_prompt_weights(q, k, i32([0, 300]), lse)
+    assert bool(torch.isnan(got[:201]).all())
+    ref.within(got[201:], want[201:], tol[201:], "sums of the keys after it")
