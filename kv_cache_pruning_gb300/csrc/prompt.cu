@@ -671,7 +671,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) prompt_attn_kernel(const Prom
           tmem_ld32(ocol + o, v);
 #pragma unroll
           for (int k = 0; k < 32; ++k) v[k] = l == 0.f ? 0.f : v[k] * inv;  // (a value that is no number counts for nothing)
-          if (some && mine)
+          if (some && mine && l != 0.f)  // (a row without a finite logit is zero, whatever it sees)
             add_bad_values(v, p.v + (t.start + t.tA * kTile) * p.vt + head / p.G * p.vh + o, p.vt, pos - t.tA * kTile);
           if (mine) {
 #pragma unroll

@@ -167,3 +167,24 @@ def test_an_infinite_normaliser_is_no_mark(kvp):
     got = kvp.kvp_prompt_weights(q, k, i32([0, 300]), lse)
     assert bool(torch.isnan(got[:201]).all())
     ref.within(got[201:], want[201:], tol[201:], "sums of the keys after it")
+
+
+# ---------------------------------------------------------------------------- rows without a finite logit
+
+@pytest.mark.parametrize("h, g, d, repeat", [(1, 2, 128, 1), (2, 4, 128, 12), (1, 3, 128, 40), (1, 3, 64, 40), (2, 2, 64, 20)])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_rows_without_a_finite_logit_see_no_value(kvp, h, g, d, repeat, bad):
+    """Such a row is zero with lse -inf wherever a value that is no number lies: in its own tile of keys or in one before."""
+    n = 300
+    start = [n * i for i in range(repeat + 1)]
+    q, k, v = (x.contiguous() for x in qkv(45, n * repeat, h * g, h, d))
+    q.copy_(q.abs())
+    at = torch.arange(n * repeat, device="cuda") % n
+    k[at < 290, :, 0] = -math.inf                            # rows 0 .. 289 see nothing finite, the last ten see the last keys
+    for row, col in ((5, 3), (130, 4), (270, 5), (280, 6), (289, 7)):
+        v[at == row, :, col] = bad
+    st, lse = status(), torch.empty(h * g, n * repeat, device="cuda")
+    out = kvp.kvp_prompt_attn(q, k, v, i32(start), lse=lse, status=st)
+    assert int(st) == 0
+    assert bool((out[at < 290] == 0).all()) and bool((lse[:, at < 290] == -math.inf).all())
+    assert bool(torch.isfinite(lse[:, at >= 290]).all())
