@@ -942,7 +942,7 @@ KVP_API kvp_status kvp_qk_norm_rope(int64_t n_tok, int n_q_heads, int n_k_heads,
  *            be NULL) and is left out, and so is one whose rows start before the
  *            end of an earlier one's (whose own numbers are right, be it left
  *            out for the same reason): no row is written twice.
- * scale      > 0, finite, or 0 for 1/sqrt(head_dim)
+ * scale      > 0, at most 2^127, or 0 for 1/sqrt(head_dim)
  * out        device bf16, strides as q's, rows that do not overlap (as
  *            kvp_read_block8's); it may not overlap an input
  * lse        device fp32 [n_q_heads, n_tok] (output; a head's rows side by side),

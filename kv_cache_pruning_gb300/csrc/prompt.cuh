@@ -338,6 +338,7 @@ kvp_status check_prompt(int n_seqs, int64_t n_tok, int n_q_heads, int n_kv_heads
                         const int32_t* seq_start, const int32_t* seq_len, float scale) {
   if (n_seqs < 0 || n_tok < 0 || n_q_heads <= 0 || n_kv_heads <= 0) return KVP_ERR_INVALID;
   if (!(scale >= 0.f) || scale > 3.402823466e38f) return KVP_ERR_INVALID;
+  if (scale > 0x1p127f) return KVP_ERR_UNSUPPORTED;  // times log2 e it would be infinite, and 0 times that NaN
   if (head_dim != 64 && head_dim != 128) return KVP_ERR_UNSUPPORTED;
   if (n_q_heads % n_kv_heads != 0) return KVP_ERR_INVALID;
   // (a tile behind the last row is an int, and so is a round of sequences behind the last one)

@@ -48,3 +48,17 @@ def test_prompt_calls_refuse_counts_that_pass_32_bits(L, n_seqs):
                                None, None, None) == L.KVP_ERR_UNSUPPORTED
     assert lib.kvp_prompt_weights(n_seqs, 10, 4, 2, 64, 16, 256, 64, 16, 128, 64, 16, None, 16, 0.0, 0, 16, -1, 2, 1, 0,
                                   None, None) == L.KVP_ERR_UNSUPPORTED
+
+
+# ---------------------------------------------------------------------------- a scale whose product with log2 e is no number
+
+@pytest.mark.parametrize("scale, name", [(1.1 * 2.0 ** 127, "UNSUPPORTED"), (3.4e38, "UNSUPPORTED"), (2.0 ** 127, "CUDA")])
+def test_prompt_calls_refuse_scales_that_overflow(L, scale, name):
+    import torch
+    if name == "CUDA" and torch.cuda.is_available():
+        pytest.skip("reaches the device")
+    lib = L.library()
+    assert lib.kvp_prompt_attn(2, 10, 4, 2, 128, 16, 512, 128, 16, 256, 128, 16, 256, 128, 16, None, scale, 16, 512, 128,
+                               None, None, None) == getattr(L, "KVP_ERR_" + name)
+    assert lib.kvp_prompt_weights(2, 10, 4, 2, 64, 16, 256, 64, 16, 128, 64, 16, None, 16, scale, 0, 16, -1, 2, 1, 0,
+                                  None, None) == getattr(L, "KVP_ERR_" + name)
