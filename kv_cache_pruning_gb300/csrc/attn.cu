@@ -1625,28 +1625,31 @@ __global__ void __launch_bounds__(kThreads, 1) attn_mma_kernel(const AttnParams 
   }
 }
 
-// Grid of the persistent kernel on this process's device: one CTA per SM
-// times the CTAs an SM holds, computed once (with the shared-memory opt-in).
-template <int D, int G, bool kQ, bool kA>
-int attn_grid() {
-  static const int grid = [] {
-    using C = AttnCfg<D, G>;
-    auto kern = attn_decode_kernel<D, G, kQ, kA>;
-    int dev = 0, nsm = 0, occ = 0;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess ||
-        cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kern, kThreads, C::SMEM) != cudaSuccess || occ <= 0)
-      return 0;
-    return nsm * occ < kMaxCtas ? nsm * occ : kMaxCtas;
-  }();
+// Grid of a persistent kernel on the current device: one CTA per SM times the CTAs
+// an SM holds (0 where that cannot be asked), with the shared-memory opt-in, which
+// is a property of the kernel on each device. Worked out once for each, and kept in
+// `known` once it has succeeded.
+template <typename Kern>
+int persistent_grid(Kern kern, int smem, std::atomic<int> (&known)[64]) {
+  int device = 0, occ = 0, grid = 0;
+  const int sms = current_sms(&device);
+  if (sms == 0) return 0;
+  if (device < 64 && (grid = known[device].load(std::memory_order_relaxed)) != 0) return grid;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kern, kThreads, smem) != cudaSuccess || occ <= 0) {
+    (void)cudaGetLastError();
+    return 0;
+  }
+  grid = sms * occ < kMaxCtas ? sms * occ : kMaxCtas;
+  if (device < 64) known[device].store(grid, std::memory_order_relaxed);
   return grid;
 }
 
 template <int D, int G, bool kQ, bool kA>
 kvp_status launch_attn(const AttnParams& p, int grid_limit, cudaStream_t st) {
   using C = AttnCfg<D, G>;
-  int grid = attn_grid<D, G, kQ, kA>();
+  static std::atomic<int> known[64];
+  int grid = persistent_grid(attn_decode_kernel<D, G, kQ, kA>, C::SMEM, known);
   if (grid <= 0) return KVP_ERR_CUDA;
   if (grid_limit > 0 && grid > grid_limit) grid = grid_limit;
   if (launch_pdl(attn_decode_kernel<D, G, kQ, kA>, dim3(grid), dim3(kThreads), C::SMEM, st, p) != cudaSuccess)
@@ -1655,26 +1658,11 @@ kvp_status launch_attn(const AttnParams& p, int grid_limit, cudaStream_t st) {
 }
 
 template <int D, int G, bool kQ, bool kA>
-int attn_mma_grid() {
-  static const int grid = [] {
-    using C = MmaCfg<D, kA>;
-    auto kern = attn_mma_kernel<D, G, kQ, kA>;
-    int dev = 0, nsm = 0, occ = 0;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess ||
-        cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kern, kThreads, C::SMEM) != cudaSuccess || occ <= 0)
-      return 0;
-    return nsm * occ < kMaxCtas ? nsm * occ : kMaxCtas;
-  }();
-  return grid;
-}
-
-template <int D, int G, bool kQ, bool kA>
 kvp_status launch_attn_mma(const AttnParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV,
                            const CUtensorMap& tmKq, const CUtensorMap& tmVq, int grid_limit, cudaStream_t st) {
   using C = MmaCfg<D, kA>;
-  int grid = attn_mma_grid<D, G, kQ, kA>();
+  static std::atomic<int> known[64];
+  int grid = persistent_grid(attn_mma_kernel<D, G, kQ, kA>, C::SMEM, known);
   if (grid <= 0) return KVP_ERR_CUDA;
   if (grid_limit > 0 && grid > grid_limit) grid = grid_limit;
   if (launch_pdl(attn_mma_kernel<D, G, kQ, kA>, dim3(grid), dim3(kThreads), C::SMEM, st, p, tmK, tmV, tmKq, tmVq) !=
