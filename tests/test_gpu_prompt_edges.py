@@ -188,3 +188,22 @@ def test_rows_without_a_finite_logit_see_no_value(kvp, h, g, d, repeat, bad):
     assert int(st) == 0
     assert bool((out[at < 290] == 0).all()) and bool((lse[:, at < 290] == -math.inf).all())
     assert bool(torch.isfinite(lse[:, at >= 290]).all())
+
+
+# ---------------------------------------------------------------------------- sums beside pages that are not there
+
+@pytest.mark.parametrize("g, d", [(1, 64), (2, 128), (4, 64), (8, 128)])
+def test_decode_sums_beside_bad_pages(kvp, g, d):
+    """A page whose number is out of range counts as empty: its slots' sums stay, the others' are those of the rest."""
+    cache = cache_of(kvp, 5, [[100, 100], [700, 40]], 44, d, 2, 760, expired=0.1)
+    cache.page_table[0, 0, 2], cache.page_table[0, 1, 0], cache.page_table[1, 0, 30] = cache.n_pages_cap, -5, 2**31 - 1
+    cache.page_table[1, 1, :3] = -1
+    q, acc, st = normal(6, 2, 2 * g, d), torch.rand(2, 2, 800, device="cuda"), status()
+    before = acc.clone()
+    want, tol = ref.decode(q, cache, 759, acc)
+    lse = torch.empty(2, 2 * g, device="cuda")
+    out = kvp.kvp_decode_attn_acc(q, cache, 759, acc, lse=lse, status=st)
+    assert int(st) == kvp.KVP_ERR_BOUNDS
+    for got, w, e, name in zip((out, lse, acc), want, tol, ("out", "lse", "acc")):
+        ref.within(got, w, e, name)
+    assert torch.equal(acc[1, 1], before[1, 1]) and bool((out[1, g:] == 0).all())
