@@ -28,10 +28,10 @@ namespace {
 // Warps 0-7 and 8-15 sum for A and B, warp 16 issues the products, warp 17
 // copies, warp 18 brings the normalisers, warp 19 works out items ahead.
 //
-// A query whose lse is -inf pays nothing, whatever its logits are: an addend of -inf
-// sees to that while they are finite. Where a sum is no number the tile is summed
-// again without such columns, which come with the normalisers, a bit for each. (With
-// the bits looked at before each tile: 261 us for 251, and 198 for 185 with 64 heads.)
+// A query whose lse is -inf pays nothing, whatever its logits are: its addend is the
+// lowest number, which sees to that while they are finite. Where a sum is no number
+// the tile is summed again without the columns of that addend. (With a bit for each such
+// column, looked at before each tile: 261 us for 251, and 198 for 185 with 64 heads.)
 
 // The warp that brings the normalisers reads kAhead tiles on, which may be as many items, before it writes the first of
 // them, and no item's place is taken again before every warp has read it.
@@ -52,8 +52,7 @@ struct WeightsCfg {
   static constexpr int kRingOff = 2 * kKeyBufs * kTileBytes;
   static constexpr int kLseOff = kRingOff + kStages * kTileBytes;  // normalisers of each buffer of S
   static constexpr int kXchOff = kLseOff + 2 * kTile * 4;          // a sum for each key
-  static constexpr int kNilOff = kXchOff + 2 * kTile * 4;          // a bit for each column of each buffer of S that pays nothing
-  static constexpr int kBarOff = kNilOff + 2 * kTile / 8;
+  static constexpr int kBarOff = kXchOff + 2 * kTile * 4;
   static constexpr int kBars = 2 * kStages + 2 * kKeyBufs + 8 + 1 + 2 * kItems;
   static constexpr int kInfoOff = (kBarOff + kBars * 8 + 15) / 16 * 16;  // [slot]{sequence, first row, length, head}, {pair}
   static constexpr int kFlagOff = kInfoOff + kItems * 32;                // tensor memory's address, abort
@@ -70,7 +69,8 @@ struct WeightsMaps {
   CUtensorMap q, k;  // [D, heads, rows], boxes of 64 x 1 x QB and 64 x 1 x 128
 };
 
-enum Columns { kWhole, kCut, kNil };   // which columns of a tile are left out
+enum Columns { kWhole, kCut, kMarked };             // which columns of a tile are left out
+constexpr float kPaysNothing = -3.402823466e38f;    // addend of a column whose lse is -inf
 
 template <int D, int QB>
 __global__ void __launch_bounds__(kWeightsThreads, 1) prompt_weights_kernel(const PromptParams p,
@@ -279,13 +279,8 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) prompt_weights_kernel(cons
         if (g >= 2) ok = wait_all(&s_empty[buf], ((g >> 1) - 1) & 1);
         if (!ok) return;
         float* to = reinterpret_cast<float*>(smem + C::kLseOff) + buf * kTile;
-        uint32_t* nil = reinterpret_cast<uint32_t*>(smem + C::kNilOff) + buf * (kTile / 32);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          to[lane + 32 * k] = v[k] == -INFINITY ? v[k] : -v[k] * kLog2e;
-          const uint32_t bits = __ballot_sync(0xffffffffu, v[k] == -INFINITY);
-          if (lane == 0) nil[k] = bits;
-        }
+        for (int k = 0; k < 4; ++k) to[lane + 32 * k] = v[k] == -INFINITY ? kPaysNothing : -v[k] * kLog2e;
         __syncwarp();
         if (lane == 0) mbar_arrive(&lse_full[buf]);
         ++g;
@@ -361,7 +356,6 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) prompt_weights_kernel(cons
     const int x = warp >> 3, half = (warp >> 2) & 1, quad = warp & 3, row = quad * 32 + lane;
     const uint32_t scol = tmem + (static_cast<uint32_t>(quad * 32) << 16) + 2 * x * kTile + half * 64;
     const float* lse = reinterpret_cast<const float*>(smem + C::kLseOff) + half * 64;
-    const uint2* nil = reinterpret_cast<const uint2*>(smem + C::kNilOff) + half;
     float* xch = reinterpret_cast<float*>(smem + C::kXchOff) + x * kTile + row;
     const uint64_t c2 = pack2(p.qscale, p.qscale);
     const int pair = 1 + x * 4 + quad;  // named barrier of the two warps of a key, which leave together
@@ -386,7 +380,7 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) prompt_weights_kernel(cons
             tc_fence_after();
             const int q0 = t.q0(qi);
             uint64_t sum[4] = {0, 0, 0, 0};
-            // kCut: a tile with columns that this key does not see, or that are no query; kNil: that pay nothing too. They
+            // kCut: a tile with columns that this key does not see, or that are no query; kMarked: that pay nothing too. They
             // count for nothing, whatever their logits and normalisers are.
             auto add_up = [&](auto how) {
               constexpr int kHow = decltype(how)::value;
@@ -399,18 +393,22 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) prompt_weights_kernel(cons
                 // columns o + k with from <= k < to are queries that see the key
                 const int first = QB == kTile ? half * 64 + o : 0;
                 const int from = pos - q0 - first, to = t.len - q0 - first;
-                uint32_t leave = 0;
-                if constexpr (kHow == kNil) leave = o == 0 ? nil[buf * 2].x : nil[buf * 2].y;
 #pragma unroll
                 for (int k = 0; k < 32; k += 4) {
                   const float4 r = to_add[k / 4];
                   float e[4];
                   unpack2(fma2(pack2(s[k], s[k + 1]), c2, pack2(r.x, r.y)), e[0], e[1]);
                   unpack2(fma2(pack2(s[k + 2], s[k + 3]), c2, pack2(r.z, r.w)), e[2], e[3]);
+                  if constexpr (kHow == kMarked) {
+                    const float mark[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                      if (mark[j] == kPaysNothing) e[j] = -INFINITY;
+                  }
                   if constexpr (kHow != kWhole) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                      if (k + j < from || k + j >= to || (kHow == kNil && (leave >> (k + j) & 1u) != 0)) e[j] = -INFINITY;
+                      if (k + j < from || k + j >= to) e[j] = -INFINITY;
                   }
                   sum[k / 2 & 3] = add2(sum[k / 2 & 3], pack2(ex2_approx(e[0]), ex2_approx(e[1])));
                   sum[(k / 2 + 1) & 3] = add2(sum[(k / 2 + 1) & 3], pack2(ex2_approx(e[2]), ex2_approx(e[3])));
@@ -430,7 +428,7 @@ __global__ void __launch_bounds__(kWeightsThreads, 1) prompt_weights_kernel(cons
             total_of();
             if (__any_sync(0xffffffffu, !(a < INFINITY))) {
               sum[0] = sum[1] = sum[2] = sum[3] = 0;
-              add_up(std::integral_constant<int, kNil>{});
+              add_up(std::integral_constant<int, kMarked>{});
               total_of();
             }
             // total + a exactly: the rounded sum, and the rest kept apart
