@@ -207,3 +207,41 @@ def test_decode_sums_beside_bad_pages(kvp, g, d):
     for got, w, e, name in zip((out, lse, acc), want, tol, ("out", "lse", "acc")):
         ref.within(got, w, e, name)
     assert torch.equal(acc[1, 1], before[1, 1]) and bool((out[1, g:] == 0).all())
+
+
+# ---------------------------------------------------------------------------- rows that share a warp
+
+@pytest.mark.parametrize("h, g, d, repeat", [(1, 2, 128, 1), (1, 2, 64, 1), (2, 4, 128, 12), (2, 3, 128, 24), (2, 3, 64, 24)])
+@pytest.mark.parametrize("what", ["large", "nan", "first"])
+def test_what_lies_behind_a_sequence_changes_no_bit(kvp, h, g, d, repeat, what):
+    """The rows behind a sequence's last one share its tile. Logits of the last rows rise in their second block of keys by
+    2^8 to 2^15 over the first's, where a row may keep its reference or move it; what they do is theirs alone."""
+    n, gap = 200, 56
+    start = [(n + gap) * i for i in range(repeat + 1)]
+    q, k, v = (x.contiguous() for x in qkv(71, start[-1], h * g, h, d))
+    at = torch.arange(start[-1], device="cuda") % (n + gap)
+    q[..., 0], k[..., 0] = 1.0, 0.0
+    k[(at >= 150) & (at < 153), :, 0] = 7.3                  # in base 2: 10.5 over the others, at a scale of 1
+    q[..., 1:] *= 0.05
+    lens = i32([n] * repeat)
+    behind = at >= n
+    outs = []
+    for fill in (0.0, 1.0):
+        for x in (q, k, v):
+            x[behind] = 0.0
+        if fill and what == "large":
+            q[behind], k[behind] = 3.0, 30.0
+        if fill and what == "nan":
+            q[behind], k[behind], v[behind] = math.nan, math.nan, math.inf
+        if fill and what == "first":                         # rows without a finite logit in their first block
+            q[behind], k[behind] = -math.inf, 1.0
+        lse = torch.zeros(h * g, start[-1], device="cuda")
+        out = kvp.kvp_prompt_attn(q, k, v, i32(start), seq_len=lens, scale=1.0, lse=lse)
+        outs.append((out[~behind], lse[:, ~behind]))
+    for x, y in zip(*outs):
+        assert torch.equal(x, y)
+    for x in (q, k, v):
+        x[behind] = 0.0
+    want, want_lse, tol, lse_tol = ref.attention(q, k, v, [(a, n) for a in start[:-1]], 1.0)
+    ref.within(outs[1][0], want[~behind], tol[~behind], "out")
+    ref.within(outs[1][1], want_lse[:, ~behind], lse_tol[:, ~behind], "lse")
