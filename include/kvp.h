@@ -925,9 +925,12 @@ KVP_API kvp_status kvp_qk_norm_rope(int64_t n_tok, int n_q_heads, int n_k_heads,
  *
  * Sums, maxima and products accumulate in fp32. The softmax weights enter the
  * product with V as bf16 (relative error <= 2^-8 each; the normaliser sums the
- * unrounded ones), and out is rounded to bf16 once. Weights are carried at
- * 2^-28 or less, so that sums of any bf16 values stay in range; values below
- * 2^-98 lose precision.
+ * unrounded ones), and out is rounded to bf16 once. A row's weights are carried
+ * as 2^-28 times those against a reference, its largest logit so far or one that
+ * 128 keys in a row together pass by 2^15 at most: any 128 come to 2^-13 or less.
+ * So the sums stay in range for values of any size in sequences of up to 2^19
+ * rows, and in longer ones for values up to 2^147 / rows. Values below 2^-98 lose
+ * precision. A row's bits depend on its own sequence alone.
  *
  * n_seqs     0 .. 2^31 - 2^16;  n_tok rows in all, 0 .. 2^31 - 2^16
  * n_q_heads  a multiple of n_kv_heads, any quotient, 65535 at most; head_dim 64 or

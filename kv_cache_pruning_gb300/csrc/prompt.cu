@@ -20,9 +20,16 @@ namespace {
 // is masked.
 //
 // The reference M of a row's weights 2^(x c - M), c = scale log2 e, is its first
-// block's maximum and moves only when a later one passes it by 2^8; then the
-// softmax warps rescale O themselves, once the products of the block before are
-// done (at D = 128 a block's S comes after them).
+// block's maximum. It moves only when a block's weights come to more than 128 that
+// pass it by 2^8 would (so a single one may pass it by 2^15) and its maximum does
+// pass it by 2^8; then the softmax warps rescale O themselves, once the products of
+// the block before are done (at D = 128 a block's S comes after them).
+//
+// P in bf16: both operands of a product are of one type, and V is bf16. A weight is off by
+// 2^-8 at most, at random, so that it moves a row of many keys by 2e-4 to 3e-4 (2-norm,
+// the measured cases) where out's own rounding to bf16 moves it by 1.6e-3: 1.67e-3
+// against 1.65e-3 with exact weights. A second product for the rest of P would take
+// half as much tensor time again. Sums of weights are of the unrounded ones, in fp32.
 //
 // A masked weight is 0, but 0 times an infinite or NaN value is NaN: before the
 // products of a masked block its V tile is searched and such values are zeroed.
@@ -36,9 +43,9 @@ namespace {
 //
 // Bound: 4 D flops and an exponential for each (query, key) pair. 128 x 128 pairs
 // take the special-function units 512 cycles, and at D = 128 the tensor cores 512
-// for each of the two products. 16,384 tokens, 32/8 heads of 128: 1.33 ms, 1.66
-// PFLOP/s (88 % of the measured burst rate of a bf16 GEMM, 98 % of its sustained one),
-// at the power limit. Two threads a row with 64 logits each, for twice the warps:
+// for each of the two products. 16,384 tokens, 32/8 heads of 128: 1.33 to 1.36 ms
+// replayed from a graph, 1.62 to 1.66 PFLOP/s (86 to 88 % of the measured burst rate
+// of a bf16 GEMM, 95 to 98 % of its sustained one), at the power limit. Two threads a row with 64 logits each, for twice the warps:
 // 1,858 us for 1,529 at that stage. 8,192 tokens at D = 64: 252 us, bound by the chain
 // of a block in its softmax warp (the exponentials alone 112 us at their rate).
 constexpr int kInfo = 2;                    // work items written down ahead of their use

@@ -11,8 +11,8 @@ namespace {
 constexpr int kTile = 128;       // rows of a sequence that one product takes
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.4426950408889634f;
-// A weight is held as 2^(x - reference - kHeadroom): sums of up to 2^20 values of any bf16 size (the reference may
-// lag by 2^8) stay below 2^128 that way.
+// A weight is held as 2^(x - reference - kHeadroom). The attention lets the reference lag while a block's 128 weights come to
+// 2^-13 or less, so that 2^12 blocks of values of any bf16 size (2^19 keys) sum up to 2^127 at most.
 constexpr float kHeadroom = 28.f;
 
 struct Seqs {

@@ -22,7 +22,7 @@ namespace {
 // each thread sums half the queries, 32 at a time, in a loop short enough to stay
 // in the instruction cache. (Eight warps with 128 logits in registers each: 281 us
 // for 267 at that stage; 64 logits a round of a loop unrolled further: 294.) 8,192
-// tokens, 32/8 heads of 128: 251 us, 1.10 PFLOP/s; its longest items, which see every
+// tokens, 32/8 heads of 128: 246 us, 1.12 PFLOP/s; its longest items, which see every
 // query, are 15 % longer than an SM's share.
 //
 // Warps 0-7 and 8-15 sum for A and B, warp 16 issues the products, warp 17
