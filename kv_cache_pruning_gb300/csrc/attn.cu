@@ -1652,9 +1652,9 @@ kvp_status launch_attn(const AttnParams& p, int grid_limit, cudaStream_t st) {
   int grid = persistent_grid(attn_decode_kernel<D, G, kQ, kA>, C::SMEM, known);
   if (grid <= 0) return KVP_ERR_CUDA;
   if (grid_limit > 0 && grid > grid_limit) grid = grid_limit;
-  if (launch_pdl(attn_decode_kernel<D, G, kQ, kA>, dim3(grid), dim3(kThreads), C::SMEM, st, p) != cudaSuccess)
-    return KVP_ERR_CUDA;
-  return cudaGetLastError() == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
+  return launch_pdl(attn_decode_kernel<D, G, kQ, kA>, dim3(grid), dim3(kThreads), C::SMEM, st, p) == cudaSuccess
+             ? KVP_OK
+             : KVP_ERR_CUDA;
 }
 
 template <int D, int G, bool kQ, bool kA>
@@ -1665,10 +1665,10 @@ kvp_status launch_attn_mma(const AttnParams& p, const CUtensorMap& tmK, const CU
   int grid = persistent_grid(attn_mma_kernel<D, G, kQ, kA>, C::SMEM, known);
   if (grid <= 0) return KVP_ERR_CUDA;
   if (grid_limit > 0 && grid > grid_limit) grid = grid_limit;
-  if (launch_pdl(attn_mma_kernel<D, G, kQ, kA>, dim3(grid), dim3(kThreads), C::SMEM, st, p, tmK, tmV, tmKq, tmVq) !=
-      cudaSuccess)
-    return KVP_ERR_CUDA;
-  return cudaGetLastError() == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
+  return launch_pdl(attn_mma_kernel<D, G, kQ, kA>, dim3(grid), dim3(kThreads), C::SMEM, st, p, tmK, tmV, tmKq, tmVq) ==
+                 cudaSuccess
+             ? KVP_OK
+             : KVP_ERR_CUDA;
 }
 
 template <int D, bool kQ, bool kA>

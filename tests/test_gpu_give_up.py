@@ -42,6 +42,10 @@ extern "C" __attribute__((visibility("default"))) int get_waits() {
   int n = -1;
   return cudaMemcpyFromSymbol(&n, kvp::waits, sizeof n) == cudaSuccess ? n : -1;
 }
+extern "C" __attribute__((visibility("default"))) int leave_error() {   // refused on the host: no such device
+  return static_cast<int>(cudaSetDevice(1 << 20));
+}
+extern "C" __attribute__((visibility("default"))) int take_error() { return static_cast<int>(cudaGetLastError()); }
 """
 QUIETLY = """
 namespace {
@@ -176,3 +180,32 @@ def test_prompt_calls_end_where_a_wait_gave_up(kvp, libs, h, g, d, lens):
             assert time.monotonic() - before < 1.5                # one wait gave up: no other runs to the limit of two seconds
             assert code == kvp.KVP_ERR_TIMEOUT or at > 0 and code == 0 and torch.equal(acc, want_acc), at
         assert weigh(-1, n_last, acc) == 0 and torch.equal(acc, want_acc)
+
+
+# ---------------------------------------------------------------------------- a caller's pending error
+
+@pytest.mark.parametrize("g", [1, 2, 4, 8])
+def test_a_pending_error_stays_the_callers(kvp, libs, g):
+    """An error of the runtime's that the caller has left pending is neither taken away nor reported by a call: reported
+    between the attention and the kernel that adds, it left the sums out."""
+    lib, h, d, t = libs["attn"], 2, 64, 400
+    cache = cache_of(kvp, 3, [[300, 40]], 20, d, h, t)
+    q, acc, want = normal(5, 1, h * g, d), torch.zeros(1, h, t, device="cuda"), torch.zeros(1, h, t, device="cuda")
+    st, out = status(), torch.empty(1, h * g, d, device="cuda")
+    n = kvp.kvp_decode_attn_acc_workspace_bytes(1, h * g, h, d, 20)
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    kvp.kvp_decode_attn_acc(q, cache, t - 1, want)
+    assert lib.set_give_up(-1) == 0 and lib.take_error() == 0
+    for turn in range(2):                                    # (the runtime drops it itself where it first loads a kernel)
+        acc.zero_()
+        left = lib.leave_error()
+        assert left != 0
+        code = lib.kvp_decode_attn_acc(
+            1, h * g, h, d, q.data_ptr(), cache.k_pool.data_ptr(), cache.v_pool.data_ptr(), cache.expire_pool.data_ptr(),
+            cache.n_pages_cap, cache.page_table.data_ptr(), 20, cache.remap.data_ptr(), cache.count.data_ptr(), t - 1, 0.0,
+            out.data_ptr(), None, acc.data_ptr(), acc.stride(0), acc.stride(1), t, 0, ws.data_ptr(), n, st.data_ptr(),
+            stream())
+        pending = lib.take_error()
+        torch.cuda.synchronize()
+        assert code == kvp.KVP_OK and int(st) == 0 and torch.equal(acc, want)
+        assert turn == 0 or pending == left
