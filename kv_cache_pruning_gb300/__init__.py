@@ -1199,10 +1199,10 @@ def kvp_prompt_attn(q, k, v, seq_start, *, seq_len=None, scale=0.0, out=None, ls
 
 def kvp_prompt_weights(q, k, seq_start, lse, *, seq_len=None, scale=0.0, n_last=0, acc=None, status=None, stream=None):
     """acc fp32: the weight that each key of k [n_tok, H, d] received from the queries q [n_tok, Hq, d] of its sequence
-    (the last n_last of each sequence, 0: all), given kvp_prompt_attn's lse [Hq, n_tok]. acc is [n_tok, H] (the scores
-    that kvp_threshold and kvp_compact_masked take, where sequences are of one length) or [n_seqs, H, T] (the sums by
-    position that kvp_evict and kvp_decode_attn_acc take, T at least the longest sequence), of any strides; None: a new
-    [n_tok, H], zero in rows of no sequence."""
+    (the last n_last of each sequence, 0: all), given kvp_prompt_attn's lse [Hq, n_tok]; a query whose lse is -inf pays
+    nothing, whatever it holds. acc is [n_tok, H] (the scores that kvp_threshold and kvp_compact_masked take, where sequences
+    are of one length) or [n_seqs, H, T] (the sums by position that kvp_evict and kvp_decode_attn_acc take, T at least the
+    longest sequence), of any strides; None: a new [n_tok, H], zero in rows of no sequence."""
     dev = _device_of(q, "q")
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q and k must be [n_tok, heads, d]")
@@ -1262,7 +1262,8 @@ def kvp_decode_attn_acc(q, cache: PagedKV, now, acc, *, scale=0.0, out=None, lse
                         status=None, stream=None):
     """kvp_decode_attn_lse (lse optional) that adds the weights it pays, over the query heads of a kv head, to
     acc[b, h, position] (fp32 [B, H, T], positions side by side; zeros where none has been paid yet). A caller-provided
-    workspace must be zero-filled before its first use (torch.zeros)."""
+    workspace must be zero-filled before its first use (torch.zeros), and again after a call that recorded an error; after a
+    time-out the sums are as they were before the call."""
     return _attn_acc(_lib.kvp_decode_attn_acc, q, cache, now, acc, scale, out, lse, grid_limit, workspace, status, stream)
 
 
