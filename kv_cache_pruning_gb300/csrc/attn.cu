@@ -92,8 +92,10 @@ struct AttnParams {
   // accumulating kernels only
   float* logits;           // [B*H, max_pages, 16, G]: each slot's base-2 logits, -inf where it is not present
   float2* row_ml;          // [B, Hq]: each row's base-2 reference and its sum
-  int32_t* unfinished;     // nonzero: a wait gave up since the workspace was zeroed; nothing is added then
+  uint64_t* unfinished;    // kUnfinished: a wait gave up since the workspace was zeroed; nothing is added then
 };
+// No two fp32 sums: where the mark is, a call of another kind that the workspace served may have left its partial sums.
+constexpr uint64_t kUnfinished = 0x7fa5c3e17f9b2d4full;   // (the pattern of two signalling NaN, which no arithmetic leaves)
 
 // A row's natural log-sum-exp from its base-2 reference m2 and its sum
 // l = sum 2^(x - m2) of the base-2 logits x (-inf when the row is empty).
@@ -111,7 +113,7 @@ KVP_DEV void put_row(const AttnParams& p, size_t row, float m2, float l) {
 template <bool kA>
 KVP_DEV void gave_up(const AttnParams& p) {
   record_error(p.status, KVP_ERR_TIMEOUT);
-  if constexpr (kA) *static_cast<volatile int32_t*>(p.unfinished) = 1;
+  if constexpr (kA) *static_cast<volatile uint64_t*>(p.unfinished) = kUnfinished;
 }
 
 // Eight E4M3 codes (bytes of x then y, element 0 in the lowest byte) to fp32,
@@ -1742,7 +1744,7 @@ __global__ void __launch_bounds__(kAccThreads) acc_kernel(const AttnParams p, co
   const int first = blockIdx.x * (kAccThreads * kAccSlots) + threadIdx.x;
   const int n = clamp_count(p.count, bh, p.max_pages);
   if (first - static_cast<int>(threadIdx.x) >= n) return;
-  const bool unfinished = __ldcg(p.unfinished) != 0;
+  const bool unfinished = __ldcg(reinterpret_cast<const unsigned long long*>(p.unfinished)) == kUnfinished;
   float m[G], inv[G];
 #pragma unroll
   for (int i = 0; i < G; ++i) {
@@ -1923,7 +1925,7 @@ kvp_status decode_attn_impl(int batch, int n_q_heads, int n_kv_heads, int head_d
                ac ? ac->logits : nullptr,
                ac ? ac->row_ml : nullptr,
                // (m, l) of the last slot, which no warp has: the last one's, of the largest grid, is the one before
-               ac ? reinterpret_cast<int32_t*>(part_ml + (ws_slots(BH) - 1) * G * 2) : nullptr};
+               ac ? reinterpret_cast<uint64_t*>(part_ml + (ws_slots(BH) - 1) * G * 2) : nullptr};
   if (ac != nullptr) {
     // a thread's slots past the last one are ints; and as below, pools of 2^31 rows and more do not fit the device
     if (static_cast<int64_t>(max_pages) * kPage > 0x7fff0000) return KVP_ERR_UNSUPPORTED;

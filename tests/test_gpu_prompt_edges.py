@@ -245,3 +245,22 @@ def test_what_lies_behind_a_sequence_changes_no_bit(kvp, h, g, d, repeat, what):
     want, want_lse, tol, lse_tol = ref.attention(q, k, v, [(a, n) for a in start[:-1]], 1.0)
     ref.within(outs[1][0], want[~behind], tol[~behind], "out")
     ref.within(outs[1][1], want_lse[:, ~behind], lse_tol[:, ~behind], "lse")
+
+
+# ---------------------------------------------------------------------------- one workspace for calls of several kinds
+
+def test_decode_sums_share_a_workspace_with_other_groups(kvp):
+    """Layers of one batch and as many kv heads, whose query heads, widths and lengths differ: what one call leaves behind its
+    arrival counters says nothing to the next."""
+    b, h, t = 2, 4, 5200
+    kinds = [(8, 128, 5000), (1, 128, 5000), (4, 64, 300), (2, 128, 5000), (1, 64, 40), (8, 64, 5000), (2, 64, 5000), (4, 128, 5000)]
+    need = max(kvp.kvp_decode_attn_acc_workspace_bytes(b, h * g, h, d, n // 16 + 2) for g, d, n in kinds)
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    for i, (g, d, n) in enumerate(kinds * 2):
+        cache = cache_of(kvp, i, [[n, 17, n // 2, n], [1, n, n, 0]], n // 16 + 2, d, h, t)
+        q, acc = normal(i, b, h * g, d), torch.rand(b, h, t, device="cuda")
+        want = acc.clone()
+        fresh = kvp.kvp_decode_attn_acc(q, cache, t - 1, want)
+        st = status()
+        out = kvp.kvp_decode_attn_acc(q, cache, t - 1, acc, workspace=ws, status=st)
+        assert int(st) == 0 and torch.equal(out, fresh) and torch.equal(acc, want), (g, d, n)
