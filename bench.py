@@ -54,11 +54,11 @@ C2 = dict(name="llama3_8b_layer", d_model=4096, n_q_heads=32, n_kv_heads=8, head
 
 # DRAM read + write bytes per surviving page of the decode attention kernel at
 # this workload (attn_decode_kernel<128, 1>), from an ncu capture of one launch
-# of layer 0 (147,229 surviving pages): (1,216,815,872 + 3,043,072) B / 147,229,
+# of layer 0 (147,229 surviving pages): (1,216,812,288 + 2,759,424) B / 147,229,
 # against 8,256 B of K, V and expire values per page. The SHA-256 of attn.cu it
 # was taken on: the figure is reported only while the kernel source is unchanged.
-ATTN_DRAM_BYTES_PER_PAGE = 1219858944 / 147229
-ATTN_SRC_SHA = "e9dfbbac2fa53d4cc1a1fb9599472041e1e2bab652d519960c7d8e03a4b98bcd"
+ATTN_DRAM_BYTES_PER_PAGE = 1219571712 / 147229
+ATTN_SRC_SHA = "c1a67b18ad9a0afce6ad72d74053c00fa0b7999297fb2d9629f202463035a0d8"
 
 
 def c5_desc(w=C5):
